@@ -1,0 +1,453 @@
+// grouped.cu -- products grouped by expert (dg_layer_grouped_matmul,
+// dg_layer_grouped_weight_grad).
+//
+//   D[t, n]     = sa[t] sb[e, n] sum_k A[t, k] B[e, n, k]      for the rows t of group e
+//   dB[e, n, k] = sum over the rows t of group e of dD[t, n] A[t, k]
+//
+// One persistent kernel over CTA pairs, D^T orientation (ptx.cuh): P is the
+// operand of the output's contiguous dimension (B's features; A's columns for
+// the gradient), Q that of the output's rows (tokens; dD's columns).  A tile is
+// 256 features x up to 256 rows.  The groups' ends live on the device, so every
+// CTA scans them once into shared memory and walks the same list of tiles.
+//
+// Warp 0 loads (TMA, 128-byte swizzle, kStages stages), warp 1 issues the MMAs
+// (even CTA of the pair), warps 2-5 empty the two accumulators.
+
+#include <atomic>
+#include <cuda_bf16.h>
+
+#include "layer_common.h"
+#include "ptx.cuh"
+
+namespace {
+
+using namespace dgl;
+
+constexpr int kTileRows = 256;
+constexpr int kMaxExperts = 1024;
+constexpr int kStages = 6;
+constexpr uint32_t kStageQ = (kTileRows / 2) * kRowBytes;
+constexpr uint32_t kStage = kStageP + kStageQ;
+constexpr uint32_t kTableBytes = 2 * (kMaxExperts + 2) * 4;
+constexpr uint32_t kSmem = kStages * kStage + 4 * kStoreBuf + kTableBytes + 256 + 1024;
+constexpr uint32_t kTmemCols = 2 * kTileRows;
+constexpr int kBand = 8;      // row tiles swept together, for reuse in L2
+constexpr int kTailRows = 64; // rows of a K block in the gradient
+
+struct Args {
+  CUtensorMap p;           // 3-d: (K or features, features or K, expert)
+  CUtensorMap q;           // rows: box of 128 rows; gradient: box of 64 columns x 64 rows
+  CUtensorMap q16;         // rows: box of 16 rows
+  CUtensorMap p_tail, q_tail;  // gradient: each group's last rows, padded with zeros
+  const int32_t* ends;
+  int experts, T;
+  int feats, rows, red;    // output features; gradient: output rows; forward: reduction length
+  void* out;
+  const float *sa, *sb;
+  int64_t sa_s, sb_e, sb_n;
+  uint32_t idesc;
+  Watch watch;
+};
+
+struct Tile {
+  int e, row0, rows, f0, kblocks, k0, tail;
+};
+
+// Group starts (start[e], e <= experts; start[experts + 1] = T) and the number
+// of tiles before each group, by one warp.  Ends are clamped to [previous end,
+// T]; the forward's group `experts` is the rows past the last end.
+template <bool GRAD>
+__device__ void scan_groups(const Args& p, int* start, int* first, int lane) {
+  const int nf = (p.feats + kPairFeats - 1) / kPairFeats;
+  const int groups = GRAD ? p.experts : p.experts + 1;
+  int end = 0, tiles = 0;
+  if (lane == 0) start[0] = first[0] = 0;
+  for (int b = 0; b < groups; b += 32) {
+    const int e = b + lane;
+    int v = e < p.experts ? min(max(__ldg(p.ends + e), 0), p.T) : p.T;
+    if (lane == 0) v = max(v, end);
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v = max(v, u);
+    }
+    int s = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) s = end;
+    const int rows = GRAD ? p.rows : v - s;
+    int t = e < groups ? (rows + kTileRows - 1) / kTileRows * nf : 0;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, t, o);
+      if (lane >= o) t += u;
+    }
+    t += tiles;
+    if (e < groups) start[e + 1] = v, first[e + 1] = t;
+    end = __shfl_sync(0xffffffffu, v, 31);
+    tiles = __shfl_sync(0xffffffffu, t, 31);
+  }
+}
+
+// Tile t of the list; `e`: a cursor that only moves forward.  Within a group,
+// bands of kBand row tiles are swept feature tile by feature tile.
+template <bool GRAD, bool F8>
+__device__ __forceinline__ Tile tile_at(const Args& p, const int* start, const int* first, int t, int& e) {
+  while (t >= first[e + 1]) ++e;
+  const int len = start[e + 1] - start[e], rows = GRAD ? p.rows : len;
+  const int nt = (rows + kTileRows - 1) / kTileRows, nf = (p.feats + kPairFeats - 1) / kPairFeats;
+  const int j = t - first[e], band = j / (kBand * nf), in = j - band * kBand * nf;
+  const int wide = min(kBand, nt - band * kBand), f = in / wide, r = band * kBand + in - f * wide;
+  Tile tl;
+  tl.e = e;
+  tl.rows = min(kTileRows, rows - r * kTileRows);
+  tl.f0 = f * kPairFeats;
+  if (GRAD) {
+    tl.row0 = r * kTileRows;
+    tl.k0 = start[e];
+    tl.kblocks = (len + kTailRows - 1) / kTailRows;
+    tl.tail = len % kTailRows;
+  } else {
+    constexpr int kb = F8 ? 128 : 64;
+    tl.row0 = start[e] + r * kTileRows;
+    tl.k0 = 0;
+    tl.kblocks = e < p.experts ? (p.red + kb - 1) / kb : 0;  // rows past the last group: zeros
+    tl.tail = 0;
+  }
+  return tl;
+}
+
+// Accumulator columns of a tile: its rows rounded up to what a pair's MMA takes
+// (the gradient's operand boxes are whole).
+template <bool GRAD>
+__device__ __forceinline__ int columns(const Tile& t) {
+  return GRAD ? kTileRows : (t.rows + 31) / 32 * 32;
+}
+
+template <bool F8, bool PMN, bool GRAD, bool OUT32>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    grouped_kernel(const __grid_constant__ Args p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* store_buf = smem + kStages * kStage;
+  int* start = reinterpret_cast<int*>(store_buf + 4 * kStoreBuf);
+  int* first = start + kMaxExperts + 2;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(start) + kTableBytes);
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t half = cluster_ctarank();
+  const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 8);
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(s_tmem), kTmemCols);
+  if (warp == 2) scan_groups<GRAD>(p, start, first, lane);
+  fence_before();
+  __syncwarp();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = *s_tmem;
+  const int total = first[GRAD ? p.experts : p.experts + 1];
+  const uint32_t base = smem_u32(smem);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ------------------------------------------------------------ producer
+      prefetch_map(&p.p);
+      prefetch_map(&p.q);
+      uint32_t stage = 0, phase = 0;
+      int e = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units) {
+        const Tile tl = tile_at<GRAD, F8>(p, start, first, t, e);
+        const int n = columns<GRAD>(tl), mine = n / 2;  // this CTA's share of the rows operand
+        const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
+        for (int kb = 0; kb < tl.kblocks; ++kb) {
+          if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
+          const uint32_t fb = mapa(full + 8 * stage, 0);
+          if (half == 0) mbar_expect(full + 8 * stage, 2 * (kStageP + (uint32_t)mine * kRowBytes));
+          const uint32_t sp = base + stage * kStage, sq = sp + kStageP;
+          if constexpr (GRAD) {
+            // 64 columns x 64 rows per box, MN-major; a group's last rows come
+            // from their zero-padded copy, so no other group's rows enter
+            const bool tail = tl.tail != 0 && kb == tl.kblocks - 1;
+            const CUtensorMap* pm = tail ? &p.p_tail : &p.p;
+            const CUtensorMap* qm = tail ? &p.q_tail : &p.q;
+            const int y = tl.k0 + kb * kTailRows;
+            for (int i = 0; i < 2; ++i) {
+              tma_3d(sp + i * (kStageP / 2), pm, fb, f + i * 64, tail ? 0 : y, tail ? tl.e : 0);
+              tma_2d(sq + i * (kStageQ / 2), qm, fb, q0 + i * 64, tail ? tl.e * kTailRows : y);
+            }
+          } else {
+            const int x = kb * (F8 ? 128 : 64);
+            if constexpr (PMN) {
+              tma_3d(sp, &p.p, fb, f, x, tl.e);
+              tma_3d(sp + kStageP / 2, &p.p, fb, f + 64, x, tl.e);
+            } else {
+              tma_3d(sp, &p.p, fb, x, f, tl.e);
+            }
+            if (n == kTileRows)
+              tma_2d(sq, &p.q, fb, x, q0);
+            else
+              for (int i = 0; i < mine; i += 16) tma_2d(sq + i * kRowBytes, &p.q16, fb, x, q0 + i);
+          }
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && half == 0) {
+      // ----------------------------------------------------------------- MMA
+      uint32_t stage = 0, phase = 0, it = 0;
+      int e = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units, ++it) {
+        const Tile tl = tile_at<GRAD, F8>(p, start, first, t, e);
+        const uint32_t idesc = p.idesc | idesc_columns((uint32_t)columns<GRAD>(tl));
+        const uint32_t buf = it & 1;
+        if (!(ok = mbar_wait(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
+        fence_after();
+        const uint32_t d = tmem + buf * kTileRows;
+        for (int kb = 0; kb < tl.kblocks; ++kb) {
+          if (!(ok = mbar_wait(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
+          fence_after();
+          const uint32_t sp = base + stage * kStage, sq = sp + kStageP;
+          const uint64_t pd = PMN ? desc_mn_major(sp, kStageP / 2) : desc_k_major(sp);
+          const uint64_t qd = GRAD ? desc_mn_major(sq, kStageQ / 2) : desc_k_major(sq);
+          // per instruction: 32 bytes along a K-major row, or 16 rows of 128 bytes
+          constexpr uint64_t p_step = PMN ? 16 * kRowBytes / 16 : 2, q_step = GRAD ? 16 * kRowBytes / 16 : 2;
+          const int subs = GRAD && tl.tail != 0 && kb == tl.kblocks - 1 ? (tl.tail + 15) / 16 : 4;
+          for (int s = 0; s < subs; ++s)
+            mma_pair<F8>(d, pd + s * p_step, qd + s * q_step, idesc, (kb | s) != 0);
+          commit_pair(empty + 8 * stage);
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+        if (ok) commit_pair(tfull + 8 * buf);
+      }
+    }
+  } else {
+    // ------------------------------------------------------------- epilogue
+    const int q = warp & 3;  // the TMEM lanes that this warp may read
+    uint8_t* box = store_buf + q * kStoreBuf;
+    uint32_t it = 0;
+    int e = 0;
+    for (int t = unit; t < total; t += units, ++it) {
+      const Tile tl = tile_at<GRAD, F8>(p, start, first, t, e);
+      const uint32_t buf = it & 1;
+      uint32_t go = 1;
+      if (lane == 0) go = mbar_wait(p.watch, tfull + 8 * buf, (it >> 1) & 1, 0x400u | buf);
+      if (!__shfl_sync(0xffffffffu, go, 0)) {
+        settle();
+        break;
+      }
+      fence_after();
+      const int f0 = tl.f0 + (int)half * kLanes + q * 32;  // this warp's first feature
+      const int feats_ok = min(32, p.feats - f0);
+      const int64_t row0 = (int64_t)tl.row0 + (GRAD ? (int64_t)tl.e * p.rows : 0);
+      float sb = 1.f;
+      if (!GRAD && p.sb && lane < feats_ok && tl.e < p.experts)
+        sb = __ldg(p.sb + tl.e * p.sb_e + (int64_t)(f0 + lane) * p.sb_n);
+      const int nch = (tl.rows + kChunk - 1) / kChunk;
+#pragma unroll 1
+      for (int c = 0; c < nch; ++c) {
+        float v[32];
+        if (tl.kblocks > 0) {
+          uint32_t u[32];
+          tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * kTileRows + c * kChunk, u);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] = 0.f;
+        }
+        if (c == nch - 1) {  // the accumulator has been read
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa(tempty + 8 * buf, 0));
+        }
+        const int rows_ok = min(kChunk, tl.rows - c * kChunk);
+        const int64_t r0 = row0 + c * kChunk;
+        if (!GRAD && (p.sa || p.sb) && tl.kblocks > 0) {
+          float sa = 1.f;
+          if (p.sa && lane < rows_ok) sa = __ldg(p.sa + (r0 + lane) * p.sa_s);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, sa, i) * sb;
+        }
+        const int64_t at = r0 * p.feats + f0;
+        if constexpr (OUT32)
+          store_box_f32(static_cast<float*>(p.out) + at, p.feats, rows_ok, feats_ok, lane, v);
+        else
+          store_box_bf16(static_cast<__nv_bfloat16*>(p.out) + at, p.feats, rows_ok, feats_ok, lane, v, box);
+      }
+    }
+  }
+  fence_before();
+  __syncwarp();
+  cluster_sync();  // both CTAs are done with each other's barriers and shared memory
+  fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_free(tmem, kTmemCols);
+  }
+}
+
+// The gradient's last rows of each group (its row count modulo 64), copied to
+// [expert][64][columns] with zeros up to the next multiple of 16 rows.
+__global__ void __launch_bounds__(256) grouped_tail_kernel(const int32_t* ends, int T, const __nv_bfloat16* a,
+                                                           int64_t ld_a, int64_t ka, __nv_bfloat16* a_tail,
+                                                           const __nv_bfloat16* d, int64_t ld_d, int64_t kd,
+                                                           __nv_bfloat16* d_tail) {
+  __shared__ int s_from[8], s_to[8];
+  const int e = blockIdx.y;
+  int from = 0, to = 0;  // this group's clamped start and end: the largest ends before and up to it
+  for (int i = threadIdx.x; i <= e; i += blockDim.x) {
+    const int v = min(max(__ldg(ends + i), 0), T);
+    to = max(to, v);
+    if (i < e) from = max(from, v);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    from = max(from, __shfl_xor_sync(0xffffffffu, from, o));
+    to = max(to, __shfl_xor_sync(0xffffffffu, to, o));
+  }
+  if ((threadIdx.x & 31) == 0) s_from[threadIdx.x >> 5] = from, s_to[threadIdx.x >> 5] = to;
+  __syncthreads();
+  for (int i = 0; i < 8; ++i) from = max(from, s_from[i]), to = max(to, s_to[i]);
+  const int tail = (to - from) % kTailRows;
+  if (tail == 0) return;
+  const int padded = (tail + 15) / 16 * 16;
+  const int64_t t0 = to - tail, va = ka / 8, vd = kd / 8, n = padded * (va + vd);
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < n; i += (int64_t)gridDim.x * blockDim.x) {
+    const bool of_a = i < padded * va;
+    const int64_t j = of_a ? i : i - padded * va, per = of_a ? va : vd, r = j / per, c = j - r * per;
+    uint4 u = make_uint4(0, 0, 0, 0);
+    if (r < tail)
+      u = *reinterpret_cast<const uint4*>((of_a ? a + (t0 + r) * ld_a : d + (t0 + r) * ld_d) + c * 8);
+    *reinterpret_cast<uint4*>((of_a ? a_tail + ((int64_t)e * kTailRows + r) * ka
+                                    : d_tail + ((int64_t)e * kTailRows + r) * kd) + c * 8) = u;
+  }
+}
+
+std::atomic<uint32_t> g_epoch{1};
+
+template <bool F8, bool PMN, bool GRAD, bool OUT32>
+int launch(const Args& p, int64_t most_tiles, cudaStream_t s) {
+  auto* kernel = grouped_kernel<F8, PMN, GRAD, OUT32>;
+  int sms = 0;
+  if (int rc = sm_count(&sms)) return rc;
+  DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+  const int64_t units = most_tiles < sms / 2 ? most_tiles : sms / 2;
+  kernel<<<(unsigned)(2 * units), kThreads, kSmem, s>>>(p);
+  DGL_LAUNCHED();
+  return DG_OK;
+}
+
+uint32_t format_of(int type) { return type == DG_TYPE_BF16 ? 1u : type == DG_TYPE_E5M2 ? 1u : 0u; }
+bool is8(int type) { return type == DG_TYPE_E4M3 || type == DG_TYPE_E5M2; }
+
+int check_sizes(int64_t T, int64_t N, int64_t K, int experts) {
+  if (T < 0 || N < 0 || K < 0 || T > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
+    return fail(DG_ERR_ARG, "T %lld, N %lld, K %lld out of range", (long long)T, (long long)N, (long long)K);
+  if (experts < 1 || experts > kMaxExperts) return fail(DG_ERR_ARG, "experts (%d) must be 1 to %d", experts, kMaxExperts);
+  return DG_OK;
+}
+
+Watch watch_of(void* status) {
+  return Watch{static_cast<unsigned long long*>(status), g_epoch.fetch_add(1, std::memory_order_relaxed), 4000000000ull};
+}
+
+}  // namespace
+
+extern "C" size_t dg_layer_grouped_workspace(void) { return 256; }
+
+extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, const void* B, int64_t ld_b,
+                                       int64_t ld_e, int b_type, int b_n_major, const int32_t* ends, int experts,
+                                       const float* scale_a, int64_t sa, const float* scale_b, int64_t sb_e,
+                                       int64_t sb_n, void* D, int d_type, int64_t T, int64_t N, int64_t K,
+                                       void* workspace, void* status, void* stream) {
+  if (int rc = check_sizes(T, N, K, experts)) return rc;
+  const bool f8 = is8(a_type) && is8(b_type);
+  if (!f8 && (a_type != DG_TYPE_BF16 || b_type != DG_TYPE_BF16))
+    return fail(DG_ERR_ARG, "A and B are both bf16 or both 8-bit (types %d, %d)", a_type, b_type);
+  if (f8 && b_n_major) return fail(DG_ERR_ARG, "an 8-bit B must be contiguous along K");
+  if (d_type != DG_TYPE_BF16 && d_type != DG_TYPE_F32) return fail(DG_ERR_ARG, "D is bf16 or fp32 (got type %d)", d_type);
+  const int64_t esz = f8 ? 1 : 2;
+  if (N % 8 || K * esz % 16) return fail(DG_ERR_SHAPE, "N %% 8 and K %% %d must be 0 (N %lld, K %lld)", f8 ? 16 : 8, (long long)N, (long long)K);
+  if (T == 0 || N == 0) return DG_OK;
+  if (!D || !ends || !status) return fail(DG_ERR_ARG, "D, ends and status must not be null");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (K == 0) {
+    DGL_CUDA(cudaMemsetAsync(D, 0, (size_t)T * N * (d_type == DG_TYPE_F32 ? 4 : 2), s));
+    return DG_OK;
+  }
+  if (!A || !B || !workspace) return fail(DG_ERR_ARG, "A, B and workspace must not be null");
+  const int64_t inner = b_n_major ? N : K;
+  if (!aligned16(A) || !aligned16(B) || !aligned16(D) || ld_a * esz % 16 || ld_b * esz % 16 || ld_e * esz % 16)
+    return fail(DG_ERR_ARG, "A, B, D and their pitches must be multiples of 16 bytes");
+  if (ld_a < K || ld_b < inner || (experts > 1 && ld_e <= 0)) return fail(DG_ERR_ARG, "a pitch is shorter than its rows");
+  Args p{};
+  const int64_t pd[3] = {inner, b_n_major ? K : N, experts}, ps[2] = {ld_b, experts > 1 ? ld_e : ld_b * pd[1]};
+  const int64_t qd[2] = {K, T}, qs[1] = {ld_a};
+  if (int rc = encode_map(&p.p, B, (int)esz, 3, pd, ps, b_n_major ? 64 : kLanes)) return rc;
+  if (int rc = encode_map(&p.q, A, (int)esz, 2, qd, qs, kTileRows / 2)) return rc;
+  if (int rc = encode_map(&p.q16, A, (int)esz, 2, qd, qs, 16)) return rc;
+  p.ends = ends, p.experts = experts, p.T = (int)T, p.feats = (int)N, p.rows = 0, p.red = (int)K, p.out = D;
+  p.sa = scale_a, p.sb = scale_b, p.sa_s = sa, p.sb_e = sb_e, p.sb_n = sb_n;
+  p.idesc = idesc_of(format_of(b_type), format_of(a_type), b_n_major != 0, false);
+  p.watch = watch_of(status);
+  const int64_t most = (T / kTileRows + experts + 1) * ((N + kPairFeats - 1) / kPairFeats);
+  if (most > INT32_MAX) return fail(DG_ERR_ARG, "T x N is too large (%lld tiles)", (long long)most);
+  const bool f32 = d_type == DG_TYPE_F32;
+  if (f8) return f32 ? launch<true, false, false, true>(p, most, s) : launch<true, false, false, false>(p, most, s);
+  if (b_n_major) return f32 ? launch<false, true, false, true>(p, most, s) : launch<false, true, false, false>(p, most, s);
+  return f32 ? launch<false, false, false, true>(p, most, s) : launch<false, false, false, false>(p, most, s);
+}
+
+extern "C" size_t dg_layer_grouped_grad_workspace(int experts, int64_t N, int64_t K) {
+  if (experts < 1 || N <= 0 || K <= 0) return 256;
+  return (size_t)experts * kTailRows * (size_t)(N + K) * 2 + 256;
+}
+
+extern "C" int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const void* A, int64_t ld_a,
+                                            const int32_t* ends, int experts, void* dB, int d_type, int64_t T,
+                                            int64_t N, int64_t K, void* workspace, void* status, void* stream) {
+  if (int rc = check_sizes(T, N, K, experts)) return rc;
+  if (d_type != DG_TYPE_BF16 && d_type != DG_TYPE_F32) return fail(DG_ERR_ARG, "dB is bf16 or fp32 (got type %d)", d_type);
+  if (N % 8 || K % 8) return fail(DG_ERR_SHAPE, "N %% 8 and K %% 8 must be 0 (N %lld, K %lld)", (long long)N, (long long)K);
+  if (N == 0 || K == 0) return DG_OK;
+  if (!dB) return fail(DG_ERR_ARG, "dB must not be null");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool f32 = d_type == DG_TYPE_F32;
+  if (T == 0) {
+    DGL_CUDA(cudaMemsetAsync(dB, 0, (size_t)experts * N * K * (f32 ? 4 : 2), s));
+    return DG_OK;
+  }
+  if (!dD || !A || !ends || !workspace || !status) return fail(DG_ERR_ARG, "a required pointer is null");
+  if (!aligned16(dD) || !aligned16(A) || !aligned16(dB) || !aligned16(workspace) || ld_d % 8 || ld_a % 8)
+    return fail(DG_ERR_ARG, "dD, A, dB, their pitches and the workspace must be multiples of 16 bytes");
+  if (ld_d < N || ld_a < K) return fail(DG_ERR_ARG, "a pitch is shorter than its rows");
+  const int64_t tiles = (int64_t)experts * ((N + kTileRows - 1) / kTileRows) * ((K + kPairFeats - 1) / kPairFeats);
+  if (tiles > INT32_MAX) return fail(DG_ERR_ARG, "experts x N x K is too large (%lld tiles)", (long long)tiles);
+  __nv_bfloat16* a_tail = static_cast<__nv_bfloat16*>(workspace);
+  __nv_bfloat16* d_tail = a_tail + (int64_t)experts * kTailRows * K;
+  Args p{};
+  const int64_t pd[3] = {K, T, 1}, ps[2] = {ld_a, ld_a * T}, ptd[3] = {K, kTailRows, experts}, pts[2] = {K, K * kTailRows};
+  const int64_t qd[2] = {N, T}, qs[1] = {ld_d}, qtd[2] = {N, (int64_t)experts * kTailRows}, qts[1] = {N};
+  if (int rc = encode_map(&p.p, A, 2, 3, pd, ps, 64)) return rc;
+  if (int rc = encode_map(&p.q, dD, 2, 2, qd, qs, 64)) return rc;
+  if (int rc = encode_map(&p.p_tail, a_tail, 2, 3, ptd, pts, 64)) return rc;
+  if (int rc = encode_map(&p.q_tail, d_tail, 2, 2, qtd, qts, 64)) return rc;
+  p.ends = ends, p.experts = experts, p.T = (int)T, p.feats = (int)K, p.rows = (int)N, p.red = 0, p.out = dB;
+  p.idesc = idesc_of(1, 1, true, true);
+  p.watch = watch_of(status);
+  const int64_t vecs = 64 * (N + K) / 8;
+  const unsigned gx = (unsigned)((vecs + 1023) / 1024 < 64 ? (vecs + 1023) / 1024 : 64);
+  grouped_tail_kernel<<<dim3(gx, experts), 256, 0, s>>>(ends, (int)T, static_cast<const __nv_bfloat16*>(A), ld_a, K,
+                                                        a_tail, static_cast<const __nv_bfloat16*>(dD), ld_d, N, d_tail);
+  DGL_LAUNCHED();
+  return f32 ? launch<false, true, true, true>(p, tiles, s) : launch<false, true, true, false>(p, tiles, s);
+}

@@ -1,0 +1,258 @@
+// mx4_gemm.cu -- product of two microscaled 4-bit tensors (dg_layer_mx4_matmul).
+//
+//   D[m, n] = sum over 32-blocks j of 2^(ea[m, j] + eb[n, j]) sum_{k in j} a[m, k] b[n, k]
+//
+// The block-scaled tensor core instruction (tcgen05.mma kind::mxf4, K = 64, two
+// scales per row) applies the scales itself: codes stay packed in shared
+// memory, the scales go to tensor memory.  CTA pairs, D^T orientation
+// (ptx.cuh): P = b (features), Q = a (rows); a tile is 256 features x up to 192
+// rows, so that two fp32 accumulators (384 columns) leave tensor memory for the
+// scales of four K blocks.
+//
+// Scales of 128 rows x 128 columns are one 512-byte tile of the scale layout
+// and four columns of tensor memory (tcgen05.cp 32x128b, copied to all four
+// lane quarters).  A row tile of 192 starts at an even or odd multiple of 64:
+// the odd ones start two columns into their scales.
+
+#include <atomic>
+#include <cuda_bf16.h>
+
+#include "layer_common.h"
+#include "ptx.cuh"
+
+namespace {
+
+using namespace dgl;
+
+constexpr int kTileRows = 192;
+constexpr int kStages = 7;
+constexpr int kBlockK = 256;                     // columns per K block: 128 bytes of codes
+constexpr uint32_t kStageQ = (kTileRows / 2) * kRowBytes;
+constexpr uint32_t kScaleP = 1024, kScaleQ = 2048;  // scales of 128 and of 256 rows x 256 columns
+constexpr uint32_t kStage = kStageP + kStageQ + kScaleP + kScaleQ;
+constexpr uint32_t kSmem = kStages * kStage + 4 * kStoreBuf + 256 + 1024;
+constexpr uint32_t kTmemCols = 512, kScaleCol = 2 * kTileRows;
+constexpr int kScaleBufs = 4;                    // 24 columns each: 2 x 4 for P, 2 x 8 for Q
+constexpr int kBand = 8;
+
+struct Args {
+  CUtensorMap p, q, q16;   // codes as bytes: boxes of 128, 96 and 16 rows
+  CUtensorMap sp, sq;      // scales: (256 words, K block, row tile), boxes of one and two row tiles
+  int rows, feats, kblocks;
+  void* out;
+  Watch watch;
+};
+
+__device__ __forceinline__ void scale_copy(uint32_t taddr, uint32_t saddr) {
+  // 32 rows of 16 bytes without swizzle: groups of 8 rows 128 bytes apart
+  const uint64_t desc = (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 32) | (1ull << 46);
+  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_mx4(uint32_t d, uint64_t pdesc, uint64_t qdesc, uint32_t idesc, uint32_t psf,
+                                        uint32_t qsf, uint32_t acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %6, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}\n" ::"r"(d),
+      "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(psf), "r"(qsf), "r"(acc)
+      : "memory");
+}
+
+// Instruction descriptor of the block-scaled kinds: scale ids at bits 4 (Q) and
+// 29 (P), e2m1 formats (1) at bits 7 and 10, columns / 8 at bit 17, e8m0 scales
+// (bit 23), lanes / 16 at bit 24.
+__device__ __forceinline__ uint32_t idesc_mx4(uint32_t n, uint32_t sf) {
+  return (sf << 4) | (1u << 7) | (1u << 10) | ((n >> 3) << 17) | (1u << 23) | ((uint32_t)(kPairFeats >> 4) << 24) |
+         (sf << 29);
+}
+
+struct Tile {
+  int row0, rows, f0;
+};
+__device__ __forceinline__ Tile tile_at(const Args& p, int t) {
+  const int nt = (p.rows + kTileRows - 1) / kTileRows, nf = (p.feats + kPairFeats - 1) / kPairFeats;
+  const int band = t / (kBand * nf), in = t - band * kBand * nf;
+  const int wide = min(kBand, nt - band * kBand), f = in / wide, r = band * kBand + in - f * wide;
+  return Tile{r * kTileRows, min(kTileRows, p.rows - r * kTileRows), f * kPairFeats};
+}
+
+template <bool OUT32>
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_kernel(const __grid_constant__ Args p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  uint8_t* store_buf = smem + kStages * kStage;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(store_buf + 4 * kStoreBuf);
+  const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16;
+  uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t half = cluster_ctarank();
+  const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
+    for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 8);
+    mbar_init_fence();
+  }
+  if (warp == 1) tmem_alloc(smem_u32(s_tmem), kTmemCols);
+  fence_before();
+  __syncwarp();
+  cluster_sync();
+  fence_after();
+  const uint32_t tmem = *s_tmem, base = smem_u32(smem);
+  const int total = ((p.rows + kTileRows - 1) / kTileRows) * ((p.feats + kPairFeats - 1) / kPairFeats);
+
+  if (warp == 0) {
+    if (lane == 0) {
+      prefetch_map(&p.p);
+      prefetch_map(&p.q);
+      uint32_t stage = 0, phase = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units) {
+        const Tile tl = tile_at(p, t);
+        const int n = (tl.rows + 31) / 32 * 32, mine = n / 2;
+        const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
+          const uint32_t fb = mapa(full + 8 * stage, 0);
+          if (half == 0) mbar_expect(full + 8 * stage, 2 * (kStageP + (uint32_t)mine * kRowBytes + kScaleP + kScaleQ));
+          const uint32_t sp = base + stage * kStage, sq = sp + kStageP, ss = sq + kStageQ;
+          tma_2d(sp, &p.p, fb, kb * 128, f);
+          if (n == kTileRows)
+            tma_2d(sq, &p.q, fb, kb * 128, q0);
+          else
+            for (int i = 0; i < mine; i += 16) tma_2d(sq + i * kRowBytes, &p.q16, fb, kb * 128, q0 + i);
+          tma_3d(ss, &p.sp, fb, 0, kb, f / 128);
+          tma_3d(ss + kScaleP, &p.sq, fb, 0, kb, tl.row0 / 128);  // every row's: each CTA needs them all
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && half == 0) {
+      uint32_t stage = 0, phase = 0, it = 0, sbuf = 0;
+      bool ok = true;
+      for (int t = unit; t < total && ok; t += units, ++it) {
+        const Tile tl = tile_at(p, t);
+        const uint32_t n = (uint32_t)(tl.rows + 31) / 32 * 32, buf = it & 1;
+        const uint32_t odd = (tl.row0 & 64) ? 2u : 0u;  // columns into the first scale tile
+        if (!(ok = mbar_wait(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
+        fence_after();
+        const uint32_t d = tmem + buf * kTileRows;
+        for (int kb = 0; kb < p.kblocks; ++kb) {
+          if (!(ok = mbar_wait(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
+          fence_after();
+          const uint32_t sp = base + stage * kStage, sq = sp + kStageP, ss = sq + kStageQ;
+          const uint32_t tp = tmem + kScaleCol + sbuf * 24, tq = tp + 8;
+          // copies and MMAs of one thread run in order
+#pragma unroll
+          for (uint32_t k = 0; k < 2; ++k) {
+            scale_copy(tp + 4 * k, ss + 512 * k);
+            scale_copy(tq + 8 * k, ss + kScaleP + 512 * k);
+            scale_copy(tq + 8 * k + 4, ss + kScaleP + 1024 + 512 * k);
+          }
+          const uint64_t pd = desc_k_major(sp), qd = desc_k_major(sq);
+#pragma unroll
+          for (uint32_t s = 0; s < 4; ++s)
+            mma_mx4(d, pd + 2 * s, qd + 2 * s, idesc_mx4(n, (s & 1) * 2), tp + 4 * (s >> 1), tq + 8 * (s >> 1) + odd,
+                    (kb | s) != 0);
+          commit_pair(empty + 8 * stage);
+          sbuf = (sbuf + 1) % kScaleBufs;
+          if (++stage == kStages) stage = 0, phase ^= 1;
+        }
+        if (ok) commit_pair(tfull + 8 * buf);
+      }
+    }
+  } else {
+    const int q = warp & 3;
+    uint8_t* box = store_buf + q * kStoreBuf;
+    uint32_t it = 0;
+    for (int t = unit; t < total; t += units, ++it) {
+      const Tile tl = tile_at(p, t);
+      const uint32_t buf = it & 1;
+      uint32_t go = 1;
+      if (lane == 0) go = mbar_wait(p.watch, tfull + 8 * buf, (it >> 1) & 1, 0x400u | buf);
+      if (!__shfl_sync(0xffffffffu, go, 0)) {
+        settle();
+        break;
+      }
+      fence_after();
+      const int f0 = tl.f0 + (int)half * kLanes + q * 32, feats_ok = min(32, p.feats - f0);
+      const int nch = (tl.rows + kChunk - 1) / kChunk;
+#pragma unroll 1
+      for (int c = 0; c < nch; ++c) {
+        uint32_t u[32];
+        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * kTileRows + c * kChunk, u);
+        tmem_ld_wait();
+        if (c == nch - 1) {
+          fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(mapa(tempty + 8 * buf, 0));
+        }
+        float v[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+        const int64_t at = (int64_t)(tl.row0 + c * kChunk) * p.feats + f0;
+        const int rows_ok = min(kChunk, tl.rows - c * kChunk);
+        if constexpr (OUT32)
+          store_box_f32(static_cast<float*>(p.out) + at, p.feats, rows_ok, feats_ok, lane, v);
+        else
+          store_box_bf16(static_cast<__nv_bfloat16*>(p.out) + at, p.feats, rows_ok, feats_ok, lane, v, box);
+      }
+    }
+  }
+  fence_before();
+  __syncwarp();
+  cluster_sync();
+  fence_after();
+  if (warp == 1) {
+    __syncwarp();
+    tmem_free(tmem, kTmemCols);
+  }
+}
+
+std::atomic<uint32_t> g_epoch{0x80000001u};
+
+template <bool OUT32>
+int launch(const Args& p, int64_t tiles, cudaStream_t s) {
+  int sms = 0;
+  if (int rc = sm_count(&sms)) return rc;
+  DGL_CUDA(cudaFuncSetAttribute(mx4_kernel<OUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+  const int64_t units = tiles < sms / 2 ? tiles : sms / 2;
+  mx4_kernel<OUT32><<<(unsigned)(2 * units), kThreads, kSmem, s>>>(p);
+  DGL_LAUNCHED();
+  return DG_OK;
+}
+
+}  // namespace
+
+extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, const void* b_codes,
+                                   const void* b_scales, void* D, int d_type, int64_t M, int64_t N, int64_t K,
+                                   void* workspace, void* status, void* stream) {
+  (void)workspace;
+  if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
+    return fail(DG_ERR_ARG, "M %lld, N %lld, K %lld out of range", (long long)M, (long long)N, (long long)K);
+  if (d_type != DG_TYPE_BF16 && d_type != DG_TYPE_F32) return fail(DG_ERR_ARG, "D is bf16 or fp32 (got type %d)", d_type);
+  if (N % 8 || K % 32) return fail(DG_ERR_SHAPE, "N %% 8 and K %% 32 must be 0 (N %lld, K %lld)", (long long)N, (long long)K);
+  if (M == 0 || N == 0) return DG_OK;
+  if (!D || !status) return fail(DG_ERR_ARG, "D and status must not be null");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (K == 0) {
+    DGL_CUDA(cudaMemsetAsync(D, 0, (size_t)M * N * (d_type == DG_TYPE_F32 ? 4 : 2), s));
+    return DG_OK;
+  }
+  if (!a_codes || !a_scales || !b_codes || !b_scales) return fail(DG_ERR_ARG, "codes and scales must not be null");
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(D))
+    return fail(DG_ERR_ARG, "codes, scales and D must be 16-byte aligned");
+  const int64_t tiles = ((M + kTileRows - 1) / kTileRows) * ((N + kPairFeats - 1) / kPairFeats);
+  if (tiles > INT32_MAX) return fail(DG_ERR_ARG, "M x N is too large (%lld tiles)", (long long)tiles);
+  Args p{};
+  const int64_t pitch[1] = {K / 2}, pd[2] = {K / 2, N}, qd[2] = {K / 2, M};
+  if (int rc = encode_map(&p.p, b_codes, 1, 2, pd, pitch, kLanes)) return rc;
+  if (int rc = encode_map(&p.q, a_codes, 1, 2, qd, pitch, kTileRows / 2)) return rc;
+  if (int rc = encode_map(&p.q16, a_codes, 1, 2, qd, pitch, 16)) return rc;
+  p.kblocks = (int)((K + kBlockK - 1) / kBlockK);
+  if (int rc = encode_scale_map(&p.sp, b_scales, p.kblocks, (N + 127) / 128, 1)) return rc;
+  if (int rc = encode_scale_map(&p.sq, a_scales, p.kblocks, (M + 127) / 128, 2)) return rc;
+  p.rows = (int)M, p.feats = (int)N, p.out = D;
+  p.watch = Watch{static_cast<unsigned long long*>(status), g_epoch.fetch_add(1, std::memory_order_relaxed), 4000000000ull};
+  return d_type == DG_TYPE_F32 ? launch<true>(p, tiles, s) : launch<false>(p, tiles, s);
+}

@@ -1,0 +1,565 @@
+// norm.cu -- residual add + RMS norm with 16- or 8-bit output, and its
+// gradient (dg_layer_add_rms_norm, dg_layer_add_rms_norm_backward).
+//
+//   h = x + r,  y = h s w,  s = rsqrt(mean h^2 + eps);   8 bits: q = y / c, c = max|y| / max finite
+//   dx = s (g - xh mean(g xh)) + dh,  g = dy w,  xh = h s;   dw = sum over rows of dy xh
+//
+// Both are bound by memory traffic (a handful of operations per value), so a
+// row is read once: its threads hold the row's sum in registers through the
+// reductions (sum of squares, then the maximum for an 8-bit output) and write
+// everything from there.
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "layer_common.h"
+
+namespace {
+
+constexpr float kE4M3Max = 448.f, kE5M2Max = 57344.f;
+constexpr float kMinScale = 1.1754943508222875e-38f;  // 2^-126: the reciprocal stays finite
+
+// ---------------------------------------------------------------- vectors
+
+// VW consecutive bf16 or fp32 values as floats: VW = 8 by 16-byte accesses
+// (the caller has checked alignment), VW = 1 by one element.
+template <int VW>
+__device__ __forceinline__ void load_bf16(const void* base, int64_t i, float (&v)[VW]) {
+  if constexpr (VW == 8) {
+    const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(base) + i);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      v[2 * k] = __uint_as_float(w[k] << 16);
+      v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+    }
+  } else {
+    v[0] = __bfloat162float(static_cast<const __nv_bfloat16*>(base)[i]);
+  }
+}
+
+template <int VW>
+__device__ __forceinline__ void load_f32(const void* base, int64_t i, float (&v)[VW]) {
+  if constexpr (VW == 8) {
+    const float4* p = reinterpret_cast<const float4*>(static_cast<const float*>(base) + i);
+    const float4 a = p[0], b = p[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    v[0] = static_cast<const float*>(base)[i];
+  }
+}
+
+template <int VW>
+__device__ __forceinline__ void load_any(bool f32, const void* base, int64_t i, float (&v)[VW]) {
+  if (f32)
+    load_f32<VW>(base, i, v);
+  else
+    load_bf16<VW>(base, i, v);
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+template <int VW>
+__device__ __forceinline__ void store_bf16(void* base, int64_t i, const float (&v)[VW]) {
+  if constexpr (VW == 8)
+    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(base) + i) =
+        make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+  else
+    static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v[0]);
+}
+
+template <int VW>
+__device__ __forceinline__ void store_f32(void* base, int64_t i, const float (&v)[VW]) {
+  if constexpr (VW == 8) {
+    float4* p = reinterpret_cast<float4*>(static_cast<float*>(base) + i);
+    p[0] = make_float4(v[0], v[1], v[2], v[3]);
+    p[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    static_cast<float*>(base)[i] = v[0];
+  }
+}
+
+template <int VW>
+__device__ __forceinline__ void store_fp8(void* base, int64_t i, const float (&v)[VW], __nv_fp8_interpretation_t fmt) {
+  if constexpr (VW == 8) {
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * k], v[4 * k + 1]), __NV_SATFINITE, fmt);
+      const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * k + 2], v[4 * k + 3]), __NV_SATFINITE, fmt);
+      w[k] = lo | (hi << 16);
+    }
+    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(base) + i) = make_uint2(w[0], w[1]);
+  } else {
+    static_cast<uint8_t*>(base)[i] = __nv_cvt_float_to_fp8(v[0], __NV_SATFINITE, fmt);
+  }
+}
+
+// --------------------------------------------------------------- reductions
+
+struct Add {
+  __device__ static float of(float a, float b) { return a + b; }
+};
+struct Max {
+  __device__ static float of(float a, float b) { return fmaxf(a, b); }  // ignores NaN
+};
+
+// Over the blockDim.x threads of one row (threadIdx.y: the block's rows, one
+// warp each when there are several); every thread gets the result, always
+// added in the same order.  `part`: 33 floats of shared memory per use.
+template <class Op>
+__device__ __forceinline__ float row_reduce(float v, float* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = Op::of(v, __shfl_xor_sync(0xffffffffu, v, o));
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return v;
+  const int lane = threadIdx.x & 31;
+  if (lane == 0) part[threadIdx.x >> 5] = v;
+  __syncthreads();
+  // the neutral value of both uses (sums of squares, maxima of magnitudes) is 0,
+  // and every partial result of a plain sum meets lanes of zeros
+  v = lane < warps ? part[lane] : 0.f;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v = Op::of(v, __shfl_xor_sync(0xffffffffu, v, o));
+  return v;
+}
+
+// ------------------------------------------------------------------ forward
+
+struct NormArgs {
+  const void *x, *residual, *weight;
+  void *y, *sum;
+  float *scale, *rstd;
+  const float* scale_in;
+  int64_t ld_x, ld_residual, ld_sum, rows;
+  int hidden;
+  float eps;
+  int weight_f32, fp8;  // fp8: 0 bf16 output, else the dg_type
+};
+
+__device__ __forceinline__ float row_scale(float amax, bool e5m2) {
+  return amax > 0.f ? fmaxf(amax / (e5m2 ? kE5M2Max : kE4M3Max), kMinScale) : 1.f;
+}
+
+// RT: the residual's type (0 none, 1 bf16, 2 fp32).  The row stays in
+// registers: NV vectors of VW values per thread.
+template <int RT, int VW, int NV, bool OUT8>
+__global__ void __launch_bounds__(NV * VW > 16 ? 512 : 1024) add_rms_norm_kernel(const NormArgs p) {
+  __shared__ float part[66];
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= p.rows) return;  // several rows per block only with one warp each: no barrier below
+  const int step = blockDim.x * VW;
+  float h[NV][VW];
+  float ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = threadIdx.x * VW + k * step;
+    if (i < p.hidden) {
+      load_bf16<VW>(p.x, row * p.ld_x + i, h[k]);
+      if constexpr (RT != 0) {
+        float r[VW];
+        load_any<VW>(RT == 2, p.residual, row * p.ld_residual + i, r);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+          h[k][j] += r[j];
+          // the norm is of the sum as it is stored, so that the gradient sees the same values
+          if constexpr (RT == 1) h[k][j] = __bfloat162float(__float2bfloat16_rn(h[k][j]));
+        }
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < VW; ++j) h[k][j] = 0.f;
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = threadIdx.x * VW + k * step;
+    if constexpr (RT != 0) {
+      if (i < p.hidden) {
+        if constexpr (RT == 2)
+          store_f32<VW>(p.sum, row * p.ld_sum + i, h[k]);
+        else
+          store_bf16<VW>(p.sum, row * p.ld_sum + i, h[k]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < VW; ++j) ss = fmaf(h[k][j], h[k][j], ss);
+  }
+  ss = row_reduce<Add>(ss, part);
+  const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
+  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  float amax = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = threadIdx.x * VW + k * step;
+    if (i < p.hidden) {
+      float w[VW];
+      load_any<VW>(p.weight_f32 != 0, p.weight, i, w);
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+        h[k][j] = h[k][j] * rstd * w[j];
+        // an infinity (only of a weight, or of a sum of squares below the
+        // smallest normal value) saturates and stays out of the scale
+        if constexpr (OUT8) amax = fmaxf(amax, isinf(h[k][j]) ? 0.f : fabsf(h[k][j]));
+      }
+      if constexpr (!OUT8) store_bf16<VW>(p.y, row * p.hidden + i, h[k]);
+    }
+  }
+  if constexpr (OUT8) {
+    const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
+    float c;
+    if (p.scale_in) {
+      c = __ldg(p.scale_in);
+    } else {
+      amax = row_reduce<Max>(amax, part + 33);
+      c = row_scale(amax, e5m2);
+      if (threadIdx.x == 0) p.scale[row] = c;
+    }
+    const float inv = 1.f / c;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = threadIdx.x * VW + k * step;
+      if (i < p.hidden) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) h[k][j] *= inv;
+        store_fp8<VW>(p.y, row * p.hidden + i, h[k], e5m2 ? __NV_E5M2 : __NV_E4M3);
+      }
+    }
+  }
+}
+
+// Rows longer than the register kernel holds: each thread goes over its values
+// again (its own stores of the sum, still in cache) for the maximum and the
+// output.  Same order of additions for every row of one size.
+template <int RT, int VW, bool OUT8>
+__global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const NormArgs p) {
+  __shared__ float part[66];
+  const int64_t row = blockIdx.x;
+  const int step = blockDim.x * VW;
+  const void* hp = RT == 0 ? p.x : p.sum;
+  const int64_t h0 = row * (RT == 0 ? p.ld_x : p.ld_sum);
+  float ss = 0.f;
+  for (int64_t i = threadIdx.x * VW; i < p.hidden; i += step) {
+    float h[VW];
+    load_bf16<VW>(p.x, row * p.ld_x + i, h);
+    if constexpr (RT != 0) {
+      float r[VW];
+      load_any<VW>(RT == 2, p.residual, row * p.ld_residual + i, r);
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+        h[j] += r[j];
+        if constexpr (RT == 1) h[j] = __bfloat162float(__float2bfloat16_rn(h[j]));
+      }
+      if constexpr (RT == 2)
+        store_f32<VW>(p.sum, h0 + i, h);
+      else
+        store_bf16<VW>(p.sum, h0 + i, h);
+    }
+#pragma unroll
+    for (int j = 0; j < VW; ++j) ss = fmaf(h[j], h[j], ss);
+  }
+  ss = row_reduce<Add>(ss, part);
+  const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
+  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  // (the sum was written by this thread just above)
+  auto value = [&](int64_t i, float(&h)[VW]) {
+    float w[VW];
+    load_any<VW>(RT == 2, hp, h0 + i, h);
+    load_any<VW>(p.weight_f32 != 0, p.weight, i, w);
+#pragma unroll
+    for (int j = 0; j < VW; ++j) h[j] = h[j] * rstd * w[j];
+  };
+  float inv = 1.f;
+  const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
+  if constexpr (OUT8) {
+    float c;
+    if (p.scale_in) {
+      c = __ldg(p.scale_in);
+    } else {
+      float amax = 0.f;
+      for (int64_t i = threadIdx.x * VW; i < p.hidden; i += step) {
+        float h[VW];
+        value(i, h);
+#pragma unroll
+        for (int j = 0; j < VW; ++j) amax = fmaxf(amax, isinf(h[j]) ? 0.f : fabsf(h[j]));
+      }
+      c = row_scale(row_reduce<Max>(amax, part + 33), e5m2);
+      if (threadIdx.x == 0) p.scale[row] = c;
+    }
+    inv = 1.f / c;
+  }
+  for (int64_t i = threadIdx.x * VW; i < p.hidden; i += step) {
+    float h[VW];
+    value(i, h);
+    if constexpr (OUT8) {
+#pragma unroll
+      for (int j = 0; j < VW; ++j) h[j] *= inv;
+      store_fp8<VW>(p.y, row * p.hidden + i, h, e5m2 ? __NV_E5M2 : __NV_E4M3);
+    } else {
+      store_bf16<VW>(p.y, row * p.hidden + i, h);
+    }
+  }
+}
+
+template <int RT, int VW, int NV, bool OUT8>
+int launch_norm(const NormArgs& p, int threads, cudaStream_t s) {
+  const int per = threads == 32 ? 4 : 1;  // one warp per row: four rows to a block
+  add_rms_norm_kernel<RT, VW, NV, OUT8><<<(unsigned)((p.rows + per - 1) / per), dim3(threads, per), 0, s>>>(p);
+  DGL_LAUNCHED();
+  return DG_OK;
+}
+
+int round32(int v) { return (v + 31) / 32 * 32; }
+
+template <int RT, bool OUT8>
+int run_norm(const NormArgs& p, bool vec, int sms, cudaStream_t s) {
+  if (vec) {
+    // Few rows: as many threads as the row has vectors, for the shortest chain
+    // of loads.  Many rows: four vectors per thread, so that enough bytes are
+    // in flight with few barriers.
+    const int n = p.hidden / 8;
+    const bool few = p.rows <= 2 * sms;
+    if (n <= 32 || (few && n <= 1024)) return launch_norm<RT, 8, 1, OUT8>(p, round32(n), s);
+    if (n <= 128 || (few && n <= 2048)) return launch_norm<RT, 8, 2, OUT8>(p, round32((n + 1) / 2), s);
+    if (n <= 2048) return launch_norm<RT, 8, 4, OUT8>(p, round32((n + 3) / 4), s);
+    if (n <= 4096) return launch_norm<RT, 8, 8, OUT8>(p, round32((n + 7) / 8), s);
+    add_rms_norm_long_kernel<RT, 8, OUT8><<<(unsigned)p.rows, 1024, 0, s>>>(p);
+  } else {
+    if (p.hidden <= 4096) return launch_norm<RT, 1, 4, OUT8>(p, round32((p.hidden + 3) / 4), s);
+    if (p.hidden <= 16384) return launch_norm<RT, 1, 16, OUT8>(p, round32((p.hidden + 15) / 16), s);
+    add_rms_norm_long_kernel<RT, 1, OUT8><<<(unsigned)p.rows, 1024, 0, s>>>(p);
+  }
+  DGL_LAUNCHED();
+  return DG_OK;
+}
+
+// ----------------------------------------------------------------- gradient
+
+struct GradArgs {
+  const void *dy, *h, *weight, *dh;
+  const float* rstd;
+  void *dx, *dweight;
+  float* partial;  // blocks x hidden
+  int64_t ld_dy, ld_h, ld_dh, rows;
+  int hidden, weight_f32;
+};
+
+// A block walks the rows blockIdx.x, + gridDim.x, ...; the weight's gradient is
+// summed in registers over its rows and written once as a row of `partial`.
+template <bool F32, int VW, int NV, bool HAS_DH>
+__global__ void __launch_bounds__(NV * VW > 8 ? 512 : 1024) add_rms_norm_grad_kernel(const GradArgs p) {
+  __shared__ float part[2][33];
+  const int step = blockDim.x * VW;
+  float dw[NV][VW], w[NV][VW];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = threadIdx.x * VW + k * step;
+#pragma unroll
+    for (int j = 0; j < VW; ++j) dw[k][j] = w[k][j] = 0.f;
+    if (i < p.hidden) load_any<VW>(p.weight_f32 != 0, p.weight, i, w[k]);
+  }
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    const float rstd = __ldg(p.rstd + row);
+    float dy[NV][VW], h[NV][VW], dh[NV][VW];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = threadIdx.x * VW + k * step;
+#pragma unroll
+      for (int j = 0; j < VW; ++j) dy[k][j] = h[k][j] = dh[k][j] = 0.f;
+      if (i < p.hidden) {
+        load_bf16<VW>(p.dy, row * p.ld_dy + i, dy[k]);
+        load_any<VW>(F32, p.h, row * p.ld_h + i, h[k]);
+        if constexpr (HAS_DH) load_any<VW>(F32, p.dh, row * p.ld_dh + i, dh[k]);
+      }
+    }
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int j = 0; j < VW; ++j) {
+        h[k][j] *= rstd;
+        dw[k][j] = fmaf(dy[k][j], h[k][j], dw[k][j]);
+        dy[k][j] *= w[k][j];
+        dot = fmaf(dy[k][j], h[k][j], dot);
+      }
+    // two sets of partials: a block's next row may start while a slow warp reads these
+    dot = row_reduce<Add>(dot, part[flip]) / (float)p.hidden;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = threadIdx.x * VW + k * step;
+      if (i < p.hidden) {
+#pragma unroll
+        for (int j = 0; j < VW; ++j) h[k][j] = fmaf(rstd, dy[k][j] - h[k][j] * dot, dh[k][j]);
+        if constexpr (F32)
+          store_f32<VW>(p.dx, row * p.hidden + i, h[k]);
+        else
+          store_bf16<VW>(p.dx, row * p.hidden + i, h[k]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = threadIdx.x * VW + k * step;
+    if (i < p.hidden) store_f32<VW>(p.partial, (int64_t)blockIdx.x * p.hidden + i, dw[k]);
+  }
+}
+
+// Rows longer than the register kernel holds: two passes over each row; the
+// weight's gradient accumulates in the block's row of `partial`.
+template <bool F32, bool HAS_DH>
+__global__ void __launch_bounds__(1024) add_rms_norm_grad_long_kernel(const GradArgs p) {
+  __shared__ float part[2][33];
+  float* mine = p.partial + (int64_t)blockIdx.x * p.hidden;
+  for (int64_t i = threadIdx.x; i < p.hidden; i += blockDim.x) mine[i] = 0.f;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    const float rstd = __ldg(p.rstd + row);
+    float dot = 0.f;
+    for (int64_t i = threadIdx.x; i < p.hidden; i += blockDim.x) {
+      float dy[1], h[1], w[1];
+      load_bf16<1>(p.dy, row * p.ld_dy + i, dy);
+      load_any<1>(F32, p.h, row * p.ld_h + i, h);
+      load_any<1>(p.weight_f32 != 0, p.weight, i, w);
+      mine[i] = fmaf(dy[0], h[0] * rstd, mine[i]);
+      dot = fmaf(dy[0] * w[0], h[0] * rstd, dot);
+    }
+    dot = row_reduce<Add>(dot, part[flip]) / (float)p.hidden;
+    for (int64_t i = threadIdx.x; i < p.hidden; i += blockDim.x) {
+      float dy[1], h[1], w[1], d[1] = {0.f}, o[1];
+      load_bf16<1>(p.dy, row * p.ld_dy + i, dy);
+      load_any<1>(F32, p.h, row * p.ld_h + i, h);
+      load_any<1>(p.weight_f32 != 0, p.weight, i, w);
+      if constexpr (HAS_DH) load_any<1>(F32, p.dh, row * p.ld_dh + i, d);
+      o[0] = fmaf(rstd, dy[0] * w[0] - h[0] * rstd * dot, d[0]);
+      if constexpr (F32)
+        store_f32<1>(p.dx, row * p.hidden + i, o);
+      else
+        store_bf16<1>(p.dx, row * p.hidden + i, o);
+    }
+  }
+}
+
+// dweight[i] = sum over the blocks' partial rows, in a fixed order: 32 columns
+// x 32 threads, each thread a strided share of the rows, then a tree.
+__global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* partial, int blocks, int hidden,
+                                                                void* dweight, int f32) {
+  __shared__ float s[32][33];
+  const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  float v = 0.f;
+  if (col < hidden)
+    for (int b = threadIdx.y; b < blocks; b += 32) v += partial[(int64_t)b * hidden + col];
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  v = s[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int64_t out = (int64_t)blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && out < hidden) {
+    if (f32)
+      static_cast<float*>(dweight)[out] = v;
+    else
+      static_cast<__nv_bfloat16*>(dweight)[out] = __float2bfloat16_rn(v);
+  }
+}
+
+// Blocks of the gradient kernel: at most two per SM (and a fixed bound that the
+// workspace is sized by), so that the partial sums stay small beside the rows.
+constexpr int kGradBlocks = 304;
+
+template <bool F32, bool HAS_DH>
+int run_grad(const GradArgs& p, bool vec, int blocks, cudaStream_t s) {
+  const int n = p.hidden / 8;
+  if (vec && n <= 1024)
+    add_rms_norm_grad_kernel<F32, 8, 1, HAS_DH><<<blocks, round32(n), 0, s>>>(p);
+  else if (vec && n <= 2048)
+    add_rms_norm_grad_kernel<F32, 8, 4, HAS_DH><<<blocks, round32((n + 3) / 4), 0, s>>>(p);
+  else if (!vec && p.hidden <= 4096)
+    add_rms_norm_grad_kernel<F32, 1, 4, HAS_DH><<<blocks, round32((p.hidden + 3) / 4), 0, s>>>(p);
+  else if (!vec && p.hidden <= 8192)
+    add_rms_norm_grad_kernel<F32, 1, 16, HAS_DH><<<blocks, round32((p.hidden + 15) / 16), 0, s>>>(p);
+  else
+    add_rms_norm_grad_long_kernel<F32, HAS_DH><<<blocks, 1024, 0, s>>>(p);
+  DGL_LAUNCHED();
+  return DG_OK;
+}
+
+bool rows16(const void* p, int64_t ld, int64_t esz) {
+  return !p || (dgl::aligned16(p) && (ld * esz) % 16 == 0);
+}
+
+bool bf16_or_f32(int t) { return t == DG_TYPE_BF16 || t == DG_TYPE_F32; }
+
+}  // namespace
+
+extern "C" int dg_layer_add_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
+                                     int residual_type, const void* weight, int weight_type, void* y, int y_type,
+                                     void* sum_out, int64_t ld_sum, float* scale_out, const float* scale_in,
+                                     float* rstd_out, int64_t rows, int64_t hidden, float eps, void* stream) {
+  if (rows < 0 || hidden < 0 || rows > INT32_MAX || hidden > INT32_MAX)
+    return dgl::fail(DG_ERR_ARG, "rows %lld, hidden %lld out of range", (long long)rows, (long long)hidden);
+  if (!bf16_or_f32(weight_type) || (residual && !bf16_or_f32(residual_type)))
+    return dgl::fail(DG_ERR_ARG, "the weight and the residual are bf16 or fp32");
+  const bool out8 = y_type == DG_TYPE_E4M3 || y_type == DG_TYPE_E5M2;
+  if (!out8 && y_type != DG_TYPE_BF16) return dgl::fail(DG_ERR_ARG, "y is bf16, e4m3 or e5m2 (got type %d)", y_type);
+  if (!(eps >= 0.f)) return dgl::fail(DG_ERR_ARG, "eps must not be negative");
+  if (rows == 0 || hidden == 0) return DG_OK;
+  if (!x || !weight || !y) return dgl::fail(DG_ERR_ARG, "x, weight and y must not be null");
+  if ((residual != nullptr) != (sum_out != nullptr))
+    return dgl::fail(DG_ERR_ARG, "a residual and its sum come together");
+  if (out8 && !scale_in && !scale_out) return dgl::fail(DG_ERR_ARG, "an 8-bit output needs scale_out or scale_in");
+  int sms = 0;
+  if (int rc = dgl::sm_count(&sms)) return rc;
+  const int64_t rsz = residual_type == DG_TYPE_F32 ? 4 : 2;
+  const bool vec = hidden % 8 == 0 && rows16(x, ld_x, 2) && rows16(residual, ld_residual, rsz) &&
+                   rows16(sum_out, ld_sum, rsz) && dgl::aligned16(weight) && dgl::aligned16(y);
+  NormArgs p{x, residual, weight, y, sum_out, scale_out, rstd_out, scale_in, ld_x, ld_residual, ld_sum, rows,
+             (int)hidden, eps, weight_type == DG_TYPE_F32, out8 ? y_type : 0};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (!residual) return out8 ? run_norm<0, true>(p, vec, sms, s) : run_norm<0, false>(p, vec, sms, s);
+  if (residual_type == DG_TYPE_F32) return out8 ? run_norm<2, true>(p, vec, sms, s) : run_norm<2, false>(p, vec, sms, s);
+  return out8 ? run_norm<1, true>(p, vec, sms, s) : run_norm<1, false>(p, vec, sms, s);
+}
+
+extern "C" size_t dg_layer_add_rms_norm_backward_workspace(int64_t rows, int64_t hidden) {
+  if (rows <= 0 || hidden <= 0) return 0;
+  return (size_t)(rows < kGradBlocks ? rows : kGradBlocks) * (size_t)hidden * sizeof(float);
+}
+
+extern "C" int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, int h_type,
+                                              const void* weight, int weight_type, const float* rstd, const void* dh,
+                                              int64_t ld_dh, void* dx, void* dweight, void* workspace, int64_t rows,
+                                              int64_t hidden, void* stream) {
+  if (rows < 0 || hidden < 0 || rows > INT32_MAX || hidden > INT32_MAX)
+    return dgl::fail(DG_ERR_ARG, "rows %lld, hidden %lld out of range", (long long)rows, (long long)hidden);
+  if (!bf16_or_f32(weight_type) || !bf16_or_f32(h_type)) return dgl::fail(DG_ERR_ARG, "h and the weight are bf16 or fp32");
+  if (hidden == 0) return DG_OK;
+  if (!dweight) return dgl::fail(DG_ERR_ARG, "dweight must not be null");
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    DGL_CUDA(cudaMemsetAsync(dweight, 0, (size_t)hidden * (weight_type == DG_TYPE_F32 ? 4 : 2), s));
+    return DG_OK;
+  }
+  if (!dy || !h || !weight || !rstd || !dx || !workspace) return dgl::fail(DG_ERR_ARG, "a required pointer is null");
+  if (!dgl::aligned16(workspace)) return dgl::fail(DG_ERR_ARG, "the workspace must be 16-byte aligned");
+  int sms = 0;
+  if (int rc = dgl::sm_count(&sms)) return rc;
+  const int64_t hsz = h_type == DG_TYPE_F32 ? 4 : 2;
+  const bool vec = hidden % 8 == 0 && rows16(dy, ld_dy, 2) && rows16(h, ld_h, hsz) && rows16(dh, ld_dh, hsz) &&
+                   dgl::aligned16(weight) && dgl::aligned16(dx);
+  GradArgs p{dy, h, weight, dh, rstd, dx, dweight, static_cast<float*>(workspace), ld_dy, ld_h, ld_dh, rows,
+             (int)hidden, weight_type == DG_TYPE_F32};
+  int blocks = 2 * sms < kGradBlocks ? 2 * sms : kGradBlocks;
+  if (rows < blocks) blocks = (int)rows;
+  const bool f32 = h_type == DG_TYPE_F32;
+  int rc = f32 ? (dh ? run_grad<true, true>(p, vec, blocks, s) : run_grad<true, false>(p, vec, blocks, s))
+               : (dh ? run_grad<false, true>(p, vec, blocks, s) : run_grad<false, false>(p, vec, blocks, s));
+  if (rc != DG_OK) return rc;
+  norm_weight_grad_kernel<<<(unsigned)((hidden + 31) / 32), dim3(32, 32), 0, s>>>(p.partial, blocks, (int)hidden,
+                                                                                   dweight, weight_type == DG_TYPE_F32);
+  DGL_LAUNCHED();
+  return DG_OK;
+}

@@ -1,0 +1,234 @@
+// ptx.cuh -- PTX wrappers of the matrix-product kernels behind
+// include/dg_layer.h (CTA pairs: tcgen05 cta_group::2, TMA into a pair,
+// mbarriers), their bounded waits and the epilogue's stores.
+//
+// The kernels compute D^T: the dimension that is contiguous in memory (the
+// output features) lies on the accumulator's 128 x 2 lanes, the output's rows
+// on its columns.  A column count is a run-time field of the instruction
+// descriptor, so a ragged group of rows costs its own rows (rounded up to 32)
+// and not a whole tile, and a handful of rows still fills the tensor core's M.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+namespace dgl {
+
+constexpr int kThreads = 192;         // producer warp, MMA warp, four epilogue warps
+constexpr int kLanes = 128;           // output features per CTA (accumulator lanes)
+constexpr int kPairFeats = 2 * kLanes;
+constexpr uint32_t kRowBytes = 128;   // one operand row of a K block (the swizzle span)
+constexpr uint32_t kStageP = kLanes * kRowBytes;
+constexpr int kChunk = 32;            // output rows (accumulator columns) per epilogue step
+constexpr uint32_t kStoreBuf = kChunk * 32 * 2;  // one warp's 32 x 32 bf16 box
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ uint64_t globaltimer() {
+  uint64_t t;
+  asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+  return t;
+}
+__device__ __forceinline__ uint32_t cluster_ctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t mapa(uint32_t addr, uint32_t rank) {
+  uint32_t r;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ----------------------------------------------------------------- mbarriers
+
+__device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void mbar_init_fence() { asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory"); }
+__device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+
+// Pipeline waits are bounded: after `limit_ns` the waiter records the wait in
+// the caller's status word, tagged with the launch's epoch, and every role of
+// every CTA of the launch that waits from then on gives up too.
+struct Watch {
+  unsigned long long* status;
+  uint32_t epoch;
+  uint64_t limit_ns;
+};
+__device__ __forceinline__ bool gave_up(const Watch& w) {
+  unsigned long long v;
+  asm volatile("ld.relaxed.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(w.status) : "memory");
+  return (uint32_t)(v >> 32) == w.epoch;
+}
+static __device__ __noinline__ bool mbar_wait_slow(const Watch& w, uint32_t bar, uint32_t parity, uint32_t what) {
+  const uint64_t t0 = globaltimer();
+  for (uint32_t n = 1;; ++n) {
+    if (mbar_try(bar, parity)) return true;
+    if ((n & 255u) == 0) {
+      if (gave_up(w)) return false;
+      if (globaltimer() - t0 > w.limit_ns) {
+        atomicExch(w.status, ((unsigned long long)w.epoch << 32) | what);
+        return false;
+      }
+    }
+  }
+}
+__device__ __forceinline__ bool mbar_wait(const Watch& w, uint32_t bar, uint32_t parity, uint32_t what) {
+  if (mbar_try(bar, parity)) return true;
+  return mbar_wait_slow(w, bar, parity, what);
+}
+// Before a launch that gave up ends, its copies and MMAs in flight land.
+static __device__ __noinline__ void settle() {
+  const uint64_t t0 = globaltimer();
+  while (globaltimer() - t0 < 20000000ull) __nanosleep(1000);
+}
+
+// ----------------------------------------------------------------------- TMA
+
+// Loads into this CTA's shared memory that complete on a barrier of either CTA
+// of the pair (here: the even CTA's).
+__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t x, int32_t y,
+                                       int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+  asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
+// ------------------------------------------------------------------- tcgen05
+
+__device__ __forceinline__ void tmem_alloc(uint32_t dst_smem, uint32_t ncols) {
+  asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(dst_smem), "r"(ncols) : "memory");
+  asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void tmem_free(uint32_t taddr, uint32_t ncols) {
+  asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// D (both CTAs' accumulators) = P Q [+ D]; bf16 (K = 16) or 8-bit (K = 32) operands.
+template <bool F8>
+__device__ __forceinline__ void mma_pair(uint32_t d, uint64_t pdesc, uint64_t qdesc, uint32_t idesc, uint32_t acc) {
+  if constexpr (F8)
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(acc)
+        : "memory");
+  else
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d),
+        "l"(pdesc), "l"(qdesc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// One arrival on the barrier at this offset in both CTAs of the pair once the
+// issuing thread's earlier tcgen05 operations are complete.
+__device__ __forceinline__ void commit_pair(uint32_t bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+      "h"((uint16_t)3)
+      : "memory");
+}
+// 32 lanes x 32 columns: thread i of the warp gets columns 0..31 of lane i.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+      "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]), "=r"(v[16]),
+        "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]), "=r"(v[24]),
+        "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+      : "r"(taddr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+
+// Shared-memory descriptors of operand tiles that TMA wrote with the 128-byte
+// swizzle: version 1 (bit 46), swizzle code 2 (bits 61-63), offsets in 16-byte
+// units.  K-major: rows of 128 bytes along K, groups of 8 rows 1024 bytes apart
+// (stride offset).  MN-major: rows of 64 values along M (or N), one row per k;
+// groups of 8 k 1024 bytes apart (stride offset), the next 64 values
+// `next_bytes` further (leading offset).
+__device__ __forceinline__ uint64_t desc_k_major(uint32_t addr) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | (1ull << 16) | ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn_major(uint32_t addr, uint32_t next_bytes) {
+  return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(next_bytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+// Instruction descriptor: fp32 accumulator (bits 4-5), P and Q formats (bits
+// 7-9, 10-12), MN-major flags (bits 15, 16), columns / 8 (bit 17), lanes / 16 (bit 24).
+__host__ __device__ constexpr uint32_t idesc_of(uint32_t p_fmt, uint32_t q_fmt, bool p_mn, bool q_mn) {
+  return (1u << 4) | (p_fmt << 7) | (q_fmt << 10) | ((p_mn ? 1u : 0u) << 15) | ((q_mn ? 1u : 0u) << 16) |
+         ((uint32_t)(kPairFeats >> 4) << 24);
+}
+__device__ __forceinline__ uint32_t idesc_columns(uint32_t n) { return (n >> 3) << 17; }
+
+// ------------------------------------------------------------ epilogue stores
+
+// A warp's box of 32 features x 32 rows from registers (v[i]: row i, this
+// lane's feature) to row-major memory: `d` points at (first row, first feature
+// of the warp), `pitch` elements from row to row; rows_ok rows and feats_ok
+// features (a multiple of 8) are stored.  bf16 goes through `buf` (kStoreBuf
+// bytes of the warp's own) so that each lane stores 16 bytes; fp32 rows are
+// whole 128-byte lines as they are.
+__device__ __forceinline__ void store_box_f32(float* d, int64_t pitch, int rows_ok, int feats_ok, int lane,
+                                              const float (&v)[32]) {
+  if (lane < feats_ok) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (i < rows_ok) d[i * pitch + lane] = v[i];
+  }
+}
+__device__ __forceinline__ void store_box_bf16(__nv_bfloat16* d, int64_t pitch, int rows_ok, int feats_ok, int lane,
+                                               const float (&v)[32], uint8_t* buf) {
+  __nv_bfloat16* b = reinterpret_cast<__nv_bfloat16*>(buf);
+#pragma unroll
+  for (int i = 0; i < 32; ++i) b[i * 32 + lane] = __float2bfloat16_rn(v[i]);
+  __syncwarp();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int r = j * 8 + (lane >> 2), f = (lane & 3) * 8;
+    const uint4 u = *reinterpret_cast<const uint4*>(b + r * 32 + f);
+    if (r < rows_ok && f < feats_ok) *reinterpret_cast<uint4*>(d + r * pitch + f) = u;
+  }
+  __syncwarp();  // the box may be overwritten
+}
+
+}  // namespace dgl

@@ -32,6 +32,11 @@ in ``libdg.so``.  Beyond the torch ops, the non-scaled calls accept
 ``alpha``/``beta`` and a C operand (the CUTLASS problem's epilogue), and the
 all-gather calls ``rotate="B"`` (AllGather1D_TilingCD_RotatingB: the ranks
 keep their rows of A and the B shards rotate instead).
+
+The operators around these products (:mod:`reduce_scatter_gb300.layer`) are
+exported here too: ``add_rms_norm`` and ``add_rms_norm_backward``,
+``grouped_matmul`` and ``grouped_matmul_backward``, ``quantize_mx4``,
+``dequantize_mx4``, ``mx4_matmul``, ``check_products``.
 """
 
 from __future__ import annotations
@@ -41,6 +46,8 @@ import threading
 import torch
 
 from . import dg
+from .layer import (MX4Tensor, NormResult, add_rms_norm, add_rms_norm_backward, check_products,  # noqa: F401
+                    dequantize_mx4, grouped_matmul, grouped_matmul_backward, mx4_matmul, quantize_mx4)
 
 _lock = threading.Lock()
 _plans: dict = {}

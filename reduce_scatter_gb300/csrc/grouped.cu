@@ -154,22 +154,22 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t base = smem_u32(smem);
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ------------------------------------------------------------ producer
-      prefetch_map(&p.p);
-      prefetch_map(&p.q);
-      uint32_t stage = 0, phase = 0;
-      int e = 0;
-      bool ok = true;
-      for (int t = unit; t < total && ok; t += units) {
-        const Tile tl = tile_at<GRAD, F8>(p, start, first, t, e);
-        const int n = columns<GRAD>(tl), mine = n / 2;  // this CTA's share of the rows operand
-        const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
-        for (int kb = 0; kb < tl.kblocks; ++kb) {
-          if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
-          const uint32_t fb = mapa(full + 8 * stage, 0);
+    // -------------------------------------------------------------- producer
+    prefetch_map(&p.p);
+    prefetch_map(&p.q);
+    uint32_t stage = 0, phase = 0;
+    int e = 0;
+    bool ok = true;
+    for (int t = unit; t < total && ok; t += units) {
+      const Tile tl = tile_at<GRAD, F8>(p, start, first, t, e);
+      const int n = columns<GRAD>(tl), mine = n / 2;  // this CTA's share of the rows operand
+      const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
+      for (int kb = 0; kb < tl.kblocks; ++kb) {
+        if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
+        const uint32_t fb = mapa(full + 8 * stage, 0);
+        const uint32_t sp = base + stage * kStage, sq = sp + kStageP;
+        if (elect_one()) {
           if (half == 0) mbar_expect(full + 8 * stage, 2 * (kStageP + (uint32_t)mine * kRowBytes));
-          const uint32_t sp = base + stage * kStage, sq = sp + kStageP;
           if constexpr (GRAD) {
             // 64 columns x 64 rows per box, MN-major; a group's last rows come
             // from their zero-padded copy, so no other group's rows enter
@@ -177,6 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             const CUtensorMap* pm = tail ? &p.p_tail : &p.p;
             const CUtensorMap* qm = tail ? &p.q_tail : &p.q;
             const int y = tl.k0 + kb * kTailRows;
+#pragma unroll
             for (int i = 0; i < 2; ++i) {
               tma_3d(sp + i * (kStageP / 2), pm, fb, f + i * 64, tail ? 0 : y, tail ? tl.e : 0);
               tma_2d(sq + i * (kStageQ / 2), qm, fb, q0 + i * 64, tail ? tl.e * kTailRows : y);
@@ -194,12 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             else
               for (int i = 0; i < mine; i += 16) tma_2d(sq + i * kRowBytes, &p.q16, fb, x, q0 + i);
           }
-          if (++stage == kStages) stage = 0, phase ^= 1;
         }
+        __syncwarp();
+        if (++stage == kStages) stage = 0, phase ^= 1;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && half == 0) {
+    if (half == 0) {
       // ----------------------------------------------------------------- MMA
       uint32_t stage = 0, phase = 0, it = 0;
       int e = 0;
@@ -220,12 +222,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           // per instruction: 32 bytes along a K-major row, or 16 rows of 128 bytes
           constexpr uint64_t p_step = PMN ? 16 * kRowBytes / 16 : 2, q_step = GRAD ? 16 * kRowBytes / 16 : 2;
           const int subs = GRAD && tl.tail != 0 && kb == tl.kblocks - 1 ? (tl.tail + 15) / 16 : 4;
-          for (int s = 0; s < subs; ++s)
-            mma_pair<F8>(d, pd + s * p_step, qd + s * q_step, idesc, (kb | s) != 0);
-          commit_pair(empty + 8 * stage);
+          if (elect_one()) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+              if (!GRAD || s < subs) mma_pair<F8>(d, pd + s * p_step, qd + s * q_step, idesc, (kb | s) != 0);
+            commit_pair(empty + 8 * stage);
+          }
+          __syncwarp();
           if (++stage == kStages) stage = 0, phase ^= 1;
         }
-        if (ok) commit_pair(tfull + 8 * buf);
+        if (ok && elect_one()) commit_pair(tfull + 8 * buf);
+        __syncwarp();
       }
     }
   } else {

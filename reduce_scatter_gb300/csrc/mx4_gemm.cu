@@ -101,20 +101,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   const int total = ((p.rows + kTileRows - 1) / kTileRows) * ((p.feats + kPairFeats - 1) / kPairFeats);
 
   if (warp == 0) {
-    if (lane == 0) {
-      prefetch_map(&p.p);
-      prefetch_map(&p.q);
-      uint32_t stage = 0, phase = 0;
-      bool ok = true;
-      for (int t = unit; t < total && ok; t += units) {
-        const Tile tl = tile_at(p, t);
-        const int n = (tl.rows + 31) / 32 * 32, mine = n / 2;
-        const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
-        for (int kb = 0; kb < p.kblocks; ++kb) {
-          if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
-          const uint32_t fb = mapa(full + 8 * stage, 0);
+    prefetch_map(&p.p);
+    prefetch_map(&p.q);
+    uint32_t stage = 0, phase = 0;
+    bool ok = true;
+    for (int t = unit; t < total && ok; t += units) {
+      const Tile tl = tile_at(p, t);
+      const int n = (tl.rows + 31) / 32 * 32, mine = n / 2;
+      const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
+      for (int kb = 0; kb < p.kblocks; ++kb) {
+        if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
+        const uint32_t fb = mapa(full + 8 * stage, 0);
+        const uint32_t sp = base + stage * kStage, sq = sp + kStageP, ss = sq + kStageQ;
+        if (elect_one()) {
           if (half == 0) mbar_expect(full + 8 * stage, 2 * (kStageP + (uint32_t)mine * kRowBytes + kScaleP + kScaleQ));
-          const uint32_t sp = base + stage * kStage, sq = sp + kStageP, ss = sq + kStageQ;
           tma_2d(sp, &p.p, fb, kb * 128, f);
           if (n == kTileRows)
             tma_2d(sq, &p.q, fb, kb * 128, q0);
@@ -122,12 +122,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
             for (int i = 0; i < mine; i += 16) tma_2d(sq + i * kRowBytes, &p.q16, fb, kb * 128, q0 + i);
           tma_3d(ss, &p.sp, fb, 0, kb, f / 128);
           tma_3d(ss + kScaleP, &p.sq, fb, 0, kb, tl.row0 / 128);  // every row's: each CTA needs them all
-          if (++stage == kStages) stage = 0, phase ^= 1;
         }
+        __syncwarp();
+        if (++stage == kStages) stage = 0, phase ^= 1;
       }
     }
   } else if (warp == 1) {
-    if (lane == 0 && half == 0) {
+    if (half == 0) {
       uint32_t stage = 0, phase = 0, it = 0, sbuf = 0;
       bool ok = true;
       for (int t = unit; t < total && ok; t += units, ++it) {
@@ -137,28 +138,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
         if (!(ok = mbar_wait(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
         fence_after();
         const uint32_t d = tmem + buf * kTileRows;
+        const uint32_t idesc0 = idesc_mx4(n, 0), idesc2 = idesc_mx4(n, 2);
         for (int kb = 0; kb < p.kblocks; ++kb) {
           if (!(ok = mbar_wait(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
           fence_after();
           const uint32_t sp = base + stage * kStage, sq = sp + kStageP, ss = sq + kStageQ;
           const uint32_t tp = tmem + kScaleCol + sbuf * 24, tq = tp + 8;
-          // copies and MMAs of one thread run in order
-#pragma unroll
-          for (uint32_t k = 0; k < 2; ++k) {
-            scale_copy(tp + 4 * k, ss + 512 * k);
-            scale_copy(tq + 8 * k, ss + kScaleP + 512 * k);
-            scale_copy(tq + 8 * k + 4, ss + kScaleP + 1024 + 512 * k);
-          }
           const uint64_t pd = desc_k_major(sp), qd = desc_k_major(sq);
+          if (elect_one()) {
+            // copies and MMAs of one thread run in order
 #pragma unroll
-          for (uint32_t s = 0; s < 4; ++s)
-            mma_mx4(d, pd + 2 * s, qd + 2 * s, idesc_mx4(n, (s & 1) * 2), tp + 4 * (s >> 1), tq + 8 * (s >> 1) + odd,
-                    (kb | s) != 0);
-          commit_pair(empty + 8 * stage);
+            for (uint32_t k = 0; k < 2; ++k) {
+              scale_copy(tp + 4 * k, ss + 512 * k);
+              scale_copy(tq + 8 * k, ss + kScaleP + 512 * k);
+              scale_copy(tq + 8 * k + 4, ss + kScaleP + 1024 + 512 * k);
+            }
+#pragma unroll
+            for (uint32_t s = 0; s < 4; ++s)
+              mma_mx4(d, pd + 2 * s, qd + 2 * s, s & 1 ? idesc2 : idesc0, tp + 4 * (s >> 1), tq + 8 * (s >> 1) + odd,
+                      (kb | s) != 0);
+            commit_pair(empty + 8 * stage);
+          }
+          __syncwarp();
           sbuf = (sbuf + 1) % kScaleBufs;
           if (++stage == kStages) stage = 0, phase ^= 1;
         }
-        if (ok) commit_pair(tfull + 8 * buf);
+        if (ok && elect_one()) commit_pair(tfull + 8 * buf);
+        __syncwarp();
       }
     }
   } else {

@@ -45,6 +45,22 @@ __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// One lane of a converged warp.  The loading and the issuing warp run their
+// loops with all lanes and let the elected one act: the compiler then keeps
+// descriptors and addresses in uniform registers, where the asynchronous
+// instructions take them from.  (With the loop inside a one-lane branch each
+// such instruction took 58-70 cycles to issue, which bounded the 4-bit product
+// and short reductions.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}\n"
+      : "=r"(ok));
+  return ok != 0;
+}
+
 // ----------------------------------------------------------------- mbarriers
 
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

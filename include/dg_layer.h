@@ -75,10 +75,12 @@ int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h,
  * scale_b: NULL, or fp32 with strides in elements (0 = shared): scale_a[t * sa],
  * scale_b[e * sb_e + n * sb_n].  D: bf16 or fp32 (d_type), T x N densely packed.
  * N % 8 == 0 and K % 8 == 0 (bf16) or K % 16 == 0 (8 bits).  T, N, K < 2^31;
- * experts <= 1024.  workspace: dg_layer_grouped_workspace() bytes, 256-byte
- * aligned, zeroed once before its first use (each call leaves its counters
- * zero); calls that may run at the same time need different ones. */
-size_t dg_layer_grouped_workspace(void);
+ * experts <= 1024.  workspace: dg_layer_products_workspace() bytes of the
+ * current device, 16-byte aligned, its first DG_LAYER_COUNTER_BYTES zeroed once
+ * before its first use (each call leaves them zero); calls that may run at the
+ * same time need different ones. */
+#define DG_LAYER_COUNTER_BYTES ((size_t)2048)
+size_t dg_layer_products_workspace(void);
 int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, const void* B, int64_t ld_b, int64_t ld_e,
                             int b_type, int b_n_major, const int32_t* ends, int experts, const float* scale_a,
                             int64_t sa, const float* scale_b, int64_t sb_e, int64_t sb_n, void* D, int d_type,
@@ -113,7 +115,7 @@ int dg_layer_mx4_dequantize(const void* codes, const void* scales, void* y, int 
                             int64_t cols, void* stream);
 /* D[m, n] = sum_k a[m, k] * b[n, k] over the values of two such tensors (M x K
  * and N x K), fp32 accumulation, D bf16 or fp32 (d_type), M x N densely
- * packed.  N % 8 == 0. */
+ * packed.  N % 8 == 0.  workspace as for dg_layer_grouped_matmul. */
 int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales,
                         void* D, int d_type, int64_t M, int64_t N, int64_t K, void* workspace, void* status,
                         void* stream);

@@ -31,6 +31,7 @@ constexpr uint32_t kStage = kStageP + kStageQ;
 constexpr uint32_t kTableBytes = 2 * (kMaxExperts + 2) * 4;
 constexpr uint32_t kSmem = kStages * kStage + 4 * kStoreBuf + kTableBytes + 256 + 1024;
 constexpr uint32_t kTmemCols = 2 * kTileRows;
+constexpr int64_t kSlot = (int64_t)cut_slot_floats(kTileRows);
 constexpr int kBand = 8;      // row tiles swept together, for reuse in L2
 constexpr int kTailRows = 64; // rows of a K block in the gradient
 
@@ -46,12 +47,21 @@ struct Args {
   const float *sa, *sb;
   int64_t sa_s, sb_e, sb_n;
   uint32_t idesc;
+  uint32_t* counters;      // cut tiles
+  float* partial;
   Watch watch;
 };
 
 struct Tile {
   int e, row0, rows, f0, kblocks, k0, tail;
 };
+
+// Rows of a group's tiles: as few tiles as 256 rows allow, of equal height (a
+// multiple of 32), because a short tile still loads all of its features.
+__device__ __forceinline__ int tile_height(int rows) {
+  const int nt = (rows + kTileRows - 1) / kTileRows;
+  return nt > 1 ? ((rows + nt - 1) / nt + 31) / 32 * 32 : kTileRows;
+}
 
 // Group starts (start[e], e <= experts; start[experts + 1] = T) and the number
 // of tiles before each group, by one warp.  Ends are clamped to [previous end,
@@ -96,18 +106,19 @@ __device__ __forceinline__ Tile tile_at(const Args& p, const int* start, const i
   const int nt = (rows + kTileRows - 1) / kTileRows, nf = (p.feats + kPairFeats - 1) / kPairFeats;
   const int j = t - first[e], band = j / (kBand * nf), in = j - band * kBand * nf;
   const int wide = min(kBand, nt - band * kBand), f = in / wide, r = band * kBand + in - f * wide;
+  const int high = GRAD ? kTileRows : tile_height(rows);
   Tile tl;
   tl.e = e;
-  tl.rows = min(kTileRows, rows - r * kTileRows);
+  tl.rows = min(high, rows - r * high);
   tl.f0 = f * kPairFeats;
   if (GRAD) {
-    tl.row0 = r * kTileRows;
+    tl.row0 = r * high;
     tl.k0 = start[e];
     tl.kblocks = (len + kTailRows - 1) / kTailRows;
     tl.tail = len % kTailRows;
   } else {
     constexpr int kb = F8 ? 128 : 64;
-    tl.row0 = start[e] + r * kTileRows;
+    tl.row0 = start[e] + r * high;
     tl.k0 = 0;
     tl.kblocks = e < p.experts ? (p.red + kb - 1) / kb : 0;  // rows past the last group: zeros
     tl.tail = 0;
@@ -133,6 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(start) + kTableBytes);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+  volatile uint32_t* s_last = s_tmem + 1;
+  volatile uint32_t* s_go = s_tmem + 2;  // [2]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t half = cluster_ctarank();
@@ -150,7 +163,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   cluster_sync();
   fence_after();
   const uint32_t tmem = *s_tmem;
-  const int total = first[GRAD ? p.experts : p.experts + 1];
+  // the tiles with work, then (forward) those of the rows past the last group
+  const int real = first[p.experts], total = first[GRAD ? p.experts : p.experts + 1];
+  constexpr int kb_red = F8 ? 128 : 64;
+  Cut cut{0, 1, 0};
+  if (!GRAD) {
+    const int nf = (p.feats + kPairFeats - 1) / kPairFeats;
+    cut = cut_of(real, units, (p.red + kb_red - 1) / kb_red, (int)((int64_t)start[p.experts] * nf / max(real, 1)));
+  }
   const uint32_t base = smem_u32(smem);
 
   if (warp == 0) {
@@ -160,11 +180,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t stage = 0, phase = 0;
     int e = 0;
     bool ok = true;
-    for (int t = unit; t < total && ok; t += units) {
-      const Tile tl = tile_at<GRAD, F8>(p, start, first, t, e);
+    Item w;
+    for (Walk walk(cut, unit, units, total); ok && walk.get(w);) {
+      const Tile tl = tile_at<GRAD, F8>(p, start, first, w.tile, e);
+      const int kb1 = GRAD ? tl.kblocks : min(w.kb1, tl.kblocks);
       const int n = columns<GRAD>(tl), mine = n / 2;  // this CTA's share of the rows operand
       const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
-      for (int kb = 0; kb < tl.kblocks; ++kb) {
+      for (int kb = w.kb0; kb < kb1; ++kb) {
         if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
         const uint32_t fb = mapa(full + 8 * stage, 0);
         const uint32_t sp = base + stage * kStage, sq = sp + kStageP;
@@ -206,14 +228,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       uint32_t stage = 0, phase = 0, it = 0;
       int e = 0;
       bool ok = true;
-      for (int t = unit; t < total && ok; t += units, ++it) {
-        const Tile tl = tile_at<GRAD, F8>(p, start, first, t, e);
+      Item w;
+      for (Walk walk(cut, unit, units, total); ok && walk.get(w); ++it) {
+        const Tile tl = tile_at<GRAD, F8>(p, start, first, w.tile, e);
+        const int kb1 = GRAD ? tl.kblocks : min(w.kb1, tl.kblocks);
         const uint32_t idesc = p.idesc | idesc_columns((uint32_t)columns<GRAD>(tl));
         const uint32_t buf = it & 1;
         if (!(ok = mbar_wait(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
         fence_after();
         const uint32_t d = tmem + buf * kTileRows;
-        for (int kb = 0; kb < tl.kblocks; ++kb) {
+        for (int kb = w.kb0; kb < kb1; ++kb) {
           if (!(ok = mbar_wait(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
           fence_after();
           const uint32_t sp = base + stage * kStage, sq = sp + kStageP;
@@ -225,7 +249,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           if (elect_one()) {
 #pragma unroll
             for (int s = 0; s < 4; ++s)
-              if (!GRAD || s < subs) mma_pair<F8>(d, pd + s * p_step, qd + s * q_step, idesc, (kb | s) != 0);
+              if (!GRAD || s < subs) mma_pair<F8>(d, pd + s * p_step, qd + s * q_step, idesc, kb != w.kb0 || s != 0);
             commit_pair(empty + 8 * stage);
           }
           __syncwarp();
@@ -241,16 +265,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint8_t* box = store_buf + q * kStoreBuf;
     uint32_t it = 0;
     int e = 0;
-    for (int t = unit; t < total; t += units, ++it) {
-      const Tile tl = tile_at<GRAD, F8>(p, start, first, t, e);
+    Item w;
+    for (Walk walk(cut, unit, units, total); walk.get(w); ++it) {
+      const Tile tl = tile_at<GRAD, F8>(p, start, first, w.tile, e);
       const uint32_t buf = it & 1;
-      uint32_t go = 1;
-      if (lane == 0) go = mbar_wait(p.watch, tfull + 8 * buf, (it >> 1) & 1, 0x400u | buf);
-      if (!__shfl_sync(0xffffffffu, go, 0)) {
-        settle();
-        break;
-      }
-      fence_after();
+      if (!epilogue_wait(p.watch, tfull, it, s_go)) break;
       const int f0 = tl.f0 + (int)half * kLanes + q * 32;  // this warp's first feature
       const int feats_ok = min(32, p.feats - f0);
       const int64_t row0 = (int64_t)tl.row0 + (GRAD ? (int64_t)tl.e * p.rows : 0);
@@ -258,24 +277,48 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (!GRAD && p.sb && lane < feats_ok && tl.e < p.experts)
         sb = __ldg(p.sb + tl.e * p.sb_e + (int64_t)(f0 + lane) * p.sb_n);
       const int nch = (tl.rows + kChunk - 1) / kChunk;
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kTileRows;
+      auto read = [&](int c, float(&v)[32]) {
+        uint32_t u[32];
+        tmem_ld32(acc + c * kChunk, u);
+        tmem_ld_wait();
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+      };
+      auto release = [&]() {  // the accumulator has been read
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa(tempty + 8 * buf, 0));
+      };
+      int ways = 1, head = 0;
+      if (!GRAD && w.tile < cut.tiles && (ways = cut_ways(cut, w.tile)) > 1) {
+        head = cut_first(cut, w.tile);
+        float* mine = p.partial + cut_slot(cut, w.tile, unit) * kSlot + half * (kSlot / 2);
+#pragma unroll 1
+        for (int c = 0; c < nch; ++c) {
+          float v[32];
+          read(c, v);
+          store_partial(mine, c * kChunk, q * 32 + lane, v);
+        }
+        if (!cut_last(p.counters + 2 * w.tile + half, ways, s_last)) {
+          release();
+          continue;
+        }
+      }
 #pragma unroll 1
       for (int c = 0; c < nch; ++c) {
         float v[32];
-        if (tl.kblocks > 0) {
-          uint32_t u[32];
-          tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * kTileRows + c * kChunk, u);
-          tmem_ld_wait();
-#pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+        if (ways > 1) {
+          join_partials(
+              ways, [&](int j) { return p.partial + cut_slot(cut, w.tile, head + j) * kSlot + half * (kSlot / 2); },
+              c * kChunk, q * 32 + lane, v);
+        } else if (tl.kblocks > 0) {
+          read(c, v);
         } else {
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
-        if (c == nch - 1) {  // the accumulator has been read
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa(tempty + 8 * buf, 0));
-        }
+        if (c == nch - 1) release();
         const int rows_ok = min(kChunk, tl.rows - c * kChunk);
         const int64_t r0 = row0 + c * kChunk;
         if (!GRAD && (p.sa || p.sb) && tl.kblocks > 0) {
@@ -347,7 +390,8 @@ int launch(const Args& p, int64_t most_tiles, cudaStream_t s) {
   int sms = 0;
   if (int rc = sm_count(&sms)) return rc;
   DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
-  const int64_t units = most_tiles < sms / 2 ? most_tiles : sms / 2;
+  // the forward's tiles may be cut along K, so it takes every SM pair
+  const int64_t units = GRAD && most_tiles < sms / 2 ? most_tiles : sms / 2;
   kernel<<<(unsigned)(2 * units), kThreads, kSmem, s>>>(p);
   DGL_LAUNCHED();
   return DG_OK;
@@ -369,7 +413,11 @@ Watch watch_of(void* status) {
 
 }  // namespace
 
-extern "C" size_t dg_layer_grouped_workspace(void) { return 256; }
+extern "C" size_t dg_layer_products_workspace(void) {
+  int sms = 0;
+  if (sm_count(&sms) != DG_OK) return 0;
+  return cut_bytes(sms / 2, kTileRows);
+}
 
 extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, const void* B, int64_t ld_b,
                                        int64_t ld_e, int b_type, int b_n_major, const int32_t* ends, int experts,
@@ -393,8 +441,8 @@ extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, 
   }
   if (!A || !B || !workspace) return fail(DG_ERR_ARG, "A, B and workspace must not be null");
   const int64_t inner = b_n_major ? N : K;
-  if (!aligned16(A) || !aligned16(B) || !aligned16(D) || ld_a * esz % 16 || ld_b * esz % 16 || ld_e * esz % 16)
-    return fail(DG_ERR_ARG, "A, B, D and their pitches must be multiples of 16 bytes");
+  if (!aligned16(A) || !aligned16(B) || !aligned16(D) || !aligned16(workspace) || ld_a * esz % 16 || ld_b * esz % 16 || ld_e * esz % 16)
+    return fail(DG_ERR_ARG, "A, B, D, the workspace and the pitches must be multiples of 16 bytes");
   if (ld_a < K || ld_b < inner || (experts > 1 && ld_e <= 0)) return fail(DG_ERR_ARG, "a pitch is shorter than its rows");
   Args p{};
   const int64_t pd[3] = {inner, b_n_major ? K : N, experts}, ps[2] = {ld_b, experts > 1 ? ld_e : ld_b * pd[1]};
@@ -406,6 +454,8 @@ extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, 
   p.sa = scale_a, p.sb = scale_b, p.sa_s = sa, p.sb_e = sb_e, p.sb_n = sb_n;
   p.idesc = idesc_of(format_of(b_type), format_of(a_type), b_n_major != 0, false);
   p.watch = watch_of(status);
+  p.counters = static_cast<uint32_t*>(workspace);
+  p.partial = reinterpret_cast<float*>(p.counters + kCutCounters);
   const int64_t most = (T / kTileRows + experts + 1) * ((N + kPairFeats - 1) / kPairFeats);
   if (most > INT32_MAX) return fail(DG_ERR_ARG, "T x N is too large (%lld tiles)", (long long)most);
   const bool f32 = d_type == DG_TYPE_F32;

@@ -33,6 +33,7 @@ constexpr uint32_t kStage = kStageP + kStageQ + kScaleP + kScaleQ;
 constexpr uint32_t kSmem = kStages * kStage + 4 * kStoreBuf + 256 + 1024;
 constexpr uint32_t kTmemCols = 512, kScaleCol = 2 * kTileRows;
 constexpr int kScaleBufs = 4;                    // 24 columns each: 2 x 4 for P, 2 x 8 for Q
+constexpr int64_t kSlot = (int64_t)cut_slot_floats(kTileRows);
 constexpr int kBand = 8;
 
 struct Args {
@@ -40,6 +41,8 @@ struct Args {
   CUtensorMap sp, sq;      // scales: (256 words, K block, row tile), boxes of one and two row tiles
   int rows, feats, kblocks;
   void* out;
+  uint32_t* counters;      // cut tiles
+  float* partial;
   Watch watch;
 };
 
@@ -83,6 +86,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   uint64_t* bars = reinterpret_cast<uint64_t*>(store_buf + 4 * kStoreBuf);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+  volatile uint32_t* s_last = s_tmem + 1;
+  volatile uint32_t* s_go = s_tmem + 2;  // [2]
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t half = cluster_ctarank();
@@ -99,17 +104,19 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   fence_after();
   const uint32_t tmem = *s_tmem, base = smem_u32(smem);
   const int total = ((p.rows + kTileRows - 1) / kTileRows) * ((p.feats + kPairFeats - 1) / kPairFeats);
+  const Cut cut = cut_of(total, units, p.kblocks, min(p.rows, kTileRows));
 
   if (warp == 0) {
     prefetch_map(&p.p);
     prefetch_map(&p.q);
     uint32_t stage = 0, phase = 0;
     bool ok = true;
-    for (int t = unit; t < total && ok; t += units) {
-      const Tile tl = tile_at(p, t);
+    Item w;
+    for (Walk walk(cut, unit, units, total); ok && walk.get(w);) {
+      const Tile tl = tile_at(p, w.tile);
       const int n = (tl.rows + 31) / 32 * 32, mine = n / 2;
       const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
-      for (int kb = 0; kb < p.kblocks; ++kb) {
+      for (int kb = w.kb0; kb < w.kb1; ++kb) {
         if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
         const uint32_t fb = mapa(full + 8 * stage, 0);
         const uint32_t sp = base + stage * kStage, sq = sp + kStageP, ss = sq + kStageQ;
@@ -131,15 +138,16 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
     if (half == 0) {
       uint32_t stage = 0, phase = 0, it = 0, sbuf = 0;
       bool ok = true;
-      for (int t = unit; t < total && ok; t += units, ++it) {
-        const Tile tl = tile_at(p, t);
+      Item w;
+      for (Walk walk(cut, unit, units, total); ok && walk.get(w); ++it) {
+        const Tile tl = tile_at(p, w.tile);
         const uint32_t n = (uint32_t)(tl.rows + 31) / 32 * 32, buf = it & 1;
         const uint32_t odd = (tl.row0 & 64) ? 2u : 0u;  // columns into the first scale tile
         if (!(ok = mbar_wait(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
         fence_after();
         const uint32_t d = tmem + buf * kTileRows;
         const uint32_t idesc0 = idesc_mx4(n, 0), idesc2 = idesc_mx4(n, 2);
-        for (int kb = 0; kb < p.kblocks; ++kb) {
+        for (int kb = w.kb0; kb < w.kb1; ++kb) {
           if (!(ok = mbar_wait(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
           fence_after();
           const uint32_t sp = base + stage * kStage, sq = sp + kStageP, ss = sq + kStageQ;
@@ -156,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
 #pragma unroll
             for (uint32_t s = 0; s < 4; ++s)
               mma_mx4(d, pd + 2 * s, qd + 2 * s, s & 1 ? idesc2 : idesc0, tp + 4 * (s >> 1), tq + 8 * (s >> 1) + odd,
-                      (kb | s) != 0);
+                      kb != w.kb0 || s != 0);
             commit_pair(empty + 8 * stage);
           }
           __syncwarp();
@@ -171,31 +179,52 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
     const int q = warp & 3;
     uint8_t* box = store_buf + q * kStoreBuf;
     uint32_t it = 0;
-    for (int t = unit; t < total; t += units, ++it) {
-      const Tile tl = tile_at(p, t);
+    Item w;
+    for (Walk walk(cut, unit, units, total); walk.get(w); ++it) {
+      const Tile tl = tile_at(p, w.tile);
       const uint32_t buf = it & 1;
-      uint32_t go = 1;
-      if (lane == 0) go = mbar_wait(p.watch, tfull + 8 * buf, (it >> 1) & 1, 0x400u | buf);
-      if (!__shfl_sync(0xffffffffu, go, 0)) {
-        settle();
-        break;
-      }
-      fence_after();
+      if (!epilogue_wait(p.watch, tfull, it, s_go)) break;
       const int f0 = tl.f0 + (int)half * kLanes + q * 32, feats_ok = min(32, p.feats - f0);
       const int nch = (tl.rows + kChunk - 1) / kChunk;
-#pragma unroll 1
-      for (int c = 0; c < nch; ++c) {
+      const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kTileRows;
+      auto read = [&](int c, float(&v)[32]) {
         uint32_t u[32];
-        tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + buf * kTileRows + c * kChunk, u);
+        tmem_ld32(acc + c * kChunk, u);
         tmem_ld_wait();
-        if (c == nch - 1) {
-          fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(mapa(tempty + 8 * buf, 0));
-        }
-        float v[32];
 #pragma unroll
         for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(u[i]);
+      };
+      auto release = [&]() {  // the accumulator has been read
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(mapa(tempty + 8 * buf, 0));
+      };
+      int ways = 1, head = 0;
+      if (w.tile < cut.tiles && (ways = cut_ways(cut, w.tile)) > 1) {
+        head = cut_first(cut, w.tile);
+        float* mine = p.partial + cut_slot(cut, w.tile, unit) * kSlot + half * (kSlot / 2);
+#pragma unroll 1
+        for (int c = 0; c < nch; ++c) {
+          float v[32];
+          read(c, v);
+          store_partial(mine, c * kChunk, q * 32 + lane, v);
+        }
+        if (!cut_last(p.counters + 2 * w.tile + half, ways, s_last)) {
+          release();
+          continue;
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < nch; ++c) {
+        float v[32];
+        if (ways > 1) {
+          join_partials(
+              ways, [&](int j) { return p.partial + cut_slot(cut, w.tile, head + j) * kSlot + half * (kSlot / 2); },
+              c * kChunk, q * 32 + lane, v);
+        } else {
+          read(c, v);
+        }
+        if (c == nch - 1) release();
         const int64_t at = (int64_t)(tl.row0 + c * kChunk) * p.feats + f0;
         const int rows_ok = min(kChunk, tl.rows - c * kChunk);
         if constexpr (OUT32)
@@ -218,12 +247,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
 std::atomic<uint32_t> g_epoch{0x80000001u};
 
 template <bool OUT32>
-int launch(const Args& p, int64_t tiles, cudaStream_t s) {
+int launch(const Args& p, cudaStream_t s) {
   int sms = 0;
   if (int rc = sm_count(&sms)) return rc;
   DGL_CUDA(cudaFuncSetAttribute(mx4_kernel<OUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
-  const int64_t units = tiles < sms / 2 ? tiles : sms / 2;
-  mx4_kernel<OUT32><<<(unsigned)(2 * units), kThreads, kSmem, s>>>(p);
+  mx4_kernel<OUT32><<<(unsigned)(sms / 2 * 2), kThreads, kSmem, s>>>(p);
   DGL_LAUNCHED();
   return DG_OK;
 }
@@ -233,7 +261,6 @@ int launch(const Args& p, int64_t tiles, cudaStream_t s) {
 extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, const void* b_codes,
                                    const void* b_scales, void* D, int d_type, int64_t M, int64_t N, int64_t K,
                                    void* workspace, void* status, void* stream) {
-  (void)workspace;
   if (M < 0 || N < 0 || K < 0 || M > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
     return fail(DG_ERR_ARG, "M %lld, N %lld, K %lld out of range", (long long)M, (long long)N, (long long)K);
   if (d_type != DG_TYPE_BF16 && d_type != DG_TYPE_F32) return fail(DG_ERR_ARG, "D is bf16 or fp32 (got type %d)", d_type);
@@ -245,9 +272,10 @@ extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, co
     DGL_CUDA(cudaMemsetAsync(D, 0, (size_t)M * N * (d_type == DG_TYPE_F32 ? 4 : 2), s));
     return DG_OK;
   }
-  if (!a_codes || !a_scales || !b_codes || !b_scales) return fail(DG_ERR_ARG, "codes and scales must not be null");
-  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(D))
-    return fail(DG_ERR_ARG, "codes, scales and D must be 16-byte aligned");
+  if (!a_codes || !a_scales || !b_codes || !b_scales || !workspace)
+    return fail(DG_ERR_ARG, "codes, scales and the workspace must not be null");
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(b_codes) || !aligned16(b_scales) || !aligned16(D) || !aligned16(workspace))
+    return fail(DG_ERR_ARG, "codes, scales, D and the workspace must be 16-byte aligned");
   const int64_t tiles = ((M + kTileRows - 1) / kTileRows) * ((N + kPairFeats - 1) / kPairFeats);
   if (tiles > INT32_MAX) return fail(DG_ERR_ARG, "M x N is too large (%lld tiles)", (long long)tiles);
   Args p{};
@@ -259,6 +287,8 @@ extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, co
   if (int rc = encode_scale_map(&p.sp, b_scales, p.kblocks, (N + 127) / 128, 1)) return rc;
   if (int rc = encode_scale_map(&p.sq, a_scales, p.kblocks, (M + 127) / 128, 2)) return rc;
   p.rows = (int)M, p.feats = (int)N, p.out = D;
+  p.counters = static_cast<uint32_t*>(workspace);
+  p.partial = reinterpret_cast<float*>(p.counters + kCutCounters);
   p.watch = Watch{static_cast<unsigned long long*>(status), g_epoch.fetch_add(1, std::memory_order_relaxed), 4000000000ull};
-  return d_type == DG_TYPE_F32 ? launch<true>(p, tiles, s) : launch<false>(p, tiles, s);
+  return d_type == DG_TYPE_F32 ? launch<true>(p, s) : launch<false>(p, s);
 }

@@ -216,6 +216,127 @@ __host__ __device__ constexpr uint32_t idesc_of(uint32_t p_fmt, uint32_t q_fmt, 
 }
 __device__ __forceinline__ uint32_t idesc_columns(uint32_t n) { return (n >> 3) << 17; }
 
+// The four epilogue warps.  They decide together whether a tile's accumulator
+// arrived (one thread waits; `go`: two words of shared memory, by turns), so
+// that none is left at a barrier by one that gave up.
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ bool epilogue_wait(const Watch& w, uint32_t tfull, uint32_t it, volatile uint32_t* go) {
+  const uint32_t buf = it & 1;
+  if (threadIdx.x == 64) go[buf] = mbar_wait(w, tfull + 8 * buf, (it >> 1) & 1, 0x400u | buf) ? 1u : 0u;
+  epilogue_sync();
+  if (go[buf] == 0) {
+    settle();
+    return false;
+  }
+  fence_after();
+  return true;
+}
+
+// --------------------------------------------------------------- split tiles
+
+// The tiles of a list walked by `units` CTA pairs.  Where the last round of
+// tiles would leave many pairs idle, the list's first `cut` tiles (fewer than
+// the pairs) are cut along K into equal shares of K blocks instead, one
+// contiguous range of shares to a pair, and the rest is dealt out whole.  A
+// pair's range meets at most two tiles.  The pairs of one cut tile leave fp32
+// partial accumulators in the workspace and count themselves in; the last one
+// adds them in the order of K (the same bits every time) and stores the tile.
+// No pair waits for another.
+constexpr int kMinShare = 8;   // K blocks
+constexpr int kJoinCost = 6;   // K blocks' time that a step of 32 rows costs to leave and to join, four partials at a time
+struct Cut {
+  int tiles, kblocks, share;
+};
+// `rows`: of a tile (on average).  Cutting pays for short tiles (a decoding
+// step's 32 columns are joined in a microsecond) and for tall ones with a long K
+// whose round would leave most pairs idle.
+__device__ __forceinline__ Cut cut_of(int total, int units, int kblocks, int rows) {
+  Cut c{total % units, kblocks, 0};
+  // (a K so long that the products below would pass 32 bits is left whole)
+  if (c.tiles == 0 || kblocks > (1 << 20)) return Cut{0, kblocks, 0};
+  c.share = max(kMinShare, (c.tiles * kblocks + units - 1) / units);
+  const int ways = kblocks / c.share + 1, cost = kJoinCost * ((rows + kChunk - 1) / kChunk) * ((ways + 3) / 4);
+  return kblocks - c.share > cost ? c : Cut{0, kblocks, 0};
+}
+// How many pairs share tile t of the cut ones, the first of them, and the
+// workspace slot of the j-th pair's partial.
+__device__ __forceinline__ int cut_first(const Cut& c, int t) { return t * c.kblocks / c.share; }
+__device__ __forceinline__ int cut_ways(const Cut& c, int t) {
+  return ((t + 1) * c.kblocks - 1) / c.share - cut_first(c, t) + 1;
+}
+__device__ __forceinline__ int cut_slot(const Cut& c, int t, int unit) {
+  return 2 * unit + (unit * c.share / c.kblocks < t ? 1 : 0);
+}
+
+struct Item {
+  int tile, kb0, kb1;
+};
+struct Walk {
+  int pos, end, next, total, units, kblocks;
+  __device__ __forceinline__ Walk(const Cut& c, int unit, int units_, int total_)
+      : pos(min(unit * c.share, c.tiles * c.kblocks)), end(min(pos + c.share, c.tiles * c.kblocks)), next(c.tiles + unit),
+        total(total_), units(units_), kblocks(c.kblocks) {}
+  __device__ __forceinline__ bool get(Item& it) {
+    if (pos < end) {
+      it.tile = pos / kblocks;
+      it.kb0 = pos - it.tile * kblocks;
+      it.kb1 = min(kblocks, it.kb0 + end - pos);
+      pos += it.kb1 - it.kb0;
+      return true;
+    }
+    it.tile = next;
+    it.kb0 = 0;
+    it.kb1 = kblocks;
+    next += units;
+    return it.tile < total;
+  }
+};
+
+// Workspace of the cut tiles: a counter for each (tile, half), which wraps back
+// to 0 with its last pair, then slots of [half][column][lane].
+constexpr int kCutCounters = 2 * 256;
+__host__ __device__ constexpr size_t cut_slot_floats(int columns) { return (size_t)2 * columns * kLanes; }
+__host__ __device__ constexpr size_t cut_bytes(int units, int columns) {
+  return kCutCounters * 4 + (size_t)2 * units * cut_slot_floats(columns) * 4;
+}
+
+// A warp's 32 x 32 box of a partial accumulator: to / from the slot.
+__device__ __forceinline__ void store_partial(float* slot, int column, int lane_of, const float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) __stcg(slot + (int64_t)(column + i) * kLanes + lane_of, v[i]);
+}
+// The sum of `ways` partials, in their order; slot(j): the j-th one's.
+template <class Slot>
+__device__ __forceinline__ void join_partials(int ways, Slot slot, int column, int lane_of, float (&v)[32]) {
+#pragma unroll
+  for (int i = 0; i < 32; ++i) v[i] = 0.f;
+#pragma unroll 1
+  for (int j = 0; j < ways; j += 4) {
+    float u[4][32];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float* s = slot(min(j + k, ways - 1)) + (int64_t)column * kLanes + lane_of;
+#pragma unroll
+      for (int i = 0; i < 32; ++i) u[k][i] = j + k < ways ? __ldcg(s + i * kLanes) : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] += u[k][i];
+  }
+}
+// After every epilogue thread of this half has stored its partial: whether this
+// pair is the tile's last.  `flag`: a word of shared memory.
+__device__ __forceinline__ bool cut_last(uint32_t* counter, int ways, volatile uint32_t* flag) {
+  __threadfence();
+  epilogue_sync();
+  if (threadIdx.x == 64) *flag = atomicInc(counter, (uint32_t)ways - 1) == (uint32_t)ways - 1 ? 1u : 0u;
+  epilogue_sync();
+  const bool last = *flag != 0;
+  if (last) __threadfence();
+  return last;
+}
+
 // ------------------------------------------------------------ epilogue stores
 
 // A warp's box of 32 features x 32 rows from registers (v[i]: row i, this

@@ -27,13 +27,14 @@ for _name, _t in (("float8_e4m3fn", dg.TYPE_E4M3), ("float8_e5m2", dg.TYPE_E5M2)
 
 # Every symbol include/dg_layer.h declares.
 EXPORTS = ("dg_layer_add_rms_norm", "dg_layer_add_rms_norm_backward", "dg_layer_add_rms_norm_backward_workspace",
-           "dg_layer_grouped_workspace", "dg_layer_grouped_matmul", "dg_layer_grouped_grad_workspace",
+           "dg_layer_products_workspace", "dg_layer_grouped_matmul", "dg_layer_grouped_grad_workspace",
            "dg_layer_grouped_weight_grad", "dg_layer_mx4_scale_bytes", "dg_layer_mx4_quantize",
            "dg_layer_mx4_dequantize", "dg_layer_mx4_matmul", "dg_layer_check", "dg_layer_last_error")
 
 _LIB = None
 _lock = threading.Lock()
-_state: dict = {}  # device index -> (status word, counters of the grouped products)
+_state: dict = {}  # device index -> status word and its address
+_workspaces: dict = {}  # (device index, stream) -> address of the products' workspace, and its tensor
 
 
 def lib():
@@ -45,7 +46,7 @@ def lib():
             "add_rms_norm": (i32, [vp, i64, vp, i64, i32, vp, i32, vp, i32, vp, i64, vp, vp, vp, i64, i64, f32, vp]),
             "add_rms_norm_backward_workspace": (sz, [i64, i64]),
             "add_rms_norm_backward": (i32, [vp, i64, vp, i64, i32, vp, i32, vp, vp, i64, vp, vp, vp, i64, i64, vp]),
-            "grouped_workspace": (sz, []),
+            "products_workspace": (sz, []),
             "grouped_matmul": (i32, [vp, i64, i32, vp, i64, i64, i32, i32, vp, i32, vp, i64, vp, i64, i64, vp, i32,
                                      i64, i64, i64, vp, vp, vp]),
             "grouped_grad_workspace": (sz, [i32, i64, i64]),
@@ -64,11 +65,6 @@ def lib():
     return _LIB
 
 
-def _check(rc: int):
-    if rc != dg.OK:
-        raise dg.DGError(rc, lib().dg_layer_last_error().decode())
-
-
 def _type(t: torch.dtype, what: str) -> int:
     got = _TYPES.get(t)
     if got is None:
@@ -76,47 +72,71 @@ def _type(t: torch.dtype, what: str) -> int:
     return got
 
 
-def _stream(dev: torch.device) -> int:
-    return torch.cuda.current_stream(dev).cuda_stream
+# the current stream's handle without building a Stream object (2 us a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+if _raw_stream is None:
+    def _raw_stream(index):  # noqa: F811
+        return torch.cuda.current_stream(index).cuda_stream
 
 
-class _on:
-    """The library works on the current device: a guard that costs nothing when it is already the tensors'."""
-
-    __slots__ = ("guard",)
-
-    def __init__(self, dev):
-        self.guard = None if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
-
-    def __enter__(self):
-        if self.guard is not None:
-            self.guard.__enter__()
-
-    def __exit__(self, *a):
-        if self.guard is not None:
-            self.guard.__exit__(*a)
+def _call(dev: torch.device, fn, *args):
+    """``fn(*args, stream)`` on ``dev``, whose current stream is appended; raises on an error."""
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        rc = fn(*args, _raw_stream(index))
+    else:  # the library works on the current device
+        with torch.cuda.device(index):
+            rc = fn(*args, _raw_stream(index))
+    if rc != dg.OK:
+        raise dg.DGError(rc, _LIB.dg_layer_last_error().decode())
 
 
-def _same_device(dev: torch.device, *tensors):
-    if dev.type != "cuda":
+def _same_device(x: torch.Tensor, *tensors) -> torch.device:
+    if not x.is_cuda:
         raise ValueError("inputs must be CUDA tensors")
+    dev = x.device
     for t in tensors:
         if t is not None and t.device != dev:
             raise ValueError("all tensors must be on the same CUDA device")
+    return dev
 
 
-def _device_state(dev: torch.device):
+_COUNTER_BYTES = 2048  # DG_LAYER_COUNTER_BYTES
+
+
+def _status(dev: torch.device) -> int:
+    """Address of the device's status word (created on first use)."""
     st = _state.get(dev.index)
     if st is None:
         with _lock:
-            st = _state.get(dev.index)
-            if st is None:
-                if torch.cuda.is_current_stream_capturing():
-                    raise RuntimeError("make one call outside of stream capture first")
-                words = torch.zeros(64, dtype=torch.int64, device=dev)
-                torch.cuda.current_stream(dev).synchronize()  # zero before any stream uses them
-                st = _state[dev.index] = (words, words.data_ptr())
-    return st
+            if torch.cuda.is_current_stream_capturing():
+                raise RuntimeError("make one call outside of stream capture first")
+            word = torch.zeros(32, dtype=torch.int64, device=dev)
+            torch.cuda.current_stream(dev).synchronize()  # zero before any stream uses it
+            st = _state.setdefault(dev.index, (word, word.data_ptr()))
+    return st[1]
+
+
+def _workspace(dev: torch.device):
+    """(address, tensor) of the products' workspace: one for each stream, whose calls run
+    one after another; inside a stream capture one of the graph's own, since
+    its replays may run beside the stream's later calls."""
+    key = (dev.index, _raw_stream(dev.index))
+    ws = _workspaces.get(key)
+    capturing = torch.cuda.is_current_stream_capturing()
+    if ws is None or capturing:
+        with torch.cuda.device(dev):
+            ws = torch.empty(lib().dg_layer_products_workspace(), dtype=torch.uint8, device=dev)
+        ws[:_COUNTER_BYTES].zero_()
+        if capturing:
+            return ws.data_ptr(), ws
+        ws = _workspaces[key] = (ws.data_ptr(), ws)
+    return ws
+
+
+def clear_workspaces() -> None:
+    """Drop the products' cached workspaces (``ops.clear_caches`` calls this)."""
+    _workspaces.clear()
 
 
 def check_products(device=None) -> None:
@@ -124,8 +144,9 @@ def check_products(device=None) -> None:
     a product launched there since the last check gave up a pipeline wait (its
     output is then undefined)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
-    with _on(dev):
-        _check(lib().dg_layer_check(_device_state(dev)[1], _stream(dev)))
+    if dev.index is None:
+        dev = torch.device("cuda", torch.cuda.current_device())
+    _call(dev, lib().dg_layer_check, _status(dev))
 
 
 def _ptr(t):
@@ -155,39 +176,39 @@ def _as_rows(t: torch.Tensor, hidden: int) -> torch.Tensor:
 
 
 def _norm_forward(x, weight, residual, eps, out_dtype, scale, keep_rstd, inplace):
-    hidden = x.shape[-1]
+    shape = x.shape
+    hidden = shape[-1]
     dev = x.device
     x2 = _as_rows(x, hidden)
     rows = x2.shape[0]
-    y = torch.empty(x.shape, dtype=out_dtype, device=dev)
-    row_scale = rstd = r2 = h = h2 = scale_in = None
+    y = torch.empty(shape, dtype=out_dtype, device=dev)
+    row_scale = rstd = h = scale_in = None
+    r_ptr, r_ld, r_type, h_ptr, h_ld = None, 0, 0, None, 0
     if residual is not None:
         r2 = _as_rows(residual, hidden)
         if inplace:
             if r2.data_ptr() != residual.data_ptr():
                 raise ValueError("an in-place residual must have rows that are contiguous")
-            h, h2 = residual, r2
+            h = residual
         else:
-            h = torch.empty(residual.shape, dtype=residual.dtype, device=dev)
-            h2 = h.view(rows, hidden)
+            h = torch.empty(shape, dtype=residual.dtype, device=dev)
+        r_ptr, r_ld, r_type = r2.data_ptr(), r2.stride(0), _TYPES[r2.dtype]
+        h_ptr, h_ld = (r_ptr, r_ld) if inplace else (h.data_ptr(), hidden)
     if out_dtype != torch.bfloat16:
         if scale is None:
-            row_scale = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
+            row_scale = torch.empty(shape[:-1], dtype=torch.float32, device=dev)
         elif isinstance(scale, torch.Tensor):
             if scale.numel() != 1 or scale.dtype != torch.float32:
                 raise ValueError("a given scale is a number or a one-element float32 tensor")
-            _same_device(dev, scale)
+            _same_device(x, scale)
             scale_in = scale
         else:
             scale_in = torch.full((1,), float(scale), dtype=torch.float32, device=dev)
     if keep_rstd:
         rstd = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-    with _on(dev):
-        _check(lib().dg_layer_add_rms_norm(
-            x2.data_ptr(), x2.stride(0), _ptr(r2), 0 if r2 is None else r2.stride(0),
-            0 if r2 is None else _TYPES[r2.dtype], weight.data_ptr(), _TYPES[weight.dtype], y.data_ptr(),
-            _TYPES[out_dtype], _ptr(h2), 0 if h2 is None else h2.stride(0), _ptr(row_scale), _ptr(scale_in),
-            _ptr(rstd), rows, hidden, eps, _stream(dev)))
+    _call(dev, (_LIB or lib()).dg_layer_add_rms_norm, x2.data_ptr(), x2.stride(0), r_ptr, r_ld, r_type,
+          weight.data_ptr(), _TYPES[weight.dtype], y.data_ptr(), _TYPES[out_dtype], h_ptr, h_ld, _ptr(row_scale),
+          _ptr(scale_in), _ptr(rstd), rows, hidden, eps)
     return y, x if h is None else h, row_scale, rstd
 
 
@@ -244,7 +265,7 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tenso
         raise ValueError(f"out_dtype must be bfloat16 or a float8 type, got {out_dtype}")
     if scale is not None and out_dtype == torch.bfloat16:
         raise ValueError("a scale needs a float8 out_dtype")
-    _same_device(x.device, weight, residual)
+    _same_device(x, weight, residual)
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or
                                     (residual is not None and residual.requires_grad)):
         if out_dtype != torch.bfloat16 or inplace:
@@ -269,8 +290,7 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
         raise TypeError("dy must be bfloat16 and rstd float32")
     if h.dtype not in (torch.bfloat16, torch.float32) or weight.dtype not in (torch.bfloat16, torch.float32):
         raise TypeError("h and weight must be bfloat16 or float32")
-    dev = h.device
-    _same_device(dev, dy, weight, rstd, d_residual)
+    dev = _same_device(h, dy, weight, rstd, d_residual)
     dy2, h2 = _as_rows(dy, hidden), _as_rows(h, hidden)
     d2 = None if d_residual is None else _as_rows(d_residual, hidden)
     weight, rstd = weight.contiguous(), rstd.contiguous()
@@ -279,11 +299,9 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
     dw = torch.empty_like(weight)
     L = lib()
     ws = torch.empty(L.dg_layer_add_rms_norm_backward_workspace(rows, hidden), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        _check(L.dg_layer_add_rms_norm_backward(
-            dy2.data_ptr(), dy2.stride(0), h2.data_ptr(), h2.stride(0), _TYPES[h2.dtype], weight.data_ptr(),
-            _TYPES[weight.dtype], rstd.data_ptr(), _ptr(d2), 0 if d2 is None else d2.stride(0), dx.data_ptr(),
-            dw.data_ptr(), ws.data_ptr(), rows, hidden, _stream(dev)))
+    _call(dev, L.dg_layer_add_rms_norm_backward, dy2.data_ptr(), dy2.stride(0), h2.data_ptr(), h2.stride(0),
+          _TYPES[h2.dtype], weight.data_ptr(), _TYPES[weight.dtype], rstd.data_ptr(), _ptr(d2),
+          0 if d2 is None else d2.stride(0), dx.data_ptr(), dw.data_ptr(), ws.data_ptr(), rows, hidden)
     return dx, dw
 
 
@@ -321,7 +339,7 @@ def _grouped_check(A, B, ends):
         raise ValueError(f"A must be (T, K) and B (experts, K, N), got {tuple(A.shape)} and {tuple(B.shape)}")
     if ends.dtype != torch.int32 or ends.dim() != 1 or ends.shape[0] != B.shape[0]:
         raise ValueError("group_ends must be an int32 vector with one ascending end for each expert")
-    _same_device(A.device, B, ends)
+    _same_device(A, B, ends)
 
 
 def _scale_strides(s, shape, what):
@@ -349,14 +367,12 @@ def _grouped_forward(A, B, ends, scale_a, scale_b, out_dtype):
     if scale_b is not None and isinstance(scale_b, torch.Tensor) and scale_b.dim() == 1 and scale_b.shape[0] == E:
         scale_b = scale_b[:, None]  # one for each expert
     sb, (sb_e, sb_n) = _scale_strides(scale_b, (E, N), "scale_b")
-    _same_device(dev, sa, sb)
+    _same_device(A, sa, sb)
     D = torch.empty((T, N), dtype=out_dtype, device=dev)
-    status = _device_state(dev)[1]
-    with _on(dev):
-        _check(lib().dg_layer_grouped_matmul(
-            A.data_ptr(), A.stride(0), _TYPES[A.dtype], Bt.data_ptr(), ld_b, ld_e, _TYPES[B.dtype], n_major,
-            ends.data_ptr(), E, _ptr(sa), sa_s, _ptr(sb), sb_e, sb_n, D.data_ptr(), _TYPES[out_dtype], T, N, K,
-            status + 256, status, _stream(dev)))
+    ws = _workspace(dev)
+    _call(dev, (_LIB or lib()).dg_layer_grouped_matmul, A.data_ptr(), A.stride(0), _TYPES[A.dtype], Bt.data_ptr(), ld_b,
+          ld_e, _TYPES[B.dtype], n_major, ends.data_ptr(), E, _ptr(sa), sa_s, _ptr(sb), sb_e, sb_n, D.data_ptr(),
+          _TYPES[out_dtype], T, N, K, ws[0], _status(dev))
     return D
 
 
@@ -412,10 +428,8 @@ def _weight_grad(rows, feats, ends, experts):
     out = torch.empty((experts, N, K), dtype=torch.bfloat16, device=dev)
     L = lib()
     ws = torch.empty(L.dg_layer_grouped_grad_workspace(experts, N, K), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        _check(L.dg_layer_grouped_weight_grad(rows.data_ptr(), rows.stride(0), feats.data_ptr(), feats.stride(0),
-                                              ends.data_ptr(), experts, out.data_ptr(), dg.TYPE_BF16, T, N, K,
-                                              ws.data_ptr(), _device_state(dev)[1], _stream(dev)))
+    _call(dev, L.dg_layer_grouped_weight_grad, rows.data_ptr(), rows.stride(0), feats.data_ptr(), feats.stride(0),
+          ends.data_ptr(), experts, out.data_ptr(), dg.TYPE_BF16, T, N, K, ws.data_ptr(), _status(dev))
     return out
 
 
@@ -429,7 +443,7 @@ def grouped_matmul_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor, 
         raise ValueError(f"dD must be {(A.shape[0], B.shape[2])}, got {tuple(dD.shape)}")
     if not (dD.dtype == A.dtype == B.dtype == torch.bfloat16):
         raise TypeError("dD, A and B must be bfloat16")
-    _same_device(A.device, dD)
+    _same_device(A, dD)
     dA = _grouped_forward(dD, B.transpose(1, 2), group_ends, None, None, torch.bfloat16) if need[0] else None
     dB = None
     if need[1]:
@@ -470,7 +484,7 @@ def _mx4_check(q: MX4Tensor, what: str):
         raise ValueError(f"{what}.codes must be contiguous uint8 of shape {(rows, cols // 2)}")
     if q.scales.dtype != torch.uint8 or q.scales.shape != _scale_shape(rows, cols) or not q.scales.is_contiguous():
         raise ValueError(f"{what}.scales must be contiguous uint8 of shape {_scale_shape(rows, cols)}")
-    _same_device(q.codes.device, q.scales)
+    _same_device(q.codes, q.scales)
 
 
 def quantize_mx4(x: torch.Tensor) -> MX4Tensor:
@@ -483,8 +497,7 @@ def quantize_mx4(x: torch.Tensor) -> MX4Tensor:
     if x.dim() < 1:
         raise ValueError("x must have a last dimension")
     cols = x.shape[-1]
-    dev = x.device
-    _same_device(dev)
+    dev = _same_device(x)
     x2 = _as_rows(x, cols)
     if not _pitch_ok(x2, (0,)):
         x2 = x2.contiguous() if not x2.is_contiguous() else x2.clone()
@@ -493,9 +506,8 @@ def quantize_mx4(x: torch.Tensor) -> MX4Tensor:
         raise ValueError(f"the last dimension ({cols}) must be a multiple of 32")
     codes = torch.empty((rows, cols // 2), dtype=torch.uint8, device=dev)
     scales = torch.empty(_scale_shape(rows, cols), dtype=torch.uint8, device=dev)
-    with _on(dev):
-        _check(lib().dg_layer_mx4_quantize(x2.data_ptr(), x2.stride(0), _TYPES[x2.dtype], codes.data_ptr(),
-                                           scales.data_ptr(), rows, cols, _stream(dev)))
+    _call(dev, (_LIB or lib()).dg_layer_mx4_quantize, x2.data_ptr(), x2.stride(0), _TYPES[x2.dtype], codes.data_ptr(),
+          scales.data_ptr(), rows, cols)
     return MX4Tensor(codes, scales, rows, cols)
 
 
@@ -506,9 +518,8 @@ def dequantize_mx4(q: MX4Tensor, *, out_dtype: torch.dtype = torch.bfloat16) -> 
         raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
     dev = q.codes.device
     y = torch.empty((q.rows, q.cols), dtype=out_dtype, device=dev)
-    with _on(dev):
-        _check(lib().dg_layer_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), y.data_ptr(), _TYPES[out_dtype],
-                                             q.rows, q.cols, _stream(dev)))
+    _call(dev, (_LIB or lib()).dg_layer_mx4_dequantize, q.codes.data_ptr(), q.scales.data_ptr(), y.data_ptr(),
+          _TYPES[out_dtype], q.rows, q.cols)
     return y
 
 
@@ -522,12 +533,9 @@ def mx4_matmul(a: MX4Tensor, b: MX4Tensor, *, out_dtype: torch.dtype = torch.bfl
         raise ValueError(f"a has {a.cols} columns, b {b.cols}")
     if out_dtype not in (torch.bfloat16, torch.float32):
         raise ValueError(f"out_dtype must be bfloat16 or float32, got {out_dtype}")
-    dev = a.codes.device
-    _same_device(dev, b.codes)
+    dev = _same_device(a.codes, b.codes)
     D = torch.empty((a.rows, b.rows), dtype=out_dtype, device=dev)
-    status = _device_state(dev)[1]
-    with _on(dev):
-        _check(lib().dg_layer_mx4_matmul(a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
-                                         b.scales.data_ptr(), D.data_ptr(), _TYPES[out_dtype], a.rows, b.rows, a.cols,
-                                         status + 256, status, _stream(dev)))
+    ws = _workspace(dev)
+    _call(dev, (_LIB or lib()).dg_layer_mx4_matmul, a.codes.data_ptr(), a.scales.data_ptr(), b.codes.data_ptr(),
+          b.scales.data_ptr(), D.data_ptr(), _TYPES[out_dtype], a.rows, b.rows, a.cols, ws[0], _status(dev))
     return D

@@ -45,7 +45,7 @@ import threading
 
 import torch
 
-from . import dg
+from . import dg, layer
 from .layer import (MX4Tensor, NormResult, add_rms_norm, add_rms_norm_backward, check_products,  # noqa: F401
                     dequantize_mx4, grouped_matmul, grouped_matmul_backward, mx4_matmul, quantize_mx4)
 
@@ -358,3 +358,4 @@ def clear_caches() -> None:
         _plans.clear()
         _workspaces.clear()
         _copy_streams.clear()
+        layer.clear_workspaces()

@@ -94,11 +94,11 @@ def test_mx4_refuses(L):
     assert q(None, 64, 0, 16, 16, 0, 64, None) == dg.OK
     assert L.dg_layer_mx4_dequantize(16, 16, 16, dg.TYPE_E5M2, 2, 64, None) == dg.ERR_ARG
     m = L.dg_layer_mx4_matmul
-    assert m(16, 16, 16, 16, 16, 0, 4, 60, 64, None, 16, None) == dg.ERR_SHAPE
-    assert m(16, 16, 16, 16, 16, 0, 4, 64, 48, None, 16, None) == dg.ERR_SHAPE
-    assert m(16, 16, 16, 16, 16, dg.TYPE_E4M3, 4, 64, 64, None, 16, None) == dg.ERR_ARG
-    assert m(16, None, 16, 16, 16, 0, 4, 64, 64, None, 16, None) == dg.ERR_ARG
-    assert m(24, 16, 16, 16, 16, 0, 4, 64, 64, None, 16, None) == dg.ERR_ARG
+    assert m(16, 16, 16, 16, 16, 0, 4, 60, 64, 256, 16, None) == dg.ERR_SHAPE
+    assert m(16, 16, 16, 16, 16, 0, 4, 64, 48, 256, 16, None) == dg.ERR_SHAPE
+    assert m(16, 16, 16, 16, 16, dg.TYPE_E4M3, 4, 64, 64, 256, 16, None) == dg.ERR_ARG
+    assert m(16, None, 16, 16, 16, 0, 4, 64, 64, 256, 16, None) == dg.ERR_ARG
+    assert m(24, 16, 16, 16, 16, 0, 4, 64, 64, 256, 16, None) == dg.ERR_ARG
     assert m(None, None, None, None, None, 0, 0, 64, 64, None, None, None) == dg.OK
     assert L.dg_layer_mx4_scale_bytes(129, 288) == 2 * 2 * 1024
     assert L.dg_layer_mx4_scale_bytes(0, 288) == 0

@@ -7,7 +7,11 @@
 // Both are bound by memory traffic (a handful of operations per value), so a
 // row is read once: its threads hold the row's sum in registers through the
 // reductions (sum of squares, then the maximum for an 8-bit output) and write
-// everything from there.
+// everything from there.  Many rows are streamed: a block walks rows, and each
+// thread keeps its own vectors of the next rows in flight into its own slots of
+// shared memory (asynchronous copies; no thread reads another's slots, so the
+// hand-off needs no barrier), because a block that loads, reduces and stores by
+// turns leaves the memory idle in between.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -304,6 +308,199 @@ __global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const NormArgs 
   }
 }
 
+// ---------------------------------------------------------- streamed forward
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copies_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void unpack8(const uint4 u, float (&v)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    v[2 * k] = __uint_as_float(w[k] << 16);
+    v[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+  }
+}
+
+// A thread's 16-byte slots in the dynamic shared memory: `stage`, then vector
+// and part of it, then the thread (neighbours are 16 bytes apart).
+template <int PARTS>
+struct Slots {
+  uint8_t* base;
+  __device__ __forceinline__ uint4* at(int stage, int part) const {
+    return reinterpret_cast<uint4*>(base) + ((int64_t)stage * PARTS + part) * blockDim.x + threadIdx.x;
+  }
+  __device__ __forceinline__ void fetch(int stage, int part, const void* src) const {
+    copy16((uint32_t)__cvta_generic_to_shared(at(stage, part)), src);
+  }
+  // eight values: one slot of bf16 or two of fp32
+  template <bool F32>
+  __device__ __forceinline__ void read(int stage, int part, float (&v)[8]) const {
+    const uint4 a = *at(stage, part);
+    if constexpr (F32) {
+      const uint4 b = *at(stage, part + 1);
+      v[0] = __uint_as_float(a.x), v[1] = __uint_as_float(a.y), v[2] = __uint_as_float(a.z), v[3] = __uint_as_float(a.w);
+      v[4] = __uint_as_float(b.x), v[5] = __uint_as_float(b.y), v[6] = __uint_as_float(b.z), v[7] = __uint_as_float(b.w);
+    } else {
+      unpack8(a, v);
+    }
+  }
+};
+
+constexpr int kStreamVecs = 2;        // vectors of 8 values per thread
+constexpr int kStreamThreads = 1024;  // per SM (64 registers each)
+
+template <int RT>
+__host__ __device__ constexpr int norm_parts() {
+  return kStreamVecs * (1 + RT);  // x, and the residual in 0, 1 or 2 slots
+}
+
+template <int RT, bool OUT8, int STAGES>
+__global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(const NormArgs p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float part[2][99];
+  constexpr int NV = kStreamVecs, PER = 1 + RT;
+  const Slots<norm_parts<RT>()> slots{smem};
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = i0 + k * step;
+        if (i < p.hidden) {
+          slots.fetch(stage, k * PER, static_cast<const __nv_bfloat16*>(p.x) + row * p.ld_x + i);
+          if constexpr (RT == 1)
+            slots.fetch(stage, k * PER + 1, static_cast<const __nv_bfloat16*>(p.residual) + row * p.ld_residual + i);
+          if constexpr (RT == 2) {
+            const float* r = static_cast<const float*>(p.residual) + row * p.ld_residual + i;
+            slots.fetch(stage, k * PER + 1, r);
+            slots.fetch(stage, k * PER + 2, r + 4);
+          }
+        }
+      }
+    }
+    copies_commit();
+  };
+  float w[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[k][j] = 0.f;
+    if (i0 + k * step < p.hidden) load_any<8>(p.weight_f32 != 0, p.weight, i0 + k * step, w[k]);
+  }
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  int stage = 0, flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    copies_wait<STAGES - 1>();
+    float h[NV][8], ss = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = i0 + k * step;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
+      if (i < p.hidden) {
+        slots.template read<false>(stage, k * PER, h[k]);
+        if constexpr (RT != 0) {
+          float r[8];
+          slots.template read<RT == 2>(stage, k * PER + 1, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[k][j] += r[j];
+          if constexpr (RT == 2) {
+            store_f32<8>(p.sum, row * p.ld_sum + i, h[k]);
+          } else {
+            // the norm is of the sum as it is stored, so that the gradient sees the same values
+            const uint4 u = make_uint4(pack2(h[k][0], h[k][1]), pack2(h[k][2], h[k][3]), pack2(h[k][4], h[k][5]),
+                                       pack2(h[k][6], h[k][7]));
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + row * p.ld_sum + i) = u;
+            unpack8(u, h[k]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) ss = fmaf(h[k][j], h[k][j], ss);
+    }
+    // this stage's values are in registers
+    fetch(row + (int64_t)STAGES * gridDim.x, stage);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    ss = row_reduce<Add>(ss, part[flip]);
+    const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
+    if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+    if constexpr (OUT8) {
+      float amax = 0.f;
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          h[k][j] = h[k][j] * rstd * w[k][j];
+          amax = fmaxf(amax, fabsf(h[k][j]));
+        }
+      const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
+      float c;
+      if (p.scale_in) {
+        c = __ldg(p.scale_in);
+      } else {
+        amax = row_reduce<Max>(amax, part[flip] + 33);
+        if (isinf(amax)) {  // the same for the whole row: the largest of the finite values
+          amax = 0.f;
+#pragma unroll
+          for (int k = 0; k < NV; ++k)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, isinf(h[k][j]) ? 0.f : fabsf(h[k][j]));
+          amax = row_reduce<Max>(amax, part[flip] + 66);
+        }
+        c = row_scale(amax, e5m2);
+        if (threadIdx.x == 0) p.scale[row] = c;
+      }
+      const float inv = 1.f / c;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = i0 + k * step;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[k][j] *= inv;
+        if (i < p.hidden) store_fp8<8>(p.y, row * p.hidden + i, h[k], e5m2 ? __NV_E5M2 : __NV_E4M3);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = i0 + k * step;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[k][j] = h[k][j] * rstd * w[k][j];
+        if (i < p.hidden) store_bf16<8>(p.y, row * p.hidden + i, h[k]);
+      }
+    }
+  }
+  copies_wait<0>();
+}
+
+// Blocks that fill the SMs, and the dynamic shared memory of one.
+template <class Kernel>
+int stream_shape(Kernel kernel, int hidden, int parts, int stages, int sms, int64_t rows, int* threads, int* blocks,
+                 int* bytes) {
+  *threads = (hidden / 8 + kStreamVecs - 1) / kStreamVecs;
+  *threads = (*threads + 31) / 32 * 32;
+  *bytes = stages * parts * 16 * *threads;
+  const int64_t most = (int64_t)sms * (kStreamThreads / *threads);
+  *blocks = (int)(rows < most ? rows : most);
+  DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, *bytes));
+  return DG_OK;
+}
+
+template <int RT, bool OUT8, int STAGES>
+int stream_norm(const NormArgs& p, int sms, cudaStream_t s) {
+  int threads, blocks, bytes;
+  auto* kernel = add_rms_norm_stream_kernel<RT, OUT8, STAGES>;
+  if (int rc = stream_shape(kernel, p.hidden, norm_parts<RT>(), STAGES, sms, p.rows, &threads, &blocks, &bytes)) return rc;
+  kernel<<<blocks, threads, bytes, s>>>(p);
+  DGL_LAUNCHED();
+  return DG_OK;
+}
+
 template <int RT, int VW, int NV, bool OUT8>
 int launch_norm(const NormArgs& p, int threads, cudaStream_t s) {
   const int per = threads == 32 ? 4 : 1;  // one warp per row: four rows to a block
@@ -317,14 +514,13 @@ int round32(int v) { return (v + 31) / 32 * 32; }
 template <int RT, bool OUT8>
 int run_norm(const NormArgs& p, bool vec, int sms, cudaStream_t s) {
   if (vec) {
-    // Few rows: as many threads as the row has vectors, for the shortest chain
-    // of loads.  Many rows: four vectors per thread, so that enough bytes are
-    // in flight with few barriers.
     const int n = p.hidden / 8;
-    const bool few = p.rows <= 2 * sms;
-    if (n <= 32 || (few && n <= 1024)) return launch_norm<RT, 8, 1, OUT8>(p, round32(n), s);
-    if (n <= 128 || (few && n <= 2048)) return launch_norm<RT, 8, 2, OUT8>(p, round32((n + 1) / 2), s);
-    if (n <= 2048) return launch_norm<RT, 8, 4, OUT8>(p, round32((n + 3) / 4), s);
+    // Many long rows are streamed, in three stages (two of fp32 residuals: 96 KB
+    // each at 16384).  Few rows: as many threads as the row has vectors, for the
+    // shortest chain of loads; short rows are light enough for that too.
+    if (p.rows > 2 * sms && n >= 256 && n <= 2048) return stream_norm<RT, OUT8, RT == 2 ? 2 : 3>(p, sms, s);
+    if (n <= 1024) return launch_norm<RT, 8, 1, OUT8>(p, round32(n), s);
+    if (n <= 2048) return launch_norm<RT, 8, 2, OUT8>(p, round32((n + 1) / 2), s);
     if (n <= 4096) return launch_norm<RT, 8, 8, OUT8>(p, round32((n + 7) / 8), s);
     add_rms_norm_long_kernel<RT, 8, OUT8><<<(unsigned)p.rows, 1024, 0, s>>>(p);
   } else {
@@ -408,7 +604,106 @@ __global__ void __launch_bounds__(NV * VW > 8 ? 512 : 1024) add_rms_norm_grad_ke
   }
 }
 
-// Rows longer than the register kernel holds: two passes over each row; the
+// The gradient's rows streamed like the forward's: dy, h and dh of the next row
+// are in flight while this one is reduced and written.  A row is read from its
+// slots twice (for the dot product, and again for dx), which leaves registers
+// to the weight and its gradient.
+template <bool F32, bool HAS_DH>
+__host__ __device__ constexpr int grad_parts() {
+  return kStreamVecs * (1 + (F32 ? 2 : 1) * (HAS_DH ? 2 : 1));
+}
+constexpr int kGradStages = 2;
+
+template <bool F32, bool HAS_DH>
+__global__ void __launch_bounds__(kStreamThreads) add_rms_norm_grad_stream_kernel(const GradArgs p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float part[2][33];
+  constexpr int NV = kStreamVecs, HP = F32 ? 2 : 1, PER = 1 + HP * (HAS_DH ? 2 : 1);
+  const Slots<grad_parts<F32, HAS_DH>()> slots{smem};
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
+  const int hsz = F32 ? 4 : 2;
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = i0 + k * step;
+        if (i < p.hidden) {
+          slots.fetch(stage, k * PER, static_cast<const __nv_bfloat16*>(p.dy) + row * p.ld_dy + i);
+          const uint8_t* h = static_cast<const uint8_t*>(p.h) + (row * p.ld_h + i) * hsz;
+#pragma unroll
+          for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + q, h + 16 * q);
+          if constexpr (HAS_DH) {
+            const uint8_t* d = static_cast<const uint8_t*>(p.dh) + (row * p.ld_dh + i) * hsz;
+#pragma unroll
+            for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + HP + q, d + 16 * q);
+          }
+        }
+      }
+    }
+    copies_commit();
+  };
+  float dw[NV][8], w[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[k][j] = w[k][j] = 0.f;
+    if (i0 + k * step < p.hidden) load_any<8>(p.weight_f32 != 0, p.weight, i0 + k * step, w[k]);
+  }
+#pragma unroll
+  for (int s = 0; s < kGradStages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  int stage = 0, flip = 0;
+  float rstd_next = blockIdx.x < p.rows ? __ldg(p.rstd + blockIdx.x) : 0.f;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    const float rstd = rstd_next;
+    if (row + gridDim.x < p.rows) rstd_next = __ldg(p.rstd + row + gridDim.x);
+    copies_wait<kGradStages - 1>();
+    float dot = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (i0 + k * step < p.hidden) {
+        float dy[8], h[8];
+        slots.template read<false>(stage, k * PER, dy);
+        slots.template read<F32>(stage, k * PER + 1, h);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float t = dy[j] * (h[j] * rstd);
+          dw[k][j] += t;
+          dot = fmaf(t, w[k][j], dot);
+        }
+      }
+    }
+    // two sets of partials: a block's next row may start while a slow warp reads these
+    dot = row_reduce<Add>(dot, part[flip]) / (float)p.hidden;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = i0 + k * step;
+      if (i < p.hidden) {
+        float dy[8], h[8], d[8];
+        slots.template read<false>(stage, k * PER, dy);
+        slots.template read<F32>(stage, k * PER + 1, h);
+        if constexpr (HAS_DH)
+          slots.template read<F32>(stage, k * PER + 1 + HP, d);
+        else
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, dy[j] * w[k][j] - h[j] * rstd * dot, d[j]);
+        if constexpr (F32)
+          store_f32<8>(p.dx, row * p.hidden + i, d);
+        else
+          store_bf16<8>(p.dx, row * p.hidden + i, d);
+      }
+    }
+    fetch(row + (int64_t)kGradStages * gridDim.x, stage);
+    stage ^= 1;
+  }
+  copies_wait<0>();
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (i0 + k * step < p.hidden) store_f32<8>(p.partial, (int64_t)blockIdx.x * p.hidden + i0 + k * step, dw[k]);
+}
+
+// Rows longer than the other kernels hold: two passes over each row; the
 // weight's gradient accumulates in the block's row of `partial`.
 template <bool F32, bool HAS_DH>
 __global__ void __launch_bounds__(1024) add_rms_norm_grad_long_kernel(const GradArgs p) {
@@ -466,23 +761,37 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* par
   }
 }
 
-// Blocks of the gradient kernel: at most two per SM (and a fixed bound that the
-// workspace is sized by), so that the partial sums stay small beside the rows.
-constexpr int kGradBlocks = 304;
+// Blocks of the gradient kernels: a fixed bound that the workspace is sized by,
+// so that the partial sums stay small beside the rows.
+constexpr int kGradBlocks = 608;
 
 template <bool F32, bool HAS_DH>
-int run_grad(const GradArgs& p, bool vec, int blocks, cudaStream_t s) {
+int run_grad(GradArgs p, bool vec, int sms, cudaStream_t s) {
   const int n = p.hidden / 8;
-  if (vec && n <= 1024)
-    add_rms_norm_grad_kernel<F32, 8, 1, HAS_DH><<<blocks, round32(n), 0, s>>>(p);
-  else if (vec && n <= 2048)
-    add_rms_norm_grad_kernel<F32, 8, 4, HAS_DH><<<blocks, round32((n + 3) / 4), 0, s>>>(p);
-  else if (!vec && p.hidden <= 4096)
-    add_rms_norm_grad_kernel<F32, 1, 4, HAS_DH><<<blocks, round32((p.hidden + 3) / 4), 0, s>>>(p);
-  else if (!vec && p.hidden <= 8192)
-    add_rms_norm_grad_kernel<F32, 1, 16, HAS_DH><<<blocks, round32((p.hidden + 15) / 16), 0, s>>>(p);
-  else
-    add_rms_norm_grad_long_kernel<F32, HAS_DH><<<blocks, 1024, 0, s>>>(p);
+  int blocks = (int)(p.rows < 2 * sms ? p.rows : 2 * sms);
+  // 1024 threads hold 16384 values; fp32 rows of that length do not fit twice
+  if (vec && n >= 256 && n <= 2048 && grad_parts<F32, HAS_DH>() * 16 * kGradStages * (n / kStreamVecs + 31) <= 220000) {
+    int threads, bytes;
+    auto* kernel = add_rms_norm_grad_stream_kernel<F32, HAS_DH>;
+    if (int rc = stream_shape(kernel, p.hidden, grad_parts<F32, HAS_DH>(), kGradStages, sms, p.rows, &threads, &blocks,
+                              &bytes))
+      return rc;
+    blocks = blocks < kGradBlocks ? blocks : kGradBlocks;
+    kernel<<<blocks, threads, bytes, s>>>(p);
+  } else {
+    blocks = blocks < kGradBlocks ? blocks : kGradBlocks;
+    if (vec && n <= 1024)
+      add_rms_norm_grad_kernel<F32, 8, 1, HAS_DH><<<blocks, round32(n), 0, s>>>(p);
+    else if (!vec && p.hidden <= 4096)
+      add_rms_norm_grad_kernel<F32, 1, 4, HAS_DH><<<blocks, round32((p.hidden + 3) / 4), 0, s>>>(p);
+    else if (!vec && p.hidden <= 8192)
+      add_rms_norm_grad_kernel<F32, 1, 16, HAS_DH><<<blocks, round32((p.hidden + 15) / 16), 0, s>>>(p);
+    else
+      add_rms_norm_grad_long_kernel<F32, HAS_DH><<<blocks, 1024, 0, s>>>(p);
+  }
+  DGL_LAUNCHED();
+  norm_weight_grad_kernel<<<(unsigned)((p.hidden + 31) / 32), dim3(32, 32), 0, s>>>(p.partial, blocks, p.hidden,
+                                                                                     p.dweight, p.weight_f32);
   DGL_LAUNCHED();
   return DG_OK;
 }
@@ -552,14 +861,6 @@ extern "C" int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, con
                    dgl::aligned16(weight) && dgl::aligned16(dx);
   GradArgs p{dy, h, weight, dh, rstd, dx, dweight, static_cast<float*>(workspace), ld_dy, ld_h, ld_dh, rows,
              (int)hidden, weight_type == DG_TYPE_F32};
-  int blocks = 2 * sms < kGradBlocks ? 2 * sms : kGradBlocks;
-  if (rows < blocks) blocks = (int)rows;
-  const bool f32 = h_type == DG_TYPE_F32;
-  int rc = f32 ? (dh ? run_grad<true, true>(p, vec, blocks, s) : run_grad<true, false>(p, vec, blocks, s))
-               : (dh ? run_grad<false, true>(p, vec, blocks, s) : run_grad<false, false>(p, vec, blocks, s));
-  if (rc != DG_OK) return rc;
-  norm_weight_grad_kernel<<<(unsigned)((hidden + 31) / 32), dim3(32, 32), 0, s>>>(p.partial, blocks, (int)hidden,
-                                                                                   dweight, weight_type == DG_TYPE_F32);
-  DGL_LAUNCHED();
-  return DG_OK;
+  if (h_type == DG_TYPE_F32) return dh ? run_grad<true, true>(p, vec, sms, s) : run_grad<true, false>(p, vec, sms, s);
+  return dh ? run_grad<false, true>(p, vec, sms, s) : run_grad<false, false>(p, vec, sms, s);
 }

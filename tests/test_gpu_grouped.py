@@ -171,6 +171,12 @@ def test_strides_streams_and_graph():
     same = ops.grouped_matmul(big[:, 7:135], b, e)   # misaligned rows are copied
     w2, b2 = lc.grouped(big[:, 7:135], b, ends)
     assert_within(same, w2, b2, "D")
+    three = big[:, 1:129]                         # misaligned rows in another place
+    w3, b3 = lc.grouped(three, b, ends)
+    assert_within(ops.grouped_matmul(three, b, e), w3, b3, "D")
+    rows = rand((1, K), 26).expand(T, K)          # a broadcast row
+    w4, b4 = lc.grouped(rows, b, ends)
+    assert_within(ops.grouped_matmul(rows, b, e), w4, b4, "D")
     one = rand((1, N, K), 25).transpose(1, 2)
     d1 = ops.grouped_matmul(a, one.expand(3, K, N), e)   # a broadcast expert
     w1, b1 = lc.grouped(a, one.expand(3, K, N), ends)

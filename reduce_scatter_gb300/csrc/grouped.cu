@@ -16,7 +16,7 @@
 #include <atomic>
 #include <cuda_bf16.h>
 
-#include "layer_common.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace {
@@ -151,12 +151,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t half = cluster_ctarank();
   const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
 
+  let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 8);
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_u32(s_tmem), kTmemCols);
+  wait_for_previous();
   if (warp == 2) scan_groups<GRAD>(p, start, first, lane);
   fence_before();
   __syncwarp();
@@ -352,6 +354,7 @@ __global__ void __launch_bounds__(256) grouped_tail_kernel(const int32_t* ends, 
                                                            const __nv_bfloat16* d, int64_t ld_d, int64_t kd,
                                                            __nv_bfloat16* d_tail) {
   __shared__ int s_from[8], s_to[8];
+  begin_kernel();
   const int e = blockIdx.y;
   int from = 0, to = 0;  // this group's clamped start and end: the largest ends before and up to it
   for (int i = threadIdx.x; i <= e; i += blockDim.x) {
@@ -385,16 +388,14 @@ __global__ void __launch_bounds__(256) grouped_tail_kernel(const int32_t* ends, 
 std::atomic<uint32_t> g_epoch{1};
 
 template <bool F8, bool PMN, bool GRAD, bool OUT32>
-int launch(const Args& p, int64_t most_tiles, cudaStream_t s) {
+int run(const Args& p, int64_t most_tiles, cudaStream_t s) {
   auto* kernel = grouped_kernel<F8, PMN, GRAD, OUT32>;
   int sms = 0;
   if (int rc = sm_count(&sms)) return rc;
   DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
   // the forward's tiles may be cut along K, so it takes every SM pair
   const int64_t units = GRAD && most_tiles < sms / 2 ? most_tiles : sms / 2;
-  kernel<<<(unsigned)(2 * units), kThreads, kSmem, s>>>(p);
-  DGL_LAUNCHED();
-  return DG_OK;
+  return dgl::launch(kernel, dim3((unsigned)(2 * units)), dim3(kThreads), kSmem, s, p);
 }
 
 uint32_t format_of(int type) { return type == DG_TYPE_BF16 ? 1u : type == DG_TYPE_E5M2 ? 1u : 0u; }
@@ -459,9 +460,9 @@ extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, 
   const int64_t most = (T / kTileRows + experts + 1) * ((N + kPairFeats - 1) / kPairFeats);
   if (most > INT32_MAX) return fail(DG_ERR_ARG, "T x N is too large (%lld tiles)", (long long)most);
   const bool f32 = d_type == DG_TYPE_F32;
-  if (f8) return f32 ? launch<true, false, false, true>(p, most, s) : launch<true, false, false, false>(p, most, s);
-  if (b_n_major) return f32 ? launch<false, true, false, true>(p, most, s) : launch<false, true, false, false>(p, most, s);
-  return f32 ? launch<false, false, false, true>(p, most, s) : launch<false, false, false, false>(p, most, s);
+  if (f8) return f32 ? run<true, false, false, true>(p, most, s) : run<true, false, false, false>(p, most, s);
+  if (b_n_major) return f32 ? run<false, true, false, true>(p, most, s) : run<false, true, false, false>(p, most, s);
+  return f32 ? run<false, false, false, true>(p, most, s) : run<false, false, false, false>(p, most, s);
 }
 
 extern "C" size_t dg_layer_grouped_grad_workspace(int experts, int64_t N, int64_t K) {
@@ -503,8 +504,9 @@ extern "C" int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const 
   p.watch = watch_of(status);
   const int64_t vecs = 64 * (N + K) / 8;
   const unsigned gx = (unsigned)((vecs + 1023) / 1024 < 64 ? (vecs + 1023) / 1024 : 64);
-  grouped_tail_kernel<<<dim3(gx, experts), 256, 0, s>>>(ends, (int)T, static_cast<const __nv_bfloat16*>(A), ld_a, K,
-                                                        a_tail, static_cast<const __nv_bfloat16*>(dD), ld_d, N, d_tail);
-  DGL_LAUNCHED();
-  return f32 ? launch<false, true, true, true>(p, tiles, s) : launch<false, true, true, false>(p, tiles, s);
+  if (int rc = dgl::launch(grouped_tail_kernel, dim3(gx, experts), dim3(256), 0, s, ends, (int)T,
+                           static_cast<const __nv_bfloat16*>(A), ld_a, K, a_tail, static_cast<const __nv_bfloat16*>(dD),
+                           ld_d, N, d_tail))
+    return rc;
+  return f32 ? run<false, true, true, true>(p, tiles, s) : run<false, true, true, false>(p, tiles, s);
 }

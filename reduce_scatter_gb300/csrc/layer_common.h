@@ -20,10 +20,6 @@ int cuda_fail(cudaError_t e, const char* what);
     if (e_ != cudaSuccess) return dgl::cuda_fail(e_, #call); \
   } while (0)
 
-// Launch errors of the kernel launched just before (and no earlier ones: every
-// call that can fail is checked where it is made).
-#define DGL_LAUNCHED() DGL_CUDA(cudaGetLastError())
-
 int sm_count(int* n);
 
 // A tiled tensor map with the 128-byte swizzle over `rank` (2 or 3) dimensions

@@ -10,7 +10,7 @@
 
 #include <cuda_bf16.h>
 
-#include "layer_common.h"
+#include "launch.cuh"
 
 namespace {
 
@@ -121,6 +121,7 @@ struct Place {
 template <bool F32, int ROWS>
 __global__ void __launch_bounds__(256) mx4_quantize_kernel(const void* x, int64_t ld, uint8_t* codes, uint8_t* scales,
                                                            int64_t rows, int64_t cols, int chunks) {
+  dgl::begin_kernel();
   const Place<ROWS> at(chunks);
   if (at.col < 0 || at.row0 >= (rows + 127) / 128 * 128) return;
   const int lane = threadIdx.x & 31;
@@ -175,6 +176,7 @@ __device__ __forceinline__ void e2m1x4_bf16(uint32_t c, uint32_t& lo, uint32_t& 
 template <bool F32, int ROWS>
 __global__ void __launch_bounds__(256) mx4_dequantize_kernel(const uint8_t* codes, const uint8_t* scales, void* y,
                                                              int64_t rows, int64_t cols, int chunks) {
+  dgl::begin_kernel();
   const Place<ROWS> at(chunks);
   if (at.col < 0 || at.col >= cols || at.row0 >= rows) return;
   const int lane = threadIdx.x & 31;
@@ -235,18 +237,15 @@ int check_shape(int64_t rows, int64_t cols) {
 template <bool F32, int ROWS>
 int launch_quantize(const void* x, int64_t ld, void* codes, void* scales, int64_t rows, int64_t cols, cudaStream_t s) {
   const int chunks = (int)((cols + 255) / 256);
-  mx4_quantize_kernel<F32, ROWS><<<grid_of((rows + 127) / 128 * 128, chunks, ROWS), 32 * warps_of(chunks), 0, s>>>(
-      x, ld, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales), rows, cols, chunks);
-  DGL_LAUNCHED();
-  return DG_OK;
+  return dgl::launch(mx4_quantize_kernel<F32, ROWS>, grid_of((rows + 127) / 128 * 128, chunks, ROWS),
+                     dim3(32 * warps_of(chunks)), 0, s, x, ld, static_cast<uint8_t*>(codes), static_cast<uint8_t*>(scales),
+                     rows, cols, chunks);
 }
 template <bool F32, int ROWS>
 int launch_dequantize(const void* codes, const void* scales, void* y, int64_t rows, int64_t cols, cudaStream_t s) {
   const int chunks = (int)((cols + 255) / 256);
-  mx4_dequantize_kernel<F32, ROWS><<<grid_of(rows, chunks, ROWS), 32 * warps_of(chunks), 0, s>>>(
-      static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), y, rows, cols, chunks);
-  DGL_LAUNCHED();
-  return DG_OK;
+  return dgl::launch(mx4_dequantize_kernel<F32, ROWS>, grid_of(rows, chunks, ROWS), dim3(32 * warps_of(chunks)), 0, s,
+                     static_cast<const uint8_t*>(codes), static_cast<const uint8_t*>(scales), y, rows, cols, chunks);
 }
 
 // Small inputs take one row per warp, so that more SMs take part.

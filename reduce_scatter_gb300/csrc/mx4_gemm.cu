@@ -17,7 +17,7 @@
 #include <atomic>
 #include <cuda_bf16.h>
 
-#include "layer_common.h"
+#include "launch.cuh"
 #include "ptx.cuh"
 
 namespace {
@@ -92,12 +92,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t half = cluster_ctarank();
   const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
+  let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 8);
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_u32(s_tmem), kTmemCols);
+  wait_for_previous();
   fence_before();
   __syncwarp();
   cluster_sync();
@@ -247,13 +249,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
 std::atomic<uint32_t> g_epoch{0x80000001u};
 
 template <bool OUT32>
-int launch(const Args& p, cudaStream_t s) {
+int run(const Args& p, cudaStream_t s) {
   int sms = 0;
   if (int rc = sm_count(&sms)) return rc;
   DGL_CUDA(cudaFuncSetAttribute(mx4_kernel<OUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
-  mx4_kernel<OUT32><<<(unsigned)(sms / 2 * 2), kThreads, kSmem, s>>>(p);
-  DGL_LAUNCHED();
-  return DG_OK;
+  return dgl::launch(mx4_kernel<OUT32>, dim3((unsigned)(sms / 2 * 2)), dim3(kThreads), kSmem, s, p);
 }
 
 }  // namespace
@@ -290,5 +290,5 @@ extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, co
   p.counters = static_cast<uint32_t*>(workspace);
   p.partial = reinterpret_cast<float*>(p.counters + kCutCounters);
   p.watch = Watch{static_cast<unsigned long long*>(status), g_epoch.fetch_add(1, std::memory_order_relaxed), 4000000000ull};
-  return d_type == DG_TYPE_F32 ? launch<true>(p, s) : launch<false>(p, s);
+  return d_type == DG_TYPE_F32 ? run<true>(p, s) : run<false>(p, s);
 }

@@ -16,9 +16,11 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
-#include "layer_common.h"
+#include "launch.cuh"
 
 namespace {
+
+using dgl::begin_kernel;
 
 constexpr float kE4M3Max = 448.f, kE5M2Max = 57344.f;
 constexpr float kMinScale = 1.1754943508222875e-38f;  // 2^-126: the reciprocal stays finite
@@ -151,8 +153,9 @@ __device__ __forceinline__ float row_scale(float amax, bool e5m2) {
 // RT: the residual's type (0 none, 1 bf16, 2 fp32).  The row stays in
 // registers: NV vectors of VW values per thread.
 template <int RT, int VW, int NV, bool OUT8>
-__global__ void __launch_bounds__(NV * VW > 16 ? 512 : 1024) add_rms_norm_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(NV * VW > 16 ? 512 : 1024) add_rms_norm_kernel(const __grid_constant__ NormArgs p) {
   __shared__ float part[66];
+  begin_kernel();
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= p.rows) return;  // several rows per block only with one warp each: no barrier below
   const int step = blockDim.x * VW;
@@ -239,8 +242,9 @@ __global__ void __launch_bounds__(NV * VW > 16 ? 512 : 1024) add_rms_norm_kernel
 // again (its own stores of the sum, still in cache) for the maximum and the
 // output.  Same order of additions for every row of one size.
 template <int RT, int VW, bool OUT8>
-__global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const __grid_constant__ NormArgs p) {
   __shared__ float part[66];
+  begin_kernel();
   const int64_t row = blockIdx.x;
   const int step = blockDim.x * VW;
   const void* hp = RT == 0 ? p.x : p.sum;
@@ -361,11 +365,12 @@ __host__ __device__ constexpr int norm_parts() {
 }
 
 template <int RT, bool OUT8, int STAGES>
-__global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(const NormArgs p) {
+__global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(const __grid_constant__ NormArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[2][99];
   constexpr int NV = kStreamVecs, PER = 1 + RT;
   const Slots<norm_parts<RT>()> slots{smem};
+  begin_kernel();
   const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
   auto fetch = [&](int64_t row, int stage) {
     if (row < p.rows) {
@@ -496,17 +501,14 @@ int stream_norm(const NormArgs& p, int sms, cudaStream_t s) {
   int threads, blocks, bytes;
   auto* kernel = add_rms_norm_stream_kernel<RT, OUT8, STAGES>;
   if (int rc = stream_shape(kernel, p.hidden, norm_parts<RT>(), STAGES, sms, p.rows, &threads, &blocks, &bytes)) return rc;
-  kernel<<<blocks, threads, bytes, s>>>(p);
-  DGL_LAUNCHED();
-  return DG_OK;
+  return dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);
 }
 
 template <int RT, int VW, int NV, bool OUT8>
 int launch_norm(const NormArgs& p, int threads, cudaStream_t s) {
   const int per = threads == 32 ? 4 : 1;  // one warp per row: four rows to a block
-  add_rms_norm_kernel<RT, VW, NV, OUT8><<<(unsigned)((p.rows + per - 1) / per), dim3(threads, per), 0, s>>>(p);
-  DGL_LAUNCHED();
-  return DG_OK;
+  return dgl::launch(add_rms_norm_kernel<RT, VW, NV, OUT8>, dim3((unsigned)((p.rows + per - 1) / per)),
+                     dim3(threads, per), 0, s, p);
 }
 
 int round32(int v) { return (v + 31) / 32 * 32; }
@@ -522,14 +524,12 @@ int run_norm(const NormArgs& p, bool vec, int sms, cudaStream_t s) {
     if (n <= 1024) return launch_norm<RT, 8, 1, OUT8>(p, round32(n), s);
     if (n <= 2048) return launch_norm<RT, 8, 2, OUT8>(p, round32((n + 1) / 2), s);
     if (n <= 4096) return launch_norm<RT, 8, 8, OUT8>(p, round32((n + 7) / 8), s);
-    add_rms_norm_long_kernel<RT, 8, OUT8><<<(unsigned)p.rows, 1024, 0, s>>>(p);
+    return dgl::launch(add_rms_norm_long_kernel<RT, 8, OUT8>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
   } else {
     if (p.hidden <= 4096) return launch_norm<RT, 1, 4, OUT8>(p, round32((p.hidden + 3) / 4), s);
     if (p.hidden <= 16384) return launch_norm<RT, 1, 16, OUT8>(p, round32((p.hidden + 15) / 16), s);
-    add_rms_norm_long_kernel<RT, 1, OUT8><<<(unsigned)p.rows, 1024, 0, s>>>(p);
+    return dgl::launch(add_rms_norm_long_kernel<RT, 1, OUT8>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
   }
-  DGL_LAUNCHED();
-  return DG_OK;
 }
 
 // ----------------------------------------------------------------- gradient
@@ -546,8 +546,9 @@ struct GradArgs {
 // A block walks the rows blockIdx.x, + gridDim.x, ...; the weight's gradient is
 // summed in registers over its rows and written once as a row of `partial`.
 template <bool F32, int VW, int NV, bool HAS_DH>
-__global__ void __launch_bounds__(NV * VW > 8 ? 512 : 1024) add_rms_norm_grad_kernel(const GradArgs p) {
+__global__ void __launch_bounds__(NV * VW > 8 ? 512 : 1024) add_rms_norm_grad_kernel(const __grid_constant__ GradArgs p) {
   __shared__ float part[2][33];
+  begin_kernel();
   const int step = blockDim.x * VW;
   float dw[NV][VW], w[NV][VW];
 #pragma unroll
@@ -615,11 +616,12 @@ __host__ __device__ constexpr int grad_parts() {
 constexpr int kGradStages = 2;
 
 template <bool F32, bool HAS_DH>
-__global__ void __launch_bounds__(kStreamThreads) add_rms_norm_grad_stream_kernel(const GradArgs p) {
+__global__ void __launch_bounds__(kStreamThreads) add_rms_norm_grad_stream_kernel(const __grid_constant__ GradArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float part[2][33];
   constexpr int NV = kStreamVecs, HP = F32 ? 2 : 1, PER = 1 + HP * (HAS_DH ? 2 : 1);
   const Slots<grad_parts<F32, HAS_DH>()> slots{smem};
+  begin_kernel();
   const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
   const int hsz = F32 ? 4 : 2;
   auto fetch = [&](int64_t row, int stage) {
@@ -706,8 +708,9 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_grad_stream_kerne
 // Rows longer than the other kernels hold: two passes over each row; the
 // weight's gradient accumulates in the block's row of `partial`.
 template <bool F32, bool HAS_DH>
-__global__ void __launch_bounds__(1024) add_rms_norm_grad_long_kernel(const GradArgs p) {
+__global__ void __launch_bounds__(1024) add_rms_norm_grad_long_kernel(const __grid_constant__ GradArgs p) {
   __shared__ float part[2][33];
+  begin_kernel();
   float* mine = p.partial + (int64_t)blockIdx.x * p.hidden;
   for (int64_t i = threadIdx.x; i < p.hidden; i += blockDim.x) mine[i] = 0.f;
   int flip = 0;
@@ -743,6 +746,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_grad_long_kernel(const Grad
 __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* partial, int blocks, int hidden,
                                                                 void* dweight, int f32) {
   __shared__ float s[32][33];
+  begin_kernel();
   const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (col < hidden)
@@ -777,23 +781,23 @@ int run_grad(GradArgs p, bool vec, int sms, cudaStream_t s) {
                               &bytes))
       return rc;
     blocks = blocks < kGradBlocks ? blocks : kGradBlocks;
-    kernel<<<blocks, threads, bytes, s>>>(p);
+    if (int rc = dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p)) return rc;
   } else {
     blocks = blocks < kGradBlocks ? blocks : kGradBlocks;
+    auto run = [&](void (*kernel)(GradArgs), int threads) { return dgl::launch(kernel, dim3(blocks), dim3(threads), 0, s, p); };
+    int rc;
     if (vec && n <= 1024)
-      add_rms_norm_grad_kernel<F32, 8, 1, HAS_DH><<<blocks, round32(n), 0, s>>>(p);
+      rc = run(add_rms_norm_grad_kernel<F32, 8, 1, HAS_DH>, round32(n));
     else if (!vec && p.hidden <= 4096)
-      add_rms_norm_grad_kernel<F32, 1, 4, HAS_DH><<<blocks, round32((p.hidden + 3) / 4), 0, s>>>(p);
+      rc = run(add_rms_norm_grad_kernel<F32, 1, 4, HAS_DH>, round32((p.hidden + 3) / 4));
     else if (!vec && p.hidden <= 8192)
-      add_rms_norm_grad_kernel<F32, 1, 16, HAS_DH><<<blocks, round32((p.hidden + 15) / 16), 0, s>>>(p);
+      rc = run(add_rms_norm_grad_kernel<F32, 1, 16, HAS_DH>, round32((p.hidden + 15) / 16));
     else
-      add_rms_norm_grad_long_kernel<F32, HAS_DH><<<blocks, 1024, 0, s>>>(p);
+      rc = run(add_rms_norm_grad_long_kernel<F32, HAS_DH>, 1024);
+    if (rc != DG_OK) return rc;
   }
-  DGL_LAUNCHED();
-  norm_weight_grad_kernel<<<(unsigned)((p.hidden + 31) / 32), dim3(32, 32), 0, s>>>(p.partial, blocks, p.hidden,
-                                                                                     p.dweight, p.weight_f32);
-  DGL_LAUNCHED();
-  return DG_OK;
+  return dgl::launch(norm_weight_grad_kernel, dim3((unsigned)((p.hidden + 31) / 32)), dim3(32, 32), 0, s, p.partial, blocks,
+                     p.hidden, p.dweight, p.weight_f32);
 }
 
 bool rows16(const void* p, int64_t ld, int64_t esz) {

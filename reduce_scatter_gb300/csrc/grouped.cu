@@ -11,7 +11,7 @@
 // CTA scans them once into shared memory and walks the same list of tiles.
 //
 // Warp 0 loads (TMA, 128-byte swizzle, kStages stages), warp 1 issues the MMAs
-// (even CTA of the pair), warps 2-5 empty the two accumulators.
+// (even CTA of the pair), warps 2-9 empty the two accumulators.
 
 #include <atomic>
 #include <cuda_bf16.h>
@@ -29,7 +29,7 @@ constexpr int kStages = 6;
 constexpr uint32_t kStageQ = (kTileRows / 2) * kRowBytes;
 constexpr uint32_t kStage = kStageP + kStageQ;
 constexpr uint32_t kTableBytes = 2 * (kMaxExperts + 2) * 4;
-constexpr uint32_t kSmem = kStages * kStage + 4 * kStoreBuf + kTableBytes + 256 + 1024;
+constexpr uint32_t kSmem = kStages * kStage + kEpiWarps * kStoreBuf + kTableBytes + 256 + 1024;
 constexpr uint32_t kTmemCols = 2 * kTileRows;
 constexpr int64_t kSlot = (int64_t)cut_slot_floats(kTileRows);
 constexpr int kBand = 8;      // row tiles swept together, for reuse in L2
@@ -37,8 +37,7 @@ constexpr int kTailRows = 64; // rows of a K block in the gradient
 
 struct Args {
   CUtensorMap p;           // 3-d: (K or features, features or K, expert)
-  CUtensorMap q;           // rows: box of 128 rows; gradient: box of 64 columns x 64 rows
-  CUtensorMap q16;         // rows: box of 16 rows
+  CUtensorMap q[4];        // rows: boxes of 128, 64, 32 and 16 rows; gradient: the first, of 64 columns x 64 rows
   CUtensorMap p_tail, q_tail;  // gradient: each group's last rows, padded with zeros
   const int32_t* ends;
   int experts, T;
@@ -139,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* store_buf = smem + kStages * kStage;
-  int* start = reinterpret_cast<int*>(store_buf + 4 * kStoreBuf);
+  int* start = reinterpret_cast<int*>(store_buf + kEpiWarps * kStoreBuf);
   int* first = start + kMaxExperts + 2;
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(start) + kTableBytes);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16;
@@ -154,7 +153,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 8);
+    for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 2 * kEpiWarps);
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_u32(s_tmem), kTmemCols);
@@ -178,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (warp == 0) {
     // -------------------------------------------------------------- producer
     prefetch_map(&p.p);
-    prefetch_map(&p.q);
+    prefetch_map(&p.q[GRAD ? 0 : 3]);
     uint32_t stage = 0, phase = 0;
     int e = 0;
     bool ok = true;
@@ -199,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             // from their zero-padded copy, so no other group's rows enter
             const bool tail = tl.tail != 0 && kb == tl.kblocks - 1;
             const CUtensorMap* pm = tail ? &p.p_tail : &p.p;
-            const CUtensorMap* qm = tail ? &p.q_tail : &p.q;
+            const CUtensorMap* qm = tail ? &p.q_tail : &p.q[0];
             const int y = tl.k0 + kb * kTailRows;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -214,10 +213,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             } else {
               tma_3d(sp, &p.p, fb, x, f, tl.e);
             }
-            if (n == kTileRows)
-              tma_2d(sq, &p.q, fb, x, q0);
-            else
-              for (int i = 0; i < mine; i += 16) tma_2d(sq + i * kRowBytes, &p.q16, fb, x, q0 + i);
+            // a share of up to 128 rows, in boxes as large as they come (many small ones load at half the rate)
+            if (mine == kTileRows / 2) {
+              tma_2d(sq, &p.q[0], fb, x, q0);
+            } else {
+              int i = 0;
+#pragma unroll
+              for (int b = 1, r = 64; b < 4; ++b, r /= 2)
+                if (mine & r) tma_2d(sq + i * kRowBytes, &p.q[b], fb, x, q0 + i), i += r;
+            }
           }
         }
         __syncwarp();
@@ -264,20 +268,29 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   } else {
     // ------------------------------------------------------------- epilogue
     const int q = warp & 3;  // the TMEM lanes that this warp may read
-    uint8_t* box = store_buf + q * kStoreBuf;
+    const int odd_steps = (warp - 2) >> 2;
+    uint8_t* box = store_buf + (warp - 2) * kStoreBuf;
     uint32_t it = 0;
     int e = 0;
     Item w;
     for (Walk walk(cut, unit, units, total); walk.get(w); ++it) {
       const Tile tl = tile_at<GRAD, F8>(p, start, first, w.tile, e);
       const uint32_t buf = it & 1;
-      if (!epilogue_wait(p.watch, tfull, it, s_go)) break;
       const int f0 = tl.f0 + (int)half * kLanes + q * 32;  // this warp's first feature
       const int feats_ok = min(32, p.feats - f0);
       const int64_t row0 = (int64_t)tl.row0 + (GRAD ? (int64_t)tl.e * p.rows : 0);
-      float sb = 1.f;
-      if (!GRAD && p.sb && lane < feats_ok && tl.e < p.experts)
-        sb = __ldg(p.sb + tl.e * p.sb_e + (int64_t)(f0 + lane) * p.sb_n);
+      // the scales of this lane's feature and of its rows of each step, fetched while the tile is computed
+      float sb = 1.f, sa[kTileRows / kChunk / 2];
+      if (!GRAD) {
+        if (p.sb && lane < feats_ok && tl.e < p.experts)
+          sb = __ldg(p.sb + tl.e * p.sb_e + (int64_t)(f0 + lane) * p.sb_n);
+#pragma unroll
+        for (int i = 0; i < kTileRows / kChunk / 2; ++i) {
+          const int r = (2 * i + odd_steps) * kChunk + lane;
+          sa[i] = p.sa && r < tl.rows ? __ldg(p.sa + (row0 + r) * p.sa_s) : 1.f;
+        }
+      }
+      if (!epilogue_wait(p.watch, tfull, it, s_go)) break;
       const int nch = (tl.rows + kChunk - 1) / kChunk;
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kTileRows;
       auto read = [&](int c, float(&v)[32]) {
@@ -297,18 +310,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         head = cut_first(cut, w.tile);
         float* mine = p.partial + cut_slot(cut, w.tile, unit) * kSlot + half * (kSlot / 2);
 #pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
+        for (int c = odd_steps; c < nch; c += 2) {
           float v[32];
           read(c, v);
           store_partial(mine, c * kChunk, q * 32 + lane, v);
         }
-        if (!cut_last(p.counters + 2 * w.tile + half, ways, s_last)) {
-          release();
-          continue;
-        }
+        release();
+        if (!cut_last(p.counters + 2 * w.tile + half, ways, s_last)) continue;
+      } else if (odd_steps >= nch) {
+        release();
       }
 #pragma unroll 1
-      for (int c = 0; c < nch; ++c) {
+      for (int c = odd_steps; c < nch; c += 2) {
         float v[32];
         if (ways > 1) {
           join_partials(
@@ -320,14 +333,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) v[i] = 0.f;
         }
-        if (c == nch - 1) release();
+        if (ways == 1 && c + 2 >= nch) release();
         const int rows_ok = min(kChunk, tl.rows - c * kChunk);
         const int64_t r0 = row0 + c * kChunk;
         if (!GRAD && (p.sa || p.sb) && tl.kblocks > 0) {
-          float sa = 1.f;
-          if (p.sa && lane < rows_ok) sa = __ldg(p.sa + (r0 + lane) * p.sa_s);
+          float s = sa[0];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, sa, i) * sb;
+          for (int i = 1; i < kTileRows / kChunk / 2; ++i) s = c / 2 == i ? sa[i] : s;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, s, i) * sb;
         }
         const int64_t at = r0 * p.feats + f0;
         if constexpr (OUT32)
@@ -449,8 +463,8 @@ extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, 
   const int64_t pd[3] = {inner, b_n_major ? K : N, experts}, ps[2] = {ld_b, experts > 1 ? ld_e : ld_b * pd[1]};
   const int64_t qd[2] = {K, T}, qs[1] = {ld_a};
   if (int rc = encode_map(&p.p, B, (int)esz, 3, pd, ps, b_n_major ? 64 : kLanes)) return rc;
-  if (int rc = encode_map(&p.q, A, (int)esz, 2, qd, qs, kTileRows / 2)) return rc;
-  if (int rc = encode_map(&p.q16, A, (int)esz, 2, qd, qs, 16)) return rc;
+  for (int b = 0; b < 4; ++b)
+    if (int rc = encode_map(&p.q[b], A, (int)esz, 2, qd, qs, (kTileRows / 2) >> b)) return rc;
   p.ends = ends, p.experts = experts, p.T = (int)T, p.feats = (int)N, p.rows = 0, p.red = (int)K, p.out = D;
   p.sa = scale_a, p.sb = scale_b, p.sa_s = sa, p.sb_e = sb_e, p.sb_n = sb_n;
   p.idesc = idesc_of(format_of(b_type), format_of(a_type), b_n_major != 0, false);
@@ -496,7 +510,7 @@ extern "C" int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const 
   const int64_t pd[3] = {K, T, 1}, ps[2] = {ld_a, ld_a * T}, ptd[3] = {K, kTailRows, experts}, pts[2] = {K, K * kTailRows};
   const int64_t qd[2] = {N, T}, qs[1] = {ld_d}, qtd[2] = {N, (int64_t)experts * kTailRows}, qts[1] = {N};
   if (int rc = encode_map(&p.p, A, 2, 3, pd, ps, 64)) return rc;
-  if (int rc = encode_map(&p.q, dD, 2, 2, qd, qs, 64)) return rc;
+  if (int rc = encode_map(&p.q[0], dD, 2, 2, qd, qs, 64)) return rc;
   if (int rc = encode_map(&p.p_tail, a_tail, 2, 3, ptd, pts, 64)) return rc;
   if (int rc = encode_map(&p.q_tail, d_tail, 2, 2, qtd, qts, 64)) return rc;
   p.ends = ends, p.experts = experts, p.T = (int)T, p.feats = (int)K, p.rows = (int)N, p.red = 0, p.out = dB;

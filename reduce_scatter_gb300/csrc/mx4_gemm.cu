@@ -25,19 +25,19 @@ namespace {
 using namespace dgl;
 
 constexpr int kTileRows = 192;
-constexpr int kStages = 7;
+constexpr int kStages = 6;
 constexpr int kBlockK = 256;                     // columns per K block: 128 bytes of codes
 constexpr uint32_t kStageQ = (kTileRows / 2) * kRowBytes;
 constexpr uint32_t kScaleP = 1024, kScaleQ = 2048;  // scales of 128 and of 256 rows x 256 columns
 constexpr uint32_t kStage = kStageP + kStageQ + kScaleP + kScaleQ;
-constexpr uint32_t kSmem = kStages * kStage + 4 * kStoreBuf + 256 + 1024;
+constexpr uint32_t kSmem = kStages * kStage + kEpiWarps * kStoreBuf + 256 + 1024;
 constexpr uint32_t kTmemCols = 512, kScaleCol = 2 * kTileRows;
 constexpr int kScaleBufs = 4;                    // 24 columns each: 2 x 4 for P, 2 x 8 for Q
 constexpr int64_t kSlot = (int64_t)cut_slot_floats(kTileRows);
 constexpr int kBand = 8;
 
 struct Args {
-  CUtensorMap p, q, q16;   // codes as bytes: boxes of 128, 96 and 16 rows
+  CUtensorMap p, q[4];     // codes as bytes: boxes of 128 rows; of 96, 64, 32 and 16 rows
   CUtensorMap sp, sq;      // scales: (256 words, K block, row tile), boxes of one and two row tiles
   int rows, feats, kblocks;
   void* out;
@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   uint8_t* store_buf = smem + kStages * kStage;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(store_buf + 4 * kStoreBuf);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(store_buf + kEpiWarps * kStoreBuf);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
   volatile uint32_t* s_last = s_tmem + 1;
@@ -95,7 +95,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   let_next_start();
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
-    for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 8);
+    for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 2 * kEpiWarps);
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_u32(s_tmem), kTmemCols);
@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
 
   if (warp == 0) {
     prefetch_map(&p.p);
-    prefetch_map(&p.q);
+    prefetch_map(&p.q[0]);
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     Item w;
@@ -125,10 +125,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
         if (elect_one()) {
           if (half == 0) mbar_expect(full + 8 * stage, 2 * (kStageP + (uint32_t)mine * kRowBytes + kScaleP + kScaleQ));
           tma_2d(sp, &p.p, fb, kb * 128, f);
-          if (n == kTileRows)
-            tma_2d(sq, &p.q, fb, kb * 128, q0);
-          else
-            for (int i = 0; i < mine; i += 16) tma_2d(sq + i * kRowBytes, &p.q16, fb, kb * 128, q0 + i);
+          if (mine == kTileRows / 2) {
+            tma_2d(sq, &p.q[0], fb, kb * 128, q0);
+          } else {
+            int i = 0;
+#pragma unroll
+            for (int b = 1, r = 64; b < 4; ++b, r /= 2)
+              if (mine & r) tma_2d(sq + i * kRowBytes, &p.q[b], fb, kb * 128, q0 + i), i += r;
+          }
           tma_3d(ss, &p.sp, fb, 0, kb, f / 128);
           tma_3d(ss + kScaleP, &p.sq, fb, 0, kb, tl.row0 / 128);  // every row's: each CTA needs them all
         }
@@ -179,7 +183,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
     }
   } else {
     const int q = warp & 3;
-    uint8_t* box = store_buf + q * kStoreBuf;
+    const int odd_steps = (warp - 2) >> 2;
+    uint8_t* box = store_buf + (warp - 2) * kStoreBuf;
     uint32_t it = 0;
     Item w;
     for (Walk walk(cut, unit, units, total); walk.get(w); ++it) {
@@ -206,18 +211,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
         head = cut_first(cut, w.tile);
         float* mine = p.partial + cut_slot(cut, w.tile, unit) * kSlot + half * (kSlot / 2);
 #pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
+        for (int c = odd_steps; c < nch; c += 2) {
           float v[32];
           read(c, v);
           store_partial(mine, c * kChunk, q * 32 + lane, v);
         }
-        if (!cut_last(p.counters + 2 * w.tile + half, ways, s_last)) {
-          release();
-          continue;
-        }
+        release();
+        if (!cut_last(p.counters + 2 * w.tile + half, ways, s_last)) continue;
+      } else if (odd_steps >= nch) {
+        release();
       }
 #pragma unroll 1
-      for (int c = 0; c < nch; ++c) {
+      for (int c = odd_steps; c < nch; c += 2) {
         float v[32];
         if (ways > 1) {
           join_partials(
@@ -226,7 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
         } else {
           read(c, v);
         }
-        if (c == nch - 1) release();
+        if (ways == 1 && c + 2 >= nch) release();
         const int64_t at = (int64_t)(tl.row0 + c * kChunk) * p.feats + f0;
         const int rows_ok = min(kChunk, tl.rows - c * kChunk);
         if constexpr (OUT32)
@@ -281,8 +286,8 @@ extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, co
   Args p{};
   const int64_t pitch[1] = {K / 2}, pd[2] = {K / 2, N}, qd[2] = {K / 2, M};
   if (int rc = encode_map(&p.p, b_codes, 1, 2, pd, pitch, kLanes)) return rc;
-  if (int rc = encode_map(&p.q, a_codes, 1, 2, qd, pitch, kTileRows / 2)) return rc;
-  if (int rc = encode_map(&p.q16, a_codes, 1, 2, qd, pitch, 16)) return rc;
+  for (int b = 0; b < 4; ++b)
+    if (int rc = encode_map(&p.q[b], a_codes, 1, 2, qd, pitch, b == 0 ? kTileRows / 2 : 128 >> b)) return rc;
   p.kblocks = (int)((K + kBlockK - 1) / kBlockK);
   if (int rc = encode_scale_map(&p.sp, b_scales, p.kblocks, (N + 127) / 128, 1)) return rc;
   if (int rc = encode_scale_map(&p.sq, a_scales, p.kblocks, (M + 127) / 128, 2)) return rc;

@@ -15,13 +15,15 @@
 
 namespace dgl {
 
-constexpr int kThreads = 192;         // producer warp, MMA warp, four epilogue warps
+constexpr int kEpiWarps = 8;          // two for each quarter of the lanes
+constexpr int kThreads = 64 + 32 * kEpiWarps;  // producer warp, MMA warp, epilogue warps
 constexpr int kLanes = 128;           // output features per CTA (accumulator lanes)
 constexpr int kPairFeats = 2 * kLanes;
 constexpr uint32_t kRowBytes = 128;   // one operand row of a K block (the swizzle span)
 constexpr uint32_t kStageP = kLanes * kRowBytes;
 constexpr int kChunk = 32;            // output rows (accumulator columns) per epilogue step
-constexpr uint32_t kStoreBuf = kChunk * 32 * 2;  // one warp's 32 x 32 bf16 box
+constexpr int kPairPitch = 36;        // words from one row pair of a box to the next (bank-conflict free)
+constexpr uint32_t kStoreBuf = kChunk / 2 * kPairPitch * 4;  // one warp's 32 x 32 bf16 box
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -216,10 +218,15 @@ __host__ __device__ constexpr uint32_t idesc_of(uint32_t p_fmt, uint32_t q_fmt, 
 }
 __device__ __forceinline__ uint32_t idesc_columns(uint32_t n) { return (n >> 3) << 17; }
 
-// The four epilogue warps.  They decide together whether a tile's accumulator
+// The epilogue warps: warp w reads lane quarter w % 4, and of its tile's steps of
+// 32 rows those of its half (the first four warps the even ones).  Eight warps
+// rather than four: a step is a chain of latencies (tensor memory, shared
+// memory, stores), and four left stores of short reductions at 2.4 TB/s.
+//
+// They decide together whether a tile's accumulator
 // arrived (one thread waits; `go`: two words of shared memory, by turns), so
 // that none is left at a barrier by one that gave up.
-__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void epilogue_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kEpiWarps) : "memory"); }
 __device__ __forceinline__ bool epilogue_wait(const Watch& w, uint32_t tfull, uint32_t it, volatile uint32_t* go) {
   const uint32_t buf = it & 1;
   if (threadIdx.x == 64) go[buf] = mbar_wait(w, tfull + 8 * buf, (it >> 1) & 1, 0x400u | buf) ? 1u : 0u;
@@ -243,19 +250,21 @@ __device__ __forceinline__ bool epilogue_wait(const Watch& w, uint32_t tfull, ui
 // adds them in the order of K (the same bits every time) and stores the tile.
 // No pair waits for another.
 constexpr int kMinShare = 8;   // K blocks
-constexpr int kJoinCost = 6;   // K blocks' time that a step of 32 rows costs to leave and to join, four partials at a time
+constexpr int kJoin = 3;       // partials whose loads are in flight at once
 struct Cut {
   int tiles, kblocks, share;
 };
-// `rows`: of a tile (on average).  Cutting pays for short tiles (a decoding
-// step's 32 columns are joined in a microsecond) and for tall ones with a long K
-// whose round would leave most pairs idle.
+// `rows`: of a tile (on average).  Leaving and joining partials costs about 3 us
+// for up to 64 rows and 2.2 us for each further step of 32 rows and three
+// partials (measured), a K block 0.2 us: so cutting pays for short tiles, as of
+// a decoding step, and for tall ones with a long K and few of them.
 __device__ __forceinline__ Cut cut_of(int total, int units, int kblocks, int rows) {
   Cut c{total % units, kblocks, 0};
   // (a K so long that the products below would pass 32 bits is left whole)
   if (c.tiles == 0 || kblocks > (1 << 20)) return Cut{0, kblocks, 0};
   c.share = max(kMinShare, (c.tiles * kblocks + units - 1) / units);
-  const int ways = kblocks / c.share + 1, cost = kJoinCost * ((rows + kChunk - 1) / kChunk) * ((ways + 3) / 4);
+  const int ways = kblocks / c.share + 1, steps = (rows + kChunk - 1) / kChunk;
+  const int cost = steps <= 2 ? 15 : 11 * steps * ((ways + 2) / kJoin + 1) / 2;
   return kblocks - c.share > cost ? c : Cut{0, kblocks, 0};
 }
 // How many pairs share tile t of the cut ones, the first of them, and the
@@ -300,7 +309,7 @@ __host__ __device__ constexpr size_t cut_bytes(int units, int columns) {
   return kCutCounters * 4 + (size_t)2 * units * cut_slot_floats(columns) * 4;
 }
 
-// A warp's 32 x 32 box of a partial accumulator: to / from the slot.
+// A warp's 32 x 32 box of a partial accumulator to its slot.
 __device__ __forceinline__ void store_partial(float* slot, int column, int lane_of, const float (&v)[32]) {
 #pragma unroll
   for (int i = 0; i < 32; ++i) __stcg(slot + (int64_t)(column + i) * kLanes + lane_of, v[i]);
@@ -311,16 +320,16 @@ __device__ __forceinline__ void join_partials(int ways, Slot slot, int column, i
 #pragma unroll
   for (int i = 0; i < 32; ++i) v[i] = 0.f;
 #pragma unroll 1
-  for (int j = 0; j < ways; j += 4) {
-    float u[4][32];
+  for (int j = 0; j < ways; j += kJoin) {
+    float u[kJoin][32];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
+    for (int k = 0; k < kJoin; ++k) {
       const float* s = slot(min(j + k, ways - 1)) + (int64_t)column * kLanes + lane_of;
 #pragma unroll
       for (int i = 0; i < 32; ++i) u[k][i] = j + k < ways ? __ldcg(s + i * kLanes) : 0.f;
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int k = 0; k < kJoin; ++k)
 #pragma unroll
       for (int i = 0; i < 32; ++i) v[i] += u[k][i];
   }
@@ -355,15 +364,31 @@ __device__ __forceinline__ void store_box_f32(float* d, int64_t pitch, int rows_
 }
 __device__ __forceinline__ void store_box_bf16(__nv_bfloat16* d, int64_t pitch, int rows_ok, int feats_ok, int lane,
                                                const float (&v)[32], uint8_t* buf) {
-  __nv_bfloat16* b = reinterpret_cast<__nv_bfloat16*>(buf);
+  // words of two rows' values of one feature go in, eight features of two rows
+  // come out and are sorted into the rows
+  uint32_t* w = reinterpret_cast<uint32_t*>(buf);
 #pragma unroll
-  for (int i = 0; i < 32; ++i) b[i * 32 + lane] = __float2bfloat16_rn(v[i]);
+  for (int i = 0; i < 16; ++i) {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    w[i * kPairPitch + lane] = *reinterpret_cast<const uint32_t*>(&h);
+  }
   __syncwarp();
+  const int f = (lane & 3) * 8;
+  __nv_bfloat16* at = d + (int64_t)(lane >> 2) * 2 * pitch + f;
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int r = j * 8 + (lane >> 2), f = (lane & 3) * 8;
-    const uint4 u = *reinterpret_cast<const uint4*>(b + r * 32 + f);
-    if (r < rows_ok && f < feats_ok) *reinterpret_cast<uint4*>(d + r * pitch + f) = u;
+  for (int j = 0; j < 2; ++j) {
+    const int r = (j * 8 + (lane >> 2)) * 2;  // the first of the two rows
+    const uint4* s = reinterpret_cast<const uint4*>(w + r / 2 * kPairPitch + f);
+    const uint4 a = s[0], b = s[1];
+    if (f < feats_ok) {
+      __nv_bfloat16* to = at + j * 16 * pitch;
+      if (r < rows_ok)
+        *reinterpret_cast<uint4*>(to) = make_uint4(__byte_perm(a.x, a.y, 0x5410), __byte_perm(a.z, a.w, 0x5410),
+                                                   __byte_perm(b.x, b.y, 0x5410), __byte_perm(b.z, b.w, 0x5410));
+      if (r + 1 < rows_ok)
+        *reinterpret_cast<uint4*>(to + pitch) = make_uint4(__byte_perm(a.x, a.y, 0x7632), __byte_perm(a.z, a.w, 0x7632),
+                                                           __byte_perm(b.x, b.y, 0x7632), __byte_perm(b.z, b.w, 0x7632));
+    }
   }
   __syncwarp();  // the box may be overwritten
 }

@@ -83,8 +83,13 @@ __device__ __forceinline__ bool mbar_try(uint32_t bar, uint32_t parity) {
 __device__ __forceinline__ void mbar_expect(uint32_t bar, uint32_t bytes) {
   asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
 }
+// Arrive on a barrier of either CTA.  The release is of this CTA's scope: what it
+// orders here are reads of tensor memory, complete by then (tcgen05.wait::ld),
+// not writes that the other CTA reads.  A release of the cluster's scope waits
+// for all of the thread's global stores, which held each accumulator for the
+// time that the tile before took to reach memory (7000 cycles a tile).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
 }
 
 // Pipeline waits are bounded: after `limit_ns` the waiter records the wait in

@@ -28,11 +28,10 @@ constexpr int kMaxExperts = 1024;
 constexpr int kStages = 6;
 constexpr uint32_t kStageQ = (kTileRows / 2) * kRowBytes;
 constexpr uint32_t kStage = kStageP + kStageQ;
-constexpr uint32_t kTableBytes = 2 * (kMaxExperts + 2) * 4;
+constexpr uint32_t kTableBytes = 3 * (kMaxExperts + 2) * 4;
 constexpr uint32_t kSmem = kStages * kStage + kEpiWarps * kStoreBuf + kTableBytes + 256 + 1024;
 constexpr uint32_t kTmemCols = 2 * kTileRows;
 constexpr int64_t kSlot = (int64_t)cut_slot_floats(kTileRows);
-constexpr int kBand = 8;      // row tiles swept together, for reuse in L2
 constexpr int kTailRows = 64; // rows of a K block in the gradient
 
 struct Args {
@@ -46,6 +45,7 @@ struct Args {
   const float *sa, *sb;
   int64_t sa_s, sb_e, sb_n;
   uint32_t idesc;
+  Raster raster;
   uint32_t* counters;      // cut tiles
   float* partial;
   Watch watch;
@@ -62,12 +62,12 @@ __device__ __forceinline__ int tile_height(int rows) {
   return nt > 1 ? ((rows + nt - 1) / nt + 31) / 32 * 32 : kTileRows;
 }
 
-// Group starts (start[e], e <= experts; start[experts + 1] = T) and the number
-// of tiles before each group, by one warp.  Ends are clamped to [previous end,
+// Group starts (start[e], e <= experts; start[experts + 1] = T), the number of
+// tiles before each group and the groups' row tiles and their height (shape[e] =
+// row tiles << 9 | height), by one warp.  Ends are clamped to [previous end,
 // T]; the forward's group `experts` is the rows past the last end.
 template <bool GRAD>
-__device__ void scan_groups(const Args& p, int* start, int* first, int lane) {
-  const int nf = (p.feats + kPairFeats - 1) / kPairFeats;
+__device__ void scan_groups(const Args& p, int* start, int* first, uint32_t* shape, int lane) {
   const int groups = GRAD ? p.experts : p.experts + 1;
   int end = 0, tiles = 0;
   if (lane == 0) start[0] = first[0] = 0;
@@ -82,30 +82,30 @@ __device__ void scan_groups(const Args& p, int* start, int* first, int lane) {
     }
     int s = __shfl_up_sync(0xffffffffu, v, 1);
     if (lane == 0) s = end;
-    const int rows = GRAD ? p.rows : v - s;
-    int t = e < groups ? (rows + kTileRows - 1) / kTileRows * nf : 0;
+    const int rows = GRAD ? p.rows : v - s, nt = (rows + kTileRows - 1) / kTileRows;
+    int t = e < groups ? nt * p.raster.nf : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, t, o);
       if (lane >= o) t += u;
     }
     t += tiles;
-    if (e < groups) start[e + 1] = v, first[e + 1] = t;
+    if (e < groups)
+      start[e + 1] = v, first[e + 1] = t, shape[e] = (uint32_t)nt << 9 | (uint32_t)(GRAD ? kTileRows : tile_height(rows));
     end = __shfl_sync(0xffffffffu, v, 31);
     tiles = __shfl_sync(0xffffffffu, t, 31);
   }
 }
 
-// Tile t of the list; `e`: a cursor that only moves forward.  Within a group,
-// bands of kBand row tiles are swept feature tile by feature tile.
+// Tile t of the list; `e`: a cursor that only moves forward.
 template <bool GRAD, bool F8>
-__device__ __forceinline__ Tile tile_at(const Args& p, const int* start, const int* first, int t, int& e) {
+__device__ __forceinline__ Tile tile_at(const Args& p, const int* start, const int* first, const uint32_t* shape, int t,
+                                        int& e) {
   while (t >= first[e + 1]) ++e;
   const int len = start[e + 1] - start[e], rows = GRAD ? p.rows : len;
-  const int nt = (rows + kTileRows - 1) / kTileRows, nf = (p.feats + kPairFeats - 1) / kPairFeats;
-  const int j = t - first[e], band = j / (kBand * nf), in = j - band * kBand * nf;
-  const int wide = min(kBand, nt - band * kBand), f = in / wide, r = band * kBand + in - f * wide;
-  const int high = GRAD ? kTileRows : tile_height(rows);
+  const int high = (int)(shape[e] & 511u);
+  int f, r;
+  raster_at(p.raster, t - first[e], (int)(shape[e] >> 9), r, f);
   Tile tl;
   tl.e = e;
   tl.rows = min(high, rows - r * high);
@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   uint8_t* store_buf = smem + kStages * kStage;
   int* start = reinterpret_cast<int*>(store_buf + kEpiWarps * kStoreBuf);
   int* first = start + kMaxExperts + 2;
+  uint32_t* shape = reinterpret_cast<uint32_t*>(first + kMaxExperts + 2);
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(start) + kTableBytes);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
@@ -151,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
 
   let_next_start();
+  if (threadIdx.x < 5) prefetch_map(threadIdx.x == 4 ? &p.p : &p.q[GRAD ? 0 : threadIdx.x]);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 2 * kEpiWarps);
@@ -158,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   }
   if (warp == 1) tmem_alloc(smem_u32(s_tmem), kTmemCols);
   wait_for_previous();
-  if (warp == 2) scan_groups<GRAD>(p, start, first, lane);
+  if (warp == 2) scan_groups<GRAD>(p, start, first, shape, lane);
   fence_before();
   __syncwarp();
   cluster_sync();
@@ -169,21 +171,20 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   constexpr int kb_red = F8 ? 128 : 64;
   Cut cut{0, 1, 0};
   if (!GRAD) {
-    const int nf = (p.feats + kPairFeats - 1) / kPairFeats;
-    cut = cut_of(real, units, (p.red + kb_red - 1) / kb_red, (int)((int64_t)start[p.experts] * nf / max(real, 1)));
+    // rows of a tile on average (in fp32: a division of 64 bits would stand before the first load)
+    const float rows = (float)start[p.experts] * (float)p.raster.nf / (float)max(real, 1);
+    cut = cut_of(real, units, (p.red + kb_red - 1) / kb_red, (int)rows);
   }
   const uint32_t base = smem_u32(smem);
 
   if (warp == 0) {
     // -------------------------------------------------------------- producer
-    prefetch_map(&p.p);
-    prefetch_map(&p.q[GRAD ? 0 : 3]);
     uint32_t stage = 0, phase = 0;
     int e = 0;
     bool ok = true;
     Item w;
     for (Walk walk(cut, unit, units, total); ok && walk.get(w);) {
-      const Tile tl = tile_at<GRAD, F8>(p, start, first, w.tile, e);
+      const Tile tl = tile_at<GRAD, F8>(p, start, first, shape, w.tile, e);
       const int kb1 = GRAD ? tl.kblocks : min(w.kb1, tl.kblocks);
       const int n = columns<GRAD>(tl), mine = n / 2;  // this CTA's share of the rows operand
       const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       bool ok = true;
       Item w;
       for (Walk walk(cut, unit, units, total); ok && walk.get(w); ++it) {
-        const Tile tl = tile_at<GRAD, F8>(p, start, first, w.tile, e);
+        const Tile tl = tile_at<GRAD, F8>(p, start, first, shape, w.tile, e);
         const int kb1 = GRAD ? tl.kblocks : min(w.kb1, tl.kblocks);
         const uint32_t idesc = p.idesc | idesc_columns((uint32_t)columns<GRAD>(tl));
         const uint32_t buf = it & 1;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     int e = 0;
     Item w;
     for (Walk walk(cut, unit, units, total); walk.get(w); ++it) {
-      const Tile tl = tile_at<GRAD, F8>(p, start, first, w.tile, e);
+      const Tile tl = tile_at<GRAD, F8>(p, start, first, shape, w.tile, e);
       const uint32_t buf = it & 1;
       const int f0 = tl.f0 + (int)half * kLanes + q * 32;  // this warp's first feature
       const int feats_ok = min(32, p.feats - f0);
@@ -467,6 +468,7 @@ extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, 
     if (int rc = encode_map(&p.q[b], A, (int)esz, 2, qd, qs, (kTileRows / 2) >> b)) return rc;
   p.ends = ends, p.experts = experts, p.T = (int)T, p.feats = (int)N, p.rows = 0, p.red = (int)K, p.out = D;
   p.sa = scale_a, p.sb = scale_b, p.sa_s = sa, p.sb_e = sb_e, p.sb_n = sb_n;
+  p.raster = raster_of(N);
   p.idesc = idesc_of(format_of(b_type), format_of(a_type), b_n_major != 0, false);
   p.watch = watch_of(status);
   p.counters = static_cast<uint32_t*>(workspace);
@@ -514,6 +516,7 @@ extern "C" int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const 
   if (int rc = encode_map(&p.p_tail, a_tail, 2, 3, ptd, pts, 64)) return rc;
   if (int rc = encode_map(&p.q_tail, d_tail, 2, 2, qtd, qts, 64)) return rc;
   p.ends = ends, p.experts = experts, p.T = (int)T, p.feats = (int)K, p.rows = (int)N, p.red = 0, p.out = dB;
+  p.raster = raster_of(K);
   p.idesc = idesc_of(1, 1, true, true);
   p.watch = watch_of(status);
   const int64_t vecs = 64 * (N + K) / 8;

@@ -34,12 +34,12 @@ constexpr uint32_t kSmem = kStages * kStage + kEpiWarps * kStoreBuf + 256 + 1024
 constexpr uint32_t kTmemCols = 512, kScaleCol = 2 * kTileRows;
 constexpr int kScaleBufs = 4;                    // 24 columns each: 2 x 4 for P, 2 x 8 for Q
 constexpr int64_t kSlot = (int64_t)cut_slot_floats(kTileRows);
-constexpr int kBand = 8;
 
 struct Args {
   CUtensorMap p, q[4];     // codes as bytes: boxes of 128 rows; of 96, 64, 32 and 16 rows
   CUtensorMap sp, sq;      // scales: (256 words, K block, row tile), boxes of one and two row tiles
-  int rows, feats, kblocks;
+  int rows, feats, kblocks, row_tiles;
+  Raster raster;
   void* out;
   uint32_t* counters;      // cut tiles
   float* partial;
@@ -72,9 +72,8 @@ struct Tile {
   int row0, rows, f0;
 };
 __device__ __forceinline__ Tile tile_at(const Args& p, int t) {
-  const int nt = (p.rows + kTileRows - 1) / kTileRows, nf = (p.feats + kPairFeats - 1) / kPairFeats;
-  const int band = t / (kBand * nf), in = t - band * kBand * nf;
-  const int wide = min(kBand, nt - band * kBand), f = in / wide, r = band * kBand + in - f * wide;
+  int r, f;
+  raster_at(p.raster, t, p.row_tiles, r, f);
   return Tile{r * kTileRows, min(kTileRows, p.rows - r * kTileRows), f * kPairFeats};
 }
 
@@ -93,6 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   const uint32_t half = cluster_ctarank();
   const int unit = blockIdx.x >> 1, units = gridDim.x >> 1;
   let_next_start();
+  if (threadIdx.x < 4) prefetch_map(&p.q[threadIdx.x]);
+  if (threadIdx.x >= 4 && threadIdx.x < 7) prefetch_map(threadIdx.x == 4 ? &p.p : threadIdx.x == 5 ? &p.sp : &p.sq);
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 2 * kEpiWarps);
@@ -105,12 +106,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   cluster_sync();
   fence_after();
   const uint32_t tmem = *s_tmem, base = smem_u32(smem);
-  const int total = ((p.rows + kTileRows - 1) / kTileRows) * ((p.feats + kPairFeats - 1) / kPairFeats);
+  const int total = p.row_tiles * p.raster.nf;
   const Cut cut = cut_of(total, units, p.kblocks, min(p.rows, kTileRows));
 
   if (warp == 0) {
-    prefetch_map(&p.p);
-    prefetch_map(&p.q[0]);
     uint32_t stage = 0, phase = 0;
     bool ok = true;
     Item w;
@@ -292,6 +291,8 @@ extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, co
   if (int rc = encode_scale_map(&p.sp, b_scales, p.kblocks, (N + 127) / 128, 1)) return rc;
   if (int rc = encode_scale_map(&p.sq, a_scales, p.kblocks, (M + 127) / 128, 2)) return rc;
   p.rows = (int)M, p.feats = (int)N, p.out = D;
+  p.row_tiles = (int)((M + kTileRows - 1) / kTileRows);
+  p.raster = raster_of(N);
   p.counters = static_cast<uint32_t*>(workspace);
   p.partial = reinterpret_cast<float*>(p.counters + kCutCounters);
   p.watch = Watch{static_cast<unsigned long long*>(status), g_epoch.fetch_add(1, std::memory_order_relaxed), 4000000000ull};

@@ -223,6 +223,39 @@ __host__ __device__ constexpr uint32_t idesc_of(uint32_t p_fmt, uint32_t q_fmt, 
 }
 __device__ __forceinline__ uint32_t idesc_columns(uint32_t n) { return (n >> 3) << 17; }
 
+// ------------------------------------------------------------- order of tiles
+
+// Order of a matrix's tiles: bands of kBand row tiles swept feature tile by
+// feature tile, so that the tiles in flight share operands in L2.  The division
+// by a band's tiles is a multiplication (the decoding stands before the first
+// load of a tile, and a division took a third of a microsecond): m = floor(2^(31
+// + s) / d) + 1 with s = ceil(log2 d) gives exact quotients below 2^31, and 2^32
+// / w rounded up those by w <= 8 below 2^29.
+constexpr int kBand = 8;
+struct Raster {
+  uint32_t mul, shift;
+  int nf;  // feature tiles
+};
+inline Raster raster_of(int64_t feats) {
+  Raster r;
+  r.nf = (int)((feats + kPairFeats - 1) / kPairFeats);
+  const uint64_t d = (uint64_t)kBand * r.nf;
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  r.mul = (uint32_t)((1ull << (31 + s)) / d + 1);
+  r.shift = s - 1;
+  return r;
+}
+__device__ __forceinline__ void raster_at(const Raster& o, int tile, int row_tiles, int& row, int& feat) {
+  const int band = (int)(__umulhi((uint32_t)tile, o.mul) >> o.shift), in = tile - band * kBand * o.nf;
+  const int wide = min(kBand, row_tiles - band * kBand);
+  uint32_t m = 1u << 29;
+  m = wide == 7 ? 613566757u : m, m = wide == 6 ? 715827883u : m, m = wide == 5 ? 858993460u : m;
+  m = wide == 4 ? 1u << 30 : m, m = wide == 3 ? 1431655766u : m, m = wide == 2 ? 1u << 31 : m;
+  feat = wide == 1 ? in : (int)__umulhi((uint32_t)in, m);
+  row = band * kBand + in - feat * wide;
+}
+
 // The epilogue warps: warp w reads lane quarter w % 4, and of its tile's steps of
 // 32 rows those of its half (the first four warps the even ones).  Eight warps
 // rather than four: a step is a chain of latencies (tensor memory, shared

@@ -16,6 +16,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
 
+#include <type_traits>
+
 #include "launch.cuh"
 
 namespace {
@@ -151,26 +153,26 @@ __device__ __forceinline__ float row_scale(float amax, bool e5m2) {
 }
 
 // RT: the residual's type (0 none, 1 bf16, 2 fp32).  The row stays in
-// registers: NV vectors of VW values per thread.
-template <int RT, int VW, int NV, bool OUT8>
-__global__ void __launch_bounds__(NV * VW > 16 ? 512 : 1024) add_rms_norm_kernel(const __grid_constant__ NormArgs p) {
+// registers: NV vectors of 8 values per thread.
+template <int RT, int NV, bool OUT8>
+__global__ void __launch_bounds__(NV > 2 ? 512 : 1024) add_rms_norm_kernel(const __grid_constant__ NormArgs p) {
   __shared__ float part[66];
   begin_kernel();
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= p.rows) return;  // several rows per block only with one warp each: no barrier below
-  const int step = blockDim.x * VW;
-  float h[NV][VW];
+  const int step = blockDim.x * 8;
+  float h[NV][8];
   float ss = 0.f;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x * VW + k * step;
+    const int i = threadIdx.x * 8 + k * step;
     if (i < p.hidden) {
-      load_bf16<VW>(p.x, row * p.ld_x + i, h[k]);
+      load_bf16<8>(p.x, row * p.ld_x + i, h[k]);
       if constexpr (RT != 0) {
-        float r[VW];
-        load_any<VW>(RT == 2, p.residual, row * p.ld_residual + i, r);
+        float r[8];
+        load_any<8>(RT == 2, p.residual, row * p.ld_residual + i, r);
 #pragma unroll
-        for (int j = 0; j < VW; ++j) {
+        for (int j = 0; j < 8; ++j) {
           h[k][j] += r[j];
           // the norm is of the sum as it is stored, so that the gradient sees the same values
           if constexpr (RT == 1) h[k][j] = __bfloat162float(__float2bfloat16_rn(h[k][j]));
@@ -178,22 +180,22 @@ __global__ void __launch_bounds__(NV * VW > 16 ? 512 : 1024) add_rms_norm_kernel
       }
     } else {
 #pragma unroll
-      for (int j = 0; j < VW; ++j) h[k][j] = 0.f;
+      for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
     }
   }
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x * VW + k * step;
+    const int i = threadIdx.x * 8 + k * step;
     if constexpr (RT != 0) {
       if (i < p.hidden) {
         if constexpr (RT == 2)
-          store_f32<VW>(p.sum, row * p.ld_sum + i, h[k]);
+          store_f32<8>(p.sum, row * p.ld_sum + i, h[k]);
         else
-          store_bf16<VW>(p.sum, row * p.ld_sum + i, h[k]);
+          store_bf16<8>(p.sum, row * p.ld_sum + i, h[k]);
       }
     }
 #pragma unroll
-    for (int j = 0; j < VW; ++j) ss = fmaf(h[k][j], h[k][j], ss);
+    for (int j = 0; j < 8; ++j) ss = fmaf(h[k][j], h[k][j], ss);
   }
   ss = row_reduce<Add>(ss, part);
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
@@ -201,18 +203,18 @@ __global__ void __launch_bounds__(NV * VW > 16 ? 512 : 1024) add_rms_norm_kernel
   float amax = 0.f;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x * VW + k * step;
+    const int i = threadIdx.x * 8 + k * step;
     if (i < p.hidden) {
-      float w[VW];
-      load_any<VW>(p.weight_f32 != 0, p.weight, i, w);
+      float w[8];
+      load_any<8>(p.weight_f32 != 0, p.weight, i, w);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
+      for (int j = 0; j < 8; ++j) {
         h[k][j] = h[k][j] * rstd * w[j];
         // an infinity (only of a weight, or of a sum of squares below the
         // smallest normal value) saturates and stays out of the scale
         if constexpr (OUT8) amax = fmaxf(amax, isinf(h[k][j]) ? 0.f : fabsf(h[k][j]));
       }
-      if constexpr (!OUT8) store_bf16<VW>(p.y, row * p.hidden + i, h[k]);
+      if constexpr (!OUT8) store_bf16<8>(p.y, row * p.hidden + i, h[k]);
     }
   }
   if constexpr (OUT8) {
@@ -228,12 +230,103 @@ __global__ void __launch_bounds__(NV * VW > 16 ? 512 : 1024) add_rms_norm_kernel
     const float inv = 1.f / c;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = threadIdx.x * VW + k * step;
+      const int i = threadIdx.x * 8 + k * step;
       if (i < p.hidden) {
 #pragma unroll
-        for (int j = 0; j < VW; ++j) h[k][j] *= inv;
-        store_fp8<VW>(p.y, row * p.hidden + i, h[k], e5m2 ? __NV_E5M2 : __NV_E4M3);
+        for (int j = 0; j < 8; ++j) h[k][j] *= inv;
+        store_fp8<8>(p.y, row * p.hidden + i, h[k], e5m2 ? __NV_E5M2 : __NV_E4M3);
       }
+    }
+  }
+}
+
+// Rows without 16-byte alignment, element by element: thread i holds the values
+// i, i + blockDim.x, ...  All loads of a row are issued before the first is used
+// (indices past the row read its last value, which is then dropped): with a
+// branch around each load they went out one at a time, at 1.7 TB/s.
+template <int N, class T>
+__device__ __forceinline__ void load_spread(const T* p, int hidden, T (&v)[N]) {
+#pragma unroll
+  for (int k = 0; k < N; ++k) v[k] = p[min((int)(threadIdx.x + k * blockDim.x), hidden - 1)];
+}
+__device__ __forceinline__ float as_float(uint16_t b) { return __uint_as_float((uint32_t)b << 16); }
+__device__ __forceinline__ float as_float(float f) { return f; }
+
+// N values per thread of a bf16 or fp32 row, 0 past its end.
+template <bool F32, int N>
+struct Spread {
+  using T = std::conditional_t<F32, float, uint16_t>;
+  T v[N];
+  __device__ __forceinline__ void load(const void* base, int64_t at, int hidden) {
+    load_spread<N, T>(static_cast<const T*>(base) + at, hidden, v);
+  }
+  __device__ __forceinline__ float at(int k, int hidden) const {
+    return (int)(threadIdx.x + k * blockDim.x) < hidden ? as_float(v[k]) : 0.f;
+  }
+};
+
+template <int RT, bool W32, int N, bool OUT8>
+__global__ void __launch_bounds__(N > 4 ? 512 : 1024) add_rms_norm_spread_kernel(const __grid_constant__ NormArgs p) {
+  __shared__ float part[66];
+  begin_kernel();
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= p.rows) return;  // several rows per block only with one warp each: no barrier below
+  Spread<false, N> x;
+  Spread<RT == 2, N> r;
+  Spread<W32, N> w;
+  x.load(p.x, row * p.ld_x, p.hidden);
+  if constexpr (RT != 0) r.load(p.residual, row * p.ld_residual, p.hidden);
+  w.load(p.weight, 0, p.hidden);
+  float h[N], ss = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    h[k] = x.at(k, p.hidden);
+    if constexpr (RT != 0) h[k] += r.at(k, p.hidden);
+    if constexpr (RT == 1) h[k] = __bfloat162float(__float2bfloat16_rn(h[k]));
+    ss = fmaf(h[k], h[k], ss);
+  }
+  if constexpr (RT != 0) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * blockDim.x;
+      const float v[1] = {h[k]};
+      if (i < p.hidden) {
+        if constexpr (RT == 2)
+          store_f32<1>(p.sum, row * p.ld_sum + i, v);
+        else
+          store_bf16<1>(p.sum, row * p.ld_sum + i, v);
+      }
+    }
+  }
+  ss = row_reduce<Add>(ss, part);
+  const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
+  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  float amax = 0.f, inv = 1.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    h[k] = h[k] * rstd * w.at(k, p.hidden);
+    if constexpr (OUT8) amax = fmaxf(amax, isinf(h[k]) ? 0.f : fabsf(h[k]));
+  }
+  const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
+  if constexpr (OUT8) {
+    float c;
+    if (p.scale_in) {
+      c = __ldg(p.scale_in);
+    } else {
+      c = row_scale(row_reduce<Max>(amax, part + 33), e5m2);
+      if (threadIdx.x == 0) p.scale[row] = c;
+    }
+    inv = 1.f / c;
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int i = threadIdx.x + k * blockDim.x;
+    const float v[1] = {h[k] * inv};
+    if (i < p.hidden) {
+      if constexpr (OUT8)
+        store_fp8<1>(p.y, row * p.hidden + i, v, e5m2 ? __NV_E5M2 : __NV_E4M3);
+      else
+        store_bf16<1>(p.y, row * p.hidden + i, v);
     }
   }
 }
@@ -504,14 +597,21 @@ int stream_norm(const NormArgs& p, int sms, cudaStream_t s) {
   return dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);
 }
 
-template <int RT, int VW, int NV, bool OUT8>
+template <int RT, int NV, bool OUT8>
 int launch_norm(const NormArgs& p, int threads, cudaStream_t s) {
   const int per = threads == 32 ? 4 : 1;  // one warp per row: four rows to a block
-  return dgl::launch(add_rms_norm_kernel<RT, VW, NV, OUT8>, dim3((unsigned)((p.rows + per - 1) / per)),
+  return dgl::launch(add_rms_norm_kernel<RT, NV, OUT8>, dim3((unsigned)((p.rows + per - 1) / per)),
                      dim3(threads, per), 0, s, p);
 }
 
 int round32(int v) { return (v + 31) / 32 * 32; }
+
+template <int RT, bool W32, bool OUT8>
+int spread_norm(const NormArgs& p, cudaStream_t s) {
+  const int n = p.hidden <= 1024 ? 4 : 16, threads = round32((p.hidden + n - 1) / n), per = threads == 32 ? 4 : 1;
+  return dgl::launch(n == 4 ? add_rms_norm_spread_kernel<RT, W32, 4, OUT8> : add_rms_norm_spread_kernel<RT, W32, 16, OUT8>,
+                     dim3((unsigned)((p.rows + per - 1) / per)), dim3(threads, per), 0, s, p);
+}
 
 template <int RT, bool OUT8>
 int run_norm(const NormArgs& p, bool vec, int sms, cudaStream_t s) {
@@ -521,13 +621,12 @@ int run_norm(const NormArgs& p, bool vec, int sms, cudaStream_t s) {
     // each at 16384).  Few rows: as many threads as the row has vectors, for the
     // shortest chain of loads; short rows are light enough for that too.
     if (p.rows > 2 * sms && n >= 256 && n <= 2048) return stream_norm<RT, OUT8, RT == 2 ? 2 : 3>(p, sms, s);
-    if (n <= 1024) return launch_norm<RT, 8, 1, OUT8>(p, round32(n), s);
-    if (n <= 2048) return launch_norm<RT, 8, 2, OUT8>(p, round32((n + 1) / 2), s);
-    if (n <= 4096) return launch_norm<RT, 8, 8, OUT8>(p, round32((n + 7) / 8), s);
+    if (n <= 1024) return launch_norm<RT, 1, OUT8>(p, round32(n), s);
+    if (n <= 2048) return launch_norm<RT, 2, OUT8>(p, round32((n + 1) / 2), s);
+    if (n <= 4096) return launch_norm<RT, 8, OUT8>(p, round32((n + 7) / 8), s);
     return dgl::launch(add_rms_norm_long_kernel<RT, 8, OUT8>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
   } else {
-    if (p.hidden <= 4096) return launch_norm<RT, 1, 4, OUT8>(p, round32((p.hidden + 3) / 4), s);
-    if (p.hidden <= 16384) return launch_norm<RT, 1, 16, OUT8>(p, round32((p.hidden + 15) / 16), s);
+    if (p.hidden <= 8192) return p.weight_f32 ? spread_norm<RT, true, OUT8>(p, s) : spread_norm<RT, false, OUT8>(p, s);
     return dgl::launch(add_rms_norm_long_kernel<RT, 1, OUT8>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
   }
 }
@@ -543,65 +642,53 @@ struct GradArgs {
   int hidden, weight_f32;
 };
 
+// Element by element, for rows without 16-byte alignment: N values per thread.
 // A block walks the rows blockIdx.x, + gridDim.x, ...; the weight's gradient is
 // summed in registers over its rows and written once as a row of `partial`.
-template <bool F32, int VW, int NV, bool HAS_DH>
-__global__ void __launch_bounds__(NV * VW > 8 ? 512 : 1024) add_rms_norm_grad_kernel(const __grid_constant__ GradArgs p) {
+template <bool F32, bool W32, int N, bool HAS_DH>
+__global__ void __launch_bounds__(512) add_rms_norm_grad_kernel(const __grid_constant__ GradArgs p) {
   __shared__ float part[2][33];
   begin_kernel();
-  const int step = blockDim.x * VW;
-  float dw[NV][VW], w[NV][VW];
+  Spread<W32, N> w;
+  w.load(p.weight, 0, p.hidden);
+  float dw[N];
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x * VW + k * step;
-#pragma unroll
-    for (int j = 0; j < VW; ++j) dw[k][j] = w[k][j] = 0.f;
-    if (i < p.hidden) load_any<VW>(p.weight_f32 != 0, p.weight, i, w[k]);
-  }
+  for (int k = 0; k < N; ++k) dw[k] = 0.f;
   int flip = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
     const float rstd = __ldg(p.rstd + row);
-    float dy[NV][VW], h[NV][VW], dh[NV][VW];
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int i = threadIdx.x * VW + k * step;
-#pragma unroll
-      for (int j = 0; j < VW; ++j) dy[k][j] = h[k][j] = dh[k][j] = 0.f;
-      if (i < p.hidden) {
-        load_bf16<VW>(p.dy, row * p.ld_dy + i, dy[k]);
-        load_any<VW>(F32, p.h, row * p.ld_h + i, h[k]);
-        if constexpr (HAS_DH) load_any<VW>(F32, p.dh, row * p.ld_dh + i, dh[k]);
-      }
-    }
+    Spread<false, N> dy;
+    Spread<F32, N> h, dh;
+    dy.load(p.dy, row * p.ld_dy, p.hidden);
+    h.load(p.h, row * p.ld_h, p.hidden);
+    if constexpr (HAS_DH) dh.load(p.dh, row * p.ld_dh, p.hidden);
     float dot = 0.f;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int j = 0; j < VW; ++j) {
-        h[k][j] *= rstd;
-        dw[k][j] = fmaf(dy[k][j], h[k][j], dw[k][j]);
-        dy[k][j] *= w[k][j];
-        dot = fmaf(dy[k][j], h[k][j], dot);
-      }
+    for (int k = 0; k < N; ++k) {
+      const float t = dy.at(k, p.hidden) * (h.at(k, p.hidden) * rstd);
+      dw[k] += t;
+      dot = fmaf(t, w.at(k, p.hidden), dot);
+    }
     // two sets of partials: a block's next row may start while a slow warp reads these
     dot = row_reduce<Add>(dot, part[flip]) / (float)p.hidden;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int i = threadIdx.x * VW + k * step;
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * blockDim.x;
+      float d[1] = {0.f};
+      if constexpr (HAS_DH) d[0] = dh.at(k, p.hidden);
+      d[0] = fmaf(rstd, dy.at(k, p.hidden) * w.at(k, p.hidden) - h.at(k, p.hidden) * rstd * dot, d[0]);
       if (i < p.hidden) {
-#pragma unroll
-        for (int j = 0; j < VW; ++j) h[k][j] = fmaf(rstd, dy[k][j] - h[k][j] * dot, dh[k][j]);
         if constexpr (F32)
-          store_f32<VW>(p.dx, row * p.hidden + i, h[k]);
+          store_f32<1>(p.dx, row * p.hidden + i, d);
         else
-          store_bf16<VW>(p.dx, row * p.hidden + i, h[k]);
+          store_bf16<1>(p.dx, row * p.hidden + i, d);
       }
     }
   }
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const int i = threadIdx.x * VW + k * step;
-    if (i < p.hidden) store_f32<VW>(p.partial, (int64_t)blockIdx.x * p.hidden + i, dw[k]);
+  for (int k = 0; k < N; ++k) {
+    const int i = threadIdx.x + k * blockDim.x;
+    if (i < p.hidden) p.partial[(int64_t)blockIdx.x * p.hidden + i] = dw[k];
   }
 }
 
@@ -750,6 +837,7 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* par
   const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (col < hidden)
+#pragma unroll 8
     for (int b = threadIdx.y; b < blocks; b += 32) v += partial[(int64_t)b * hidden + col];
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
@@ -765,37 +853,42 @@ __global__ void __launch_bounds__(1024) norm_weight_grad_kernel(const float* par
   }
 }
 
-// Blocks of the gradient kernels: a fixed bound that the workspace is sized by,
-// so that the partial sums stay small beside the rows.
-constexpr int kGradBlocks = 608;
+// Blocks of the gradient kernels: a fixed bound that the workspace is sized by.
+constexpr int kGradBlocks = 1216;
+
+// `most` blocks fill the SMs; a block takes four rows at least where there are
+// enough of them, so that the partial sums stay small beside the rows.
+int grad_blocks(int64_t rows, int sms, int64_t most) {
+  if (most > kGradBlocks) most = kGradBlocks;
+  const int64_t want = rows / 4 > sms ? rows / 4 : sms;
+  const int64_t n = want < most ? want : most;
+  return (int)(rows < n ? rows : n);
+}
 
 template <bool F32, bool HAS_DH>
 int run_grad(GradArgs p, bool vec, int sms, cudaStream_t s) {
   const int n = p.hidden / 8;
-  int blocks = (int)(p.rows < 2 * sms ? p.rows : 2 * sms);
+  int blocks, rc;
   // 1024 threads hold 16384 values; fp32 rows of that length do not fit twice
-  if (vec && n >= 256 && n <= 2048 && grad_parts<F32, HAS_DH>() * 16 * kGradStages * (n / kStreamVecs + 31) <= 220000) {
+  if (vec && n <= 2048 && grad_parts<F32, HAS_DH>() * 16 * kGradStages * (n / kStreamVecs + 31) <= 220000) {
     int threads, bytes;
     auto* kernel = add_rms_norm_grad_stream_kernel<F32, HAS_DH>;
-    if (int rc = stream_shape(kernel, p.hidden, grad_parts<F32, HAS_DH>(), kGradStages, sms, p.rows, &threads, &blocks,
-                              &bytes))
-      return rc;
-    blocks = blocks < kGradBlocks ? blocks : kGradBlocks;
-    if (int rc = dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p)) return rc;
-  } else {
-    blocks = blocks < kGradBlocks ? blocks : kGradBlocks;
-    auto run = [&](void (*kernel)(GradArgs), int threads) { return dgl::launch(kernel, dim3(blocks), dim3(threads), 0, s, p); };
-    int rc;
-    if (vec && n <= 1024)
-      rc = run(add_rms_norm_grad_kernel<F32, 8, 1, HAS_DH>, round32(n));
-    else if (!vec && p.hidden <= 4096)
-      rc = run(add_rms_norm_grad_kernel<F32, 1, 4, HAS_DH>, round32((p.hidden + 3) / 4));
-    else if (!vec && p.hidden <= 8192)
-      rc = run(add_rms_norm_grad_kernel<F32, 1, 16, HAS_DH>, round32((p.hidden + 15) / 16));
-    else
-      rc = run(add_rms_norm_grad_long_kernel<F32, HAS_DH>, 1024);
+    rc = stream_shape(kernel, p.hidden, grad_parts<F32, HAS_DH>(), kGradStages, sms, p.rows, &threads, &blocks, &bytes);
     if (rc != DG_OK) return rc;
+    blocks = grad_blocks(p.rows, sms, (int64_t)sms * (kStreamThreads / threads));
+    rc = dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);
+  } else {
+    const bool small = !vec && p.hidden <= 1024, regs = !vec && p.hidden <= 8192;
+    const int threads = small ? round32((p.hidden + 3) / 4) : regs ? round32((p.hidden + 15) / 16) : 1024;
+    blocks = grad_blocks(p.rows, sms, (int64_t)sms * (threads < 512 ? 512 / threads : 1));
+    auto* kernel = add_rms_norm_grad_long_kernel<F32, HAS_DH>;
+    if (small)
+      kernel = p.weight_f32 ? add_rms_norm_grad_kernel<F32, true, 4, HAS_DH> : add_rms_norm_grad_kernel<F32, false, 4, HAS_DH>;
+    else if (regs)
+      kernel = p.weight_f32 ? add_rms_norm_grad_kernel<F32, true, 16, HAS_DH> : add_rms_norm_grad_kernel<F32, false, 16, HAS_DH>;
+    rc = dgl::launch(kernel, dim3(blocks), dim3(threads), 0, s, p);
   }
+  if (rc != DG_OK) return rc;
   return dgl::launch(norm_weight_grad_kernel, dim3((unsigned)((p.hidden + 31) / 32)), dim3(32, 32), 0, s, p.partial, blocks,
                      p.hidden, p.dweight, p.weight_f32);
 }

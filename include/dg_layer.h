@@ -77,8 +77,9 @@ int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h,
  * N % 8 == 0 and K % 8 == 0 (bf16) or K % 16 == 0 (8 bits).  T, N, K < 2^31;
  * experts <= 1024.  workspace: dg_layer_products_workspace() bytes of the
  * current device, 16-byte aligned, its first DG_LAYER_COUNTER_BYTES zeroed once
- * before its first use (each call leaves them zero); calls that may run at the
- * same time need different ones. */
+ * before its first use (each call leaves them zero, except one that
+ * dg_layer_check() reports: zero them again after it); calls that may run at
+ * the same time need different ones. */
 #define DG_LAYER_COUNTER_BYTES ((size_t)2048)
 size_t dg_layer_products_workspace(void);
 int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, const void* B, int64_t ld_b, int64_t ld_e,
@@ -89,11 +90,12 @@ int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, const void*
 /* Gradient of the experts' matrices: dB[e, n, k] = sum over the rows t of
  * group e of dD[t, n] * A[t, k] (bf16 operands, fp32 accumulation; 0 for an
  * empty group), dB bf16 or fp32 (d_type), experts x N x K densely packed.
- * workspace: dg_layer_grouped_grad_workspace() bytes, 256-byte aligned. */
+ * workspace: dg_layer_grouped_grad_workspace() bytes, 16-byte aligned;
+ * products_workspace: as the workspace of dg_layer_grouped_matmul. */
 size_t dg_layer_grouped_grad_workspace(int experts, int64_t N, int64_t K);
 int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const void* A, int64_t ld_a, const int32_t* ends,
                                  int experts, void* dB, int d_type, int64_t T, int64_t N, int64_t K,
-                                 void* workspace, void* status, void* stream);
+                                 void* workspace, void* products_workspace, void* status, void* stream);
 
 /* Microscaled 4 bits (OCP MX, e2m1 elements, one e8m0 scale for each 32
  * columns): scale 2^E with E = floor(log2(max|x|)) - 2, at least -127; element

@@ -33,6 +33,7 @@ constexpr uint32_t kSmem = kStages * kStage + kEpiWarps * kStoreBuf + kTableByte
 constexpr uint32_t kTmemCols = 2 * kTileRows;
 constexpr int64_t kSlot = (int64_t)cut_slot_floats(kTileRows);
 constexpr int kTailRows = 64; // rows of a K block in the gradient
+constexpr int kBand = 8;      // row tiles of a band (4: 3 % slower on 16384 rows of 8 experts, 16: 1 %)
 
 struct Args {
   CUtensorMap p;           // 3-d: (K or features, features or K, expert)
@@ -144,8 +145,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(start) + kTableBytes);
   const uint32_t full = smem_u32(bars), empty = full + 8 * kStages, tfull = empty + 8 * kStages, tempty = tfull + 16;
   uint32_t* s_tmem = reinterpret_cast<uint32_t*>(bars + 2 * kStages + 4);
+  // after the barriers of the stages and accumulators: ten words, then the ring's barriers
   volatile uint32_t* s_last = s_tmem + 1;
   volatile uint32_t* s_go = s_tmem + 2;  // [2]
+  volatile int* s_next = reinterpret_cast<volatile int*>(s_tmem + 4);  // [2]
+  const Ring ring{smem_u32(bars + 2 * kStages + 10), smem_u32(bars + 2 * kStages + 10 + kRing),
+                  reinterpret_cast<volatile int*>(s_tmem + 6)};
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t half = cluster_ctarank();
@@ -156,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) mbar_init(full + 8 * i, 1), mbar_init(empty + 8 * i, 1);
     for (int i = 0; i < 2; ++i) mbar_init(tfull + 8 * i, 1), mbar_init(tempty + 8 * i, 2 * kEpiWarps);
+    for (int i = 0; i < kRing; ++i) mbar_init(ring.full + 8 * i, 1), mbar_init(ring.empty + 8 * i, kRingReaders);
     mbar_init_fence();
   }
   if (warp == 1) tmem_alloc(smem_u32(s_tmem), kTmemCols);
@@ -183,7 +189,36 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     int e = 0;
     bool ok = true;
     Item w;
-    for (Walk walk(cut, unit, units, total); ok && walk.get(w);) {
+    Feed feed(cut, unit, units, total);
+    // the even CTA: lane 0 holds the next draw; the tile after the one being loaded is passed on once its loads have begun
+    const uint32_t wrap = (uint32_t)(feed.rest + units - 1);
+    uint32_t drawn = 0, passed = 0;
+    int ahead = -1;  // a tile passed on and not begun
+    if (half == 0 && lane == 0 && !feed.none()) drawn = atomicInc(p.counters + kDrawCounter, wrap);
+    auto pass = [&]() {
+      const uint32_t s = passed % kRing;
+      if (!(ok = mbar_wait(p.watch, ring.empty + 8 * s, ((passed / kRing) & 1) ^ 1, 0x600u | s))) return;
+      const uint32_t d = __shfl_sync(0xffffffffu, drawn, 0);
+      ahead = d < (uint32_t)feed.rest ? cut.tiles + units + (int)d : total;
+      if (lane == 0) {
+        ring_pass(ring, s, ahead);
+        if (ahead < total) drawn = atomicInc(p.counters + kDrawCounter, wrap);
+      }
+      __syncwarp();
+      ++passed;
+    };
+    while (ok) {
+      if (!feed.own(w)) {
+        if (feed.none()) break;
+        int t = ahead;
+        if (half != 0) {
+          if (lane == 0) t = feed.read(p.watch, ring);
+          t = __shfl_sync(0xffffffffu, t, 0);
+          ++feed.n;
+        }
+        ahead = -1;
+        if (!feed.take(t, w)) break;
+      }
       const Tile tl = tile_at<GRAD, F8>(p, start, first, shape, w.tile, e);
       const int kb1 = GRAD ? tl.kblocks : min(w.kb1, tl.kblocks);
       const int n = columns<GRAD>(tl), mine = n / 2;  // this CTA's share of the rows operand
@@ -227,7 +262,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
         __syncwarp();
         if (++stage == kStages) stage = 0, phase ^= 1;
+        if (half == 0 && ahead < 0 && !feed.none()) {
+          pass();
+          if (!ok) break;
+        }
       }
+      if (ok && half == 0 && ahead < 0 && !feed.none()) pass();  // (a tile without K blocks)
     }
   } else if (warp == 1) {
     if (half == 0) {
@@ -236,7 +276,15 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       int e = 0;
       bool ok = true;
       Item w;
-      for (Walk walk(cut, unit, units, total); ok && walk.get(w); ++it) {
+      Feed feed(cut, unit, units, total);
+      for (; ok; ++it) {
+        if (!feed.own(w)) {
+          if (feed.none()) break;
+          int t = -1;
+          if (lane == 0) t = feed.read(p.watch, ring);
+          ++feed.n;
+          if (!feed.take(__shfl_sync(0xffffffffu, t, 0), w)) break;
+        }
         const Tile tl = tile_at<GRAD, F8>(p, start, first, shape, w.tile, e);
         const int kb1 = GRAD ? tl.kblocks : min(w.kb1, tl.kblocks);
         const uint32_t idesc = p.idesc | idesc_columns((uint32_t)columns<GRAD>(tl));
@@ -274,7 +322,18 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t it = 0;
     int e = 0;
     Item w;
-    for (Walk walk(cut, unit, units, total); walk.get(w); ++it) {
+    Feed feed(cut, unit, units, total);
+    for (;; ++it) {
+      if (!feed.own(w)) {
+        if (feed.none()) break;
+        // one thread reads for all the warps, which must agree
+        if (threadIdx.x == 64) s_next[feed.n & 1] = feed.read(p.watch, ring);
+        epilogue_sync();
+        const int t = s_next[feed.n & 1];
+        ++feed.n;
+        if (t < 0) settle();
+        if (!feed.take(t, w)) break;
+      }
       const Tile tl = tile_at<GRAD, F8>(p, start, first, shape, w.tile, e);
       const uint32_t buf = it & 1;
       const int f0 = tl.f0 + (int)half * kLanes + q * 32;  // this warp's first feature
@@ -468,7 +527,7 @@ extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, 
     if (int rc = encode_map(&p.q[b], A, (int)esz, 2, qd, qs, (kTileRows / 2) >> b)) return rc;
   p.ends = ends, p.experts = experts, p.T = (int)T, p.feats = (int)N, p.rows = 0, p.red = (int)K, p.out = D;
   p.sa = scale_a, p.sb = scale_b, p.sa_s = sa, p.sb_e = sb_e, p.sb_n = sb_n;
-  p.raster = raster_of(N);
+  p.raster = raster_of(N, kBand);
   p.idesc = idesc_of(format_of(b_type), format_of(a_type), b_n_major != 0, false);
   p.watch = watch_of(status);
   p.counters = static_cast<uint32_t*>(workspace);
@@ -488,7 +547,7 @@ extern "C" size_t dg_layer_grouped_grad_workspace(int experts, int64_t N, int64_
 
 extern "C" int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const void* A, int64_t ld_a,
                                             const int32_t* ends, int experts, void* dB, int d_type, int64_t T,
-                                            int64_t N, int64_t K, void* workspace, void* status, void* stream) {
+                                            int64_t N, int64_t K, void* workspace, void* products_workspace, void* status, void* stream) {
   if (int rc = check_sizes(T, N, K, experts)) return rc;
   if (d_type != DG_TYPE_BF16 && d_type != DG_TYPE_F32) return fail(DG_ERR_ARG, "dB is bf16 or fp32 (got type %d)", d_type);
   if (N % 8 || K % 8) return fail(DG_ERR_SHAPE, "N %% 8 and K %% 8 must be 0 (N %lld, K %lld)", (long long)N, (long long)K);
@@ -500,9 +559,9 @@ extern "C" int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const 
     DGL_CUDA(cudaMemsetAsync(dB, 0, (size_t)experts * N * K * (f32 ? 4 : 2), s));
     return DG_OK;
   }
-  if (!dD || !A || !ends || !workspace || !status) return fail(DG_ERR_ARG, "a required pointer is null");
-  if (!aligned16(dD) || !aligned16(A) || !aligned16(dB) || !aligned16(workspace) || ld_d % 8 || ld_a % 8)
-    return fail(DG_ERR_ARG, "dD, A, dB, their pitches and the workspace must be multiples of 16 bytes");
+  if (!dD || !A || !ends || !workspace || !products_workspace || !status) return fail(DG_ERR_ARG, "a required pointer is null");
+  if (!aligned16(dD) || !aligned16(A) || !aligned16(dB) || !aligned16(workspace) || !aligned16(products_workspace) || ld_d % 8 || ld_a % 8)
+    return fail(DG_ERR_ARG, "dD, A, dB, their pitches and the workspaces must be multiples of 16 bytes");
   if (ld_d < N || ld_a < K) return fail(DG_ERR_ARG, "a pitch is shorter than its rows");
   const int64_t tiles = (int64_t)experts * ((N + kTileRows - 1) / kTileRows) * ((K + kPairFeats - 1) / kPairFeats);
   if (tiles > INT32_MAX) return fail(DG_ERR_ARG, "experts x N x K is too large (%lld tiles)", (long long)tiles);
@@ -516,7 +575,8 @@ extern "C" int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const 
   if (int rc = encode_map(&p.p_tail, a_tail, 2, 3, ptd, pts, 64)) return rc;
   if (int rc = encode_map(&p.q_tail, d_tail, 2, 2, qtd, qts, 64)) return rc;
   p.ends = ends, p.experts = experts, p.T = (int)T, p.feats = (int)K, p.rows = (int)N, p.red = 0, p.out = dB;
-  p.raster = raster_of(K);
+  p.raster = raster_of(K, kBand);
+  p.counters = static_cast<uint32_t*>(products_workspace);
   p.idesc = idesc_of(1, 1, true, true);
   p.watch = watch_of(status);
   const int64_t vecs = 64 * (N + K) / 8;

@@ -33,6 +33,7 @@ constexpr uint32_t kStage = kStageP + kStageQ + kScaleP + kScaleQ;
 constexpr uint32_t kSmem = kStages * kStage + kEpiWarps * kStoreBuf + 256 + 1024;
 constexpr uint32_t kTmemCols = 512, kScaleCol = 2 * kTileRows;
 constexpr int kScaleBufs = 4;                    // 24 columns each: 2 x 4 for P, 2 x 8 for Q
+constexpr int kBand = 16;  // row tiles of a band (8: 3 % slower on 16384 x 13312 x 16384)
 constexpr int64_t kSlot = (int64_t)cut_slot_floats(kTileRows);
 
 struct Args {
@@ -292,7 +293,7 @@ extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, co
   if (int rc = encode_scale_map(&p.sq, a_scales, p.kblocks, (M + 127) / 128, 2)) return rc;
   p.rows = (int)M, p.feats = (int)N, p.out = D;
   p.row_tiles = (int)((M + kTileRows - 1) / kTileRows);
-  p.raster = raster_of(N);
+  p.raster = raster_of(N, kBand);
   p.counters = static_cast<uint32_t*>(workspace);
   p.partial = reinterpret_cast<float*>(p.counters + kCutCounters);
   p.watch = Watch{static_cast<unsigned long long*>(status), g_epoch.fetch_add(1, std::memory_order_relaxed), 4000000000ull};

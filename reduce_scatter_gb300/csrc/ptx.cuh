@@ -225,35 +225,34 @@ __device__ __forceinline__ uint32_t idesc_columns(uint32_t n) { return (n >> 3) 
 
 // ------------------------------------------------------------- order of tiles
 
-// Order of a matrix's tiles: bands of kBand row tiles swept feature tile by
-// feature tile, so that the tiles in flight share operands in L2.  The division
-// by a band's tiles is a multiplication (the decoding stands before the first
-// load of a tile, and a division took a third of a microsecond): m = floor(2^(31
-// + s) / d) + 1 with s = ceil(log2 d) gives exact quotients below 2^31, and 2^32
-// / w rounded up those by w <= 8 below 2^29.
-constexpr int kBand = 8;
+// Order of a matrix's tiles: bands of up to 16 row tiles swept feature tile by
+// feature tile, so that the tiles in flight share operands in L2.  The divisions
+// by a band's tiles and by its width are multiplications (the decoding stands
+// before the first load of a tile, and a division took a third of a
+// microsecond): m = floor(2^(31 + s) / d) + 1 with s = ceil(log2 d) gives exact
+// quotients below 2^31, and 2^32 / w rounded up those by w <= 16 below 2^28.
 struct Raster {
-  uint32_t mul, shift;
-  int nf;  // feature tiles
+  uint32_t mul, shift, width[17];
+  int nf, band;  // feature tiles, row tiles of a band
 };
-inline Raster raster_of(int64_t feats) {
+inline Raster raster_of(int64_t feats, int band) {
   Raster r;
   r.nf = (int)((feats + kPairFeats - 1) / kPairFeats);
-  const uint64_t d = (uint64_t)kBand * r.nf;
+  r.band = band;
+  const uint64_t d = (uint64_t)band * r.nf;
   uint32_t s = 0;
   while ((1ull << s) < d) ++s;
   r.mul = (uint32_t)((1ull << (31 + s)) / d + 1);
   r.shift = s - 1;
+  r.width[0] = r.width[1] = 0;
+  for (uint64_t w = 2; w <= 16; ++w) r.width[w] = (uint32_t)(((1ull << 32) + w - 1) / w);
   return r;
 }
 __device__ __forceinline__ void raster_at(const Raster& o, int tile, int row_tiles, int& row, int& feat) {
-  const int band = (int)(__umulhi((uint32_t)tile, o.mul) >> o.shift), in = tile - band * kBand * o.nf;
-  const int wide = min(kBand, row_tiles - band * kBand);
-  uint32_t m = 1u << 29;
-  m = wide == 7 ? 613566757u : m, m = wide == 6 ? 715827883u : m, m = wide == 5 ? 858993460u : m;
-  m = wide == 4 ? 1u << 30 : m, m = wide == 3 ? 1431655766u : m, m = wide == 2 ? 1u << 31 : m;
-  feat = wide == 1 ? in : (int)__umulhi((uint32_t)in, m);
-  row = band * kBand + in - feat * wide;
+  const int band = (int)(__umulhi((uint32_t)tile, o.mul) >> o.shift), in = tile - band * o.band * o.nf;
+  const int wide = min(o.band, row_tiles - band * o.band);
+  feat = wide == 1 ? in : (int)__umulhi((uint32_t)in, o.width[wide]);
+  row = band * o.band + in - feat * wide;
 }
 
 // The epilogue warps: warp w reads lane quarter w % 4, and of its tile's steps of
@@ -339,9 +338,69 @@ struct Walk {
   }
 };
 
+// The whole tiles of a ragged list, dealt out as pairs become free (their costs
+// differ: dealing them in turn left pairs idle for 4 to 7 % of the time).  Each
+// pair starts with its own shares and one tile of its own; further tiles (`rest`
+// of them; where there are none, nothing is drawn) come from a counter in the
+// workspace, which the even CTA's loading warp draws from ahead of its need and
+// passes on through a ring of slots in both CTAs' shared memory to the other
+// loading warp, the issuing warp and the epilogues.  Every pair draws until it
+// draws past the end, so the counter wraps back to 0 with the last draw of the
+// launch.
+constexpr int kRing = 4;
+constexpr int kRingReaders = 4;  // the issuing warp, the odd CTA's loading warp, two epilogues
+struct Ring {
+  uint32_t full, empty;  // barriers
+  volatile int* slot;    // [kRing]
+};
+// A tile into slot s of both CTAs' rings (by one thread of the even CTA): the
+// store itself completes the barrier's phase, so nothing waits for other stores.
+__device__ __forceinline__ void ring_pass(const Ring& r, uint32_t s, int tile) {
+  const uint32_t at = smem_u32((const void*)(r.slot + s));
+#pragma unroll
+  for (uint32_t c = 0; c < 2; ++c) {
+    const uint32_t bar = mapa(r.full + 8 * s, c);
+    asm volatile("mbarrier.arrive.expect_tx.shared::cluster.b64 _, [%0], %1;" ::"r"(bar), "r"(4) : "memory");
+    asm volatile("st.async.shared::cluster.mbarrier::complete_tx::bytes.u32 [%0], %1, [%2];" ::"r"(mapa(at, c)), "r"(tile),
+                 "r"(bar)
+                 : "memory");
+  }
+}
+struct Feed {
+  Walk walk;
+  bool first = true;  // the pair's own whole tile is still to come
+  int n = 0;          // tiles taken from the ring
+  int rest;           // tiles that are drawn
+  __device__ __forceinline__ Feed(const Cut& c, int unit, int units, int total)
+      : walk(c, unit, units, total), rest(max(0, total - c.tiles - units)) {}
+  // Shares and the first whole tile; false: the ring's turn, or (none) the end.
+  __device__ __forceinline__ bool own(Item& it) {
+    if (walk.pos < walk.end) return walk.get(it);
+    if (!first) return false;
+    first = false;
+    return walk.get(it);
+  }
+  __device__ __forceinline__ bool none() const { return rest == 0; }
+  __device__ __forceinline__ bool take(int tile, Item& it) {
+    it.tile = tile;
+    it.kb0 = 0;
+    it.kb1 = walk.kblocks;
+    return tile >= 0 && tile < walk.total;
+  }
+  // One thread's wait for the next tile of the ring: -1 if it gave up.
+  __device__ __forceinline__ int read(const Watch& w, const Ring& r) {
+    const uint32_t s = n % kRing;
+    if (!mbar_wait(w, r.full + 8 * s, (n / kRing) & 1, 0x500u | s)) return -1;
+    const int t = r.slot[s];
+    if (t >= 0) mbar_arrive_cluster(mapa(r.empty + 8 * s, 0));  // (always: the branch has the read complete before it)
+    return t;
+  }
+};
+
 // Workspace of the cut tiles: a counter for each (tile, half), which wraps back
 // to 0 with its last pair, then slots of [half][column][lane].
-constexpr int kCutCounters = 2 * 256;
+constexpr int kCutCounters = 2 * 256;  // the last one is the tiles' counter
+constexpr int kDrawCounter = kCutCounters - 1;
 __host__ __device__ constexpr size_t cut_slot_floats(int columns) { return (size_t)2 * columns * kLanes; }
 __host__ __device__ constexpr size_t cut_bytes(int units, int columns) {
   return kCutCounters * 4 + (size_t)2 * units * cut_slot_floats(columns) * 4;

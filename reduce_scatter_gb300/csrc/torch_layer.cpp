@@ -347,7 +347,8 @@ Tensor weight_grad(const Tensor& rows_, const Tensor& feats_, const Tensor& ends
   const Tensor ws = at::empty({(int64_t)dg_layer_grouped_grad_workspace((int)E, N, K)}, rows.options().dtype(at::kByte));
   check_status(dg_layer_grouped_weight_grad(rows.data_ptr(), rows.stride(0), feats.data_ptr(), feats.stride(0),
                                             static_cast<const int32_t*>(ends.data_ptr()), (int)E, out.data_ptr(),
-                                            DG_TYPE_BF16, T, N, K, ws.data_ptr(), status_word(at, rows), at.handle()));
+                                            DG_TYPE_BF16, T, N, K, ws.data_ptr(), products_workspace(at, rows).data_ptr(),
+                                            status_word(at, rows), at.handle()));
   return out;
 }
 
@@ -463,7 +464,13 @@ PyObject* check(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* word = status_word(at, like);
     int rc;
     Py_BEGIN_ALLOW_THREADS rc = dg_layer_check(word, at.handle());
-    Py_END_ALLOW_THREADS check_status(rc);
+    Py_END_ALLOW_THREADS if (rc != DG_OK) {
+      // a product that gave up leaves its counters as they were
+      State& st = state();
+      std::lock_guard<std::mutex> lk(st.mu);
+      st.workspace.clear();
+    }
+    check_status(rc);
     Py_RETURN_NONE;
   });
 }

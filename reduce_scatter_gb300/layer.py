@@ -54,7 +54,7 @@ def lib():
             "grouped_matmul": (i32, [vp, i64, i32, vp, i64, i64, i32, i32, vp, i32, vp, i64, vp, i64, i64, vp, i32,
                                      i64, i64, i64, vp, vp, vp]),
             "grouped_grad_workspace": (sz, [i32, i64, i64]),
-            "grouped_weight_grad": (i32, [vp, i64, vp, i64, vp, i32, vp, i32, i64, i64, i64, vp, vp, vp]),
+            "grouped_weight_grad": (i32, [vp, i64, vp, i64, vp, i32, vp, i32, i64, i64, i64, vp, vp, vp, vp]),
             "mx4_scale_bytes": (sz, [i64, i64]),
             "mx4_quantize": (i32, [vp, i64, i32, vp, vp, i64, i64, vp]),
             "mx4_dequantize": (i32, [vp, vp, vp, i32, i64, i64, vp]),

@@ -82,7 +82,7 @@ def test_grouped_of_nothing(L):
 def test_weight_grad_refuses(L, kw, code):
     v = dict(a=16, ld=64, e=2, d=16, dt=0, t=4, n=64, k=64, ws=256) | kw
     assert L.dg_layer_grouped_weight_grad(16, 64, v["a"], v["ld"], 16, v["e"], v["d"], v["dt"], v["t"], v["n"], v["k"],
-                                          v["ws"], 16, None) == code
+                                          v["ws"], 256, 16, None) == code
 
 
 def test_mx4_refuses(L):

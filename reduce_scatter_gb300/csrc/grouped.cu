@@ -47,6 +47,7 @@ struct Args {
   int64_t sa_s, sb_e, sb_n;
   uint32_t idesc;
   Raster raster;
+  Divider per_unit;        // by the pairs of the launch
   uint32_t* counters;      // cut tiles
   float* partial;
   Watch watch;
@@ -177,10 +178,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   constexpr int kb_red = F8 ? 128 : 64;
   Cut cut{0, 1, 0};
   if (!GRAD) {
-    // rows of a tile on average (in fp32: a division of 64 bits would stand before the first load)
-    const float rows = (float)start[p.experts] * (float)p.raster.nf / (float)max(real, 1);
-    cut = cut_of(real, units, (p.red + kb_red - 1) / kb_red, (int)rows);
+    cut = cut_of(real, units, p.per_unit, (p.red + kb_red - 1) / kb_red,
+                 (float)start[p.experts] * (float)p.raster.nf / (float)max(real, 1));
   }
+  const bool draw = (GRAD ? p.T / kTailRows / p.experts : (p.red + kb_red - 1) / kb_red) >= kDrawBlocks;
   const uint32_t base = smem_u32(smem);
 
   if (warp == 0) {
@@ -189,7 +190,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     int e = 0;
     bool ok = true;
     Item w;
-    Feed feed(cut, unit, units, total);
+    Feed feed(cut, unit, units, total, draw);
     // the even CTA: lane 0 holds the next draw; the tile after the one being loaded is passed on once its loads have begun
     const uint32_t wrap = (uint32_t)(feed.rest + units - 1);
     uint32_t drawn = 0, passed = 0;
@@ -276,7 +277,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       int e = 0;
       bool ok = true;
       Item w;
-      Feed feed(cut, unit, units, total);
+      Feed feed(cut, unit, units, total, draw);
       for (; ok; ++it) {
         if (!feed.own(w)) {
           if (feed.none()) break;
@@ -322,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     uint32_t it = 0;
     int e = 0;
     Item w;
-    Feed feed(cut, unit, units, total);
+    Feed feed(cut, unit, units, total, draw);
     for (;; ++it) {
       if (!feed.own(w)) {
         if (feed.none()) break;
@@ -462,13 +463,14 @@ __global__ void __launch_bounds__(256) grouped_tail_kernel(const int32_t* ends, 
 std::atomic<uint32_t> g_epoch{1};
 
 template <bool F8, bool PMN, bool GRAD, bool OUT32>
-int run(const Args& p, int64_t most_tiles, cudaStream_t s) {
+int run(Args& p, int64_t most_tiles, cudaStream_t s) {
   auto* kernel = grouped_kernel<F8, PMN, GRAD, OUT32>;
   int sms = 0;
   if (int rc = sm_count(&sms)) return rc;
   DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
   // the forward's tiles may be cut along K, so it takes every SM pair
   const int64_t units = GRAD && most_tiles < sms / 2 ? most_tiles : sms / 2;
+  p.per_unit = divider_of(units > 1 ? units : 2);  // (a single pair has the gradient's one tile, and divides nothing)
   return dgl::launch(kernel, dim3((unsigned)(2 * units)), dim3(kThreads), kSmem, s, p);
 }
 

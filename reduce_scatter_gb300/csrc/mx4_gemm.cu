@@ -41,6 +41,7 @@ struct Args {
   CUtensorMap sp, sq;      // scales: (256 words, K block, row tile), boxes of one and two row tiles
   int rows, feats, kblocks, row_tiles;
   Raster raster;
+  Divider per_unit;        // by the pairs of the launch
   void* out;
   uint32_t* counters;      // cut tiles
   float* partial;
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   fence_after();
   const uint32_t tmem = *s_tmem, base = smem_u32(smem);
   const int total = p.row_tiles * p.raster.nf;
-  const Cut cut = cut_of(total, units, p.kblocks, min(p.rows, kTileRows));
+  const Cut cut = cut_of(total, units, p.per_unit, p.kblocks, (float)min(p.rows, kTileRows));
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0;
@@ -254,10 +255,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
 std::atomic<uint32_t> g_epoch{0x80000001u};
 
 template <bool OUT32>
-int run(const Args& p, cudaStream_t s) {
+int run(Args& p, cudaStream_t s) {
   int sms = 0;
   if (int rc = sm_count(&sms)) return rc;
   DGL_CUDA(cudaFuncSetAttribute(mx4_kernel<OUT32>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
+  p.per_unit = divider_of((uint64_t)(sms / 2));
   return dgl::launch(mx4_kernel<OUT32>, dim3((unsigned)(sms / 2 * 2)), dim3(kThreads), kSmem, s, p);
 }
 

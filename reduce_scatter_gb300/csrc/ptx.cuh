@@ -231,25 +231,31 @@ __device__ __forceinline__ uint32_t idesc_columns(uint32_t n) { return (n >> 3) 
 // before the first load of a tile, and a division took a third of a
 // microsecond): m = floor(2^(31 + s) / d) + 1 with s = ceil(log2 d) gives exact
 // quotients below 2^31, and 2^32 / w rounded up those by w <= 16 below 2^28.
+struct Divider {  // by 2 <= d < 2^31
+  uint32_t mul, shift;
+  __device__ __forceinline__ int of(int n) const { return (int)(__umulhi((uint32_t)n, mul) >> shift); }
+};
+inline Divider divider_of(uint64_t d) {
+  uint32_t s = 0;
+  while ((1ull << s) < d) ++s;
+  return Divider{(uint32_t)((1ull << (31 + s)) / d + 1), s - 1};
+}
 struct Raster {
-  uint32_t mul, shift, width[17];
+  Divider per_band;
+  uint32_t width[17];
   int nf, band;  // feature tiles, row tiles of a band
 };
 inline Raster raster_of(int64_t feats, int band) {
   Raster r;
   r.nf = (int)((feats + kPairFeats - 1) / kPairFeats);
   r.band = band;
-  const uint64_t d = (uint64_t)band * r.nf;
-  uint32_t s = 0;
-  while ((1ull << s) < d) ++s;
-  r.mul = (uint32_t)((1ull << (31 + s)) / d + 1);
-  r.shift = s - 1;
+  r.per_band = divider_of((uint64_t)band * r.nf);
   r.width[0] = r.width[1] = 0;
   for (uint64_t w = 2; w <= 16; ++w) r.width[w] = (uint32_t)(((1ull << 32) + w - 1) / w);
   return r;
 }
 __device__ __forceinline__ void raster_at(const Raster& o, int tile, int row_tiles, int& row, int& feat) {
-  const int band = (int)(__umulhi((uint32_t)tile, o.mul) >> o.shift), in = tile - band * o.band * o.nf;
+  const int band = o.per_band.of(tile), in = tile - band * o.band * o.nf;
   const int wide = min(o.band, row_tiles - band * o.band);
   feat = wide == 1 ? in : (int)__umulhi((uint32_t)in, o.width[wide]);
   row = band * o.band + in - feat * wide;
@@ -295,14 +301,17 @@ struct Cut {
 // for up to 64 rows and 2.2 us for each further step of 32 rows and three
 // partials (measured), a K block 0.2 us: so cutting pays for short tiles, as of
 // a decoding step, and for tall ones with a long K and few of them.
-__device__ __forceinline__ Cut cut_of(int total, int units, int kblocks, int rows) {
-  Cut c{total % units, kblocks, 0};
+// `per_unit`: division by the pairs.
+constexpr int kShortCost = 15;  // K blocks
+__device__ __forceinline__ Cut cut_of(int total, int units, const Divider& per_unit, int kblocks, float rows) {
   // (a K so long that the products below would pass 32 bits is left whole)
-  if (c.tiles == 0 || kblocks > (1 << 20)) return Cut{0, kblocks, 0};
-  c.share = max(kMinShare, (c.tiles * kblocks + units - 1) / units);
-  const int ways = kblocks / c.share + 1, steps = (rows + kChunk - 1) / kChunk;
-  const int cost = steps <= 2 ? 15 : 11 * steps * ((ways + 2) / kJoin + 1) / 2;
-  return kblocks - c.share > cost ? c : Cut{0, kblocks, 0};
+  if (kblocks <= kMinShare + kShortCost || kblocks > (1 << 20)) return Cut{0, kblocks, 0};
+  Cut c{total - per_unit.of(total) * units, kblocks, 0};
+  if (c.tiles == 0) return Cut{0, kblocks, 0};
+  c.share = max(kMinShare, per_unit.of(c.tiles * kblocks + units - 1));
+  const float ways = (float)kblocks / (float)c.share + 1.f, steps = rows * (1.f / kChunk);
+  const float cost = steps <= 2.f ? (float)kShortCost : 11.f * steps * ((ways + 2.f) * (1.f / kJoin) + 1.f) * 0.5f;
+  return (float)(kblocks - c.share) > cost ? c : Cut{0, kblocks, 0};
 }
 // How many pairs share tile t of the cut ones, the first of them, and the
 // workspace slot of the j-th pair's partial.
@@ -347,6 +356,7 @@ struct Walk {
 // loading warp, the issuing warp and the epilogues.  Every pair draws until it
 // draws past the end, so the counter wraps back to 0 with the last draw of the
 // launch.
+constexpr int kDrawBlocks = 16;  // K blocks of a tile (on average) from which on drawing pays: it costs 0.3 us a tile
 constexpr int kRing = 4;
 constexpr int kRingReaders = 4;  // the issuing warp, the odd CTA's loading warp, two epilogues
 struct Ring {
@@ -371,11 +381,13 @@ struct Feed {
   bool first = true;  // the pair's own whole tile is still to come
   int n = 0;          // tiles taken from the ring
   int rest;           // tiles that are drawn
-  __device__ __forceinline__ Feed(const Cut& c, int unit, int units, int total)
-      : walk(c, unit, units, total), rest(max(0, total - c.tiles - units)) {}
-  // Shares and the first whole tile; false: the ring's turn, or (none) the end.
+  bool draw;
+  __device__ __forceinline__ Feed(const Cut& c, int unit, int units, int total, bool draw_)
+      : walk(c, unit, units, total), rest(draw_ ? max(0, total - c.tiles - units) : 0), draw(draw_) {}
+  // Shares and the first whole tile (every one in turn, where none are drawn);
+  // false: the ring's turn, or (none) the end.
   __device__ __forceinline__ bool own(Item& it) {
-    if (walk.pos < walk.end) return walk.get(it);
+    if (!draw || walk.pos < walk.end) return walk.get(it);
     if (!first) return false;
     first = false;
     return walk.get(it);

@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     if (half == 0 && lane == 0 && !feed.none()) drawn = atomicInc(p.counters + kDrawCounter, wrap);
     auto pass = [&]() {
       const uint32_t s = passed % kRing;
-      if (!(ok = mbar_wait(p.watch, ring.empty + 8 * s, ((passed / kRing) & 1) ^ 1, 0x600u | s))) return;
+      if (!(ok = mbar_wait_warp(p.watch, ring.empty + 8 * s, ((passed / kRing) & 1) ^ 1, 0x600u | s))) return;
       const uint32_t d = __shfl_sync(0xffffffffu, drawn, 0);
       ahead = d < (uint32_t)feed.rest ? cut.tiles + units + (int)d : total;
       if (lane == 0) {
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       const int n = columns<GRAD>(tl), mine = n / 2;  // this CTA's share of the rows operand
       const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
       for (int kb = w.kb0; kb < kb1; ++kb) {
-        if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
+        if (!(ok = mbar_wait_warp(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
         const uint32_t fb = mapa(full + 8 * stage, 0);
         const uint32_t sp = base + stage * kStage, sq = sp + kStageP;
         if (elect_one()) {
@@ -290,11 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         const int kb1 = GRAD ? tl.kblocks : min(w.kb1, tl.kblocks);
         const uint32_t idesc = p.idesc | idesc_columns((uint32_t)columns<GRAD>(tl));
         const uint32_t buf = it & 1;
-        if (!(ok = mbar_wait(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
+        if (!(ok = mbar_wait_warp(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
         fence_after();
         const uint32_t d = tmem + buf * kTileRows;
         for (int kb = w.kb0; kb < kb1; ++kb) {
-          if (!(ok = mbar_wait(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
+          if (!(ok = mbar_wait_warp(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
           fence_after();
           const uint32_t sp = base + stage * kStage, sq = sp + kStageP;
           const uint64_t pd = PMN ? desc_mn_major(sp, kStageP / 2) : desc_k_major(sp);

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
       const int n = (tl.rows + 31) / 32 * 32, mine = n / 2;
       const int f = tl.f0 + (int)half * kLanes, q0 = tl.row0 + (int)half * mine;
       for (int kb = w.kb0; kb < w.kb1; ++kb) {
-        if (!(ok = mbar_wait(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
+        if (!(ok = mbar_wait_warp(p.watch, empty + 8 * stage, phase ^ 1, 0x100u | stage))) break;
         const uint32_t fb = mapa(full + 8 * stage, 0);
         const uint32_t sp = base + stage * kStage, sq = sp + kStageP, ss = sq + kStageQ;
         if (elect_one()) {
@@ -150,12 +150,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
         const Tile tl = tile_at(p, w.tile);
         const uint32_t n = (uint32_t)(tl.rows + 31) / 32 * 32, buf = it & 1;
         const uint32_t odd = (tl.row0 & 64) ? 2u : 0u;  // columns into the first scale tile
-        if (!(ok = mbar_wait(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
+        if (!(ok = mbar_wait_warp(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
         fence_after();
         const uint32_t d = tmem + buf * kTileRows;
         const uint32_t idesc0 = idesc_mx4(n, 0), idesc2 = idesc_mx4(n, 2);
         for (int kb = w.kb0; kb < w.kb1; ++kb) {
-          if (!(ok = mbar_wait(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
+          if (!(ok = mbar_wait_warp(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
           fence_after();
           const uint32_t sp = base + stage * kStage, sq = sp + kStageP, ss = sq + kStageQ;
           const uint32_t tp = tmem + kScaleCol + sbuf * 24, tq = tp + 8;

@@ -122,6 +122,13 @@ __device__ __forceinline__ bool mbar_wait(const Watch& w, uint32_t bar, uint32_t
   if (mbar_try(bar, parity)) return true;
   return mbar_wait_slow(w, bar, parity, what);
 }
+// The same by a whole warp, which agrees on the outcome: a lane that gave up must
+// not leave the others at the next warp-wide instruction.
+__device__ __forceinline__ bool mbar_wait_warp(const Watch& w, uint32_t bar, uint32_t parity, uint32_t what) {
+  bool ok = mbar_try(bar, parity);
+  if (__any_sync(0xffffffffu, !ok)) ok = __all_sync(0xffffffffu, ok || mbar_wait_slow(w, bar, parity, what)) != 0;
+  return ok;
+}
 // Before a launch that gave up ends, its copies and MMAs in flight land.
 static __device__ __noinline__ void settle() {
   const uint64_t t0 = globaltimer();

@@ -24,6 +24,7 @@ import threading
 from typing import NamedTuple
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import dg
 
@@ -124,6 +125,7 @@ class _AddRMSNorm(torch.autograd.Function):
         return (y, h, rstd) if ctx.has_residual else (y, rstd)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dy, *rest):
         h, weight, rstd = ctx.saved_tensors
         dh = rest[0] if ctx.has_residual else None
@@ -175,6 +177,7 @@ class _GroupedMatmul(torch.autograd.Function):
         return (_EXT or _load()).grouped_matmul(A, B, ends, None, None, out_dtype)
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, dD):
         A, B, ends = ctx.saved_tensors
         dA, dB = grouped_matmul_backward(dD.to(torch.bfloat16), A, B, ends, need=ctx.needs_input_grad[:2])

@@ -219,6 +219,36 @@ def test_many_experts_and_empty_problems():
     ops.check_products()
 
 
+def test_check_reports_and_clears_a_wait_that_ran_out():
+    # the word as a kernel would leave it (launch 5 gave up wait 0x101)
+    from reduce_scatter_gb300 import layer
+
+    word = torch.tensor([(5 << 32) | 0x101], dtype=torch.int64, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    assert layer.lib().dg_layer_check(word.data_ptr(), stream) == dg.ERR_HANG
+    assert b"0x101" in layer.lib().dg_layer_last_error()
+    assert layer.lib().dg_layer_check(word.data_ptr(), stream) == dg.OK
+    assert layer.lib().dg_layer_check(None, stream) == dg.ERR_ARG
+
+
+def test_same_bits_every_time_and_side_by_side():
+    # tiles are drawn in any order and cut tiles are joined by whichever pair comes last
+    cases = [(1000, 1024, 768, [3, 260, 261, 900, 1000]), (20, 8192, 512, [7, 20]), (5000, 1024, 1024, [900, 1800, 5000])]
+    made = [(rand((T, K), 34), rand((len(e), N, K), 35).transpose(1, 2), ends_of(e), rand((T, N), 36)) for T, K, N, e in cases]
+    want = [(ops.grouped_matmul(a, b, e), *ops.grouped_matmul_backward(d, a, b, e)) for a, b, e, d in made]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    got = []
+    for turn in range(4):
+        for k, (a, b, e, d) in enumerate(made):
+            with torch.cuda.stream(streams[(turn + k) % 3]):
+                got.append((k, ops.grouped_matmul(a, b, e), *ops.grouped_matmul_backward(d, a, b, e)))
+    torch.cuda.synchronize()
+    for k, *r in got:
+        assert all(torch.equal(x, y) for x, y in zip(r, want[k])), k
+    ops.check_products()
+
+
 def test_refusals():
     a, b, e = rand((8, 64), 30), rand((2, 32, 64), 31).transpose(1, 2), ends_of([4, 8])
     with pytest.raises(TypeError):

@@ -144,6 +144,23 @@ def test_nan_blocks_and_empty():
     assert ops.mx4_matmul(ops.quantize_mx4(a[:0]), ops.quantize_mx4(b)).shape == (0, 16)
 
 
+def test_cut_tiles_same_bits():
+    # a long K over few tiles is cut among the SM pairs and joined in the order of K
+    a, w = ops.quantize_mx4(rand((3, 16384), 18)), ops.quantize_mx4(rand((520, 16384), 19))
+    want = ops.mx4_matmul(a, w, out_dtype=F32)
+    v, m = lc.product(ops.dequantize_mx4(a, out_dtype=F32), ops.dequantize_mx4(w, out_dtype=F32))
+    assert_within(want, v, lc.product_bound(v, m, 16384, False), "D")
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    torch.cuda.synchronize()
+    got = []
+    for turn in range(12):
+        with torch.cuda.stream(streams[turn % 3]):
+            got.append(ops.mx4_matmul(a, w, out_dtype=F32))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, want) for g in got)
+    ops.check_products()
+
+
 def test_graph_and_stream():
     a, w = rand((50, 512), 16), ops.quantize_mx4(rand((264, 512), 17))
     want = ops.mx4_matmul(ops.quantize_mx4(a), w)

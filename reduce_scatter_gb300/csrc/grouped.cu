@@ -48,6 +48,7 @@ struct Args {
   uint32_t idesc;
   Raster raster;
   Divider per_unit;        // by the pairs of the launch
+  int may_be_few;          // tiles of 256 rows may leave more than half of the pairs idle
   uint32_t* counters;      // cut tiles
   float* partial;
   Watch watch;
@@ -57,11 +58,20 @@ struct Tile {
   int e, row0, rows, f0, kblocks, k0, tail;
 };
 
-// Rows of a group's tiles: as few tiles as 256 rows allow, of equal height (a
+// Rows of a group's tiles: as few tiles as `most` rows allow, of equal height (a
 // multiple of 32), because a short tile still loads all of its features.
-__device__ __forceinline__ int tile_height(int rows) {
-  const int nt = (rows + kTileRows - 1) / kTileRows;
-  return nt > 1 ? ((rows + nt - 1) / nt + 31) / 32 * 32 : kTileRows;
+__device__ __forceinline__ int tile_height(int rows, int nt, int most) {
+  return nt > 1 ? ((rows + nt - 1) / nt + 31) / 32 * 32 : most;
+}
+
+// The most rows of a tile: 256, or as few (a multiple of 32) as still give every
+// tile a pair of its own where tiles of 256 would leave more than half of the
+// pairs idle.  (A K block of a tile takes about 256 + rows cycles, its loads', so
+// short tiles on more pairs end sooner, but cost more in all.)
+__device__ __forceinline__ int most_rows(int tiles, int units) {
+  if (2 * tiles > units || tiles == 0) return kTileRows;
+  const int share = (int)(__fdividef((float)units, (float)tiles) + 0.01f);
+  return max(32, ((int)__fdividef((float)kTileRows, (float)share) + 31) / 32 * 32);
 }
 
 // Group starts (start[e], e <= experts; start[experts + 1] = T), the number of
@@ -71,20 +81,37 @@ __device__ __forceinline__ int tile_height(int rows) {
 template <bool GRAD>
 __device__ void scan_groups(const Args& p, int* start, int* first, uint32_t* shape, int lane) {
   const int groups = GRAD ? p.experts : p.experts + 1;
-  int end = 0, tiles = 0;
-  if (lane == 0) start[0] = first[0] = 0;
-  for (int b = 0; b < groups; b += 32) {
+  int v = 0, s = 0;  // end and start of group b + lane
+  auto chunk = [&](int b, int before) {
     const int e = b + lane;
-    int v = e < p.experts ? min(max(__ldg(p.ends + e), 0), p.T) : p.T;
-    if (lane == 0) v = max(v, end);
+    v = e < p.experts ? min(max(__ldg(p.ends + e), 0), p.T) : p.T;
+    if (lane == 0) v = max(v, before);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v = max(v, u);
     }
-    int s = __shfl_up_sync(0xffffffffu, v, 1);
-    if (lane == 0) s = end;
-    const int rows = GRAD ? p.rows : v - s, nt = (rows + kTileRows - 1) / kTileRows;
+    s = __shfl_up_sync(0xffffffffu, v, 1);
+    if (lane == 0) s = before;
+  };
+  int most = kTileRows;
+  if (!GRAD && p.may_be_few) {
+    int count = 0, before = 0;
+    for (int b = 0; b < groups; b += 32) {
+      chunk(b, before);
+      const int rows = b + lane < p.experts ? v - s : 0;
+      count += __reduce_add_sync(0xffffffffu, (unsigned)((rows + kTileRows - 1) / kTileRows));
+      before = __shfl_sync(0xffffffffu, v, 31);
+    }
+    const int units = gridDim.x >> 1;
+    most = most_rows(min(count, units) * min(p.raster.nf, units), units);
+  }
+  int end = 0, tiles = 0;
+  if (lane == 0) start[0] = first[0] = 0;
+  for (int b = 0; b < groups; b += 32) {
+    const int e = b + lane;
+    if (!p.may_be_few || groups > 32) chunk(b, end);  // (else the one chunk is still there)
+    const int rows = GRAD ? p.rows : v - s, nt = (rows + most - 1) / most;
     int t = e < groups ? nt * p.raster.nf : 0;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -93,7 +120,8 @@ __device__ void scan_groups(const Args& p, int* start, int* first, uint32_t* sha
     }
     t += tiles;
     if (e < groups)
-      start[e + 1] = v, first[e + 1] = t, shape[e] = (uint32_t)nt << 9 | (uint32_t)(GRAD ? kTileRows : tile_height(rows));
+      start[e + 1] = v, first[e + 1] = t,
+      shape[e] = (uint32_t)nt << 9 | (uint32_t)(GRAD ? kTileRows : tile_height(rows, nt, most));
     end = __shfl_sync(0xffffffffu, v, 31);
     tiles = __shfl_sync(0xffffffffu, t, 31);
   }
@@ -179,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   Cut cut{0, 1, 0};
   if (!GRAD) {
     cut = cut_of(real, units, p.per_unit, (p.red + kb_red - 1) / kb_red,
-                 (float)start[p.experts] * (float)p.raster.nf / (float)max(real, 1));
+                 (float)start[p.experts] * (float)p.raster.nf);
   }
   const bool draw = (GRAD ? p.T / kTailRows / p.experts : (p.red + kb_red - 1) / kb_red) >= kDrawBlocks;
   const uint32_t base = smem_u32(smem);
@@ -470,6 +498,10 @@ int run(Args& p, int64_t most_tiles, cudaStream_t s) {
   DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem));
   // the forward's tiles may be cut along K, so it takes every SM pair
   const int64_t units = GRAD && most_tiles < sms / 2 ? most_tiles : sms / 2;
+  if (!GRAD) {  // whatever the groups are
+    const int64_t bytes = (int64_t)(p.T < p.experts ? p.T : p.experts) * p.feats * p.red * (F8 ? 1 : 2);
+    p.may_be_few = p.T > 32 && 2 * (int64_t)p.raster.nf * ((p.T + kTileRows - 1) / kTileRows) <= units && bytes <= kSharedBytes;
+  }
   p.per_unit = divider_of(units > 1 ? units : 2);  // (a single pair has the gradient's one tile, and divides nothing)
   return dgl::launch(kernel, dim3((unsigned)(2 * units)), dim3(kThreads), kSmem, s, p);
 }

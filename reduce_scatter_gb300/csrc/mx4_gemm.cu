@@ -40,6 +40,7 @@ struct Args {
   CUtensorMap p, q[4];     // codes as bytes: boxes of 128 rows; of 96, 64, 32 and 16 rows
   CUtensorMap sp, sq;      // scales: (256 words, K block, row tile), boxes of one and two row tiles
   int rows, feats, kblocks, row_tiles;
+  int high;                // rows of a tile: 192, or 64
   Raster raster;
   Divider per_unit;        // by the pairs of the launch
   void* out;
@@ -76,7 +77,7 @@ struct Tile {
 __device__ __forceinline__ Tile tile_at(const Args& p, int t) {
   int r, f;
   raster_at(p.raster, t, p.row_tiles, r, f);
-  return Tile{r * kTileRows, min(kTileRows, p.rows - r * kTileRows), f * kPairFeats};
+  return Tile{r * p.high, min(p.high, p.rows - r * p.high), f * kPairFeats};
 }
 
 template <bool OUT32>
@@ -109,7 +110,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   fence_after();
   const uint32_t tmem = *s_tmem, base = smem_u32(smem);
   const int total = p.row_tiles * p.raster.nf;
-  const Cut cut = cut_of(total, units, p.per_unit, p.kblocks, (float)min(p.rows, kTileRows));
+  const Cut cut = cut_of(total, units, p.per_unit, p.kblocks, (float)p.rows * (float)p.raster.nf);
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0;
@@ -294,7 +295,13 @@ extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, co
   if (int rc = encode_scale_map(&p.sp, b_scales, p.kblocks, (N + 127) / 128, 1)) return rc;
   if (int rc = encode_scale_map(&p.sq, a_scales, p.kblocks, (M + 127) / 128, 2)) return rc;
   p.rows = (int)M, p.feats = (int)N, p.out = D;
-  p.row_tiles = (int)((M + kTileRows - 1) / kTileRows);
+  // more and shorter tiles end sooner where each still has a pair of its own (64
+  // rows: a multiple of that, for the scales' columns); 2048 x 28672 with 200 rows
+  // 29 -> 20 us
+  int sms = 0;
+  if (int rc = sm_count(&sms)) return rc;
+  p.high = (M + 63) / 64 * ((N + kPairFeats - 1) / kPairFeats) > sms / 2 || N * K / 2 > kSharedBytes ? kTileRows : 64;
+  p.row_tiles = (int)((M + p.high - 1) / p.high);
   p.raster = raster_of(N, kBand);
   p.counters = static_cast<uint32_t*>(workspace);
   p.partial = reinterpret_cast<float*>(p.counters + kCutCounters);

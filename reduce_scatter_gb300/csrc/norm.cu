@@ -148,9 +148,27 @@ struct NormArgs {
   int weight_f32, fp8;  // fp8: 0 bf16 output, else the dg_type
 };
 
-__device__ __forceinline__ float row_scale(float amax, bool e5m2) {
-  return amax > 0.f ? fmaxf(amax / (e5m2 ? kE5M2Max : kE4M3Max), kMinScale) : 1.f;
+// The scale c of a row of 8-bit values, and what turns t = h w into the value
+// q = t rstd / c that is rounded.  `top`: the largest finite |t|.  With the row's
+// own scale c = top rstd / max, so rstd cancels: q = t max / top, where t is
+// exact for bf16 h and w, so q carries two roundings only and hardly ever
+// crosses a rounding boundary of the 8 bits that the exact value does not.
+struct RowScale {
+  float c, mul;
+};
+__device__ __forceinline__ RowScale row_scale(float top, float rstd, const float* given, bool e5m2) {
+  if (given) {
+    const float c = __ldg(given);
+    return RowScale{c, rstd / c};
+  }
+  const float most = e5m2 ? kE5M2Max : kE4M3Max, y = top * rstd, c = y / most;
+  if (!(y > 0.f)) return RowScale{1.f, rstd};  // a row of zeros (or one that is not finite, whose values stay so)
+  return c > kMinScale ? RowScale{c, most / top} : RowScale{kMinScale, rstd / kMinScale};
 }
+// t for one value: with rstd 0 (a sum of squares beyond fp32) a finite value
+// becomes 0 before the product can overflow.
+__device__ __forceinline__ float scaled_by(float h, float keep, float w) { return h * keep * w; }
+__device__ __forceinline__ float finite_mag(float t) { return isinf(t) ? 0.f : fabsf(t); }
 
 // RT: the residual's type (0 none, 1 bf16, 2 fp32).  The row stays in
 // registers: NV vectors of 8 values per thread.
@@ -200,7 +218,8 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) add_rms_norm_kernel(const
   ss = row_reduce<Add>(ss, part);
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-  float amax = 0.f;
+  float top = 0.f;
+  const float f = !OUT8 ? rstd : rstd > 0.f ? 1.f : 0.f;
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = threadIdx.x * 8 + k * step;
@@ -209,31 +228,23 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) add_rms_norm_kernel(const
       load_any<8>(p.weight_f32 != 0, p.weight, i, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        h[k][j] = h[k][j] * rstd * w[j];
-        // an infinity (only of a weight, or of a sum of squares below the
-        // smallest normal value) saturates and stays out of the scale
-        if constexpr (OUT8) amax = fmaxf(amax, isinf(h[k][j]) ? 0.f : fabsf(h[k][j]));
+        h[k][j] = scaled_by(h[k][j], f, w[j]);
+        if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k][j]));
       }
       if constexpr (!OUT8) store_bf16<8>(p.y, row * p.hidden + i, h[k]);
     }
   }
   if constexpr (OUT8) {
     const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
-    float c;
-    if (p.scale_in) {
-      c = __ldg(p.scale_in);
-    } else {
-      amax = row_reduce<Max>(amax, part + 33);
-      c = row_scale(amax, e5m2);
-      if (threadIdx.x == 0) p.scale[row] = c;
-    }
-    const float inv = 1.f / c;
+    if (!p.scale_in) top = row_reduce<Max>(top, part + 33);
+    const RowScale sc = row_scale(top, rstd, p.scale_in, e5m2);
+    if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = threadIdx.x * 8 + k * step;
       if (i < p.hidden) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[k][j] *= inv;
+        for (int j = 0; j < 8; ++j) h[k][j] *= sc.mul;
         store_fp8<8>(p.y, row * p.hidden + i, h[k], e5m2 ? __NV_E5M2 : __NV_E4M3);
       }
     }
@@ -266,7 +277,7 @@ struct Spread {
 };
 
 template <int RT, bool W32, int N, bool OUT8>
-__global__ void __launch_bounds__(N > 4 ? 512 : 1024) add_rms_norm_spread_kernel(const __grid_constant__ NormArgs p) {
+__global__ void __launch_bounds__(1024) add_rms_norm_spread_kernel(const __grid_constant__ NormArgs p) {
   __shared__ float part[66];
   begin_kernel();
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
@@ -276,7 +287,6 @@ __global__ void __launch_bounds__(N > 4 ? 512 : 1024) add_rms_norm_spread_kernel
   Spread<W32, N> w;
   x.load(p.x, row * p.ld_x, p.hidden);
   if constexpr (RT != 0) r.load(p.residual, row * p.ld_residual, p.hidden);
-  w.load(p.weight, 0, p.hidden);
   float h[N], ss = 0.f;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
@@ -298,30 +308,29 @@ __global__ void __launch_bounds__(N > 4 ? 512 : 1024) add_rms_norm_spread_kernel
       }
     }
   }
+  w.load(p.weight, 0, p.hidden);  // (in flight during the reduction, in the registers of x and r)
   ss = row_reduce<Add>(ss, part);
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-  float amax = 0.f, inv = 1.f;
+  float top = 0.f;
+  const float f = !OUT8 ? rstd : rstd > 0.f ? 1.f : 0.f;
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    h[k] = h[k] * rstd * w.at(k, p.hidden);
-    if constexpr (OUT8) amax = fmaxf(amax, isinf(h[k]) ? 0.f : fabsf(h[k]));
+    h[k] = scaled_by(h[k], f, w.at(k, p.hidden));
+    if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k]));
   }
   const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
+  float mul = 1.f;
   if constexpr (OUT8) {
-    float c;
-    if (p.scale_in) {
-      c = __ldg(p.scale_in);
-    } else {
-      c = row_scale(row_reduce<Max>(amax, part + 33), e5m2);
-      if (threadIdx.x == 0) p.scale[row] = c;
-    }
-    inv = 1.f / c;
+    if (!p.scale_in) top = row_reduce<Max>(top, part + 33);
+    const RowScale sc = row_scale(top, rstd, p.scale_in, e5m2);
+    if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
+    mul = sc.mul;
   }
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     const int i = threadIdx.x + k * blockDim.x;
-    const float v[1] = {h[k] * inv};
+    const float v[1] = {h[k] * mul};
     if (i < p.hidden) {
       if constexpr (OUT8)
         store_fp8<1>(p.y, row * p.hidden + i, v, e5m2 ? __NV_E5M2 : __NV_E4M3);
@@ -331,78 +340,118 @@ __global__ void __launch_bounds__(N > 4 ? 512 : 1024) add_rms_norm_spread_kernel
   }
 }
 
-// Rows longer than the register kernel holds: each thread goes over its values
-// again (its own stores of the sum, still in cache) for the maximum and the
-// output.  Same order of additions for every row of one size.
-template <int RT, int VW, bool OUT8>
+// Rows longer than the other kernels hold: each thread goes over its values, 8
+// at a time, again for the maximum and for the output (its own stores of the
+// sum, still in cache).  VEC: 8 consecutive values, else 8 spread over the block.
+template <bool F32, bool VEC>
+__device__ __forceinline__ void load_chunk(const void* base, int64_t at, int64_t from, int64_t hidden, float (&v)[8]) {
+  if constexpr (VEC) {
+    load_any<8>(F32, base, at + from + threadIdx.x * 8, v);  // (the caller has checked that the vector is in the row)
+  } else {
+    using T = std::conditional_t<F32, float, uint16_t>;
+    T t[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t i = from + threadIdx.x + k * blockDim.x;
+      t[k] = static_cast<const T*>(base)[at + (i < hidden ? i : hidden - 1)];
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k) v[k] = from + threadIdx.x + k * blockDim.x < hidden ? as_float(t[k]) : 0.f;
+  }
+}
+template <bool VEC, class Store1, class Store8>
+__device__ __forceinline__ void store_chunk(int64_t from, int64_t hidden, const float (&v)[8], Store1 store1, Store8 store8) {
+  if constexpr (VEC) {
+    store8(from + threadIdx.x * 8, v);
+  } else {
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int64_t i = from + threadIdx.x + k * blockDim.x;
+      const float one[1] = {v[k]};
+      if (i < hidden) store1(i, one);
+    }
+  }
+}
+
+template <int RT, bool VEC, bool OUT8>
 __global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const __grid_constant__ NormArgs p) {
   __shared__ float part[66];
   begin_kernel();
-  const int64_t row = blockIdx.x;
-  const int step = blockDim.x * VW;
+  const int64_t row = blockIdx.x, hidden = p.hidden, step = blockDim.x * 8;
   const void* hp = RT == 0 ? p.x : p.sum;
-  const int64_t h0 = row * (RT == 0 ? p.ld_x : p.ld_sum);
+  const int64_t h0 = row * (RT == 0 ? p.ld_x : p.ld_sum), y0 = row * hidden;
+  // (whole vectors: those past the row are skipped)
+  auto chunks = [&](auto body) {
+    for (int64_t from = 0; from < hidden; from += step)
+      if (!VEC || from + threadIdx.x * 8 < hidden) body(from);
+  };
   float ss = 0.f;
-  for (int64_t i = threadIdx.x * VW; i < p.hidden; i += step) {
-    float h[VW];
-    load_bf16<VW>(p.x, row * p.ld_x + i, h);
+  chunks([&](int64_t from) {
+    float h[8];
+    load_chunk<false, VEC>(p.x, row * p.ld_x, from, hidden, h);
     if constexpr (RT != 0) {
-      float r[VW];
-      load_any<VW>(RT == 2, p.residual, row * p.ld_residual + i, r);
+      float r[8];
+      load_chunk<RT == 2, VEC>(p.residual, row * p.ld_residual, from, hidden, r);
 #pragma unroll
-      for (int j = 0; j < VW; ++j) {
+      for (int j = 0; j < 8; ++j) {
         h[j] += r[j];
         if constexpr (RT == 1) h[j] = __bfloat162float(__float2bfloat16_rn(h[j]));
       }
       if constexpr (RT == 2)
-        store_f32<VW>(p.sum, h0 + i, h);
+        store_chunk<VEC>(from, hidden, h, [&](int64_t i, const float(&v)[1]) { store_f32<1>(p.sum, h0 + i, v); },
+                         [&](int64_t i, const float(&v)[8]) { store_f32<8>(p.sum, h0 + i, v); });
       else
-        store_bf16<VW>(p.sum, h0 + i, h);
+        store_chunk<VEC>(from, hidden, h, [&](int64_t i, const float(&v)[1]) { store_bf16<1>(p.sum, h0 + i, v); },
+                         [&](int64_t i, const float(&v)[8]) { store_bf16<8>(p.sum, h0 + i, v); });
     }
 #pragma unroll
-    for (int j = 0; j < VW; ++j) ss = fmaf(h[j], h[j], ss);
-  }
+    for (int j = 0; j < 8; ++j) ss = fmaf(h[j], h[j], ss);
+  });
   ss = row_reduce<Add>(ss, part);
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-  // (the sum was written by this thread just above)
-  auto value = [&](int64_t i, float(&h)[VW]) {
-    float w[VW];
-    load_any<VW>(RT == 2, hp, h0 + i, h);
-    load_any<VW>(p.weight_f32 != 0, p.weight, i, w);
+  const float f = !OUT8 ? rstd : rstd > 0.f ? 1.f : 0.f;
+  auto value = [&](int64_t from, float(&h)[8]) {
+    float w[8];
+    load_chunk<RT == 2, VEC>(hp, h0, from, hidden, h);
+    if (p.weight_f32)
+      load_chunk<true, VEC>(p.weight, 0, from, hidden, w);
+    else
+      load_chunk<false, VEC>(p.weight, 0, from, hidden, w);
 #pragma unroll
-    for (int j = 0; j < VW; ++j) h[j] = h[j] * rstd * w[j];
+    for (int j = 0; j < 8; ++j) h[j] = scaled_by(h[j], f, w[j]);
   };
-  float inv = 1.f;
   const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
+  float mul = 1.f;
   if constexpr (OUT8) {
-    float c;
-    if (p.scale_in) {
-      c = __ldg(p.scale_in);
-    } else {
-      float amax = 0.f;
-      for (int64_t i = threadIdx.x * VW; i < p.hidden; i += step) {
-        float h[VW];
-        value(i, h);
+    float top = 0.f;
+    if (!p.scale_in) {
+      chunks([&](int64_t from) {
+        float h[8];
+        value(from, h);
 #pragma unroll
-        for (int j = 0; j < VW; ++j) amax = fmaxf(amax, isinf(h[j]) ? 0.f : fabsf(h[j]));
-      }
-      c = row_scale(row_reduce<Max>(amax, part + 33), e5m2);
-      if (threadIdx.x == 0) p.scale[row] = c;
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(h[j]));
+      });
+      top = row_reduce<Max>(top, part + 33);
     }
-    inv = 1.f / c;
+    const RowScale sc = row_scale(top, rstd, p.scale_in, e5m2);
+    if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
+    mul = sc.mul;
   }
-  for (int64_t i = threadIdx.x * VW; i < p.hidden; i += step) {
-    float h[VW];
-    value(i, h);
+  chunks([&](int64_t from) {
+    float h[8];
+    value(from, h);
     if constexpr (OUT8) {
 #pragma unroll
-      for (int j = 0; j < VW; ++j) h[j] *= inv;
-      store_fp8<VW>(p.y, row * p.hidden + i, h, e5m2 ? __NV_E5M2 : __NV_E4M3);
+      for (int j = 0; j < 8; ++j) h[j] *= mul;
+      const __nv_fp8_interpretation_t fmt = e5m2 ? __NV_E5M2 : __NV_E4M3;
+      store_chunk<VEC>(from, hidden, h, [&](int64_t i, const float(&v)[1]) { store_fp8<1>(p.y, y0 + i, v, fmt); },
+                       [&](int64_t i, const float(&v)[8]) { store_fp8<8>(p.y, y0 + i, v, fmt); });
     } else {
-      store_bf16<VW>(p.y, row * p.hidden + i, h);
+      store_chunk<VEC>(from, hidden, h, [&](int64_t i, const float(&v)[1]) { store_bf16<1>(p.y, y0 + i, v); },
+                       [&](int64_t i, const float(&v)[8]) { store_bf16<8>(p.y, y0 + i, v); });
     }
-  }
+  });
 }
 
 // ---------------------------------------------------------- streamed forward
@@ -530,37 +579,34 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(con
     const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
     if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
     if constexpr (OUT8) {
-      float amax = 0.f;
+      float top = 0.f;
+      const float keep = rstd > 0.f ? 1.f : 0.f;
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          h[k][j] = h[k][j] * rstd * w[k][j];
-          amax = fmaxf(amax, fabsf(h[k][j]));
+          h[k][j] = scaled_by(h[k][j], keep, w[k][j]);
+          top = fmaxf(top, fabsf(h[k][j]));
         }
-      const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
-      float c;
-      if (p.scale_in) {
-        c = __ldg(p.scale_in);
-      } else {
-        amax = row_reduce<Max>(amax, part[flip] + 33);
-        if (isinf(amax)) {  // the same for the whole row: the largest of the finite values
-          amax = 0.f;
+      if (!p.scale_in) {
+        top = row_reduce<Max>(top, part[flip] + 33);
+        if (isinf(top)) {  // the same for the whole row: the largest of the finite values
+          top = 0.f;
 #pragma unroll
           for (int k = 0; k < NV; ++k)
 #pragma unroll
-            for (int j = 0; j < 8; ++j) amax = fmaxf(amax, isinf(h[k][j]) ? 0.f : fabsf(h[k][j]));
-          amax = row_reduce<Max>(amax, part[flip] + 66);
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(h[k][j]));
+          top = row_reduce<Max>(top, part[flip] + 66);
         }
-        c = row_scale(amax, e5m2);
-        if (threadIdx.x == 0) p.scale[row] = c;
       }
-      const float inv = 1.f / c;
+      const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
+      const RowScale sc = row_scale(top, rstd, p.scale_in, e5m2);
+      if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const int i = i0 + k * step;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[k][j] *= inv;
+        for (int j = 0; j < 8; ++j) h[k][j] *= sc.mul;
         if (i < p.hidden) store_fp8<8>(p.y, row * p.hidden + i, h[k], e5m2 ? __NV_E5M2 : __NV_E4M3);
       }
     } else {
@@ -624,10 +670,10 @@ int run_norm(const NormArgs& p, bool vec, int sms, cudaStream_t s) {
     if (n <= 1024) return launch_norm<RT, 1, OUT8>(p, round32(n), s);
     if (n <= 2048) return launch_norm<RT, 2, OUT8>(p, round32((n + 1) / 2), s);
     if (n <= 4096) return launch_norm<RT, 8, OUT8>(p, round32((n + 7) / 8), s);
-    return dgl::launch(add_rms_norm_long_kernel<RT, 8, OUT8>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
+    return dgl::launch(add_rms_norm_long_kernel<RT, true, OUT8>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
   } else {
-    if (p.hidden <= 8192) return p.weight_f32 ? spread_norm<RT, true, OUT8>(p, s) : spread_norm<RT, false, OUT8>(p, s);
-    return dgl::launch(add_rms_norm_long_kernel<RT, 1, OUT8>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
+    if (p.hidden <= 16384) return p.weight_f32 ? spread_norm<RT, true, OUT8>(p, s) : spread_norm<RT, false, OUT8>(p, s);
+    return dgl::launch(add_rms_norm_long_kernel<RT, false, OUT8>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
   }
 }
 

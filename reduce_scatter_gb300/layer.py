@@ -197,7 +197,8 @@ def grouped_matmul(A: torch.Tensor, B: torch.Tensor, group_ends: torch.Tensor, *
     is copied.  ``scale_a`` (T,) or one element, ``scale_b`` (experts, N),
     (experts,) or one element: float32 factors of D's rows and of each expert's
     columns.  ``out_dtype``: bfloat16 or float32.  K % 8 == 0 (16 for float8)
-    and N % 8 == 0.  Differentiable in bfloat16 without scales.
+    and N % 8 == 0.  Differentiable in bfloat16 without scales (the gradients are
+    products of bfloat16 operands, accumulated in fp32).
     """
     if torch.is_grad_enabled() and (A.requires_grad or B.requires_grad):
         if scale_a is not None or scale_b is not None or A.dtype != torch.bfloat16:

@@ -274,39 +274,41 @@ void check_grouped(const Tensor& A, const Tensor& B, const Tensor& ends) {
   same_device(A, {&B, &ends});
 }
 
-// How a (experts, K, N) B is read: in place when its K rows (or, in bf16, its N
-// rows) are contiguous, aligned and apart from each other, else from a copy
-// with K rows.
+// How a (experts, K, N) B (`swapped`: its transpose) is read: in place when its K
+// rows (or, in bf16, its N rows) are contiguous, aligned and apart from each
+// other, else from a copy with K rows.
 struct Experts {
   Tensor B;
-  int64_t ld, ld_e;
+  int64_t K, N, ld, ld_e;
   int n_major;
-  Experts(const Tensor& b, bool f8) : B(b) {
-    const int64_t E = b.size(0), K = b.size(1), N = b.size(2);
-    const bool apart = E == 1 || (b.stride(0) > 0 && b.stride(0) * b.element_size() % 16 == 0);
-    if (apart && b.stride(1) == 1 && b.stride(2) >= K && aligned(b, b.stride(2))) {
-      ld = b.stride(2), ld_e = b.stride(0), n_major = 0;
-    } else if (apart && !f8 && b.stride(2) == 1 && b.stride(1) >= N && aligned(b, b.stride(1))) {
-      ld = b.stride(1), ld_e = b.stride(0), n_major = 1;
+  Experts(const Tensor& b, bool f8, bool swapped) : B(b) {
+    const int dk = swapped ? 2 : 1, dn = swapped ? 1 : 2;
+    const int64_t E = b.size(0), sk = b.stride(dk), sn = b.stride(dn);
+    K = b.size(dk), N = b.size(dn), ld_e = b.stride(0);
+    const bool apart = E == 1 || (ld_e > 0 && ld_e * b.element_size() % 16 == 0);
+    if (apart && sk == 1 && sn >= K && aligned(b, sn)) {
+      ld = sn, n_major = 0;
+    } else if (apart && !f8 && sn == 1 && sk >= N && aligned(b, sk)) {
+      ld = sk, n_major = 1;
     } else {
-      B = fresh(b, {E, N, K}, b.scalar_type()).copy_(b.transpose(1, 2));
+      B = fresh(b, {E, N, K}, b.scalar_type()).copy_(swapped ? b : b.transpose(1, 2));
       ld = K, ld_e = N * K, n_major = 0;
     }
   }
 };
 
-Tensor grouped(const Tensor& A_, const Tensor& B, const Tensor& ends_, const Tensor& sa, const Tensor& sb,
+Tensor grouped(const Tensor& A_, const Tensor& B, bool swapped, const Tensor& ends_, const Tensor& sa, const Tensor& sb,
                at::ScalarType out, const Site& at) {
-  const int64_t T = A_.size(0), K = A_.size(1), E = B.size(0), N = B.size(2);
+  const int64_t T = A_.size(0), E = B.size(0);
   const Tensor A = as_operand(A_), ends = ends_.contiguous();
-  const Experts ex(B, is8(B.scalar_type()));
-  const Tensor D = fresh(A, {T, N}, out);
+  const Experts ex(B, is8(B.scalar_type()), swapped);
+  const Tensor D = fresh(A, {T, ex.N}, out);
   const Tensor ws = products_workspace(at, A);
   auto stride = [](const Tensor& t, int d) { return t.defined() && t.size(d) > 1 ? t.stride(d) : 0; };
   check_status(dg_layer_grouped_matmul(
       A.data_ptr(), A.stride(0), type_of(A.scalar_type()), ex.B.data_ptr(), ex.ld, ex.ld_e, type_of(B.scalar_type()),
       ex.n_major, static_cast<const int32_t*>(ends.data_ptr()), (int)E, static_cast<const float*>(ptr(sa)), stride(sa, 0),
-      static_cast<const float*>(ptr(sb)), stride(sb, 0), stride(sb, 1), D.data_ptr(), type_of(out), T, N, K,
+      static_cast<const float*>(ptr(sb)), stride(sb, 0), stride(sb, 1), D.data_ptr(), type_of(out), T, ex.N, ex.K,
       ws.data_ptr(), status_word(at, A), at.handle()));
   return D;
 }
@@ -337,16 +339,17 @@ PyObject* grouped_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor sa = scale_as(a[3], {A.size(0)}, "scale_a"), sb = scale_as(a[4], {B.size(0), B.size(2)}, "scale_b");
     same_device(A, {&sa, &sb});
     const Site at(A);
-    return wrap(grouped(A, B, ends, sa, sb, out, at));
+    return wrap(grouped(A, B, false, ends, sa, sb, out, at));
   });
 }
 
 // (experts, rows' columns, feats' columns): the sum over each group of
-// rows[t, :, None] * feats[t, None, :].
-Tensor weight_grad(const Tensor& rows_, const Tensor& feats_, const Tensor& ends_, const Site& at) {
+// rows[t, :, None] * feats[t, None, :]; `swapped`: seen as its transpose.
+Tensor weight_grad(const Tensor& rows_, const Tensor& feats_, bool swapped, const Tensor& ends_, const Site& at) {
   const Tensor rows = as_operand(rows_), feats = as_operand(feats_), ends = ends_.contiguous();
   const int64_t T = rows.size(0), N = rows.size(1), K = feats.size(1), E = ends.size(0);
-  const Tensor out = fresh(rows, {E, N, K}, rows.scalar_type());
+  const Tensor out = swapped ? at::detail::empty_strided_cuda({E, K, N}, {N * K, 1, K}, rows.scalar_type(), rows.device())
+                             : at::detail::empty_cuda({E, N, K}, rows.scalar_type(), rows.device(), std::nullopt);
   const Tensor ws = fresh(rows, {(int64_t)dg_layer_grouped_grad_workspace((int)E, N, K)}, at::kByte);
   check_status(dg_layer_grouped_weight_grad(rows.data_ptr(), rows.stride(0), feats.data_ptr(), feats.stride(0),
                                             static_cast<const int32_t*>(ends.data_ptr()), (int)E, out.data_ptr(),
@@ -368,10 +371,10 @@ PyObject* grouped_matmul_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     same_device(A, {&dD});
     const Site at(A);
     Tensor dA, dB;
-    if (a[4] == Py_True) dA = grouped(dD, B.transpose(1, 2), ends, Tensor(), Tensor(), at::kBFloat16, at);
+    if (a[4] == Py_True) dA = grouped(dD, B, true, ends, Tensor(), Tensor(), at::kBFloat16, at);
     if (a[5] == Py_True)
-      dB = B.stride(2) == 1 && B.stride(1) != 1 ? weight_grad(A, dD, ends, at)  // contiguous along N
-                                                : weight_grad(dD, A, ends, at).transpose(1, 2);
+      dB = B.stride(2) == 1 && B.stride(1) != 1 ? weight_grad(A, dD, false, ends, at)  // contiguous along N
+                                                : weight_grad(dD, A, true, ends, at);
     return Py_BuildValue("(NN)", wrap(dA), wrap(dB));
   });
 }

@@ -15,7 +15,7 @@
 //
 // A tile of 256 rows moves 128 bytes a cycle through its SM's shared memory (what
 // the loads write and the MMAs read), which is all it has: the tensor pipe is
-// busy for 96 % of the cycles.  A shorter tile of n rows needs about 256 + n
+// busy for 95 % of the cycles.  A shorter tile of n rows needs about 256 + n
 // cycles a K block against 2 n of the MMAs, so few tall tiles are best where
 // there are enough of them.  Back to back on a GB300: 16384 rows of 8 experts of
 // 8192 x 8192 in bf16 1215 us even, 1290 uneven (1810, 1700 TFLOP/s, under the

@@ -13,7 +13,7 @@
 // hand-off needs no barrier), because a block that loads, reduces and stores by
 // turns leaves the memory idle in between.
 //
-// Back to back on a GB300: 8192 x 16384, bf16 residual, to e4m3 141 us (6.6 TB/s;
+// Back to back on a GB300: 8192 x 16384, bf16 residual, to e4m3 142 us (6.6 TB/s;
 // 186 us before streaming), 8192 x 8192 80 us, 16384 x 2048 46 us; 4 rows of 8192
 // 2.9 us; the gradient of 4099 x 8192 53 us and 4 us for the weight's (4.9 TB/s);
 // rows of 10945 (no vectors) 3.1 TB/s.  One vector per thread, or four, instead
@@ -31,7 +31,8 @@ namespace {
 using dgl::begin_kernel;
 
 constexpr float kE4M3Max = 448.f, kE5M2Max = 57344.f;
-constexpr float kMinScale = 1.1754943508222875e-38f;  // 2^-126: the reciprocal stays finite
+constexpr float kMinScale = 0x1p-126f;  // the least row scale: the smallest normal number
+constexpr float kMaxFinite = 3.4028234663852886e38f;
 
 // ---------------------------------------------------------------- vectors
 
@@ -154,27 +155,46 @@ struct NormArgs {
   int weight_f32, fp8;  // fp8: 0 bf16 output, else the dg_type
 };
 
-// The scale c of a row of 8-bit values, and what turns t = h w into the value
-// q = t rstd / c that is rounded.  `top`: the largest finite |t|.  With the row's
-// own scale c = top rstd / max, so rstd cancels: q = t max / top, where t is
-// exact for bf16 h and w, so q carries two roundings only and hardly ever
-// crosses a rounding boundary of the 8 bits that the exact value does not.
+// The 8-bit value of y = h rstd w is y / c.  With rstd = f r, f a power of two and
+// 1 <= r < 2, a thread forms t = (h f) w, where the product with f is exact, and
+// rounds t mul to 8 bits.  |y| / 2 < |t| <= |y|: t leaves fp32's range only where y
+// does, and mul stays below 2^128 (h w alone may be far below 1 or overflow while
+// y is an ordinary number).  With the row's own scale c = top r / max, `top` the
+// largest |t| of a finite y, r cancels: mul = max / top, so q carries two
+// roundings for bf16 h and w and hardly ever crosses a rounding boundary of the 8
+// bits that the exact value does not.
+struct RowFactor {
+  float f, r, most;  // most: the largest |t| whose y is finite
+};
+__device__ __forceinline__ RowFactor row_factor(float rstd, const float* given) {
+  if (!(rstd > 0.f)) return RowFactor{0.f, rstd, 0.f};  // a sum of squares beyond fp32 (finite values become 0), or a NaN
+  if (isinf(rstd)) return RowFactor{1.f, rstd, 0.f};    // a row of zeros without eps: NaN
+  const uint32_t b = __float_as_uint(rstd);             // normal: rsqrt of an fp32 value
+  float f = __uint_as_float(b & 0x7f800000u), r = __uint_as_float((b & 0x007fffffu) | 0x3f800000u);
+  // r / c stays finite for a subnormal c as well
+  if (given && fabsf(__ldg(given)) < kMinScale) f *= 0x1p24f, r *= 0x1p-24f;
+  return RowFactor{f, r, kMaxFinite / r};
+}
 struct RowScale {
   float c, mul;
 };
-__device__ __forceinline__ RowScale row_scale(float top, float rstd, const float* given, bool e5m2) {
+__device__ __forceinline__ RowScale row_scale(float top, float r, const float* given, bool e5m2) {
   if (given) {
     const float c = __ldg(given);
-    return RowScale{c, rstd / c};
+    return RowScale{c, r / c};
   }
-  const float most = e5m2 ? kE5M2Max : kE4M3Max, y = top * rstd, c = y / most;
-  if (!(y > 0.f)) return RowScale{1.f, rstd};  // a row of zeros (or one that is not finite, whose values stay so)
-  return c > kMinScale ? RowScale{c, most / top} : RowScale{kMinScale, rstd / kMinScale};
+  const float most = e5m2 ? kE5M2Max : kE4M3Max, y = top * r, c = y / most;
+  if (!(y > 0.f)) return RowScale{1.f, r};  // a row of zeros (or one that is not finite, whose values stay so)
+  return c > kMinScale ? RowScale{c, most / top} : RowScale{kMinScale, r / kMinScale};
 }
-// t for one value: with rstd 0 (a sum of squares beyond fp32) a finite value
-// becomes 0 before the product can overflow.
+// Where t = h w without the factor f serves as well, in the streamed kernel: a
+// top product from 2^-64 (its row's 8-bit steps are then far above the subnormal
+// one) to 2^60, with rstd below that, so that y is finite; and, with a given
+// scale, no infinite product and no multiplier above 2^100.
+constexpr float kOrdinaryMin = 0x1p-64f, kOrdinaryMax = 0x1p60f, kOrdinaryMul = 0x1p100f;
 __device__ __forceinline__ float scaled_by(float h, float keep, float w) { return h * keep * w; }
-__device__ __forceinline__ float finite_mag(float t) { return isinf(t) ? 0.f : fabsf(t); }
+// |t|, or 0 where y is not finite (a NaN stays, and the maximum ignores it)
+__device__ __forceinline__ float finite_mag(float t, float most) { return fabsf(t) > most ? 0.f : fabsf(t); }
 
 // RT: the residual's type (0 none, 1 bf16, 2 fp32).  The row stays in
 // registers: NV vectors of 8 values per thread.
@@ -225,7 +245,7 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) add_rms_norm_kernel(const
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
   float top = 0.f;
-  const float f = !OUT8 ? rstd : rstd > 0.f ? 1.f : 0.f;
+  const RowFactor by = OUT8 ? row_factor(rstd, p.scale_in) : RowFactor{rstd, 1.f, 0.f};
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = threadIdx.x * 8 + k * step;
@@ -234,8 +254,8 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) add_rms_norm_kernel(const
       load_any<8>(p.weight_f32 != 0, p.weight, i, w);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        h[k][j] = scaled_by(h[k][j], f, w[j]);
-        if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k][j]));
+        h[k][j] = scaled_by(h[k][j], by.f, w[j]);
+        if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k][j], by.most));
       }
       if constexpr (!OUT8) store_bf16<8>(p.y, row * p.hidden + i, h[k]);
     }
@@ -243,7 +263,7 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) add_rms_norm_kernel(const
   if constexpr (OUT8) {
     const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
     if (!p.scale_in) top = row_reduce<Max>(top, part + 33);
-    const RowScale sc = row_scale(top, rstd, p.scale_in, e5m2);
+    const RowScale sc = row_scale(top, by.r, p.scale_in, e5m2);
     if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -319,17 +339,17 @@ __global__ void __launch_bounds__(1024) add_rms_norm_spread_kernel(const __grid_
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
   float top = 0.f;
-  const float f = !OUT8 ? rstd : rstd > 0.f ? 1.f : 0.f;
+  const RowFactor by = OUT8 ? row_factor(rstd, p.scale_in) : RowFactor{rstd, 1.f, 0.f};
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    h[k] = scaled_by(h[k], f, w.at(k, p.hidden));
-    if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k]));
+    h[k] = scaled_by(h[k], by.f, w.at(k, p.hidden));
+    if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k], by.most));
   }
   const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
   float mul = 1.f;
   if constexpr (OUT8) {
     if (!p.scale_in) top = row_reduce<Max>(top, part + 33);
-    const RowScale sc = row_scale(top, rstd, p.scale_in, e5m2);
+    const RowScale sc = row_scale(top, by.r, p.scale_in, e5m2);
     if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
     mul = sc.mul;
   }
@@ -416,7 +436,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const __grid_co
   ss = row_reduce<Add>(ss, part);
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-  const float f = !OUT8 ? rstd : rstd > 0.f ? 1.f : 0.f;
+  const RowFactor by = OUT8 ? row_factor(rstd, p.scale_in) : RowFactor{rstd, 1.f, 0.f};
   auto value = [&](int64_t from, float(&h)[8]) {
     float w[8];
     load_chunk<RT == 2, VEC>(hp, h0, from, hidden, h);
@@ -425,7 +445,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const __grid_co
     else
       load_chunk<false, VEC>(p.weight, 0, from, hidden, w);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = scaled_by(h[j], f, w[j]);
+    for (int j = 0; j < 8; ++j) h[j] = scaled_by(h[j], by.f, w[j]);
   };
   const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
   float mul = 1.f;
@@ -436,11 +456,11 @@ __global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const __grid_co
         float h[8];
         value(from, h);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(h[j]));
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(h[j], by.most));
       });
       top = row_reduce<Max>(top, part + 33);
     }
-    const RowScale sc = row_scale(top, rstd, p.scale_in, e5m2);
+    const RowScale sc = row_scale(top, by.r, p.scale_in, e5m2);
     if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
     mul = sc.mul;
   }
@@ -586,12 +606,8 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(con
     if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
     if constexpr (OUT8) {
       float top = 0.f;
-      if (!(rstd > 0.f)) {  // as scaled_by; the same for the whole row
-#pragma unroll
-        for (int k = 0; k < NV; ++k)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) h[k][j] *= 0.f;
-      }
+      // Ordinary rows do without the factor f, which costs a product per value (8192 x
+      // 16384: 142 us, 162 with f in every row).
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -599,18 +615,46 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(con
           h[k][j] *= w[k][j];
           top = fmaxf(top, fabsf(h[k][j]));
         }
-      if (!p.scale_in) {
+      const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
+      bool ordinary = rstd > 0.f && rstd < kOrdinaryMax;
+      if (p.scale_in) {  // (each thread for itself)
+        ordinary = ordinary && !isinf(top) && fabsf(rstd / __ldg(p.scale_in)) < kOrdinaryMul;
+      } else {  // the same for the whole row
         top = row_reduce<Max>(top, part[flip] + 33);
-        if (isinf(top)) {  // the same for the whole row: the largest of the finite values
-          top = 0.f;
+        ordinary = ordinary && top > kOrdinaryMin && top < kOrdinaryMax;
+      }
+      if (!ordinary) {  // products that left the range, or lost bits at its lower end: again from the stored sum, with f
+        const RowFactor by = row_factor(rstd, p.scale_in);
+        auto value = [&](int i, float(&t)[8]) {
+          float v[8];
+          load_any<8>(RT == 2, RT == 0 ? p.x : p.sum, row * (RT == 0 ? p.ld_x : p.ld_sum) + i, t);
+          load_any<8>(p.weight_f32 != 0, p.weight, i, v);
 #pragma unroll
-          for (int k = 0; k < NV; ++k)
+          for (int j = 0; j < 8; ++j) t[j] = scaled_by(t[j], by.f, v[j]);
+        };
+        top = 0.f;
+        if (!p.scale_in) {
+#pragma unroll 1
+          for (int i = i0; i < p.hidden; i += step) {
+            float t[8];
+            value(i, t);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(h[k][j]));
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(t[j], by.most));
+          }
           top = row_reduce<Max>(top, part[flip] + 66);
         }
+        const RowScale sc = row_scale(top, by.r, p.scale_in, e5m2);
+        if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
+#pragma unroll 1
+        for (int i = i0; i < p.hidden; i += step) {
+          float t[8];
+          value(i, t);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t[j] *= sc.mul;
+          store_fp8<8>(p.y, row * p.hidden + i, t, e5m2 ? __NV_E5M2 : __NV_E4M3);
+        }
+        continue;
       }
-      const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
       const RowScale sc = row_scale(top, rstd, p.scale_in, e5m2);
       if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
 #pragma unroll

@@ -1,0 +1,80 @@
+"""Residual add + RMS norm on the GPU at the edges: values near the ends of
+fp32's range, in-place sums and the tensors they touch, host threads, rows of
+no values, special rows among streamed ones."""
+
+import threading
+
+import pytest
+import torch
+
+from reduce_scatter_gb300 import dg, layer, ops
+from tests import layer_common as lc
+from tests.layer_common import U16, U32, assert_within, rand
+from tests.test_gpu_layer_norm import FP8
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+LEAST = 2.0 ** -126                                   # the least row scale
+
+# rows x hidden of every forward kernel: registers (one warp, 1, 2 and 8 vectors), element-wise (4 and 16 values),
+# looping (vectors and elements), streamed
+PATHS = [(5, 256), (3, 8192), (2, 16384), (2, 24576), (4, 259), (3, 4099), (2, 40000), (2, 40001), (700, 2048), (400, 16384)]
+
+
+def check_q(q, scale, y, hidden, dtype):
+    """q * scale within half a step of y (the step: 2^-mantissa of the value, at least the subnormal one), beside the
+    relative errors of rstd and four more roundings, and 2^-22: the products before the last factor (at most 2^127)
+    may be subnormal, off by 2^-150."""
+    top, mant, emin = FP8[dtype]
+    rel = lc.norm_rel(hidden) + 4 * U32
+    want = (y / scale.double()[..., None]).clamp(-top, top)
+    step = torch.maximum(want.abs() * 2.0 ** -mant, torch.full_like(want, 2.0 ** (emin - mant)))
+    assert_within(q.float(), want, step / 2 * (1 + rel) + want.abs() * rel + 2.0 ** -22, "q")
+
+
+def patterned(rows, hidden, size):
+    """Rows of 0, 1/4, 1/2 and 1 with both signs, times `size` of each row's turn."""
+    at = torch.arange(hidden, device="cuda")
+    row = torch.tensor([0.0, 0.25, 0.5, 1.0], device="cuda")[at % 4] * torch.where(at % 8 < 4, 1.0, -1.0)
+    sizes = torch.tensor([size[i % len(size)] for i in range(rows)], dtype=torch.float64, device="cuda")
+    return sizes[:, None] * row
+
+
+@pytest.mark.parametrize("rows,hidden", PATHS)
+@pytest.mark.parametrize("dtype", [E4M3, E5M2])
+def test_values_near_the_ends_of_the_range(rows, hidden, dtype):
+    # products h w far below 1 and above fp32's range: the values that they stand for are finite, zeros stay zeros
+    for size, w in (([1e-38, 1e-40, 1e-37, 1e-36, 1e-34], 1.0), ([1e-35, 1e-33, 1e-30], 0.75), ([1e-18, 1e-20], 1e-19),
+                    ([1e12, 3e18 / hidden ** 0.5, 1.0], 1e30)):
+        x = patterned(rows, hidden, size).to(BF16)
+        weight = torch.full((hidden,), w, device="cuda")
+        for r in (None, torch.zeros_like(x), torch.zeros((rows, hidden), device="cuda")):
+            got = ops.add_rms_norm(x, weight, residual=r, out_dtype=dtype)
+            _, _, y = lc.norm(x, weight, r)
+            want = (y.abs().amax(-1) / FP8[dtype][0]).clamp(min=LEAST)
+            assert_within(got.scale, want, (lc.norm_rel(hidden) + 2 * U32) * want, "scale")
+            check_q(got.y, got.scale, y, hidden, dtype)
+            assert not got.y.float()[y == 0].any()
+
+
+@pytest.mark.parametrize("rows,hidden", PATHS)
+def test_given_scales_near_the_ends_of_the_range(rows, hidden):
+    # (1e-38 and 1e-40 are subnormal)
+    for s, size in ((1e-37, [1e-37, 3e-38]), (1e-38, [1e-38]), (1e-40, [1.2e-40]), (1e30, [1.0]), (1e-3, [1e-3, 1.0, 50.0])):
+        x = patterned(rows, hidden, size).to(BF16)
+        weight = torch.full((hidden,), 1.0 if s < 1 else 1e32, device="cuda")
+        scale = torch.tensor([s], dtype=F32, device="cuda")
+        got = ops.add_rms_norm(x, weight, out_dtype=E4M3, scale=scale)
+        _, _, y = lc.norm(x, weight)
+        check_q(got.y, scale.expand(rows), y, hidden, E4M3)
+        assert not got.y.float()[y == 0].any()
+
+
+def test_ordinary_rows_keep_their_bits():
+    # a power of two in the row changes the scale by it and nothing else, where eps does not count
+    x, w = rand((700, 2048), 101), rand((2048,), 102)
+    want = ops.add_rms_norm(x, w, eps=0.0, out_dtype=E4M3)
+    for e in (-30, -6, 1, 8, 40):
+        got = ops.add_rms_norm(x * 2.0 ** e, w, eps=0.0, out_dtype=E4M3)
+        assert torch.equal(got.y.view(torch.uint8), want.y.view(torch.uint8)) and torch.equal(got.scale, want.scale), e

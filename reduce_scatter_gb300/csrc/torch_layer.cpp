@@ -220,6 +220,8 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(r2.data_ptr() == residual.data_ptr(), "an in-place residual must have rows that are contiguous");
         h = residual;
         h_ld = r2.stride(0);
+        // as torch's in-place operations: a graph that saved the tensor finds it changed
+        h.unsafeGetTensorImpl()->bump_version();
       } else {
         h = fresh(x, x.sizes(), residual.scalar_type());
       }

@@ -78,3 +78,30 @@ def test_ordinary_rows_keep_their_bits():
     for e in (-30, -6, 1, 8, 40):
         got = ops.add_rms_norm(x * 2.0 ** e, w, eps=0.0, out_dtype=E4M3)
         assert torch.equal(got.y.view(torch.uint8), want.y.view(torch.uint8)) and torch.equal(got.scale, want.scale), e
+
+
+def test_in_place_sum_is_seen_by_autograd():
+    x, w = rand((6, 64), 111), rand((64,), 112)
+    r = rand((6, 64), 113)
+    weight = rand((32, 64), 114).requires_grad_()
+    out = torch.nn.functional.linear(r, weight)           # saves r
+    before = r._version
+    with torch.no_grad():
+        ops.add_rms_norm(x, w, residual=r, inplace=True)
+    assert r._version > before
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        out.sum().backward()
+    # the norm's own saved sum
+    xs = x.clone().requires_grad_()
+    n = ops.add_rms_norm(xs, w, residual=r)
+    with torch.no_grad():
+        ops.add_rms_norm(x, w, residual=n.residual, inplace=True)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        n.y.sum().backward()
+    with torch.inference_mode():                           # tensors without a version
+        t = r.clone()
+        assert ops.add_rms_norm(x, w, residual=t, inplace=True).residual is t
+    keep = t.clone()
+    with torch.no_grad(), pytest.raises(RuntimeError):
+        ops.add_rms_norm(x, w, residual=t, inplace=True)   # as torch's own in-place operations
+    assert torch.equal(t, keep)

@@ -36,7 +36,7 @@ extern "C" {
  * as y / *scale_in.
  * x: bf16; residual: NULL, or bf16 / fp32 (residual_type); sum_out: h in the
  * residual's type, required with a residual and may be the residual's own
- * memory; weight: bf16 or fp32 (weight_type); rstd_out: NULL, or the rows'
+ * memory (its rows may not overlap, nor share other values with x); weight: bf16 or fp32 (weight_type); rstd_out: NULL, or the rows'
  * fp32 reciprocal deviations, for the gradient.  ld_*: elements from row to
  * row; y, scale_out and rstd_out are densely packed.  Any hidden >= 1; rows
  * whose pointers and pitches are 16-byte aligned with hidden % 8 == 0 take

@@ -122,6 +122,31 @@ Tensor as_operand(const Tensor& t) {
   return fresh(t, t.sizes(), t.scalar_type()).copy_(t);
 }
 
+// Rows in memory, to tell whether two tensors share some.
+struct Rows {
+  uintptr_t at;
+  int64_t count, pitch, bytes;  // from row to row, and of one
+  Rows(const Tensor& t, int64_t count_, int64_t pitch_, int64_t length)
+      : at(reinterpret_cast<uintptr_t>(t.data_ptr())), count(count_), pitch(pitch_ * t.element_size()),
+        bytes(length * t.element_size()) {}
+  uintptr_t end() const { return at + (count - 1) * pitch + bytes; }
+  bool same(const Rows& o) const { return at == o.at && bytes == o.bytes && (pitch == o.pitch || count == 1); }
+  // (starts and ends ascend in both)
+  bool meet(const Rows& o) const {
+    if (count == 0 || bytes == 0 || o.count == 0 || o.bytes == 0 || end() <= o.at || o.end() <= at) return false;
+    for (int64_t i = 0, j = 0; i < count && j < o.count;) {
+      const uintptr_t a = at + i * pitch, b = o.at + j * o.pitch;
+      if (a + bytes <= b)
+        ++i;
+      else if (b + o.bytes <= a)
+        ++j;
+      else
+        return true;
+    }
+    return false;
+  }
+};
+
 // ------------------------------------------------------------- device state
 
 // The status word of each device, and the products' workspace of each stream:
@@ -220,6 +245,13 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
         TORCH_CHECK_VALUE(r2.data_ptr() == residual.data_ptr(), "an in-place residual must have rows that are contiguous");
         h = residual;
         h_ld = r2.stride(0);
+        // rows are summed in no particular order
+        TORCH_CHECK_VALUE(rows <= 1 || h_ld >= hidden, "the rows of an in-place residual must not overlap");
+        const Rows out(r2, rows, h_ld, hidden), in(x2, rows, x2.stride(0), hidden);
+        TORCH_CHECK_VALUE((x2.scalar_type() == r2.scalar_type() && out.same(in)) || !out.meet(in),
+                          "an in-place residual must not share memory with other values of x");
+        TORCH_CHECK_VALUE(!out.meet(Rows(weight, 1, 0, hidden)) && !(scale_in.defined() && out.meet(Rows(scale_in, 1, 0, 1))),
+                          "an in-place residual must not share memory with the weight or the scale");
         // as torch's in-place operations: a graph that saved the tensor finds it changed
         h.unsafeGetTensorImpl()->bump_version();
       } else {

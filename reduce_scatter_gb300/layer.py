@@ -146,7 +146,9 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tenso
     ``scale`` (a number or a one-element float32 tensor), the one given --
     ``fused_all_gather_scaled_matmul`` takes such rows with ``A_scale=scale``,
     ``grouped_matmul`` rows with either.  ``inplace`` writes the sum over
-    ``residual`` (and raises its version, as torch's in-place operations do).  Differentiable with a bfloat16 output.
+    ``residual`` (and raises its version, as torch's in-place operations do); its
+    rows may not overlap, nor share memory with the weight or with x other than
+    x's same values.  Differentiable with a bfloat16 output.
     """
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or
                                     (residual is not None and residual.requires_grad)):

@@ -105,3 +105,30 @@ def test_in_place_sum_is_seen_by_autograd():
     with torch.no_grad(), pytest.raises(RuntimeError):
         ops.add_rms_norm(x, w, residual=t, inplace=True)   # as torch's own in-place operations
     assert torch.equal(t, keep)
+
+
+def test_in_place_sum_refuses_shared_memory():
+    x, w = rand((4, 64), 121), rand((64,), 122)
+    buf = rand((5, 64), 123)
+    keep = buf.clone()
+    for r, xx, ww in ((buf[:1].expand(4, 64), x, w),                    # one row for all
+                      (buf.view(-1).as_strided((4, 64), (32, 1)), x, w),  # rows that overlap
+                      (buf[1:], buf[:4], w),                            # the sum of a row is the next row's x
+                      (buf[1:], x, buf[2])):                            # a row of it is the weight
+        with pytest.raises(ValueError):
+            ops.add_rms_norm(xx, ww, residual=r, inplace=True)
+    torch.cuda.synchronize()
+    assert torch.equal(buf, keep)
+    # the same tensor twice, and columns of one matrix, do not overlap
+    h, _, _ = lc.norm(buf, w, buf)
+    ops.add_rms_norm(buf, w, residual=buf, inplace=True)
+    assert torch.equal(buf, h)
+    both = rand((4, 128), 124)
+    h, _, _ = lc.norm(both[:, :64], w, both[:, 64:])
+    ops.add_rms_norm(both[:, :64], w, residual=both[:, 64:], inplace=True)
+    assert torch.equal(both[:, 64:], h)
+    one = rand((1, 64), 125)
+    row = one.as_strided((1, 64), (3, 1))                               # a single row has no pitch
+    h, _, _ = lc.norm(x[:1], w, row)
+    ops.add_rms_norm(x[:1], w, residual=row, inplace=True)
+    assert torch.equal(one, h)

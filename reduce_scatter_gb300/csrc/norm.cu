@@ -677,6 +677,12 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(con
   copies_wait<0>();
 }
 
+// The streamed kernels' dynamic shared memory: at most 1024 threads' slots in the
+// forward (hidden <= 16384), and what run_grad admits in the gradient.  The limit
+// is set to that whatever the call needs: it belongs to the process, and another
+// thread's call must not find it lowered between this one's setting and launch.
+constexpr int kStreamBytes = 220000;
+
 // Blocks that fill the SMs, and the dynamic shared memory of one.
 template <class Kernel>
 int stream_shape(Kernel kernel, int hidden, int parts, int stages, int sms, int64_t rows, int* threads, int* blocks,
@@ -686,7 +692,7 @@ int stream_shape(Kernel kernel, int hidden, int parts, int stages, int sms, int6
   *bytes = stages * parts * 16 * *threads;
   const int64_t most = (int64_t)sms * (kStreamThreads / *threads);
   *blocks = (int)(rows < most ? rows : most);
-  DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, *bytes));
+  DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes));
   return DG_OK;
 }
 
@@ -971,7 +977,7 @@ int run_grad(GradArgs p, bool vec, int sms, cudaStream_t s) {
   const int n = p.hidden / 8;
   int blocks, rc;
   // 1024 threads hold 16384 values; fp32 rows of that length do not fit twice
-  if (vec && n <= 2048 && grad_parts<F32, HAS_DH>() * 16 * kGradStages * (n / kStreamVecs + 31) <= 220000) {
+  if (vec && n <= 2048 && grad_parts<F32, HAS_DH>() * 16 * kGradStages * (n / kStreamVecs + 31) <= kStreamBytes) {
     int threads, bytes;
     auto* kernel = add_rms_norm_grad_stream_kernel<F32, HAS_DH>;
     rc = stream_shape(kernel, p.hidden, grad_parts<F32, HAS_DH>(), kGradStages, sms, p.rows, &threads, &blocks, &bytes);

@@ -132,3 +132,40 @@ def test_in_place_sum_refuses_shared_memory():
     h, _, _ = lc.norm(x[:1], w, row)
     ops.add_rms_norm(x[:1], w, residual=row, inplace=True)
     assert torch.equal(one, h)
+
+
+def test_long_and_short_rows_from_two_threads():
+    # the streamed kernels' shared memory depends on the row; the limit on it is the process's
+    L = layer.lib()
+    rows, failed = 400, []
+
+    def calls(hidden):
+        x, r, dy = (rand((rows, hidden), 130 + i) for i in range(3))
+        w = rand((hidden,), 133)
+        y, h, dx, dw = (torch.empty_like(t) for t in (x, x, x, w))
+        rstd = torch.empty((rows,), device="cuda")
+        ws = torch.empty((L.dg_layer_add_rms_norm_backward_workspace(rows, hidden),), dtype=torch.uint8, device="cuda")
+        torch.cuda.synchronize()
+        stream = torch.cuda.Stream().cuda_stream
+
+        def go():
+            for _ in range(2000):
+                rc = L.dg_layer_add_rms_norm(x.data_ptr(), hidden, r.data_ptr(), hidden, 0, w.data_ptr(), 0, y.data_ptr(), 0,
+                                             h.data_ptr(), hidden, None, None, rstd.data_ptr(), rows, hidden, 1e-5, stream)
+                if rc == dg.OK:
+                    rc = L.dg_layer_add_rms_norm_backward(dy.data_ptr(), hidden, h.data_ptr(), hidden, 0, w.data_ptr(), 0,
+                                                          rstd.data_ptr(), None, 0, dx.data_ptr(), dw.data_ptr(),
+                                                          ws.data_ptr(), rows, hidden, stream)
+                if rc != dg.OK:
+                    failed.append((hidden, rc, L.dg_layer_last_error()))
+                    return
+
+        return go
+
+    threads = [threading.Thread(target=calls(hidden)) for hidden in (16384, 2048)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not failed, failed

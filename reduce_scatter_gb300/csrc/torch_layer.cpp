@@ -57,9 +57,12 @@ PyObject* guarded(F body) {
 void want_args(Py_ssize_t got, Py_ssize_t want) {
   TORCH_CHECK_TYPE(got == want, "expected ", want, " arguments, got ", got);
 }
+// (No call has a forward-mode derivative, and outputs without one would pass for constants.)
 const Tensor& tensor(PyObject* o, const char* what) {
   TORCH_CHECK_TYPE(THPVariable_Check(o), what, " must be a tensor");
-  return THPVariable_Unpack(o);
+  const Tensor& t = THPVariable_Unpack(o);
+  TORCH_CHECK_VALUE(!t._fw_grad(0).defined(), what, " has a forward-mode tangent, which this operator does not carry on");
+  return t;
 }
 // A tensor or None (an undefined tensor).
 Tensor maybe(PyObject* o, const char* what) { return o == Py_None ? Tensor() : tensor(o, what); }
@@ -200,6 +203,7 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     want_args(n, 8);
     const Tensor &x = tensor(a[0], "x"), &weight = tensor(a[1], "weight");
     const Tensor residual = maybe(a[2], "residual");
+    Tensor scale_in = THPVariable_Check(a[5]) ? tensor(a[5], "scale") : Tensor();
     const double eps = PyFloat_AsDouble(a[3]);
     if (eps == -1.0 && PyErr_Occurred()) return nullptr;
     const at::ScalarType out = dtype(a[4]);
@@ -221,12 +225,11 @@ PyObject* add_rms_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Site at(x);
     const Tensor x2 = as_rows(x, hidden);
     const int64_t rows = x2.size(0);
-    Tensor scale_in, row_scale, rstd, h, r2;
+    Tensor row_scale, rstd, h, r2;
     if (is8(out)) {
       if (a[5] == Py_None) {
         row_scale = fresh(x, x.sizes().slice(0, x.dim() - 1), at::kFloat);
-      } else if (THPVariable_Check(a[5])) {
-        scale_in = THPVariable_Unpack(a[5]);
+      } else if (scale_in.defined()) {
         TORCH_CHECK_VALUE(scale_in.numel() == 1 && scale_in.scalar_type() == at::kFloat,
                           "a given scale is a number or a one-element float32 tensor");
         same_device(x, {&scale_in});
@@ -347,13 +350,16 @@ Tensor grouped(const Tensor& A_, const Tensor& B, bool swapped, const Tensor& en
   return D;
 }
 
-// A fp32 scale seen as `shape` (stride 0 where it is shared).
-Tensor scale_as(PyObject* o, at::IntArrayRef shape, const char* what) {
+// A fp32 scale or None.
+Tensor scale_of(PyObject* o, const char* what) {
   if (o == Py_None) return Tensor();
   TORCH_CHECK_TYPE(THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kFloat, what,
                    " must be a float32 tensor");
-  Tensor t = THPVariable_Unpack(o);
-  if (t.sizes() == shape) return t;
+  return tensor(o, what);
+}
+// The same seen as `shape` (stride 0 where it is shared).
+Tensor scale_as(Tensor t, at::IntArrayRef shape, const char* what) {
+  if (!t.defined() || t.sizes() == shape) return t;
   if (shape.size() == 2 && t.dim() == 1 && t.size(0) == shape[0]) t = t.unsqueeze(1);  // one for each expert
   bool fits = t.dim() <= (int64_t)shape.size();
   for (int64_t d = 1; fits && d <= t.dim(); ++d) fits = t.size(-d) == 1 || t.size(-d) == shape[shape.size() - d];
@@ -365,12 +371,13 @@ PyObject* grouped_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
     want_args(n, 6);
     const Tensor &A = tensor(a[0], "A"), &B = tensor(a[1], "B"), &ends = tensor(a[2], "group_ends");
+    const Tensor scale_a = scale_of(a[3], "scale_a"), scale_b = scale_of(a[4], "scale_b");
     const at::ScalarType out = dtype(a[5]), ta = A.scalar_type(), tb = B.scalar_type();
     check_grouped(A, B, ends);
     TORCH_CHECK_TYPE((ta == at::kBFloat16 && tb == at::kBFloat16) || (is8(ta) && is8(tb)),
                      "A and B must be both bfloat16 or both float8, got ", ta, " and ", tb);
     TORCH_CHECK_VALUE(bf16_or_f32(out), "out_dtype must be bfloat16 or float32, got ", out);
-    const Tensor sa = scale_as(a[3], {A.size(0)}, "scale_a"), sb = scale_as(a[4], {B.size(0), B.size(2)}, "scale_b");
+    const Tensor sa = scale_as(scale_a, {A.size(0)}, "scale_a"), sb = scale_as(scale_b, {B.size(0), B.size(2)}, "scale_b");
     same_device(A, {&sa, &sb});
     const Site at(A);
     return wrap(grouped(A, B, false, ends, sa, sb, out, at));

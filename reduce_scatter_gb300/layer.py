@@ -9,7 +9,8 @@ and marshalled, and outputs allocated with torch, by the extension
 without the built libraries the first call raises ``RuntimeError``.  No call
 synchronizes; each may be captured into a CUDA graph after one call outside
 capture.  ``add_rms_norm`` (bf16 output) and ``grouped_matmul`` (bf16) take part
-in autograd; their gradients can also be called directly.
+in autograd; their gradients can also be called directly.  No call carries on
+forward-mode tangents (``ValueError``).
 
 Errors: ``ValueError`` / ``TypeError`` for arguments that the front end refuses,
 ``dg.DGError`` for what the C ABI refuses.

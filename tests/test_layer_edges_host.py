@@ -1,0 +1,56 @@
+"""The layer operators without a GPU, at the edges: calls whose derivatives
+would be lost, sizes beside 2^31, the launches' tags, the status word."""
+
+import os
+import subprocess
+
+import pytest
+import torch
+from torch.autograd import forward_ad
+
+from reduce_scatter_gb300 import dg, layer, ops
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "reduce_scatter_gb300", "csrc")
+BF16, E4M3 = torch.bfloat16, torch.float8_e4m3fn
+
+
+@pytest.fixture(scope="module")
+def L():
+    if not os.path.exists(dg.LIB_PATH) or not os.path.exists(layer.EXT_PATH):
+        import __graft_entry__
+
+        __graft_entry__.build()
+    return layer.lib()
+
+
+def compiled(tmp_path, source):
+    """Output of a host program over the library's sources."""
+    cuda = "/usr/local/cuda/include"
+    cpp, exe = tmp_path / "t.cpp", tmp_path / "t"
+    cpp.write_text(source)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-pthread", f"-I{ROOT}/include", f"-I{CSRC}", f"-I{cuda}", "-o", str(exe), str(cpp)],
+                   check=True)
+    return subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60).stdout.split()
+
+
+def test_tangents_are_refused(L):
+    x, w = torch.ones(4, 64, dtype=BF16), torch.ones(64, dtype=BF16)
+    b, ends = torch.ones(2, 64, 32, dtype=BF16), torch.tensor([2, 4], dtype=torch.int32)
+    d, scale, rstd = torch.ones(4, 32, dtype=BF16), torch.ones(1), torch.ones(4)
+    calls = [(lambda x: ops.add_rms_norm(x, w), x), (lambda w: ops.add_rms_norm(x, w), w),
+             (lambda r: ops.add_rms_norm(x, w, residual=r), x.clone()),
+             (lambda s: ops.add_rms_norm(x, w, out_dtype=E4M3, scale=s), scale),
+             (lambda dy: ops.add_rms_norm_backward(dy, x, w, rstd), x), (lambda h: ops.add_rms_norm_backward(x, h, w, rstd), x),
+             (lambda w: ops.add_rms_norm_backward(x, x, w, rstd), w), (lambda r: ops.add_rms_norm_backward(x, x, w, r), rstd),
+             (lambda d: ops.add_rms_norm_backward(x, x, w, rstd, d_residual=d), x),
+             (lambda a: ops.grouped_matmul(a, b, ends), x), (lambda b: ops.grouped_matmul(x, b, ends), b),
+             (lambda s: ops.grouped_matmul(x, b, ends, scale_a=s), scale), (lambda s: ops.grouped_matmul(x, b, ends, scale_b=s), scale),
+             (lambda d: ops.grouped_matmul_backward(d, x, b, ends), d), (lambda a: ops.grouped_matmul_backward(d, a, b, ends), x),
+             (lambda b: ops.grouped_matmul_backward(d, x, b, ends), b), (lambda x: ops.quantize_mx4(x), x)]
+    for i, (call, t) in enumerate(calls):
+        with forward_ad.dual_level():
+            with pytest.raises(ValueError, match="forward-mode"):
+                call(forward_ad.make_dual(t, torch.ones_like(t)))
+            with pytest.raises(ValueError, match="CUDA"):   # (a tensor without a tangent: the next check)
+                call(t)

@@ -152,7 +152,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tenso
     x's same values.  Differentiable with a bfloat16 output.
     """
     if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad or
-                                    (residual is not None and residual.requires_grad)):
+                                    (residual is not None and residual.requires_grad) or
+                                    (scale is not None and getattr(scale, "requires_grad", False))):
         if out_dtype != torch.bfloat16 or inplace:
             raise ValueError("an 8-bit output or an in-place residual has no gradient: call under torch.no_grad()")
         out = _AddRMSNorm.apply(x, weight, residual, eps)
@@ -203,7 +204,9 @@ def grouped_matmul(A: torch.Tensor, B: torch.Tensor, group_ends: torch.Tensor, *
     and N % 8 == 0.  Differentiable in bfloat16 without scales (the gradients are
     products of bfloat16 operands, accumulated in fp32).
     """
-    if torch.is_grad_enabled() and (A.requires_grad or B.requires_grad):
+    if torch.is_grad_enabled() and (A.requires_grad or B.requires_grad or
+                                    (scale_a is not None and getattr(scale_a, "requires_grad", False)) or
+                                    (scale_b is not None and getattr(scale_b, "requires_grad", False))):
         if scale_a is not None or scale_b is not None or A.dtype != torch.bfloat16:
             raise ValueError("float8 operands and scales have no gradient: call under torch.no_grad()")
         return _GroupedMatmul.apply(A, B, group_ends, out_dtype)
@@ -239,7 +242,11 @@ def quantize_mx4(x: torch.Tensor) -> MX4Tensor:
     """``x`` (..., cols), bfloat16 or float32, its leading dimensions flattened
     into rows, in microscaled 4 bits: for each 32 columns the scale
     2^(floor(log2 max) - 2) and the nearest codes (ties to even, saturating at
-    6); a block with a NaN or an infinity becomes NaN.  cols % 32 == 0."""
+    6); a block with a NaN or an infinity becomes NaN.  cols % 32 == 0.  Not
+    differentiable: an ``x`` that requires a gradient is refused outside
+    ``torch.no_grad()``."""
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("4-bit codes have no gradient: call under torch.no_grad(), or on x.detach()")
     return MX4Tensor(*(_EXT or _load()).quantize_mx4(x))
 
 

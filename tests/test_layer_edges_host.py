@@ -54,3 +54,19 @@ def test_tangents_are_refused(L):
                 call(forward_ad.make_dual(t, torch.ones_like(t)))
             with pytest.raises(ValueError, match="CUDA"):   # (a tensor without a tangent: the next check)
                 call(t)
+
+
+def test_gradients_that_would_be_dropped_are_refused(L):
+    x, w = torch.ones(4, 64, dtype=BF16), torch.ones(64, dtype=BF16)
+    b, ends = torch.ones(2, 64, 32, dtype=BF16), torch.tensor([2, 4], dtype=torch.int32)
+    a8, b8 = x.to(E4M3), b.to(E4M3)
+    scale = torch.ones(1, requires_grad=True)
+    calls = [lambda: ops.quantize_mx4(x.clone().requires_grad_()), lambda: ops.quantize_mx4(x.float().requires_grad_()),
+             lambda: ops.add_rms_norm(x, w, out_dtype=E4M3, scale=scale),
+             lambda: ops.grouped_matmul(a8, b8, ends, scale_a=scale), lambda: ops.grouped_matmul(a8, b8, ends, scale_b=scale),
+             lambda: ops.grouped_matmul(x, b, ends, scale_a=scale), lambda: ops.grouped_matmul(x, b, ends, scale_b=scale)]
+    for call in calls:
+        with pytest.raises(ValueError, match="no gradient"):
+            call()
+        with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
+            call()

@@ -156,6 +156,8 @@ def add_rms_norm(x: torch.Tensor, weight: torch.Tensor, *, residual: torch.Tenso
                                     (scale is not None and getattr(scale, "requires_grad", False))):
         if out_dtype != torch.bfloat16 or inplace:
             raise ValueError("an 8-bit output or an in-place residual has no gradient: call under torch.no_grad()")
+        if scale is not None:
+            raise ValueError("a scale needs a float8 out_dtype")
         out = _AddRMSNorm.apply(x, weight, residual, eps)
         return NormResult(out[0], out[1] if residual is not None else x, None, out[-1] if keep_rstd else None)
     return NormResult(*(_EXT or _load()).add_rms_norm(x, weight, residual, eps, out_dtype, scale, bool(keep_rstd),

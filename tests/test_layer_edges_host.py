@@ -70,3 +70,11 @@ def test_gradients_that_would_be_dropped_are_refused(L):
             call()
         with torch.no_grad(), pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+def test_a_scale_of_16_bit_rows_is_refused_with_and_without_gradients(L):
+    x, w = torch.ones(4, 64, dtype=BF16), torch.ones(64, dtype=BF16)
+    for t in (x, x.clone().requires_grad_()):
+        for s in (1.0, torch.ones(1)):
+            with pytest.raises(ValueError, match="needs a float8 out_dtype"):
+                ops.add_rms_norm(t, w, scale=s)

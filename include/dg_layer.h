@@ -38,9 +38,10 @@ extern "C" {
  * residual's type, required with a residual and may be the residual's own
  * memory (its rows may not overlap, nor share other values with x); weight: bf16 or fp32 (weight_type); rstd_out: NULL, or the rows'
  * fp32 reciprocal deviations, for the gradient.  ld_*: elements from row to
- * row; y, scale_out and rstd_out are densely packed.  Any hidden >= 1; rows
- * whose pointers and pitches are 16-byte aligned with hidden % 8 == 0 take
- * 16-byte accesses.  Statistics and products are computed in fp32.  A NaN or
+ * row; y, scale_out and rstd_out are densely packed.  Any hidden (rows
+ * of no values have the scale 1 and rstd NaN, the mean of nothing); rows whose
+ * pointers and pitches are 16-byte aligned with hidden % 8 == 0 take 16-byte
+ * accesses.  Statistics and products are computed in fp32.  A NaN or
  * infinity in a row stays in its row and never enters a scale. */
 int dg_layer_add_rms_norm(const void* x, int64_t ld_x, const void* residual, int64_t ld_residual,
                           int residual_type, const void* weight, int weight_type, void* y, int y_type,

@@ -1000,6 +1000,16 @@ int run_grad(GradArgs p, bool vec, int sms, cudaStream_t s) {
                      p.hidden, p.dweight, p.weight_f32);
 }
 
+// Rows of no values: the scale of a row of zeros, and the reciprocal deviation of
+// the mean of nothing, a NaN.
+__global__ void __launch_bounds__(256) norm_of_nothing_kernel(float* scale, float* rstd, int64_t rows) {
+  begin_kernel();
+  const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (row >= rows) return;
+  if (scale) scale[row] = 1.f;
+  if (rstd) rstd[row] = __uint_as_float(0x7fc00000u);
+}
+
 bool rows16(const void* p, int64_t ld, int64_t esz) {
   return !p || (dgl::aligned16(p) && (ld * esz) % 16 == 0);
 }
@@ -1019,7 +1029,12 @@ extern "C" int dg_layer_add_rms_norm(const void* x, int64_t ld_x, const void* re
   const bool out8 = y_type == DG_TYPE_E4M3 || y_type == DG_TYPE_E5M2;
   if (!out8 && y_type != DG_TYPE_BF16) return dgl::fail(DG_ERR_ARG, "y is bf16, e4m3 or e5m2 (got type %d)", y_type);
   if (!(eps >= 0.f)) return dgl::fail(DG_ERR_ARG, "eps must not be negative");
-  if (rows == 0 || hidden == 0) return DG_OK;
+  if (rows == 0) return DG_OK;
+  if (hidden == 0) {
+    if (!scale_out && !rstd_out) return DG_OK;
+    return dgl::launch(norm_of_nothing_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0,
+                       static_cast<cudaStream_t>(stream), scale_out, rstd_out, rows);
+  }
   if (!x || !weight || !y) return dgl::fail(DG_ERR_ARG, "x, weight and y must not be null");
   if ((residual != nullptr) != (sum_out != nullptr))
     return dgl::fail(DG_ERR_ARG, "a residual and its sum come together");

@@ -112,7 +112,9 @@ void* ptr(const Tensor& t) { return t.defined() ? t.data_ptr() : nullptr; }
 // (..., hidden) as a matrix whose rows are contiguous; copies only where the
 // strides leave no other way.
 Tensor as_rows(const Tensor& t, int64_t hidden) {
-  Tensor r = t.dim() == 2 ? t : t.reshape({hidden > 0 ? t.numel() / hidden : 0, hidden});
+  int64_t rows = 1;
+  for (int64_t d = 0; d + 1 < t.dim(); ++d) rows *= t.size(d);
+  Tensor r = t.dim() == 2 ? t : t.reshape({rows, hidden});
   return r.stride(1) == 1 || hidden <= 1 ? r : r.contiguous();
 }
 bool aligned(const Tensor& t, int64_t pitch) {

@@ -169,3 +169,20 @@ def test_long_and_short_rows_from_two_threads():
         t.join()
     torch.cuda.synchronize()
     assert not failed, failed
+
+
+def test_rows_of_no_values():
+    for shape in ((3, 0), (2, 3, 0), (0,)):
+        x, w = torch.zeros(shape, dtype=BF16, device="cuda"), torch.zeros((0,), dtype=BF16, device="cuda")
+        dirty = torch.full((4096,), 7.0, device="cuda")    # what a fresh allocation may hold
+        del dirty
+        got = ops.add_rms_norm(x, w, out_dtype=E4M3, keep_rstd=True)
+        assert got.y.shape == shape and got.scale.shape == shape[:-1]
+        assert (got.scale == 1).all()                      # as of a row of zeros
+        assert torch.isnan(got.rstd).all()                 # the mean of nothing
+        dx, dw = ops.add_rms_norm_backward(x, x, w, got.rstd)
+        assert dx.shape == shape and dw.shape == (0,)
+    q = ops.quantize_mx4(torch.zeros((2, 3, 0), dtype=BF16, device="cuda"))
+    assert q.rows == 6 and ops.dequantize_mx4(q).shape == (6, 0)
+    d = ops.mx4_matmul(q, ops.quantize_mx4(torch.zeros((8, 0), dtype=BF16, device="cuda")))
+    assert d.shape == (6, 8) and not d.any()

@@ -559,7 +559,8 @@ extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, 
   }
   if (!A || !B || !workspace) return fail(DG_ERR_ARG, "A, B and workspace must not be null");
   const int64_t inner = b_n_major ? N : K;
-  if (!aligned16(A) || !aligned16(B) || !aligned16(D) || !aligned16(workspace) || ld_a * esz % 16 || ld_b * esz % 16 || ld_e * esz % 16)
+  if (!aligned16(A) || !aligned16(B) || !aligned16(D) || !aligned16(workspace) || ld_a * esz % 16 || ld_b * esz % 16 ||
+      (experts > 1 && ld_e * esz % 16))
     return fail(DG_ERR_ARG, "A, B, D, the workspace and the pitches must be multiples of 16 bytes");
   if (ld_a < K || ld_b < inner || (experts > 1 && ld_e <= 0)) return fail(DG_ERR_ARG, "a pitch is shorter than its rows");
   Args p{};

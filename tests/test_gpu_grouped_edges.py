@@ -1,0 +1,34 @@
+"""Products grouped by expert on the GPU at the edges: a single expert's
+strides, scales of every shape and size, gradients whose tiles are drawn, the
+32-bit weight gradient of the C ABI."""
+
+import pytest
+import torch
+
+from reduce_scatter_gb300 import dg, layer, ops
+from tests import layer_common as lc
+from tests.layer_common import assert_within, rand
+
+pytestmark = pytest.mark.gpu
+BF16, F32 = torch.bfloat16, torch.float32
+E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
+
+
+def ends_of(v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("stride", [1, 0, 64 * 72 + 3])
+def test_a_single_expert_has_no_pitch(stride):
+    # the stride of a dimension of one is anything
+    a, w = rand((20, 64), 1), rand((64 * 72,), 2)
+    for b in (w.as_strided((1, 64, 72), (stride, 1, 64)), w.as_strided((1, 64, 72), (stride, 72, 1))):
+        d = ops.grouped_matmul(a, b, ends_of([13]))
+        want, bound = lc.grouped(a, b, [13])
+        assert_within(d, want, bound, "D")
+        dd = rand((20, 72), 3)
+        da, db = ops.grouped_matmul_backward(dd, a, b, ends_of([13]))
+        want, bound = lc.grouped(dd, b.transpose(1, 2), [13])
+        assert_within(da, want, bound, "dA")
+        want, bound = lc.grouped_weight_grad(dd, a, [13])
+        assert_within(db, want, bound, "dB")

@@ -362,7 +362,7 @@ Tensor scale_of(PyObject* o, const char* what) {
 // The same seen as `shape` (stride 0 where it is shared).
 Tensor scale_as(Tensor t, at::IntArrayRef shape, const char* what) {
   if (!t.defined() || t.sizes() == shape) return t;
-  if (shape.size() == 2 && t.dim() == 1 && t.size(0) == shape[0]) t = t.unsqueeze(1);  // one for each expert
+  if (shape.size() == 2 && t.dim() == 1) t = t.unsqueeze(1);  // one for each expert
   bool fits = t.dim() <= (int64_t)shape.size();
   for (int64_t d = 1; fits && d <= t.dim(); ++d) fits = t.size(-d) == 1 || t.size(-d) == shape[shape.size() - d];
   TORCH_CHECK_VALUE(fits, what, " of shape ", t.sizes(), " does not broadcast to ", shape);

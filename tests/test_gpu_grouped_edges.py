@@ -32,3 +32,20 @@ def test_a_single_expert_has_no_pitch(stride):
         assert_within(da, want, bound, "dA")
         want, bound = lc.grouped_weight_grad(dd, a, [13])
         assert_within(db, want, bound, "dB")
+
+
+def test_a_vector_of_column_scales_is_one_for_each_expert():
+    a = rand((9, 64), 11).to(E4M3)
+    ends = ends_of([4, 9])
+    for n in (8, 16):
+        b = rand((2, n, 64), 12).to(E4M3).transpose(1, 2)
+        per_expert = torch.tensor([0.5, 2.0], device="cuda")
+        d = ops.grouped_matmul(a, b, ends, scale_b=per_expert)
+        want, bound = lc.grouped(a, b, [4, 9], sb=per_expert[:, None].expand(2, n))
+        assert_within(d, want, bound, "D")
+        one = ops.grouped_matmul(a, b, ends, scale_b=torch.tensor(0.5, device="cuda"))
+        assert torch.equal(one, ops.grouped_matmul(a, b, ends, scale_b=torch.tensor([0.5], device="cuda")))
+        row = torch.rand((1, n), device="cuda")
+        assert torch.equal(ops.grouped_matmul(a, b, ends, scale_b=row), ops.grouped_matmul(a, b, ends, scale_b=row.expand(2, n)))
+        with pytest.raises(ValueError):
+            ops.grouped_matmul(a, b, ends, scale_b=torch.ones(n, device="cuda"))   # (as many as columns)

@@ -22,7 +22,6 @@
 // power cap; alone 1087); 10007 rows of 19 of 3328 x 8192 in e4m3 201 us (2700
 // TFLOP/s); 12 rows of 12 of 2048 x 8192 37 us (5.4 TB/s of weights).
 
-#include <atomic>
 #include <cuda_bf16.h>
 
 #include "launch.cuh"
@@ -497,8 +496,6 @@ __global__ void __launch_bounds__(256) grouped_tail_kernel(const int32_t* ends, 
   }
 }
 
-std::atomic<uint32_t> g_epoch{1};
-
 template <bool F8, bool PMN, bool GRAD, bool OUT32>
 int run(Args& p, int64_t most_tiles, cudaStream_t s) {
   auto* kernel = grouped_kernel<F8, PMN, GRAD, OUT32>;
@@ -526,7 +523,7 @@ int check_sizes(int64_t T, int64_t N, int64_t K, int experts) {
 }
 
 Watch watch_of(void* status) {
-  return Watch{static_cast<unsigned long long*>(status), g_epoch.fetch_add(1, std::memory_order_relaxed), 4000000000ull};
+  return Watch{static_cast<unsigned long long*>(status), next_tag(), 4000000000ull};
 }
 
 }  // namespace

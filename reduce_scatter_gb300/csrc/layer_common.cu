@@ -40,6 +40,11 @@ int fail(int code, const char* fmt, ...) {
 
 int cuda_fail(cudaError_t e, const char* what) { return fail(DG_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e)); }
 
+uint32_t next_tag() {
+  static std::atomic<uint32_t> last{0};
+  return next_tag(last);
+}
+
 int sm_count(int* n) {
   static std::mutex mu;
   static int cached[64] = {};

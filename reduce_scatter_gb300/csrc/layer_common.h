@@ -6,6 +6,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "dg_layer.h"
 
 namespace dgl {
@@ -21,6 +23,16 @@ int cuda_fail(cudaError_t e, const char* what);
   } while (0)
 
 int sm_count(int* n);
+
+// A tag for the next launch of a product, with which it marks the status word if
+// it gives up: never 0, which the word of a device without such a launch holds.
+inline uint32_t next_tag(std::atomic<uint32_t>& last) {
+  uint32_t tag;
+  do tag = last.fetch_add(1, std::memory_order_relaxed) + 1;
+  while (tag == 0);
+  return tag;
+}
+uint32_t next_tag();  // of the process's counter
 
 // A tiled tensor map with the 128-byte swizzle over `rank` (2 or 3) dimensions
 // of esz-byte elements, innermost first; strides in elements (stride[0] is

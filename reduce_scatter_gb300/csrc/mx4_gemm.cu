@@ -19,7 +19,6 @@
 // 16384 x 13312 x 16384 back to back on a GB300: 980 us (7300 TFLOP/s, under the
 // power cap; alone 892); 8 x 8192 x 28672: 27 us (4.6 TB/s of weights).
 
-#include <atomic>
 #include <cuda_bf16.h>
 
 #include "launch.cuh"
@@ -258,8 +257,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) mx4_ker
   }
 }
 
-std::atomic<uint32_t> g_epoch{0x80000001u};
-
 template <bool OUT32>
 int run(Args& p, cudaStream_t s) {
   int sms = 0;
@@ -310,6 +307,6 @@ extern "C" int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, co
   p.raster = raster_of(N, kBand);
   p.counters = static_cast<uint32_t*>(workspace);
   p.partial = reinterpret_cast<float*>(p.counters + kCutCounters);
-  p.watch = Watch{static_cast<unsigned long long*>(status), g_epoch.fetch_add(1, std::memory_order_relaxed), 4000000000ull};
+  p.watch = Watch{static_cast<unsigned long long*>(status), next_tag(), 4000000000ull};
   return d_type == DG_TYPE_F32 ? run<true>(p, s) : run<false>(p, s);
 }

@@ -78,3 +78,15 @@ def test_a_scale_of_16_bit_rows_is_refused_with_and_without_gradients(L):
         for s in (1.0, torch.ones(1)):
             with pytest.raises(ValueError, match="needs a float8 out_dtype"):
                 ops.add_rms_norm(t, w, scale=s)
+
+
+def test_launch_tags_skip_zero(tmp_path):
+    # a status word of 0 means that nothing gave up, so no launch is tagged 0
+    out = compiled(tmp_path, """
+        #include <cstdio>
+        #include "layer_common.h"
+        int main() {
+          std::atomic<uint32_t> last{0xfffffffdu};
+          for (int i = 0; i < 4; ++i) std::printf("%u\\n", dgl::next_tag(last));
+        }""")
+    assert [int(v) for v in out] == [2 ** 32 - 2, 2 ** 32 - 1, 1, 2]

@@ -102,8 +102,9 @@ extern "C" int dg_layer_check(void* status, void* stream) {
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   unsigned long long v = 0;
   DGL_CUDA(cudaMemcpyAsync(&v, status, sizeof(v), cudaMemcpyDeviceToHost, s));
+  DGL_CUDA(cudaStreamSynchronize(s));
+  if (v == 0) return DG_OK;  // (cleared only when read: a launch on another stream may report in between)
   DGL_CUDA(cudaMemsetAsync(status, 0, sizeof(v), s));
   DGL_CUDA(cudaStreamSynchronize(s));
-  if (v != 0) return dgl::fail(DG_ERR_HANG, "a pipeline wait ran out (wait 0x%llx)", v & 0xffffffffull);
-  return DG_OK;
+  return dgl::fail(DG_ERR_HANG, "a pipeline wait ran out (wait 0x%llx)", v & 0xffffffffull);
 }

@@ -90,3 +90,36 @@ def test_launch_tags_skip_zero(tmp_path):
           for (int i = 0; i < 4; ++i) std::printf("%u\\n", dgl::next_tag(last));
         }""")
     assert [int(v) for v in out] == [2 ** 32 - 2, 2 ** 32 - 1, 1, 2]
+
+
+def test_check_loses_no_report(tmp_path):
+    # a launch on another stream that gives up just after the word was read must be found by the next check
+    out = compiled(tmp_path, """
+        #include <cstdio>
+        #include <cstring>
+        #include "layer_common.cu"
+        static unsigned long long word;
+        static int late;  // 1: a report lands after the next read of the word
+        extern "C" {
+        cudaError_t cudaMemcpyAsync(void* d, const void* s, size_t n, cudaMemcpyKind, cudaStream_t) {
+          std::memcpy(d, s, n);
+          if (late) word = (7ull << 32) | 0x203, late = 0;
+          return cudaSuccess;
+        }
+        cudaError_t cudaMemsetAsync(void* d, int v, size_t n, cudaStream_t) { std::memset(d, v, n); return cudaSuccess; }
+        cudaError_t cudaStreamSynchronize(cudaStream_t) { return cudaSuccess; }
+        const char* cudaGetErrorString(cudaError_t) { return ""; }
+        cudaError_t cudaGetDevice(int* d) { *d = 0; return cudaSuccess; }
+        cudaError_t cudaDeviceGetAttribute(int* v, cudaDeviceAttr, int) { *v = 152; return cudaSuccess; }
+        cudaError_t cudaGetDriverEntryPointByVersion(const char*, void**, unsigned, unsigned long long, cudaDriverEntryPointQueryResult*) {
+          return cudaErrorUnknown;
+        }
+        }
+        int main() {
+          std::printf("%d\\n", dg_layer_check(&word, nullptr));   // nothing
+          late = 1;
+          std::printf("%d\\n", dg_layer_check(&word, nullptr));   // nothing when read
+          std::printf("%d\\n", dg_layer_check(&word, nullptr));   // the report
+          std::printf("%d\\n", dg_layer_check(&word, nullptr));   // cleared
+        }""")
+    assert [int(v) for v in out] == [dg.OK, dg.OK, dg.ERR_HANG, dg.OK]

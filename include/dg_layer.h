@@ -71,11 +71,11 @@ int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h,
  * [previous end, T] on the device, rows past the last end are written as 0.
  * type: DG_TYPE_BF16, or DG_TYPE_E4M3 / E5M2 for A and B each.  b_n_major: 0 =
  * B's rows (fixed n) are contiguous along k, 1 (bf16 only) = contiguous along
- * n: element (e, n, k) at e * ld_e + k * ld_b + n.  ld_a, ld_b, ld_e (of
- * two experts and more) in elements; the pitches and pointers are multiples of 16 bytes.  scale_a /
- * scale_b: NULL, or fp32 with strides in elements (0 = shared): scale_a[t * sa],
+ * n: element (e, n, k) at e * ld_e + k * ld_b + n.  ld_a, ld_b, ld_e (of two
+ * experts and more) in elements; the pitches and pointers are multiples of 16
+ * bytes.  scale_a / scale_b: NULL, or fp32 with strides in elements (0 = shared): scale_a[t * sa],
  * scale_b[e * sb_e + n * sb_n].  D: bf16 or fp32 (d_type), T x N densely packed.
- * N % 8 == 0 and K % 8 == 0 (bf16) or K % 16 == 0 (8 bits).  T, N, K < 2^31;
+ * N % 8 == 0 and K % 8 == 0 (bf16) or K % 16 == 0 (8 bits).  T, N, K <= 2^31 - 256;
  * experts <= 1024.  workspace: dg_layer_products_workspace() bytes of the
  * current device, 16-byte aligned, its first DG_LAYER_COUNTER_BYTES zeroed once
  * before its first use (each call leaves them zero, except one that

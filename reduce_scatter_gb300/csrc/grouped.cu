@@ -515,8 +515,11 @@ int run(Args& p, int64_t most_tiles, cudaStream_t s) {
 uint32_t format_of(int type) { return type == DG_TYPE_BF16 ? 1u : type == DG_TYPE_E5M2 ? 1u : 0u; }
 bool is8(int type) { return type == DG_TYPE_E4M3 || type == DG_TYPE_E5M2; }
 
+// A size rounded up to whole tiles or K blocks, and their first coordinates, fit 32 bits.
+constexpr int64_t kMaxSize = INT32_MAX - 255;
+
 int check_sizes(int64_t T, int64_t N, int64_t K, int experts) {
-  if (T < 0 || N < 0 || K < 0 || T > INT32_MAX || N > INT32_MAX || K > INT32_MAX)
+  if (T < 0 || N < 0 || K < 0 || T > kMaxSize || N > kMaxSize || K > kMaxSize)
     return fail(DG_ERR_ARG, "T %lld, N %lld, K %lld out of range", (long long)T, (long long)N, (long long)K);
   if (experts < 1 || experts > kMaxExperts) return fail(DG_ERR_ARG, "experts (%d) must be 1 to %d", experts, kMaxExperts);
   return DG_OK;

@@ -123,3 +123,12 @@ def test_check_loses_no_report(tmp_path):
           std::printf("%d\\n", dg_layer_check(&word, nullptr));   // cleared
         }""")
     assert [int(v) for v in out] == [dg.OK, dg.OK, dg.ERR_HANG, dg.OK]
+
+
+@pytest.mark.parametrize("big", [dict(t=2 ** 31 - 1), dict(t=2 ** 31 - 255), dict(n=2 ** 31 - 8), dict(k=2 ** 31 - 128)])
+def test_sizes_whose_tiles_pass_32_bits_are_refused(L, big):
+    v = dict(t=4, n=64, k=64) | big
+    assert L.dg_layer_grouped_matmul(16, v["k"], 0, 16, v["k"], v["k"] * v["n"], 0, 0, 16, 1, None, 0, None, 0, 0, 16, 0, v["t"],
+                                     v["n"], v["k"], 256, 16, None) == dg.ERR_ARG
+    assert L.dg_layer_grouped_weight_grad(16, v["n"], 16, v["k"], 16, 1, 16, 0, v["t"], v["n"], v["k"], 256, 256, 16,
+                                          None) == dg.ERR_ARG

@@ -66,7 +66,8 @@ int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h,
 /* Products grouped by expert: rows ends[e-1] <= t < ends[e] of A (T x K) times
  * expert e's matrix,
  *     D[t, n] = scale_a[t] * scale_b[e, n] * sum_k A[t, k] * B[e, n, k]
- * (fp32 accumulation, the scales in fp32, one rounding to D's type).  `ends`:
+ * (fp32 accumulation, the scales in fp32, also where scale_a scale_b alone is
+ * beyond fp32's range, one rounding to D's type).  `ends`:
  * `experts` ascending int32 in device memory; values are clamped to
  * [previous end, T] on the device, rows past the last end are written as 0.
  * type: DG_TYPE_BF16, or DG_TYPE_E4M3 / E5M2 for A and B each.  b_n_major: 0 =

@@ -170,6 +170,23 @@ __device__ __forceinline__ int columns(const Tile& t) {
   return GRAD ? kTileRows : (t.rows + 31) / 32 * 32;
 }
 
+// A factor of D whose product with another such one is 0 or a normal number.
+__device__ __forceinline__ bool plain_scale(float s) {
+  return s == 0.f || (fabsf(s) >= 0x1p-60f && fabsf(s) <= 0x1p60f);
+}
+// v[i] times lane i's s and this lane's sb, whose product may be out of range
+// where the result is not: the exponents last, in two steps.  (A call of its own,
+// for the registers of the ordinary path.)
+static __device__ __noinline__ void scale_apart(float* v, float s, float sb) {
+  int es, eb;
+  const float ms = frexpf(s, &es), mb = frexpf(sb, &eb);
+  for (int i = 0; i < 32; ++i) {
+    const float m = __shfl_sync(0xffffffffu, ms, i) * mb;
+    const int e = __shfl_sync(0xffffffffu, es, i) + eb, a = min(max(e, -126), 127), b = min(max(e - a, -126), 127);
+    v[i] = v[i] * m * __uint_as_float((uint32_t)(a + 127) << 23) * __uint_as_float((uint32_t)(b + 127) << 23);
+  }
+}
+
 template <bool F8, bool PMN, bool GRAD, bool OUT32>
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     grouped_kernel(const __grid_constant__ Args p) {
@@ -387,6 +404,13 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           sa[i] = p.sa && r < tl.rows ? __ldg(p.sa + (row0 + r) * p.sa_s) : 1.f;
         }
       }
+      bool plain = true;
+      if (!GRAD && (p.sa || p.sb)) {
+        plain = plain_scale(sb);
+#pragma unroll
+        for (int i = 0; i < kTileRows / kChunk / 2; ++i) plain = plain && plain_scale(sa[i]);
+        plain = __all_sync(0xffffffffu, plain) != 0;
+      }
       if (!epilogue_wait(p.watch, tfull, it, s_go)) break;
       const int nch = (tl.rows + kChunk - 1) / kChunk;
       const uint32_t acc = tmem + ((uint32_t)(q * 32) << 16) + buf * kTileRows;
@@ -437,8 +461,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
           float s = sa[0];
 #pragma unroll
           for (int i = 1; i < kTileRows / kChunk / 2; ++i) s = c / 2 == i ? sa[i] : s;
+          if (plain) {
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, s, i) * sb;
+            for (int i = 0; i < 32; ++i) v[i] *= __shfl_sync(0xffffffffu, s, i) * sb;
+          } else {
+            float u[32];
+#pragma unroll
+            for (int i = 0; i < 32; ++i) u[i] = v[i];
+            scale_apart(u, s, sb);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) v[i] = u[i];
+          }
         }
         const int64_t at = r0 * p.feats + f0;
         if constexpr (OUT32)

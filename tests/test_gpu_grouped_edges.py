@@ -49,3 +49,27 @@ def test_a_vector_of_column_scales_is_one_for_each_expert():
         assert torch.equal(ops.grouped_matmul(a, b, ends, scale_b=row), ops.grouped_matmul(a, b, ends, scale_b=row.expand(2, n)))
         with pytest.raises(ValueError):
             ops.grouped_matmul(a, b, ends, scale_b=torch.ones(n, device="cuda"))   # (as many as columns)
+
+
+@pytest.mark.parametrize("a_scale,b_scale", [(2.0 ** -120, 2.0 ** -20), (2.0 ** -126, 2.0 ** -30), (2.0 ** 90, 2.0 ** 50),
+                                             (2.0 ** 50, 2.0 ** 90), (2.0 ** -126, 2.0 ** 100), (2.0 ** -70, 1.0), (0.01, 0.003)])
+@pytest.mark.parametrize("T,ends", [(7, [1, 5]), (5, [5, 5]), (303, [300, 301])])
+def test_products_of_scales_beyond_the_range(T, ends, a_scale, b_scale):
+    # scale_a scale_b may underflow or overflow where D does not
+    K, N = 64, 40
+    if a_scale * b_scale > 1e30:                          # sums of one product 2^-18 keep D in range
+        a, b = torch.zeros((T, K), device="cuda"), torch.zeros((2, N, K), device="cuda")
+        a[:, 5], b[:, :, 5] = 2.0 ** -9, -2.0 ** -9
+    else:
+        a, b = (rand(s, 21 + i, 100.0, F32).clamp(-448, 448) for i, s in enumerate(((T, K), (2, N, K))))
+    a, b = a.to(E4M3), b.to(E4M3).transpose(1, 2)
+    g = torch.Generator(device="cuda").manual_seed(23)
+    sa = (1 + torch.rand((T,), device="cuda", generator=g)) * a_scale
+    sb = (1 + torch.rand((2, N), device="cuda", generator=g)) * b_scale
+    sa[0], sb[0, 3] = 0.0, 0.0
+    d = ops.grouped_matmul(a, b, ends_of(ends), scale_a=sa, scale_b=sb, out_dtype=F32)
+    want, bound = lc.grouped(a, b, ends, sa, sb, out16=False)
+    # beside the sum's and the factors' bound two roundings to the subnormal step, 2^-149
+    assert_within(d, want, bound + 2.0 ** -148, "D")
+    same = ops.grouped_matmul(a, b, ends_of(ends), scale_a=sa, scale_b=sb)
+    assert torch.equal(same, d.to(BF16))

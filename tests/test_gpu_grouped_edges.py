@@ -73,3 +73,74 @@ def test_products_of_scales_beyond_the_range(T, ends, a_scale, b_scale):
     assert_within(d, want, bound + 2.0 ** -148, "D")
     same = ops.grouped_matmul(a, b, ends_of(ends), scale_a=sa, scale_b=sb)
     assert torch.equal(same, d.to(BF16))
+
+
+def workspace():
+    """A products' workspace of the test's own."""
+    return torch.zeros(layer.lib().dg_layer_products_workspace(), dtype=torch.uint8, device="cuda")
+
+
+@pytest.mark.parametrize("ends", [[2100, 2100, 4096], [1400, 2800, 4000]])
+@pytest.mark.parametrize("f32", [False, True])
+def test_weight_gradient_with_drawn_tiles(ends, f32):
+    # 192 tiles of 16 and more K blocks over the SM pairs, an empty group's without any; through the C ABI, in both types
+    T, N, K, E = 4096, 2048, 2048, len(ends)
+    a, dd, e = rand((T, K), 31), rand((T, N), 32), ends_of(ends)
+    L = layer.lib()
+    ws, status = workspace(), torch.zeros(1, dtype=torch.int64, device="cuda")
+    tails = torch.empty(L.dg_layer_grouped_grad_workspace(E, N, K), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    db = [torch.full((E, N, K), 7.0, dtype=F32 if f32 else BF16, device="cuda") for _ in range(3)]
+    for out in db:
+        assert L.dg_layer_grouped_weight_grad(dd.data_ptr(), N, a.data_ptr(), K, e.data_ptr(), E, out.data_ptr(),
+                                              dg.TYPE_F32 if f32 else dg.TYPE_BF16, T, N, K, tails.data_ptr(),
+                                              ws.data_ptr(), status.data_ptr(), stream) == dg.OK
+    assert L.dg_layer_check(status.data_ptr(), stream) == dg.OK
+    start = 0
+    for k, end in enumerate(ends):
+        v, m = lc.product(dd[start:end].t(), a[start:end].t())
+        assert_within(db[0][k], v, lc.product_bound(v, m, end - start, not f32), k)
+        start = end
+    assert torch.equal(db[0], db[1]) and torch.equal(db[0], db[2])
+    assert not ws[:2048].any()
+    if not f32:
+        got = ops.grouped_matmul_backward(dd, a, torch.empty((E, N, K), dtype=BF16, device="cuda").transpose(1, 2), e,
+                                          need=(False, True))[1]
+        assert torch.equal(got.transpose(1, 2), db[0])
+
+
+@pytest.mark.parametrize("T,N,K,ends", [(65, 64, 72, [64, 65]), (300, 264, 200, [0, 100, 100, 131, 300]), (63, 40, 72, [16, 32, 63])])
+def test_weight_gradient_in_32_bits(T, N, K, ends):
+    a, dd, e, E = rand((T, K), 33), rand((T, N), 34), ends_of(ends), len(ends)
+    L = layer.lib()
+    ws, status = workspace(), torch.zeros(1, dtype=torch.int64, device="cuda")
+    tails = torch.empty(L.dg_layer_grouped_grad_workspace(E, N, K), dtype=torch.uint8, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    db = torch.full((E, N, K), 7.0, device="cuda")
+    assert L.dg_layer_grouped_weight_grad(dd.data_ptr(), N, a.data_ptr(), K, e.data_ptr(), E, db.data_ptr(), dg.TYPE_F32, T,
+                                          N, K, tails.data_ptr(), ws.data_ptr(), status.data_ptr(), stream) == dg.OK
+    assert L.dg_layer_check(status.data_ptr(), stream) == dg.OK
+    want, _ = lc.grouped_weight_grad(dd, a, ends)
+    start = 0
+    for k, end in enumerate(ends):
+        _, m = lc.product(dd[start:end].t(), a[start:end].t())
+        assert_within(db[k], want[k].t(), lc.product_bound(want[k].t(), m, end - start, False), k)
+        start = end
+
+
+def test_8bit_rows_with_drawn_tiles():
+    # 16 K blocks and more, 11 x 11 tiles and more: drawn; twice on one workspace, whose counters end at zero
+    T, N, K, ends = 2400, 2816, 2048, [700, 700, 1500, 2300]
+    a, b = rand((T, K), 41, 60.0).to(E4M3), rand((4, N, K), 42, 60.0).to(E4M3)
+    L, e = layer.lib(), ends_of(ends)
+    ws, status = workspace(), torch.zeros(1, dtype=torch.int64, device="cuda")
+    stream = torch.cuda.current_stream().cuda_stream
+    want, bound = lc.grouped(a, b.transpose(1, 2), ends)
+    for _ in range(2):
+        d = torch.full((T, N), 7.0, dtype=BF16, device="cuda")
+        assert L.dg_layer_grouped_matmul(a.data_ptr(), K, dg.TYPE_E4M3, b.data_ptr(), K, N * K, dg.TYPE_E4M3, 0, e.data_ptr(),
+                                         4, None, 0, None, 0, 0, d.data_ptr(), dg.TYPE_BF16, T, N, K, ws.data_ptr(),
+                                         status.data_ptr(), stream) == dg.OK
+        assert_within(d, want, bound, "D")
+        assert not ws[:2048].any()
+    assert L.dg_layer_check(status.data_ptr(), stream) == dg.OK

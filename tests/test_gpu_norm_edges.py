@@ -186,3 +186,46 @@ def test_rows_of_no_values():
     assert q.rows == 6 and ops.dequantize_mx4(q).shape == (6, 0)
     d = ops.mx4_matmul(q, ops.quantize_mx4(torch.zeros((8, 0), dtype=BF16, device="cuda")))
     assert d.shape == (6, 8) and not d.any()
+
+
+@pytest.mark.parametrize("rows,hidden", [(700, 2048), (400, 8200)])
+@pytest.mark.parametrize("res", [None, BF16, F32])
+def test_special_rows_among_streamed_ones(rows, hidden, res):
+    # the same rows a few at a time take another kernel, whose results are known
+    x, w = rand((rows, hidden), 141), rand((hidden,), 142, dtype=F32)
+    r = None if res is None else rand((rows, hidden), 143, 2.0, res)
+    x[0] = x[rows // 2] = 0
+    x[1, 3] = x[rows - 1, hidden - 1] = float("nan")
+    x[2, 3], x[rows - 2, 5] = float("inf"), -float("inf")
+    w[7] = 3e38                                            # products beyond fp32 where the row's value is above 1
+    if r is not None:
+        r[0] = r[rows // 2] = 0
+    at = [0, 1, 2, 3, 4, rows // 2, rows - 3, rows - 2, rows - 1]
+    for kw in (dict(), dict(scale=0.01)):
+        got = ops.add_rms_norm(x, w, residual=r, out_dtype=E4M3, keep_rstd=True, **kw)
+        few = ops.add_rms_norm(x[at], w, residual=None if r is None else r[at], out_dtype=E4M3, keep_rstd=True, **kw)
+        assert torch.equal(got.residual[at].view(torch.uint8), few.residual.view(torch.uint8))
+        # sums of squares are added in another order
+        rel = 2 * lc.norm_rel(hidden)
+        ok = torch.isfinite(few.rstd)
+        assert torch.equal(torch.isfinite(got.rstd[at]), ok)
+        assert_within(got.rstd[at][ok], few.rstd[ok].double(), rel * few.rstd[ok].double(), "rstd")
+        a, b = got.y.view(torch.uint8)[at].view(E4M3).float(), few.y.float()
+        assert torch.equal(torch.isnan(a), torch.isnan(b))
+        a, b = torch.nan_to_num(a).double(), torch.nan_to_num(b).double()
+        assert_within(a, b, torch.maximum(b.abs() * 2.0 ** -3, torch.full_like(b, 2.0 ** -9)), "q")
+        if not kw:
+            assert got.scale[0] == 1 and got.scale[1] == 1 and torch.isfinite(got.scale).all()
+            assert_within(got.scale[at], few.scale.double(), (rel + 4 * U32) * few.scale.double(), "scale")
+
+
+@pytest.mark.parametrize("res", [BF16, F32])
+def test_streamed_in_place_and_given_scale(res):
+    rows, hidden = 700, 2048
+    x, w, r = rand((rows, hidden), 151), rand((hidden,), 152), rand((rows, hidden), 153, 2.0, res)
+    h, _, y = lc.norm(x, w, r)
+    apart = ops.add_rms_norm(x, w, residual=r, out_dtype=E4M3, scale=2.0 ** -6)
+    got = ops.add_rms_norm(x, w, residual=r, out_dtype=E4M3, scale=2.0 ** -6, inplace=True)
+    assert got.residual is r and torch.equal(r, h) and torch.equal(apart.residual, h)
+    assert torch.equal(got.y.view(torch.uint8), apart.y.view(torch.uint8))
+    check_q(got.y, torch.full((rows,), 2.0 ** -6, device="cuda"), y, hidden, E4M3)

@@ -13,7 +13,7 @@
 // hand-off needs no barrier), because a block that loads, reduces and stores by
 // turns leaves the memory idle in between.
 //
-// Back to back on a GB300: 8192 x 16384, bf16 residual, to e4m3 142 us (6.6 TB/s;
+// Back to back on a GB300: 8192 x 16384, bf16 residual, to e4m3 141 us (6.7 TB/s;
 // 186 us before streaming), 8192 x 8192 80 us, 16384 x 2048 46 us; 4 rows of 8192
 // 2.9 us; the gradient of 4099 x 8192 53 us and 4 us for the weight's (4.9 TB/s);
 // rows of 10945 (no vectors) 3.1 TB/s.  One vector per thread, or four, instead
@@ -32,7 +32,6 @@ using dgl::begin_kernel;
 
 constexpr float kE4M3Max = 448.f, kE5M2Max = 57344.f;
 constexpr float kMinScale = 0x1p-126f;  // the least row scale: the smallest normal number
-constexpr float kMaxFinite = 3.4028234663852886e38f;
 
 // ---------------------------------------------------------------- vectors
 
@@ -160,41 +159,43 @@ struct NormArgs {
 // rounds t mul to 8 bits.  |y| / 2 < |t| <= |y|: t leaves fp32's range only where y
 // does, and mul stays below 2^128 (h w alone may be far below 1 or overflow while
 // y is an ordinary number).  With the row's own scale c = top r / max, `top` the
-// largest |t| of a finite y, r cancels: mul = max / top, so q carries two
-// roundings for bf16 h and w and hardly ever crosses a rounding boundary of the 8
-// bits that the exact value does not.
+// largest finite |t|, r cancels: mul = max / top, so q carries two roundings for
+// bf16 h and w and hardly ever crosses a rounding boundary of the 8 bits that the
+// exact value does not.
 struct RowFactor {
-  float f, r, most;  // most: the largest |t| whose y is finite
+  float f, r;
 };
 __device__ __forceinline__ RowFactor row_factor(float rstd, const float* given) {
-  if (!(rstd > 0.f)) return RowFactor{0.f, rstd, 0.f};  // a sum of squares beyond fp32 (finite values become 0), or a NaN
-  if (isinf(rstd)) return RowFactor{1.f, rstd, 0.f};    // a row of zeros without eps: NaN
-  const uint32_t b = __float_as_uint(rstd);             // normal: rsqrt of an fp32 value
+  if (!(rstd > 0.f)) return RowFactor{0.f, rstd};  // a sum of squares beyond fp32 (finite values become 0), or a NaN
+  const uint32_t b = __float_as_uint(rstd);        // normal (rsqrt of an fp32 value), or infinite: t and r are then too
   float f = __uint_as_float(b & 0x7f800000u), r = __uint_as_float((b & 0x007fffffu) | 0x3f800000u);
   // r / c stays finite for a subnormal c as well
   if (given && fabsf(__ldg(given)) < kMinScale) f *= 0x1p24f, r *= 0x1p-24f;
-  return RowFactor{f, r, kMaxFinite / r};
+  return RowFactor{f, r};
 }
 struct RowScale {
   float c, mul;
 };
+// ORDINARY: `top` and r are within the bounds below, so that y and c are normal numbers.
+template <bool ORDINARY = false>
 __device__ __forceinline__ RowScale row_scale(float top, float r, const float* given, bool e5m2) {
   if (given) {
     const float c = __ldg(given);
     return RowScale{c, r / c};
   }
-  const float most = e5m2 ? kE5M2Max : kE4M3Max, y = top * r, c = y / most;
+  const float most = e5m2 ? kE5M2Max : kE4M3Max, y = top * r;
+  if (ORDINARY) return RowScale{y / most, most / top};
   if (!(y > 0.f)) return RowScale{1.f, r};  // a row of zeros (or one that is not finite, whose values stay so)
+  const float c = isinf(y) ? top / most * r : y / most;
   return c > kMinScale ? RowScale{c, most / top} : RowScale{kMinScale, r / kMinScale};
 }
-// Where t = h w without the factor f serves as well, in the streamed kernel: a
-// top product from 2^-64 (its row's 8-bit steps are then far above the subnormal
-// one) to 2^60, with rstd below that, so that y is finite; and, with a given
-// scale, no infinite product and no multiplier above 2^100.
-constexpr float kOrdinaryMin = 0x1p-64f, kOrdinaryMax = 0x1p60f, kOrdinaryMul = 0x1p100f;
+// Where t = h w without the factor f serves as well, in the streamed kernel: rstd
+// from 2^-40 to 2^60; a top product from 2^-64 (its row's 8-bit steps are then far
+// above the subnormal one) to 2^60; with a given scale instead no infinite product
+// and no multiplier above 2^100.
+constexpr float kOrdinaryDev = 0x1p-40f, kOrdinaryMin = 0x1p-64f, kOrdinaryMax = 0x1p60f, kOrdinaryMul = 0x1p100f;
 __device__ __forceinline__ float scaled_by(float h, float keep, float w) { return h * keep * w; }
-// |t|, or 0 where y is not finite (a NaN stays, and the maximum ignores it)
-__device__ __forceinline__ float finite_mag(float t, float most) { return fabsf(t) > most ? 0.f : fabsf(t); }
+__device__ __forceinline__ float finite_mag(float t) { return isinf(t) ? 0.f : fabsf(t); }
 
 // RT: the residual's type (0 none, 1 bf16, 2 fp32).  The row stays in
 // registers: NV vectors of 8 values per thread.
@@ -245,7 +246,7 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) add_rms_norm_kernel(const
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
   float top = 0.f;
-  const RowFactor by = OUT8 ? row_factor(rstd, p.scale_in) : RowFactor{rstd, 1.f, 0.f};
+  const RowFactor by = OUT8 ? row_factor(rstd, p.scale_in) : RowFactor{rstd, 1.f};
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = threadIdx.x * 8 + k * step;
@@ -255,7 +256,7 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) add_rms_norm_kernel(const
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         h[k][j] = scaled_by(h[k][j], by.f, w[j]);
-        if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k][j], by.most));
+        if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k][j]));
       }
       if constexpr (!OUT8) store_bf16<8>(p.y, row * p.hidden + i, h[k]);
     }
@@ -339,11 +340,11 @@ __global__ void __launch_bounds__(1024) add_rms_norm_spread_kernel(const __grid_
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
   float top = 0.f;
-  const RowFactor by = OUT8 ? row_factor(rstd, p.scale_in) : RowFactor{rstd, 1.f, 0.f};
+  const RowFactor by = OUT8 ? row_factor(rstd, p.scale_in) : RowFactor{rstd, 1.f};
 #pragma unroll
   for (int k = 0; k < N; ++k) {
     h[k] = scaled_by(h[k], by.f, w.at(k, p.hidden));
-    if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k], by.most));
+    if constexpr (OUT8) top = fmaxf(top, finite_mag(h[k]));
   }
   const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
   float mul = 1.f;
@@ -436,7 +437,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const __grid_co
   ss = row_reduce<Add>(ss, part);
   const float rstd = rsqrtf(ss / (float)p.hidden + p.eps);
   if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-  const RowFactor by = OUT8 ? row_factor(rstd, p.scale_in) : RowFactor{rstd, 1.f, 0.f};
+  const RowFactor by = OUT8 ? row_factor(rstd, p.scale_in) : RowFactor{rstd, 1.f};
   auto value = [&](int64_t from, float(&h)[8]) {
     float w[8];
     load_chunk<RT == 2, VEC>(hp, h0, from, hidden, h);
@@ -456,7 +457,7 @@ __global__ void __launch_bounds__(1024) add_rms_norm_long_kernel(const __grid_co
         float h[8];
         value(from, h);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(h[j], by.most));
+        for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(h[j]));
       });
       top = row_reduce<Max>(top, part + 33);
     }
@@ -607,7 +608,7 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(con
     if constexpr (OUT8) {
       float top = 0.f;
       // Ordinary rows do without the factor f, which costs a product per value (8192 x
-      // 16384: 142 us, 162 with f in every row).
+      // 16384: 141 us, 162 with f in every row).
 #pragma unroll
       for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -616,7 +617,7 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(con
           top = fmaxf(top, fabsf(h[k][j]));
         }
       const bool e5m2 = p.fp8 == DG_TYPE_E5M2;
-      bool ordinary = rstd > 0.f && rstd < kOrdinaryMax;
+      bool ordinary = rstd > kOrdinaryDev && rstd < kOrdinaryMax;
       if (p.scale_in) {  // (each thread for itself)
         ordinary = ordinary && !isinf(top) && fabsf(rstd / __ldg(p.scale_in)) < kOrdinaryMul;
       } else {  // the same for the whole row
@@ -639,7 +640,7 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(con
             float t[8];
             value(i, t);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(t[j], by.most));
+            for (int j = 0; j < 8; ++j) top = fmaxf(top, finite_mag(t[j]));
           }
           top = row_reduce<Max>(top, part[flip] + 66);
         }
@@ -655,7 +656,7 @@ __global__ void __launch_bounds__(kStreamThreads) add_rms_norm_stream_kernel(con
         }
         continue;
       }
-      const RowScale sc = row_scale(top, rstd, p.scale_in, e5m2);
+      const RowScale sc = row_scale<true>(top, rstd, p.scale_in, e5m2);
       if (p.scale && threadIdx.x == 0) p.scale[row] = sc.c;
 #pragma unroll
       for (int k = 0; k < NV; ++k) {

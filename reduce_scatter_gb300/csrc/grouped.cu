@@ -17,10 +17,12 @@
 // the loads write and the MMAs read), which is all it has: the tensor pipe is
 // busy for 95 % of the cycles.  A shorter tile of n rows needs about 256 + n
 // cycles a K block against 2 n of the MMAs, so few tall tiles are best where
-// there are enough of them.  Back to back on a GB300: 16384 rows of 8 experts of
-// 8192 x 8192 in bf16 1215 us even, 1290 uneven (1810, 1700 TFLOP/s, under the
-// power cap; alone 1087); 10007 rows of 19 of 3328 x 8192 in e4m3 201 us (2700
-// TFLOP/s); 12 rows of 12 of 2048 x 8192 37 us (5.4 TB/s of weights).
+// there are enough of them.  (That model gives 130 to 155 us of the 197 below; the
+// rest is not accounted for.)  Back to back on a GB300: 16384 rows of 8 experts of
+// 8192 x 8192 in bf16 1253 us even, 1317 uneven (1755, 1670 TFLOP/s, under the
+// power cap; alone 1138, 1195); 10007 rows of 24 (5 empty) of 3328 x 8192 in e4m3 197
+// us (2770 TFLOP/s), of 19 188 us; 12 rows of 12 of 2048 x 8192 39 us (5.2 TB/s of
+// weights).
 
 #include <cuda_bf16.h>
 

@@ -6,8 +6,8 @@
 // The exponent is read from the maximum's bits, 2^-E is exact in fp32 and so is
 // the scaled value, so the one rounding is the conversion to e2m1 (nearest,
 // ties to even, saturating at 6).  Bound by memory: 2 bytes read and 17/32
-// written per bf16 value.  8192 x 16384 back to back on a GB300: 54 us (6.3 TB/s),
-// the way back 55 us (6.2 TB/s); two rows per warp 64 us, eight 59 and 55.
+// written per bf16 value.  8192 x 16384 back to back on a GB300: 53 us (6.4 TB/s),
+// the way back 54 us (6.2 TB/s); two rows per warp 64 us, eight 59 and 55.
 
 #include <cuda_bf16.h>
 

@@ -16,8 +16,10 @@
 //
 // Bound by the tensor cores, and by the scales' copies between the MMAs: per K
 // block four MMAs of 83 cycles and six copies of about 40 take about 500.
-// 16384 x 13312 x 16384 back to back on a GB300: 980 us (7300 TFLOP/s, under the
-// power cap; alone 892); 8 x 8192 x 28672: 27 us (4.6 TB/s of weights).
+// 16384 x 13312 x 16384 back to back on a GB300: 1010 us (7070 TFLOP/s, under the
+// power cap; alone 930); 8 x 8192 x 28672: 28 us (4.5 TB/s of weights).  At six
+// times the measured bf16 rate, the chip's nominal ratio, the operations of the
+// first take 630 us.
 
 #include <cuda_bf16.h>
 

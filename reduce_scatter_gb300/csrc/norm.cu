@@ -14,10 +14,14 @@
 // turns leaves the memory idle in between.
 //
 // Back to back on a GB300: 8192 x 16384, bf16 residual, to e4m3 141 us (6.7 TB/s;
-// 186 us before streaming), 8192 x 8192 80 us, 16384 x 2048 46 us; 4 rows of 8192
-// 2.9 us; the gradient of 4099 x 8192 53 us and 4 us for the weight's (4.9 TB/s);
-// rows of 10945 (no vectors) 3.1 TB/s.  One vector per thread, or four, instead
-// of two: 97 and 121 us for 8192 x 8192.
+// 186 us before streaming), 8192 x 8192 80 us, 16384 x 2048 45 us; 4 rows of 8192
+// 2.8 us; fp32 residual, 8192 x 16384 316 us (4.7 TB/s, two stages), 8192 x 8192 144
+// us; the gradient of 4099 x 8192 54 us with the weight's (4.9 TB/s), in fp32 114 us
+// (4.1).  Without vectors 8192 x 3001 65 us (2.7 TB/s; bf16 output 56, gradient 94),
+// 6437 x 10945 254 us (1.9; 222).  The gradients that loop (fp32 of 4099 x 16384 494
+// us, 6437 x 10945 538) stay at 1.1 to 1.9 TB/s: partial sums in global memory, values
+// loaded twice and one by one.  One vector per thread, or four, instead of two: 97
+// and 121 us for 8192 x 8192.
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

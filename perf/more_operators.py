@@ -155,7 +155,8 @@ def _plain_blocks(x, kind, block_rows, pow2=False):
     scale, num, den = amax / top, torch.full_like(amax, top), amax
     if pow2:
         m, e = torch.frexp(amax)  # top = 0.875 * 2^9 or 2^16
-        scale = torch.ldexp(torch.ones_like(amax), e - (9 if kind == "e4m3" else 16) + (m > 0.875).to(e.dtype))
+        e = e - (9 if kind == "e4m3" else 16) + (m > 0.875).to(e.dtype)
+        scale = ((e.clamp(min=-126) + 127) << 23).view(torch.float32)  # (exp2 is not exact on the GPU)
         num, den = 1.0 / scale, torch.ones_like(amax)
     least, one = scale <= MIN_SCALE, torch.ones_like(amax)
     scale, num, den = torch.where(least, MIN_SCALE * one, scale), torch.where(least, one / MIN_SCALE, num), torch.where(least, one, den)

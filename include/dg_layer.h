@@ -2,7 +2,8 @@
  * dg_layer.h -- C ABI of the operators around the tensor-parallel GEMM of
  * dg.h: residual add with RMS norm (16- or 8-bit output, and its gradient),
  * products grouped by expert (forward and gradients), microscaled 4-bit
- * quantisation and the product of microscaled 4-bit tensors.
+ * quantisation and the product of microscaled 4-bit tensors, 8-bit tensors
+ * with a scale for each block of 128 and their product.
  *
  * Every call checks its arguments, enqueues its work on `stream` (a
  * cudaStream_t of the current device) and returns a dg_status (dg.h);
@@ -123,6 +124,36 @@ int dg_layer_mx4_dequantize(const void* codes, const void* scales, void* y, int 
 int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, const void* b_codes, const void* b_scales,
                         void* D, int d_type, int64_t M, int64_t N, int64_t K, void* workspace, void* status,
                         void* stream);
+
+/* 8-bit values (e4m3 / e5m2) with an fp32 scale for each block of 128 columns of
+ * one row (block_rows 1) or of 128 rows (block_rows 128); the blocks at the
+ * edges hold what is left.  With amax the largest finite |x| of a block and top
+ * the type's largest finite value, c = amax / top (1 for a block of zeros, at
+ * least 2^-126) and the values are those nearest to x top / amax, ties to even;
+ * with pow2, c = 2^ceil(log2(amax / top)) and the values are those nearest to
+ * x / c.  A NaN or an infinity becomes NaN, stays alone and does not enter the
+ * scale.
+ *   values  rows x cols, densely packed, 16-byte aligned; cols % 16 == 0
+ *   scales  of block (i, j) at scales[i * s_row + j * s_block]
+ * x: bf16 or fp32 (x_type), ld_x elements from row to row, rows 16-byte aligned. */
+int dg_layer_block8_quantize(const void* x, int64_t ld_x, int x_type, void* values, int type, float* scales,
+                             int64_t s_row, int64_t s_block, int block_rows, int pow2, int64_t rows, int64_t cols,
+                             void* stream);
+/* The values times their scales, as bf16 (one rounding) or fp32, densely packed, 16-byte aligned. */
+int dg_layer_block8_dequantize(const void* values, int type, const float* scales, int64_t s_row, int64_t s_block,
+                               int block_rows, void* y, int y_type, int64_t rows, int64_t cols, void* stream);
+/* Product of two such tensors,
+ *     D[m, n] = sum over blocks j of 128 k of sa[m, j] sb[n, j] sum_{k in j} A[m, k] B[n, k]
+ * (fp32 sums; a block's two scales are multiplied first, in fp32).  a holds A
+ * (M x K) or, with trans_a, its transpose (K x M); b holds the transpose (N x K)
+ * of the product's second matrix with trans_b, or that matrix (K x N) without.  An operand whose rows
+ * are K's has blocks of 128 rows.  D: bf16 or fp32 (d_type), M x N densely
+ * packed.  N % 8 == 0, the columns of a and of b % 16 == 0; M, N, K <= 2^31 - 256.
+ * workspace as for dg_layer_grouped_matmul. */
+int dg_layer_block8_matmul(const void* a, int a_type, const float* a_scales, int64_t sa_row, int64_t sa_block,
+                           int a_block_rows, int trans_a, const void* b, int b_type, const float* b_scales,
+                           int64_t sb_row, int64_t sb_block, int b_block_rows, int trans_b, void* D, int d_type,
+                           int64_t M, int64_t N, int64_t K, void* workspace, void* status, void* stream);
 
 /* Synchronize `stream`, read the status word and clear it: DG_OK, or
  * DG_ERR_HANG if a product's pipeline wait ran out since the last check. */

@@ -69,7 +69,9 @@ int encode_map(CUtensorMap* map, const void* base, int esz, int rank, const int6
   for (int i = 0; i < rank; ++i) d[i] = (cuuint64_t)dims[i];
   for (int i = 0; i + 1 < rank; ++i) s[i] = (cuuint64_t)(strides[i] * esz);
   const CUresult r =
-      fn(map, esz == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, (cuuint32_t)rank,
+      fn(map, esz == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+             : esz == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                        : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, (cuuint32_t)rank,
          const_cast<void*>(base), d, s, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS)

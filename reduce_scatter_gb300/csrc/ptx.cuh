@@ -228,7 +228,7 @@ __host__ __device__ constexpr uint32_t idesc_of(uint32_t p_fmt, uint32_t q_fmt, 
   return (1u << 4) | (p_fmt << 7) | (q_fmt << 10) | ((p_mn ? 1u : 0u) << 15) | ((q_mn ? 1u : 0u) << 16) |
          ((uint32_t)(kPairFeats >> 4) << 24);
 }
-__device__ __forceinline__ uint32_t idesc_columns(uint32_t n) { return (n >> 3) << 17; }
+__host__ __device__ __forceinline__ uint32_t idesc_columns(uint32_t n) { return (n >> 3) << 17; }
 
 // ------------------------------------------------------------- order of tiles
 

@@ -12,6 +12,7 @@
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/core/grad_mode.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <ATen/ops/full.h>
@@ -500,6 +501,114 @@ PyObject* mx4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ------------------------------------------------------ 8-bit blocks of 128
+
+int64_t whole(PyObject* o, const char* what) {
+  const int64_t v = PyLong_AsLongLong(o);
+  TORCH_CHECK_TYPE(!(v == -1 && PyErr_Occurred()), what, " must be a whole number");
+  return v;
+}
+
+// Scales of a rows x cols matrix: those of neighbouring rows lie next to each other.
+Tensor fresh_scales(const Tensor& like, int64_t rows, int64_t cols) {
+  const int64_t blocks = (cols + 127) / 128;
+  return at::detail::empty_strided_cuda({rows, blocks}, {1, rows > 0 ? rows : 1}, at::kFloat, like.device());
+}
+
+PyObject* quantize_block8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 4);
+    const Tensor& x = tensor(a[0], "x");
+    const int64_t br = whole(a[1], "block_rows");
+    const at::ScalarType type = dtype(a[2]);
+    TORCH_CHECK_TYPE(bf16_or_f32(x.scalar_type()), "x must be bfloat16 or float32, got ", x.scalar_type());
+    TORCH_CHECK_VALUE(is8(type), "dtype must be a float8 type, got ", type);
+    TORCH_CHECK_VALUE(br == 1 || br == 128, "block_rows must be 1 or 128, got ", br);
+    TORCH_CHECK_VALUE(x.dim() >= 1, "x must have a last dimension");
+    const int64_t cols = x.size(-1);
+    same_device(x, {});
+    TORCH_CHECK_VALUE(cols % 16 == 0, "the last dimension (", cols, ") must be a multiple of 16");
+    const Site at(x);
+    const Tensor x2 = as_operand(as_rows(x, cols));
+    const int64_t rows = x2.size(0);
+    const Tensor values = fresh(x, {rows, cols}, type), scales = fresh_scales(x, (rows + br - 1) / br, cols);
+    check_status(dg_layer_block8_quantize(x2.data_ptr(), x2.stride(0), type_of(x2.scalar_type()), values.data_ptr(), type_of(type),
+                                          static_cast<float*>(scales.data_ptr()), scales.stride(0), scales.stride(1), (int)br,
+                                          a[3] == Py_True, rows, cols, at.handle()));
+    return Py_BuildValue("(NNL)", wrap(values), wrap(scales), (long long)br);
+  });
+}
+
+// A (values, scales, block_rows) tuple.
+struct Block8 {
+  Tensor values, scales;
+  int64_t rows, cols, block_rows;
+  Block8(PyObject* o, const char* what) {
+    TORCH_CHECK_TYPE(PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 3, what, " must be a Block8Tensor");
+    values = tensor(PyTuple_GET_ITEM(o, 0), "values");
+    scales = tensor(PyTuple_GET_ITEM(o, 1), "scales");
+    block_rows = whole(PyTuple_GET_ITEM(o, 2), "block_rows");
+    TORCH_CHECK_VALUE(block_rows == 1 || block_rows == 128, what, ".block_rows must be 1 or 128, got ", block_rows);
+    TORCH_CHECK_VALUE(is8(values.scalar_type()) && values.dim() == 2 && values.is_contiguous() && values.size(1) % 16 == 0, what,
+                      ".values must be a contiguous float8 matrix whose columns are a multiple of 16, got ", values.scalar_type(),
+                      " ", values.sizes());
+    rows = values.size(0), cols = values.size(1);
+    const int64_t sr = (rows + block_rows - 1) / block_rows, sc = (cols + 127) / 128;
+    TORCH_CHECK_VALUE(scales.scalar_type() == at::kFloat && scales.dim() == 2 && scales.size(0) == sr && scales.size(1) == sc, what,
+                      ".scales must be float32 of shape (", sr, ", ", sc, "), got ", scales.scalar_type(), " ", scales.sizes());
+    TORCH_CHECK_VALUE(!at::GradMode::is_enabled() || !(values.requires_grad() || scales.requires_grad()), what,
+                      ": 8-bit blocks have no gradient: call under torch.no_grad()");
+  }
+  // (a view may start off the alignment that the kernels need)
+  void align() {
+    if (reinterpret_cast<uintptr_t>(values.data_ptr()) % 16 != 0) values = fresh(values, values.sizes(), values.scalar_type()).copy_(values);
+  }
+  const float* scale_ptr() const { return static_cast<const float*>(scales.data_ptr()); }
+};
+
+PyObject* dequantize_block8(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 2);
+    Block8 q(a[0], "q");
+    const at::ScalarType out = dtype(a[1]);
+    TORCH_CHECK_VALUE(bf16_or_f32(out), "out_dtype must be bfloat16 or float32, got ", out);
+    same_device(q.values, {&q.scales});
+    const Site at(q.values);
+    q.align();
+    const Tensor y = fresh(q.values, {q.rows, q.cols}, out);
+    check_status(dg_layer_block8_dequantize(q.values.data_ptr(), type_of(q.values.scalar_type()), q.scale_ptr(), q.scales.stride(0),
+                                            q.scales.stride(1), (int)q.block_rows, y.data_ptr(), type_of(out), q.rows, q.cols,
+                                            at.handle()));
+    return wrap(y);
+  });
+}
+
+PyObject* block8_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 5);
+    Block8 a(args[0], "a"), b(args[1], "b");
+    const bool ta = args[2] == Py_True, tb = args[3] == Py_True;
+    const at::ScalarType out = dtype(args[4]);
+    const int64_t M = ta ? a.cols : a.rows, K = ta ? a.rows : a.cols, N = tb ? b.rows : b.cols;
+    TORCH_CHECK_VALUE((tb ? b.cols : b.rows) == K, "a ", a.values.sizes(), ta ? " (transposed)" : "", " and b ", b.values.sizes(),
+                      tb ? " (transposed)" : "", " do not fit");
+    TORCH_CHECK_VALUE((!ta || a.block_rows == 128) && (tb || b.block_rows == 128),
+                      "an operand whose rows are summed over needs blocks of 128 rows");
+    TORCH_CHECK_VALUE(bf16_or_f32(out), "out_dtype must be bfloat16 or float32, got ", out);
+    same_device(a.values, {&a.scales, &b.values, &b.scales});
+    const Site at(a.values);
+    a.align(), b.align();
+    const Tensor D = fresh(a.values, {M, N}, out);
+    const Tensor ws = products_workspace(at, a.values);
+    check_status(dg_layer_block8_matmul(
+        a.values.data_ptr(), type_of(a.values.scalar_type()), a.scale_ptr(), a.scales.stride(0), a.scales.stride(1),
+        (int)a.block_rows, ta, b.values.data_ptr(), type_of(b.values.scalar_type()), b.scale_ptr(), b.scales.stride(0),
+        b.scales.stride(1), (int)b.block_rows, tb, D.data_ptr(), type_of(out), M, N, K, ws.data_ptr(),
+        status_word(at, a.values), at.handle()));
+    return wrap(D);
+  });
+}
+
 // ------------------------------------------------------------------- module
 
 PyObject* check(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -550,6 +659,9 @@ PyMethodDef g_methods[] = {DGL_METHOD(add_rms_norm),
                            DGL_METHOD(quantize_mx4),
                            DGL_METHOD(dequantize_mx4),
                            DGL_METHOD(mx4_matmul),
+                           DGL_METHOD(quantize_block8),
+                           DGL_METHOD(dequantize_block8),
+                           DGL_METHOD(block8_matmul),
                            DGL_METHOD(check),
                            DGL_METHOD(clear_workspaces),
                            DGL_METHOD(set_error),

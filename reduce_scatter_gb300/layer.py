@@ -35,7 +35,8 @@ EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "dg_
 EXPORTS = ("dg_layer_add_rms_norm", "dg_layer_add_rms_norm_backward", "dg_layer_add_rms_norm_backward_workspace",
            "dg_layer_products_workspace", "dg_layer_grouped_matmul", "dg_layer_grouped_grad_workspace",
            "dg_layer_grouped_weight_grad", "dg_layer_mx4_scale_bytes", "dg_layer_mx4_quantize",
-           "dg_layer_mx4_dequantize", "dg_layer_mx4_matmul", "dg_layer_check", "dg_layer_last_error")
+           "dg_layer_mx4_dequantize", "dg_layer_mx4_matmul", "dg_layer_block8_quantize", "dg_layer_block8_dequantize",
+           "dg_layer_block8_matmul", "dg_layer_check", "dg_layer_last_error")
 
 _LIB = None
 _EXT = None
@@ -61,6 +62,10 @@ def lib():
             "mx4_quantize": (i32, [vp, i64, i32, vp, vp, i64, i64, vp]),
             "mx4_dequantize": (i32, [vp, vp, vp, i32, i64, i64, vp]),
             "mx4_matmul": (i32, [vp, vp, vp, vp, vp, i32, i64, i64, i64, vp, vp, vp]),
+            "block8_quantize": (i32, [vp, i64, i32, vp, i32, vp, i64, i64, i32, i32, i64, i64, vp]),
+            "block8_dequantize": (i32, [vp, i32, vp, i64, i64, i32, vp, i32, i64, i64, vp]),
+            "block8_matmul": (i32, [vp, i32, vp, i64, i64, i32, i32, vp, i32, vp, i64, i64, i32, i32, vp, i32, i64, i64,
+                                    i64, vp, vp, vp]),
             "check": (i32, [vp, vp]),
             "last_error": (ctypes.c_char_p, []),
         }
@@ -262,3 +267,52 @@ def mx4_matmul(a: MX4Tensor, b: MX4Tensor, *, out_dtype: torch.dtype = torch.bfl
     activations), ``b`` N x K (a weight as it is stored), N % 8 == 0; fp32
     accumulation, ``out_dtype`` bfloat16 or float32."""
     return (_EXT or _load()).mx4_matmul(a, b, out_dtype)
+
+
+# ------------------------------------------------------ 8-bit blocks of 128
+
+
+class Block8Tensor(NamedTuple):
+    """A matrix in 8 bits with a scale for each block of 128: ``values`` (rows,
+    cols), contiguous, float8_e4m3fn or float8_e5m2; ``scales`` float32
+    (ceil(rows / block_rows), ceil(cols / 128)), of any strides (those that
+    :func:`quantize_block8` makes have neighbouring rows next to each other);
+    ``block_rows``: 1 or 128, the rows that share a scale.  Stands for
+    ``values * scales``, each scale over its block."""
+
+    values: torch.Tensor
+    scales: torch.Tensor
+    block_rows: int
+
+
+def quantize_block8(x: torch.Tensor, *, block_rows: int = 1, dtype: torch.dtype = torch.float8_e4m3fn,
+                    pow2: bool = False) -> Block8Tensor:
+    """``x`` (..., cols), bfloat16 or float32, its leading dimensions flattened
+    into rows, in 8 bits with a float32 scale for each ``block_rows`` x 128:
+    ``max|x| / top`` (``top``: the type's largest finite value; 1 for a block of
+    zeros, at least 2^-126), the values nearest to ``x * top / max|x|``, ties to
+    even.  ``pow2`` rounds the scale up to a power of two, so that the values
+    are exact in bfloat16.  A NaN or an infinity becomes NaN, alone, and does
+    not enter the scale.  cols % 16 == 0.  Not differentiable: an ``x`` that
+    requires a gradient is refused outside ``torch.no_grad()``."""
+    if x.requires_grad and torch.is_grad_enabled():
+        raise ValueError("8-bit values have no gradient: call under torch.no_grad(), or on x.detach()")
+    return Block8Tensor(*(_EXT or _load()).quantize_block8(x, block_rows, dtype, bool(pow2)))
+
+
+def dequantize_block8(q: Block8Tensor, *, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """The (rows, cols) values of ``q`` in bfloat16 (one rounding; none for
+    power-of-two scales) or float32."""
+    return (_EXT or _load()).dequantize_block8(q, out_dtype)
+
+
+def block8_matmul(a: Block8Tensor, b: Block8Tensor, *, trans_a: bool = False, trans_b: bool = True,
+                  out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+    """``a @ b.T`` over the values of two tensors in 8-bit blocks: ``a`` M x K
+    (the activations), ``b`` N x K (a weight as it is stored); with ``trans_a``
+    ``a.T @ ...`` of a K x M ``a``, without ``trans_b`` ``... @ b`` of a K x N
+    ``b``.  An operand whose rows are summed over (those two) needs blocks of
+    128 rows.  The element types may differ.  fp32 accumulation, each block's
+    sum times its two scales (their product in fp32); N % 8 == 0; ``out_dtype``
+    bfloat16 or float32."""
+    return (_EXT or _load()).block8_matmul(a, b, bool(trans_a), bool(trans_b), out_dtype)

@@ -36,7 +36,8 @@ keep their rows of A and the B shards rotate instead).
 The operators around these products (:mod:`reduce_scatter_gb300.layer`) are
 exported here too: ``add_rms_norm`` and ``add_rms_norm_backward``,
 ``grouped_matmul`` and ``grouped_matmul_backward``, ``quantize_mx4``,
-``dequantize_mx4``, ``mx4_matmul``, ``check_products``.
+``dequantize_mx4``, ``mx4_matmul``, ``quantize_block8``,
+``dequantize_block8``, ``block8_matmul``, ``check_products``.
 """
 
 from __future__ import annotations
@@ -46,8 +47,9 @@ import threading
 import torch
 
 from . import dg, layer
-from .layer import (MX4Tensor, NormResult, add_rms_norm, add_rms_norm_backward, check_products,  # noqa: F401
-                    dequantize_mx4, grouped_matmul, grouped_matmul_backward, mx4_matmul, quantize_mx4)
+from .layer import (Block8Tensor, MX4Tensor, NormResult, add_rms_norm, add_rms_norm_backward, block8_matmul,  # noqa: F401
+                    check_products, dequantize_block8, dequantize_mx4, grouped_matmul, grouped_matmul_backward,
+                    mx4_matmul, quantize_block8, quantize_mx4)
 
 _lock = threading.Lock()
 _plans: dict = {}

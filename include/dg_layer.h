@@ -1,6 +1,6 @@
 /*
  * dg_layer.h -- C ABI of the operators around the tensor-parallel GEMM of
- * dg.h: residual add with RMS norm (16- or 8-bit output, and its gradient),
+ * dg.h: residual add with RMS norm or layer norm (16- or 8-bit output, and their gradients),
  * products grouped by expert (forward and gradients), microscaled 4-bit
  * quantisation and the product of microscaled 4-bit tensors, 8-bit tensors
  * with a scale for each block of 128 and their product.
@@ -64,6 +64,44 @@ int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h,
                                    int64_t ld_dh, void* dx, void* dweight, void* workspace, int64_t rows,
                                    int64_t hidden, void* stream);
 
+/* Residual add and layer norm over rows of `hidden` values:
+ *     h = x + residual        rounded to the residual's type (h = x without one)
+ *     y = (h - mean(h)) * rsqrt(mean((h - mean(h))^2) + eps) * weight + bias
+ * written as bf16 (y_type DG_TYPE_BF16), or as 8-bit blocks of 1 x 128
+ * (DG_TYPE_E4M3 / E5M2; scales of block (i, j) at y_scales[i * ys_row + j *
+ * ys_block]) as dg_layer_block8_quantize makes them of y in fp32.  kept: NULL,
+ * or h in 8-bit blocks of 1 x 128 with power-of-two scales (kept_type), for the
+ * gradient.  x, residual, weight, bias: bf16 or fp32 each; residual, weight and
+ * bias may be NULL (then 0, 1 and 0); sum_out: h in the residual's type,
+ * required with a residual.  mean_out, rstd_out: NULL, or fp32 per row.  ld_*:
+ * elements from row to row; y and kept are densely packed.  Any hidden (rows of
+ * no values have NaN as their mean and deviation); 8-bit blocks need hidden %
+ * 16 == 0 and pointers and pitches of 16 bytes.  Statistics are computed in fp32. */
+int dg_layer_layer_norm(const void* x, int64_t ld_x, int x_type, const void* residual, int64_t ld_residual,
+                        int residual_type, const void* weight, int weight_type, const void* bias, int bias_type,
+                        void* y, int y_type, float* y_scales, int64_t ys_row, int64_t ys_block, void* sum_out,
+                        int64_t ld_sum, void* kept, int kept_type, float* kept_scales, int64_t ks_row,
+                        int64_t ks_block, float* mean_out, float* rstd_out, int64_t rows, int64_t hidden, float eps,
+                        void* stream);
+
+/* Gradient of dg_layer_layer_norm with a bf16 output: with xh = (h - mean) *
+ * rstd and g = dy * weight,
+ *     dx = rstd * (g - mean(g) - xh * mean(g * xh)) + dh
+ *     dweight = sum over rows of dy * xh,     dbias = sum over rows of dy.
+ * dy: bf16; h: bf16 or fp32, or 8-bit blocks of 1 x 128 (h_type e4m3 / e5m2,
+ * h_scales as y_scales above; else ignored); dh: NULL or the gradient that
+ * reaches h on its other way, of dx's type: h's, or bf16 for an 8-bit h.
+ * weight: NULL for 1; dweight (in weight_type), dbias (in dbias_type): NULL if not wanted.
+ * workspace: dg_layer_layer_norm_backward_workspace() bytes, 16-byte aligned
+ * (not needed without dweight and dbias).  The row sums are added in a fixed
+ * order (the same bits every time). */
+size_t dg_layer_layer_norm_backward_workspace(int64_t rows, int64_t hidden);
+int dg_layer_layer_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, int h_type,
+                                 const float* h_scales, int64_t hs_row, int64_t hs_block, const void* weight,
+                                 int weight_type, const float* mean, const float* rstd, const void* dh,
+                                 int64_t ld_dh, void* dx, void* dweight, void* dbias, int dbias_type,
+                                 void* workspace, int64_t rows, int64_t hidden, void* stream);
+
 /* Products grouped by expert: rows ends[e-1] <= t < ends[e] of A (T x K) times
  * expert e's matrix,
  *     D[t, n] = scale_a[t] * scale_b[e, n] * sum_k A[t, k] * B[e, n, k]
@@ -99,6 +137,18 @@ size_t dg_layer_grouped_grad_workspace(int experts, int64_t N, int64_t K);
 int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const void* A, int64_t ld_a, const int32_t* ends,
                                  int experts, void* dB, int d_type, int64_t T, int64_t N, int64_t K,
                                  void* workspace, void* products_workspace, void* status, void* stream);
+
+/* The same from rows that were kept in 8 bits: A = values (e4m3 / e5m2, T x K,
+ * densely packed, 16-byte aligned) times a scale for each block of 1 x 128
+ * columns, of block (i, j) at scales[i * s_row + j * s_block], rounded to bf16
+ * (exact for power-of-two scales).  K % 16 == 0.  n_major: dB is experts x K x
+ * N (dB[e, k, n]) instead.  workspace:
+ * dg_layer_grouped_grad8_workspace() bytes, 16-byte aligned. */
+size_t dg_layer_grouped_grad8_workspace(int64_t T, int experts, int64_t N, int64_t K);
+int dg_layer_grouped_weight_grad8(const void* dD, int64_t ld_d, const void* values, int type, const float* scales,
+                                  int64_t s_row, int64_t s_block, const int32_t* ends, int experts, void* dB,
+                                  int n_major, int d_type, int64_t T, int64_t N, int64_t K, void* workspace,
+                                  void* products_workspace, void* status, void* stream);
 
 /* Microscaled 4 bits (OCP MX, e2m1 elements, one e8m0 scale for each 32
  * columns): scale 2^E with E = floor(log2(max|x|)) - 2, at least -127; element

@@ -668,3 +668,33 @@ extern "C" int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const 
     return rc;
   return f32 ? run<false, true, true, true>(p, tiles, s) : run<false, true, true, false>(p, tiles, s);
 }
+
+extern "C" size_t dg_layer_grouped_grad8_workspace(int64_t T, int experts, int64_t N, int64_t K) {
+  if (T <= 0 || N <= 0 || K <= 0) return 256;
+  return dg_layer_grouped_grad_workspace(experts, N, K) + (size_t)T * (size_t)K * 2;
+}
+
+extern "C" int dg_layer_grouped_weight_grad8(const void* dD, int64_t ld_d, const void* values, int type, const float* scales,
+                                             int64_t s_row, int64_t s_block, const int32_t* ends, int experts, void* dB, int n_major,
+                                             int d_type, int64_t T, int64_t N, int64_t K, void* workspace,
+                                             void* products_workspace, void* status, void* stream) {
+  if (int rc = check_sizes(T, N, K, experts)) return rc;
+  if (!is8(type)) return fail(DG_ERR_ARG, "8-bit blocks hold e4m3 or e5m2 (got type %d)", type);
+  if (K % 16) return fail(DG_ERR_SHAPE, "K %% 16 must be 0 (got %lld)", (long long)K);
+  if (d_type != DG_TYPE_BF16 && d_type != DG_TYPE_F32) return fail(DG_ERR_ARG, "dB is bf16 or fp32 (got type %d)", d_type);
+  if (N % 8) return fail(DG_ERR_SHAPE, "N %% 8 must be 0 (got %lld)", (long long)N);
+  if (T > 0 && N > 0 && K > 0) {
+    if (!dD || !values || !scales || !ends || !dB || !workspace || !products_workspace || !status)
+      return fail(DG_ERR_ARG, "a required pointer is null");
+    if (!aligned16(dD) || !aligned16(values) || !aligned16(dB) || !aligned16(workspace) || !aligned16(products_workspace) || ld_d % 8)
+      return fail(DG_ERR_ARG, "dD, its pitch, the values, dB and the workspaces must be multiples of 16 bytes");
+    if (ld_d < N) return fail(DG_ERR_ARG, "a pitch is shorter than its rows");
+    if (int rc = dg_layer_block8_dequantize(values, type, scales, s_row, s_block, 1, workspace, DG_TYPE_BF16, T, K, stream)) return rc;
+  }
+  void* rest = workspace ? static_cast<uint8_t*>(workspace) + (size_t)T * (size_t)K * 2 : nullptr;
+  if (n_major)  // the gradient's transpose: the other operand's columns are the contiguous ones
+    return dg_layer_grouped_weight_grad(workspace, K, dD, ld_d, ends, experts, dB, d_type, T, K, N, rest, products_workspace, status,
+                                        stream);
+  return dg_layer_grouped_weight_grad(dD, ld_d, workspace, K, ends, experts, dB, d_type, T, N, K, rest, products_workspace, status,
+                                      stream);
+}

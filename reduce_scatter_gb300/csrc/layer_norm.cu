@@ -1,0 +1,918 @@
+// layer_norm.cu -- residual add + layer norm with 16-bit output or 8-bit blocks
+// of 128, its input kept in 8 bits on request, and the gradient
+// (dg_layer_layer_norm, dg_layer_layer_norm_backward).
+//
+//   h = x + r,  y = (h - mu) s w + b,  mu = mean h,  s = rsqrt(mean (h - mu)^2 + eps)
+//   dx = s (g - mean g - xh mean(g xh)) + dh,  g = dy w,  xh = (h - mu) s
+//   dw = sum over rows of dy xh,  db = sum over rows of dy
+//
+// Bound by memory traffic.  A row is read once and stays in its threads'
+// registers: first its sum, then, around the mean that it gives, the sums of the
+// differences and of their squares (the first corrects the mean by what its
+// rounding left, which matters where it is large beside the deviation), then the
+// output.  A block of 128 columns lies with the 16 neighbouring threads of half
+// a warp, so that its largest magnitude is four shuffles away.  Many rows are
+// streamed as in norm.cu: a block walks rows, each thread with its vectors of the
+// next rows in flight into its own slots of shared memory.
+
+#include "block8.cuh"
+
+namespace {
+
+using namespace dgl;
+
+struct Affine {
+  const void *w, *b;  // null: 1 and 0
+  int w_f32, b_f32;
+};
+
+// A matrix in 8-bit blocks of 1 x 128 as it is written.
+struct Blocks {
+  uint8_t* values;
+  float* scales;
+  int64_t s_row, s_block;
+  int e5m2;
+};
+
+struct Args {
+  const void *x, *residual;
+  void *sum, *y;
+  Blocks y8, kept;  // y8: the output (y null); kept: h, with power-of-two scales (values null: not kept)
+  float *mean, *rstd;
+  Affine affine;
+  int64_t ld_x, ld_residual, ld_sum, rows;
+  int hidden, x_f32, r_f32;
+  float eps;
+};
+
+// Eight values of w (or 1) and b (or 0).
+__device__ __forceinline__ void affine8(const Affine& a, int i, float (&w)[8], float (&b)[8]) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j) w[j] = 1.f, b[j] = 0.f;
+  if (a.w) load_any<8>(a.w_f32 != 0, a.w, i, w);
+  if (a.b) load_any<8>(a.b_f32 != 0, a.b, i, b);
+}
+
+// Eight values of each thread (`in`: they are in the row) as 8-bit blocks.
+__device__ __forceinline__ void store_blocks(const Blocks& o, bool pow2, int64_t row, int hidden, int i, bool in, float (&v)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    v[j] = block_value(v[j]);
+    m = fmaxf(m, in ? fabsf(v[j]) : 0.f);
+  }
+  const Quantizer q(block_max16(m), o.e5m2 != 0, pow2);
+  if (!in) return;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) v[j] = q(v[j]);
+  *reinterpret_cast<uint2*>(o.values + row * hidden + i) = pack_fp8(v, o.e5m2 ? __NV_E5M2 : __NV_E4M3);
+  if ((threadIdx.x & 15) == 0) o.scales[row * o.s_row + (int64_t)(i >> 7) * o.s_block] = q.c;
+}
+
+// The mean and the reciprocal deviation from the sum, and the sums of the
+// differences from its mean and of their squares.
+struct Moments {
+  float mean, rstd;
+};
+__device__ __forceinline__ Moments moments(float mean, float2 d, int hidden, float eps) {
+  const float n = (float)hidden, off = d.x / n, v = d.y / n;
+  // (below 2^-21 of the deviation the differences' own rounding is what their sum shows)
+  const bool far = off * off > 0x1p-42f * v;
+  const float var = v - off * off;
+  return Moments{far ? mean + off : mean, rsqrtf((var < 0.f ? 0.f : var) + eps)};  // (a NaN stays)
+}
+__device__ __forceinline__ void keep_moments(const Args& p, int64_t row, const Moments& m) {
+  if (threadIdx.x == 0) {
+    if (p.mean) p.mean[row] = m.mean;
+    if (p.rstd) p.rstd[row] = m.rstd;
+  }
+}
+
+// x + r, in the type that it is stored in.
+__device__ __forceinline__ void round_sum(bool r_f32, float (&h)[8]) {
+  if (!r_f32)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[j] = __bfloat162float(__float2bfloat16_rn(h[j]));
+}
+__device__ __forceinline__ void store_any(bool f32, void* base, int64_t i, const float (&v)[8]) {
+  if (f32)
+    store_f32<8>(base, i, v);
+  else
+    store_bf16<8>(base, i, v);
+}
+
+// Vector i of a row's output, from h.
+template <bool OUT8>
+__device__ __forceinline__ void finish(const Args& p, int64_t row, int i, bool in, const Moments& m, const float (&h)[8],
+                                       const float (&w)[8], const float (&b)[8]) {
+  if (p.kept.values) {
+    float v[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = h[j];
+    store_blocks(p.kept, true, row, p.hidden, i, in, v);
+  }
+  float y[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) y[j] = fmaf((h[j] - m.mean) * m.rstd, w[j], b[j]);
+  if constexpr (OUT8)
+    store_blocks(p.y8, false, row, p.hidden, i, in, y);
+  else if (in)
+    store_bf16<8>(p.y, row * p.hidden + i, y);
+}
+
+// ------------------------------------------------------ a row in registers
+
+// NV vectors of 8 values per thread.
+template <int NV, bool OUT8>
+__global__ void __launch_bounds__(NV > 2 ? 512 : 1024) layer_norm_kernel(const __grid_constant__ Args p) {
+  __shared__ float part[100];
+  begin_kernel();
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= p.rows) return;  // several rows per block only with one warp each: no barrier below
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
+  float h[NV][8], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = i0 + k * step;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
+    if (i < p.hidden) {
+      load_any<8>(p.x_f32 != 0, p.x, row * p.ld_x + i, h[k]);
+      if (p.residual) {
+        float r[8];
+        load_any<8>(p.r_f32 != 0, p.residual, row * p.ld_residual + i, r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[k][j] += r[j];
+        // the norm is of the sum as it is stored, so that the gradient sees the same values
+        round_sum(p.r_f32 != 0, h[k]);
+        store_any(p.r_f32 != 0, p.sum, row * p.ld_sum + i, h[k]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += h[k][j];
+  }
+  const float mean = row_reduce<Add>(sum, part) / (float)p.hidden;
+  float d1 = 0.f, d2 = 0.f;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (i0 + k * step < p.hidden)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float d = h[k][j] - mean;
+        d1 += d, d2 = fmaf(d, d, d2);
+      }
+  const Moments m = moments(mean, row_sum2(d1, d2, part + 34), p.hidden, p.eps);
+  keep_moments(p, row, m);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = i0 + k * step;
+    const bool in = i < p.hidden;
+    float w[8], b[8];
+    affine8(p.affine, in ? i : 0, w, b);
+    finish<OUT8>(p, row, i, in, m, h[k], w, b);
+  }
+}
+
+// ------------------------------------------------------------ streamed rows
+
+constexpr int kStreamVecs = 2;        // vectors of 8 values per thread
+constexpr int kStreamThreads = 1024;  // per SM (64 registers each)
+constexpr int kStreamBytes = 220000;  // dynamic shared memory that the streamed kernels may take, whatever the call needs
+
+// XP, RP: 16-byte slots of eight values of x (1 bf16, 2 fp32) and of the
+// residual (0 none).
+template <int XP, int RP, bool OUT8, int STAGES>
+__global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const __grid_constant__ Args p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float part[2][100];
+  constexpr int NV = kStreamVecs, PER = XP + RP;
+  const Slots<NV * PER> slots{smem};
+  begin_kernel();
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = i0 + k * step;
+        if (i < p.hidden) {
+          const uint8_t* x = static_cast<const uint8_t*>(p.x) + (row * p.ld_x + i) * (2 * XP);
+#pragma unroll
+          for (int q = 0; q < XP; ++q) slots.fetch(stage, k * PER + q, x + 16 * q);
+          if constexpr (RP != 0) {
+            const uint8_t* r = static_cast<const uint8_t*>(p.residual) + (row * p.ld_residual + i) * (2 * RP);
+#pragma unroll
+            for (int q = 0; q < RP; ++q) slots.fetch(stage, k * PER + XP + q, r + 16 * q);
+          }
+        }
+      }
+    }
+    copies_commit();
+  };
+  // w and b in 16 bits stay in registers
+  uint4 w16[NV], b16[NV];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = i0 + k * step;
+    w16[k] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    b16[k] = make_uint4(0, 0, 0, 0);
+    if (i < p.hidden) {
+      if (p.affine.w && !p.affine.w_f32) w16[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.affine.w) + i));
+      if (p.affine.b && !p.affine.b_f32) b16[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.affine.b) + i));
+    }
+  }
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  int stage = 0, flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    copies_wait<STAGES - 1>();
+    float h[NV][8], sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = i0 + k * step;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
+      if (i < p.hidden) {
+        slots.template read<XP == 2>(stage, k * PER, h[k]);
+        if constexpr (RP != 0) {
+          float r[8];
+          slots.template read<RP == 2>(stage, k * PER + XP, r);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) h[k][j] += r[j];
+          if constexpr (RP == 2) {
+            store_f32<8>(p.sum, row * p.ld_sum + i, h[k]);
+          } else {
+            // the norm is of the sum as it is stored, so that the gradient sees the same values
+            const uint4 u = make_uint4(pack2(h[k][0], h[k][1]), pack2(h[k][2], h[k][3]), pack2(h[k][4], h[k][5]),
+                                       pack2(h[k][6], h[k][7]));
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + row * p.ld_sum + i) = u;
+            unpack8(u, h[k]);
+          }
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) sum += h[k][j];
+    }
+    // this stage's values are in registers
+    fetch(row + (int64_t)STAGES * gridDim.x, stage);
+    stage = stage + 1 == STAGES ? 0 : stage + 1;
+    const float mean = row_reduce<Add>(sum, part[flip]) / (float)p.hidden;
+    float d1 = 0.f, d2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (i0 + k * step < p.hidden)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float d = h[k][j] - mean;
+          d1 += d, d2 = fmaf(d, d, d2);
+        }
+    const Moments m = moments(mean, row_sum2(d1, d2, part[flip] + 34), p.hidden, p.eps);
+    keep_moments(p, row, m);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = i0 + k * step;
+      const bool in = i < p.hidden;
+      float w[8], b[8];
+      unpack8(w16[k], w);
+      unpack8(b16[k], b);
+      if (in && p.affine.w_f32) load_f32<8>(p.affine.w, i, w);
+      if (in && p.affine.b_f32) load_f32<8>(p.affine.b, i, b);
+      finish<OUT8>(p, row, i, in, m, h[k], w, b);
+    }
+  }
+  copies_wait<0>();
+}
+
+// ------------------------------------------------ rows without alignment
+
+// (16-bit output: rows of 8-bit blocks are multiples of 16 values, and come aligned)
+template <bool X32, int RT, int N>
+__global__ void __launch_bounds__(1024) layer_norm_spread_kernel(const __grid_constant__ Args p) {
+  __shared__ float part[100];
+  begin_kernel();
+  const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (row >= p.rows) return;
+  Spread<X32, N> x;
+  Spread<RT == 2, N> r;
+  x.load(p.x, row * p.ld_x, p.hidden);
+  if constexpr (RT != 0) r.load(p.residual, row * p.ld_residual, p.hidden);
+  float h[N], sum = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int i = threadIdx.x + k * blockDim.x;
+    h[k] = x.at(k, p.hidden);
+    if constexpr (RT != 0) h[k] += r.at(k, p.hidden);
+    if constexpr (RT == 1) h[k] = __bfloat162float(__float2bfloat16_rn(h[k]));
+    if (RT != 0 && i < p.hidden) {
+      const float v[1] = {h[k]};
+      if constexpr (RT == 2)
+        store_f32<1>(p.sum, row * p.ld_sum + i, v);
+      else
+        store_bf16<1>(p.sum, row * p.ld_sum + i, v);
+    }
+    sum += h[k];
+  }
+  const float mean = row_reduce<Add>(sum, part) / (float)p.hidden;
+  float d1 = 0.f, d2 = 0.f;
+#pragma unroll
+  for (int k = 0; k < N; ++k)
+    if ((int)(threadIdx.x + k * blockDim.x) < p.hidden) {
+      const float d = h[k] - mean;
+      d1 += d, d2 = fmaf(d, d, d2);
+    }
+  const Moments m = moments(mean, row_sum2(d1, d2, part + 34), p.hidden, p.eps);
+  keep_moments(p, row, m);
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const int i = threadIdx.x + k * blockDim.x;
+    if (i < p.hidden) {
+      float w[1] = {1.f}, b[1] = {0.f};
+      if (p.affine.w) load_any<1>(p.affine.w_f32 != 0, p.affine.w, i, w);
+      if (p.affine.b) load_any<1>(p.affine.b_f32 != 0, p.affine.b, i, b);
+      const float v[1] = {fmaf((h[k] - m.mean) * m.rstd, w[0], b[0])};
+      store_bf16<1>(p.y, row * p.hidden + i, v);
+    }
+  }
+}
+
+// ------------------------------------------------------------- longer rows
+
+// Rows longer than the other kernels hold: each thread goes over its values, 8
+// at a time, again for the differences and for the output.
+template <bool VEC, bool OUT8>
+__global__ void __launch_bounds__(1024) layer_norm_long_kernel(const __grid_constant__ Args p) {
+  static_assert(VEC || !OUT8, "8-bit blocks come in vectors");
+  __shared__ float part[100];
+  begin_kernel();
+  const int64_t row = blockIdx.x, hidden = p.hidden, step = blockDim.x * 8;
+  const bool h_f32 = p.residual ? p.r_f32 != 0 : p.x_f32 != 0;
+  const void* hp = p.residual ? p.sum : p.x;
+  const int64_t h0 = row * (p.residual ? p.ld_sum : p.ld_x);
+  auto load = [&](bool f32, const void* base, int64_t at, int64_t from, float (&v)[8]) {
+    if (VEC && from + threadIdx.x * 8 >= hidden) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.f;
+    } else if (f32) {
+      load_chunk<true, VEC>(base, at, from, hidden, v);
+    } else {
+      load_chunk<false, VEC>(base, at, from, hidden, v);
+    }
+  };
+  auto in_row = [&](int64_t from, int k) {
+    return VEC ? from + threadIdx.x * 8 < hidden : from + threadIdx.x + (int64_t)k * blockDim.x < hidden;
+  };
+  float sum = 0.f;
+  for (int64_t from = 0; from < hidden; from += step) {
+    float h[8];
+    load(p.x_f32 != 0, p.x, row * p.ld_x, from, h);
+    if (p.residual) {
+      float r[8];
+      load(p.r_f32 != 0, p.residual, row * p.ld_residual, from, r);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] += r[j];
+      round_sum(p.r_f32 != 0, h);
+      if (!VEC || in_row(from, 0)) {
+        if (p.r_f32)
+          store_chunk<VEC>(from, hidden, h, [&](int64_t i, const float(&v)[1]) { store_f32<1>(p.sum, h0 + i, v); },
+                           [&](int64_t i, const float(&v)[8]) { store_f32<8>(p.sum, h0 + i, v); });
+        else
+          store_chunk<VEC>(from, hidden, h, [&](int64_t i, const float(&v)[1]) { store_bf16<1>(p.sum, h0 + i, v); },
+                           [&](int64_t i, const float(&v)[8]) { store_bf16<8>(p.sum, h0 + i, v); });
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum += h[j];
+  }
+  const float mean = row_reduce<Add>(sum, part) / (float)p.hidden;
+  float d1 = 0.f, d2 = 0.f;
+  for (int64_t from = 0; from < hidden; from += step) {  // (a thread's own stores of the sum)
+    float h[8];
+    load(h_f32, hp, h0, from, h);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float d = in_row(from, j) ? h[j] - mean : 0.f;
+      d1 += d, d2 = fmaf(d, d, d2);
+    }
+  }
+  const Moments m = moments(mean, row_sum2(d1, d2, part + 34), p.hidden, p.eps);
+  keep_moments(p, row, m);
+  for (int64_t from = 0; from < hidden; from += step) {
+    float h[8], w[8], b[8];
+    load(h_f32, hp, h0, from, h);
+    if constexpr (VEC) {
+      const int i = (int)from + threadIdx.x * 8;  // (beyond the row by less than a step)
+      const bool in = in_row(from, 0);
+      affine8(p.affine, in ? i : 0, w, b);
+      finish<OUT8>(p, row, i, in, m, h, w, b);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = 1.f, b[j] = 0.f;
+      if (p.affine.w) load(p.affine.w_f32 != 0, p.affine.w, 0, from, w);
+      if (p.affine.b) load(p.affine.b_f32 != 0, p.affine.b, 0, from, b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[j] = fmaf((h[j] - m.mean) * m.rstd, w[j], b[j]);
+      store_chunk<false>(from, hidden, h, [&](int64_t i, const float(&v)[1]) { store_bf16<1>(p.y, row * hidden + i, v); },
+                         [&](int64_t, const float(&)[8]) {});
+    }
+  }
+}
+
+// ------------------------------------------------------------ forward launch
+
+template <class Kernel>
+int stream_shape(Kernel kernel, int hidden, int parts, int stages, int sms, int64_t rows, int* threads, int* blocks, int* bytes) {
+  *threads = round32((hidden / 8 + kStreamVecs - 1) / kStreamVecs);
+  *bytes = stages * parts * 16 * *threads;
+  const int64_t most = (int64_t)sms * (kStreamThreads / *threads);
+  *blocks = (int)(rows < most ? rows : most);
+  DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes));
+  return DG_OK;
+}
+
+template <int XP, int RP, bool OUT8>
+int stream_norm(const Args& p, int sms, cudaStream_t s) {
+  constexpr int stages = XP + RP > 2 ? 2 : 3;  // (192 KB for 16384 values; two fp32 operands only fit to 13744)
+  int threads, blocks, bytes;
+  auto* kernel = layer_norm_stream_kernel<XP, RP, OUT8, stages>;
+  if (int rc = stream_shape(kernel, p.hidden, kStreamVecs * (XP + RP), stages, sms, p.rows, &threads, &blocks, &bytes)) return rc;
+  return dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);
+}
+
+template <int XP, int RP>
+int run_spread(const Args& p, cudaStream_t s) {
+  const int n = p.hidden <= 1024 ? 4 : 16, threads = round32((p.hidden + n - 1) / n), per = threads == 32 ? 4 : 1;
+  return dgl::launch(n == 4 ? layer_norm_spread_kernel<XP == 2, RP, 4> : layer_norm_spread_kernel<XP == 2, RP, 16>,
+                     dim3((unsigned)((p.rows + per - 1) / per)), dim3(threads, per), 0, s, p);
+}
+
+template <int XP, int RP, bool OUT8>
+int run_norm(const Args& p, bool vec, int sms, cudaStream_t s) {
+  if (!vec) {
+    if constexpr (!OUT8) {
+      if (p.hidden <= 16384) return run_spread<XP, RP>(p, s);
+      return dgl::launch(layer_norm_long_kernel<false, false>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
+    }
+    return fail(DG_ERR_ARG, "8-bit blocks need rows of whole 16-byte vectors");
+  }
+  const int n = p.hidden / 8;
+  // Many long rows are streamed; few rows take as many threads as they have vectors,
+  // for the shortest chain of loads.
+  if (p.rows > 2 * sms && n >= 256 && n <= 2048 && (XP + RP) * 2 * 16 * 2 * round32((n + 1) / 2) <= kStreamBytes)
+    return stream_norm<XP, RP, OUT8>(p, sms, s);
+  auto launch_rows = [&](auto* kernel, int threads) {
+    const int per = threads == 32 ? 4 : 1;  // one warp per row: four rows to a block
+    return dgl::launch(kernel, dim3((unsigned)((p.rows + per - 1) / per)), dim3(threads, per), 0, s, p);
+  };
+  if (n <= 1024) return launch_rows(layer_norm_kernel<1, OUT8>, round32(n));
+  if (n <= 2048) return launch_rows(layer_norm_kernel<2, OUT8>, round32((n + 1) / 2));
+  if (n <= 4096) return launch_rows(layer_norm_kernel<8, OUT8>, round32((n + 7) / 8));
+  return dgl::launch(layer_norm_long_kernel<true, OUT8>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
+}
+
+template <int XP, int RP>
+int run_out(const Args& p, bool vec, int sms, cudaStream_t s) {
+  return p.y ? run_norm<XP, RP, false>(p, vec, sms, s) : run_norm<XP, RP, true>(p, vec, sms, s);
+}
+
+// ----------------------------------------------------------------- gradient
+
+struct GradArgs {
+  const void *dy, *h, *dh;
+  const float *scales;  // of an 8-bit h
+  int64_t s_row, s_block;
+  Affine affine;
+  const float *mean, *rstd;
+  void *dx, *dweight, *dbias;
+  float* partial;  // weight, then bias: blocks x hidden each; null without them
+  int64_t ld_dy, ld_h, ld_dh, rows;
+  int hidden, e5m2, w_f32, b_f32;
+};
+
+// The type of h: bf16, fp32, or 8-bit blocks of 1 x 128.
+enum { kH16 = 0, kH32 = 1, kH8 = 2 };
+
+constexpr int kGradStages = 2;
+template <int HT, bool HAS_DH>
+__host__ __device__ constexpr int grad_parts() {
+  return kStreamVecs * (1 + (HT == kH32 ? 2 : 1) * (HAS_DH ? 2 : 1));
+}
+
+__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+
+// Rows streamed like the forward's: dy, h and dh of the next row are in flight
+// while this one is reduced and written.  A row is read from its slots twice (for
+// the sums, and again for dx), which leaves registers to the weight and the two
+// gradients that are summed over the block's rows.
+template <int HT, bool HAS_DH>
+__global__ void __launch_bounds__(kStreamThreads) layer_norm_grad_stream_kernel(const __grid_constant__ GradArgs p) {
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ float part[2][66];
+  constexpr int NV = kStreamVecs, HP = HT == kH32 ? 2 : 1, PER = 1 + HP * (HAS_DH ? 2 : 1), hsz = HT == kH32 ? 4 : 2;
+  const Slots<grad_parts<HT, HAS_DH>()> slots{smem};
+  begin_kernel();
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
+  auto fetch = [&](int64_t row, int stage) {
+    if (row < p.rows) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int i = i0 + k * step;
+        if (i < p.hidden) {
+          slots.fetch(stage, k * PER, static_cast<const __nv_bfloat16*>(p.dy) + row * p.ld_dy + i);
+          if constexpr (HT == kH8) {
+            copy8((uint32_t)__cvta_generic_to_shared(slots.at(stage, k * PER + 1)), static_cast<const uint8_t*>(p.h) + row * p.ld_h + i);
+          } else {
+            const uint8_t* h = static_cast<const uint8_t*>(p.h) + (row * p.ld_h + i) * hsz;
+#pragma unroll
+            for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + q, h + 16 * q);
+          }
+          if constexpr (HAS_DH) {
+            const uint8_t* d = static_cast<const uint8_t*>(p.dh) + (row * p.ld_dh + i) * hsz;
+#pragma unroll
+            for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + HP + q, d + 16 * q);
+          }
+        }
+      }
+    }
+    copies_commit();
+  };
+  float scale_next[HT == kH8 ? NV : 1];
+  auto fetch_scale = [&](int64_t row) {
+    if constexpr (HT == kH8)
+#pragma unroll
+      for (int k = 0; k < NV; ++k)
+        if (row < p.rows && i0 + k * step < p.hidden)
+          scale_next[k] = __ldg(p.scales + row * p.s_row + (int64_t)((i0 + k * step) >> 7) * p.s_block);
+  };
+  uint4 w16[NV];
+  float dw[NV][8], db[NV][8];
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const int i = i0 + k * step;
+    w16[k] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    if (i < p.hidden && p.affine.w && !p.affine.w_f32)
+      w16[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.affine.w) + i));
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.f;
+  }
+#pragma unroll
+  for (int s = 0; s < kGradStages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
+  fetch_scale(blockIdx.x);
+  int stage = 0, flip = 0;
+  float mean_next = 0.f, rstd_next = 0.f;
+  if (blockIdx.x < p.rows) mean_next = __ldg(p.mean + blockIdx.x), rstd_next = __ldg(p.rstd + blockIdx.x);
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    const float mean = mean_next, rstd = rstd_next;
+    float scale[HT == kH8 ? NV : 1];
+    if constexpr (HT == kH8)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) scale[k] = scale_next[k];
+    if (row + gridDim.x < p.rows) mean_next = __ldg(p.mean + row + gridDim.x), rstd_next = __ldg(p.rstd + row + gridDim.x);
+    fetch_scale(row + gridDim.x);
+    copies_wait<kGradStages - 1>();
+    // dy, the normed values and the weight of vector k
+    auto read = [&](int k, float(&dy)[8], float(&xh)[8], float(&w)[8]) {
+      slots.template read<false>(stage, k * PER, dy);
+      if constexpr (HT == kH8) {
+        unpack_fp8(*reinterpret_cast<const uint2*>(slots.at(stage, k * PER + 1)), p.e5m2 ? __NV_E5M2 : __NV_E4M3, xh);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) xh[j] *= scale[k];
+      } else {
+        slots.template read<HT == kH32>(stage, k * PER + 1, xh);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) xh[j] = (xh[j] - mean) * rstd;
+      unpack8(w16[k], w);
+      if (p.affine.w_f32) load_f32<8>(p.affine.w, i0 + k * step, w);
+    };
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (i0 + k * step < p.hidden) {
+        float dy[8], xh[8], w[8];
+        read(k, dy, xh, w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          db[k][j] += dy[j];
+          dw[k][j] = fmaf(dy[j], xh[j], dw[k][j]);
+          const float g = dy[j] * w[j];
+          s1 += g;
+          s2 = fmaf(g, xh[j], s2);
+        }
+      }
+    }
+    // two sets of partials: a block's next row may start while a slow warp reads these
+    const float2 s = row_sum2(s1, s2, part[flip]);
+    const float m1 = s.x / (float)p.hidden, m2 = s.y / (float)p.hidden;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int i = i0 + k * step;
+      if (i < p.hidden) {
+        float dy[8], xh[8], w[8], d[8];
+        read(k, dy, xh, w);
+        if constexpr (HAS_DH)
+          slots.template read<HT == kH32>(stage, k * PER + 1 + HP, d);
+        else
+#pragma unroll
+          for (int j = 0; j < 8; ++j) d[j] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, fmaf(dy[j], w[j], -m1) - xh[j] * m2, d[j]);
+        if constexpr (HT == kH32)
+          store_f32<8>(p.dx, row * p.hidden + i, d);
+        else
+          store_bf16<8>(p.dx, row * p.hidden + i, d);
+      }
+    }
+    fetch(row + (int64_t)kGradStages * gridDim.x, stage);
+    stage ^= 1;
+  }
+  copies_wait<0>();
+  if (p.partial) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+      if (i0 + k * step < p.hidden) {
+        store_f32<8>(p.partial, (int64_t)blockIdx.x * p.hidden + i0 + k * step, dw[k]);
+        store_f32<8>(p.partial, (int64_t)(gridDim.x + blockIdx.x) * p.hidden + i0 + k * step, db[k]);
+      }
+  }
+}
+
+// Rows of any alignment, element by element: N values per thread.
+template <bool F32, int N, bool HAS_DH>
+__global__ void __launch_bounds__(512) layer_norm_grad_kernel(const __grid_constant__ GradArgs p) {
+  __shared__ float part[2][66];
+  begin_kernel();
+  float dw[N], db[N], w[N];
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    dw[k] = db[k] = 0.f;
+    float v[1] = {1.f};
+    const int i = threadIdx.x + k * blockDim.x;
+    if (p.affine.w && i < p.hidden) load_any<1>(p.affine.w_f32 != 0, p.affine.w, i, v);
+    w[k] = v[0];
+  }
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
+    Spread<false, N> dy;
+    Spread<F32, N> h, dh;
+    dy.load(p.dy, row * p.ld_dy, p.hidden);
+    h.load(p.h, row * p.ld_h, p.hidden);
+    if constexpr (HAS_DH) dh.load(p.dh, row * p.ld_dh, p.hidden);
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {  // (dy is 0 past the row)
+      const float d = dy.at(k, p.hidden), xh = (h.at(k, p.hidden) - mean) * rstd;
+      if ((int)(threadIdx.x + k * blockDim.x) < p.hidden) {
+        db[k] += d;
+        dw[k] = fmaf(d, xh, dw[k]);
+        s1 += d * w[k];
+        s2 = fmaf(d * w[k], xh, s2);
+      }
+    }
+    const float2 s = row_sum2(s1, s2, part[flip]);
+    const float m1 = s.x / (float)p.hidden, m2 = s.y / (float)p.hidden;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * blockDim.x;
+      float d[1] = {0.f};
+      if constexpr (HAS_DH) d[0] = dh.at(k, p.hidden);
+      d[0] = fmaf(rstd, fmaf(dy.at(k, p.hidden), w[k], -m1) - (h.at(k, p.hidden) - mean) * rstd * m2, d[0]);
+      if (i < p.hidden) {
+        if constexpr (F32)
+          store_f32<1>(p.dx, row * p.hidden + i, d);
+        else
+          store_bf16<1>(p.dx, row * p.hidden + i, d);
+      }
+    }
+  }
+  if (p.partial)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * blockDim.x;
+      if (i < p.hidden) {
+        p.partial[(int64_t)blockIdx.x * p.hidden + i] = dw[k];
+        p.partial[(int64_t)(gridDim.x + blockIdx.x) * p.hidden + i] = db[k];
+      }
+    }
+}
+
+// Rows longer than the other kernels hold: two passes over each row; the weight's
+// and the bias's gradients accumulate in the block's rows of `partial`.
+template <int HT, bool HAS_DH>
+__global__ void __launch_bounds__(1024) layer_norm_grad_long_kernel(const __grid_constant__ GradArgs p) {
+  __shared__ float part[2][66];
+  begin_kernel();
+  float* mw = p.partial ? p.partial + (int64_t)blockIdx.x * p.hidden : nullptr;
+  float* mb = p.partial ? p.partial + (int64_t)(gridDim.x + blockIdx.x) * p.hidden : nullptr;
+  if (p.partial)
+    for (int64_t i = threadIdx.x; i < p.hidden; i += blockDim.x) mw[i] = mb[i] = 0.f;
+  int flip = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    const float mean = __ldg(p.mean + row), rstd = __ldg(p.rstd + row);
+    auto value = [&](int64_t i, float& dy, float& xh, float& w) {
+      float d[1], h[1], v[1] = {1.f};
+      load_bf16<1>(p.dy, row * p.ld_dy + i, d);
+      if constexpr (HT == kH8)
+        h[0] = unpack_fp8x2(static_cast<const uint8_t*>(p.h)[row * p.ld_h + i], p.e5m2 ? __NV_E5M2 : __NV_E4M3).x *
+               __ldg(p.scales + row * p.s_row + (i >> 7) * p.s_block);
+      else
+        load_any<1>(HT == kH32, p.h, row * p.ld_h + i, h);
+      if (p.affine.w) load_any<1>(p.affine.w_f32 != 0, p.affine.w, i, v);
+      dy = d[0], xh = (h[0] - mean) * rstd, w = v[0];
+    };
+    float s1 = 0.f, s2 = 0.f;
+    for (int64_t i = threadIdx.x; i < p.hidden; i += blockDim.x) {
+      float dy, xh, w;
+      value(i, dy, xh, w);
+      if (p.partial) mw[i] = fmaf(dy, xh, mw[i]), mb[i] += dy;
+      s1 += dy * w;
+      s2 = fmaf(dy * w, xh, s2);
+    }
+    const float2 s = row_sum2(s1, s2, part[flip]);
+    const float m1 = s.x / (float)p.hidden, m2 = s.y / (float)p.hidden;
+    for (int64_t i = threadIdx.x; i < p.hidden; i += blockDim.x) {
+      float dy, xh, w, d[1] = {0.f};
+      value(i, dy, xh, w);
+      if constexpr (HAS_DH) load_any<1>(HT == kH32, p.dh, row * p.ld_dh + i, d);
+      d[0] = fmaf(rstd, fmaf(dy, w, -m1) - xh * m2, d[0]);
+      if constexpr (HT == kH32)
+        store_f32<1>(p.dx, row * p.hidden + i, d);
+      else
+        store_bf16<1>(p.dx, row * p.hidden + i, d);
+    }
+  }
+}
+
+// The weight's and the bias's gradient (blockIdx.y): sums over the blocks' partial
+// rows, in a fixed order: 32 columns x 32 threads, each thread a strided share of
+// the rows, then a tree.
+__global__ void __launch_bounds__(1024) layer_norm_weight_grad_kernel(const __grid_constant__ GradArgs p, int blocks) {
+  __shared__ float s[32][33];
+  begin_kernel();
+  const float* partial = p.partial + (blockIdx.y ? (int64_t)blocks * p.hidden : 0);
+  const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
+  float v = 0.f;
+  if (col < p.hidden)
+#pragma unroll 8
+    for (int b = threadIdx.y; b < blocks; b += 32) v += partial[(int64_t)b * p.hidden + col];
+  s[threadIdx.y][threadIdx.x] = v;
+  __syncthreads();
+  v = s[threadIdx.x][threadIdx.y];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  const int64_t out = (int64_t)blockIdx.x * 32 + threadIdx.y;
+  if (threadIdx.x == 0 && out < p.hidden) {
+    void* to = blockIdx.y ? p.dbias : p.dweight;
+    if (!to) return;
+    if (blockIdx.y ? p.b_f32 : p.w_f32)
+      static_cast<float*>(to)[out] = v;
+    else
+      static_cast<__nv_bfloat16*>(to)[out] = __float2bfloat16_rn(v);
+  }
+}
+
+// Blocks of the gradient kernels: a fixed bound that the workspace is sized by.
+constexpr int kGradBlocks = 1216;
+
+// `most` blocks fill the SMs; a block takes four rows at least where there are
+// enough of them, so that the partial sums stay small beside the rows.
+int grad_blocks(int64_t rows, int sms, int64_t most) {
+  if (most > kGradBlocks) most = kGradBlocks;
+  const int64_t want = rows / 4 > sms ? rows / 4 : sms;
+  const int64_t n = want < most ? want : most;
+  return (int)(rows < n ? rows : n);
+}
+
+template <int HT, bool HAS_DH>
+int run_grad(const GradArgs& p, bool vec, int sms, cudaStream_t s) {
+  const int n = p.hidden / 8;
+  int blocks, rc;
+  if (vec && n <= 2048 && grad_parts<HT, HAS_DH>() * 16 * kGradStages * round32((n + 1) / 2) <= kStreamBytes) {
+    int threads, bytes;
+    auto* kernel = layer_norm_grad_stream_kernel<HT, HAS_DH>;
+    rc = stream_shape(kernel, p.hidden, grad_parts<HT, HAS_DH>(), kGradStages, sms, p.rows, &threads, &blocks, &bytes);
+    if (rc != DG_OK) return rc;
+    blocks = grad_blocks(p.rows, sms, (int64_t)sms * (kStreamThreads / threads));
+    rc = dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);
+  } else {
+    const bool small = HT != kH8 && p.hidden <= 1024, regs = HT != kH8 && p.hidden <= 8192;
+    const int threads = small ? round32((p.hidden + 3) / 4) : regs ? round32((p.hidden + 15) / 16) : 1024;
+    blocks = grad_blocks(p.rows, sms, (int64_t)sms * (threads < 512 ? 512 / threads : 1));
+    auto* kernel = layer_norm_grad_long_kernel<HT, HAS_DH>;
+    if constexpr (HT != kH8) {
+      if (small)
+        kernel = layer_norm_grad_kernel<HT == kH32, 4, HAS_DH>;
+      else if (regs)
+        kernel = layer_norm_grad_kernel<HT == kH32, 16, HAS_DH>;
+    }
+    rc = dgl::launch(kernel, dim3(blocks), dim3(threads), 0, s, p);
+  }
+  if (rc != DG_OK || !p.partial) return rc;
+  return dgl::launch(layer_norm_weight_grad_kernel, dim3((unsigned)((p.hidden + 31) / 32), 2), dim3(32, 32), 0, s, p, blocks);
+}
+
+// Rows of no values: the deviation's reciprocal and the mean of nothing, a NaN.
+__global__ void __launch_bounds__(256) layer_norm_of_nothing_kernel(float* mean, float* rstd, int64_t rows) {
+  begin_kernel();
+  const int64_t row = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (row >= rows) return;
+  if (mean) mean[row] = __uint_as_float(0x7fc00000u);
+  if (rstd) rstd[row] = __uint_as_float(0x7fc00000u);
+}
+
+int check_affine(const void* weight, int weight_type, const void* bias, int bias_type) {
+  if ((weight && !bf16_or_f32(weight_type)) || (bias && !bf16_or_f32(bias_type)))
+    return fail(DG_ERR_ARG, "the weight and the bias are bf16 or fp32");
+  return DG_OK;
+}
+
+}  // namespace
+
+extern "C" int dg_layer_layer_norm(const void* x, int64_t ld_x, int x_type, const void* residual, int64_t ld_residual,
+                                   int residual_type, const void* weight, int weight_type, const void* bias, int bias_type,
+                                   void* y, int y_type, float* y_scales, int64_t ys_row, int64_t ys_block, void* sum_out,
+                                   int64_t ld_sum, void* kept, int kept_type, float* kept_scales, int64_t ks_row, int64_t ks_block,
+                                   float* mean_out, float* rstd_out, int64_t rows, int64_t hidden, float eps, void* stream) {
+  if (rows < 0 || hidden < 0 || rows > INT32_MAX || hidden > INT32_MAX - 8192)
+    return fail(DG_ERR_ARG, "rows %lld, hidden %lld out of range", (long long)rows, (long long)hidden);
+  if (!bf16_or_f32(x_type) || (residual && !bf16_or_f32(residual_type))) return fail(DG_ERR_ARG, "x and the residual are bf16 or fp32");
+  if (int rc = check_affine(weight, weight_type, bias, bias_type)) return rc;
+  const bool out8 = is_fp8(y_type);
+  if (!out8 && y_type != DG_TYPE_BF16) return fail(DG_ERR_ARG, "y is bf16, e4m3 or e5m2 (got type %d)", y_type);
+  if (kept && !is_fp8(kept_type)) return fail(DG_ERR_ARG, "kept rows are e4m3 or e5m2 (got type %d)", kept_type);
+  if (!(eps >= 0.f)) return fail(DG_ERR_ARG, "eps must not be negative");
+  if ((out8 || kept) && hidden % 16) return fail(DG_ERR_SHAPE, "8-bit blocks need hidden %% 16 == 0 (got %lld)", (long long)hidden);
+  if (rows == 0) return DG_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (hidden == 0) {
+    if (!mean_out && !rstd_out) return DG_OK;
+    return dgl::launch(layer_norm_of_nothing_kernel, dim3((unsigned)((rows + 255) / 256)), dim3(256), 0, s, mean_out, rstd_out, rows);
+  }
+  if (!x || !y) return fail(DG_ERR_ARG, "x and y must not be null");
+  if ((residual != nullptr) != (sum_out != nullptr)) return fail(DG_ERR_ARG, "a residual and its sum come together");
+  if ((out8 && !y_scales) || (kept && !kept_scales)) return fail(DG_ERR_ARG, "8-bit blocks need their scales");
+  int sms = 0;
+  if (int rc = sm_count(&sms)) return rc;
+  const int64_t xsz = x_type == DG_TYPE_F32 ? 4 : 2, rsz = residual_type == DG_TYPE_F32 ? 4 : 2;
+  const bool vec = hidden % 8 == 0 && rows16(x, ld_x, xsz) && rows16(residual, ld_residual, rsz) && rows16(sum_out, ld_sum, rsz) &&
+                   (!weight || aligned16(weight)) && (!bias || aligned16(bias)) && aligned16(y);
+  if ((out8 || kept) && (!vec || (kept && !aligned16(kept))))
+    return fail(DG_ERR_ARG, "8-bit blocks need 16-byte aligned pointers and pitches");
+  Args p{};
+  p.x = x, p.residual = residual, p.sum = sum_out, p.y = out8 ? nullptr : y;
+  p.y8 = Blocks{out8 ? static_cast<uint8_t*>(y) : nullptr, y_scales, ys_row, ys_block, y_type == DG_TYPE_E5M2};
+  p.kept = Blocks{static_cast<uint8_t*>(kept), kept_scales, ks_row, ks_block, kept_type == DG_TYPE_E5M2};
+  p.mean = mean_out, p.rstd = rstd_out;
+  p.affine = Affine{weight, bias, weight && weight_type == DG_TYPE_F32, bias && bias_type == DG_TYPE_F32};
+  p.ld_x = ld_x, p.ld_residual = ld_residual, p.ld_sum = ld_sum, p.rows = rows;
+  p.hidden = (int)hidden, p.x_f32 = x_type == DG_TYPE_F32, p.r_f32 = residual_type == DG_TYPE_F32, p.eps = eps;
+  const int rp = !residual ? 0 : residual_type == DG_TYPE_F32 ? 2 : 1;
+  if (x_type == DG_TYPE_F32)
+    return rp == 0 ? run_out<2, 0>(p, vec, sms, s) : rp == 1 ? run_out<2, 1>(p, vec, sms, s) : run_out<2, 2>(p, vec, sms, s);
+  return rp == 0 ? run_out<1, 0>(p, vec, sms, s) : rp == 1 ? run_out<1, 1>(p, vec, sms, s) : run_out<1, 2>(p, vec, sms, s);
+}
+
+extern "C" size_t dg_layer_layer_norm_backward_workspace(int64_t rows, int64_t hidden) {
+  if (rows <= 0 || hidden <= 0) return 0;
+  return 2 * (size_t)(rows < kGradBlocks ? rows : kGradBlocks) * (size_t)hidden * sizeof(float);
+}
+
+extern "C" int dg_layer_layer_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, int h_type,
+                                            const float* h_scales, int64_t hs_row, int64_t hs_block, const void* weight,
+                                            int weight_type, const float* mean, const float* rstd, const void* dh, int64_t ld_dh,
+                                            void* dx, void* dweight, void* dbias, int dbias_type, void* workspace, int64_t rows,
+                                            int64_t hidden, void* stream) {
+  if (rows < 0 || hidden < 0 || rows > INT32_MAX || hidden > INT32_MAX)
+    return fail(DG_ERR_ARG, "rows %lld, hidden %lld out of range", (long long)rows, (long long)hidden);
+  const bool h8 = is_fp8(h_type);
+  if (!h8 && !bf16_or_f32(h_type)) return fail(DG_ERR_ARG, "h is bf16, fp32, e4m3 or e5m2 (got type %d)", h_type);
+  if (int rc = check_affine(weight, weight_type, dbias, dbias_type)) return rc;
+  if (dweight && !bf16_or_f32(weight_type)) return fail(DG_ERR_ARG, "the weight's gradient is bf16 or fp32");
+  if (h8 && hidden % 16) return fail(DG_ERR_SHAPE, "8-bit blocks need hidden %% 16 == 0 (got %lld)", (long long)hidden);
+  if (hidden == 0) return DG_OK;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (rows == 0) {
+    if (dweight) DGL_CUDA(cudaMemsetAsync(dweight, 0, (size_t)hidden * (weight_type == DG_TYPE_F32 ? 4 : 2), s));
+    if (dbias) DGL_CUDA(cudaMemsetAsync(dbias, 0, (size_t)hidden * (dbias_type == DG_TYPE_F32 ? 4 : 2), s));
+    return DG_OK;
+  }
+  if (!dy || !h || !mean || !rstd || !dx || (h8 && !h_scales)) return fail(DG_ERR_ARG, "a required pointer is null");
+  const bool sums = dweight || dbias;
+  if (sums && (!workspace || !aligned16(workspace))) return fail(DG_ERR_ARG, "the workspace must be there and 16-byte aligned");
+  int sms = 0;
+  if (int rc = sm_count(&sms)) return rc;
+  const int64_t hsz = h_type == DG_TYPE_F32 ? 4 : h8 ? 1 : 2, dsz = h_type == DG_TYPE_F32 ? 4 : 2;
+  const bool vec = hidden % 8 == 0 && rows16(dy, ld_dy, 2) && rows16(h, ld_h, hsz) && rows16(dh, ld_dh, dsz) &&
+                   (!weight || aligned16(weight)) && aligned16(dx);
+  GradArgs p{};
+  p.dy = dy, p.h = h, p.dh = dh, p.scales = h_scales, p.s_row = hs_row, p.s_block = hs_block;
+  p.affine = Affine{weight, nullptr, weight && weight_type == DG_TYPE_F32, 0};
+  p.mean = mean, p.rstd = rstd, p.dx = dx, p.dweight = dweight, p.dbias = dbias;
+  p.partial = sums ? static_cast<float*>(workspace) : nullptr;
+  p.ld_dy = ld_dy, p.ld_h = ld_h, p.ld_dh = ld_dh, p.rows = rows, p.hidden = (int)hidden;
+  p.e5m2 = h_type == DG_TYPE_E5M2, p.w_f32 = weight_type == DG_TYPE_F32, p.b_f32 = dbias_type == DG_TYPE_F32;
+  if (h8) return dh ? run_grad<kH8, true>(p, vec, sms, s) : run_grad<kH8, false>(p, vec, sms, s);
+  if (h_type == DG_TYPE_F32) return dh ? run_grad<kH32, true>(p, vec, sms, s) : run_grad<kH32, false>(p, vec, sms, s);
+  return dh ? run_grad<kH16, true>(p, vec, sms, s) : run_grad<kH16, false>(p, vec, sms, s);
+}

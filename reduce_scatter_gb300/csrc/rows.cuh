@@ -123,6 +123,23 @@ __device__ __forceinline__ float row_reduce(float v, float* part) {
   return v;
 }
 
+// The sums of two values at once; `part`: 66 floats.
+__device__ __forceinline__ float2 row_sum2(float a, float b, float* part) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o), b += __shfl_xor_sync(0xffffffffu, b, o);
+  const int warps = blockDim.x >> 5;
+  if (warps == 1) return make_float2(a, b);
+  const int lane = threadIdx.x & 31;
+  float2* p2 = reinterpret_cast<float2*>(part);
+  if (lane == 0) p2[threadIdx.x >> 5] = make_float2(a, b);
+  __syncthreads();
+  const float2 v = lane < warps ? p2[lane] : make_float2(0.f, 0.f);
+  a = v.x, b = v.y;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o), b += __shfl_xor_sync(0xffffffffu, b, o);
+  return make_float2(a, b);
+}
+
 // ------------------------------------------------------------------ spread
 
 // Rows without 16-byte alignment, element by element: thread i holds the values

@@ -304,203 +304,6 @@ PyObject* add_rms_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
-// ----------------------------------------------------------------- products
-
-void check_grouped(const Tensor& A, const Tensor& B, const Tensor& ends) {
-  TORCH_CHECK_VALUE(A.dim() == 2 && B.dim() == 3 && B.size(1) == A.size(1), "A must be (T, K) and B (experts, K, N), got ",
-                    A.sizes(), " and ", B.sizes());
-  TORCH_CHECK_VALUE(ends.scalar_type() == at::kInt && ends.dim() == 1 && ends.size(0) == B.size(0),
-                    "group_ends must be an int32 vector with one ascending end for each expert");
-  same_device(A, {&B, &ends});
-}
-
-// How a (experts, K, N) B (`swapped`: its transpose) is read: in place when its K
-// rows (or, in bf16, its N rows) are contiguous, aligned and apart from each
-// other, else from a copy with K rows.
-struct Experts {
-  Tensor B;
-  int64_t K, N, ld, ld_e;
-  int n_major;
-  Experts(const Tensor& b, bool f8, bool swapped) : B(b) {
-    const int dk = swapped ? 2 : 1, dn = swapped ? 1 : 2;
-    const int64_t E = b.size(0), sk = b.stride(dk), sn = b.stride(dn);
-    K = b.size(dk), N = b.size(dn), ld_e = b.stride(0);
-    const bool apart = E == 1 || (ld_e > 0 && ld_e * b.element_size() % 16 == 0);
-    if (apart && sk == 1 && sn >= K && aligned(b, sn)) {
-      ld = sn, n_major = 0;
-    } else if (apart && !f8 && sn == 1 && sk >= N && aligned(b, sk)) {
-      ld = sk, n_major = 1;
-    } else {
-      B = fresh(b, {E, N, K}, b.scalar_type()).copy_(swapped ? b : b.transpose(1, 2));
-      ld = K, ld_e = N * K, n_major = 0;
-    }
-  }
-};
-
-Tensor grouped(const Tensor& A_, const Tensor& B, bool swapped, const Tensor& ends_, const Tensor& sa, const Tensor& sb,
-               at::ScalarType out, const Site& at) {
-  const int64_t T = A_.size(0), E = B.size(0);
-  const Tensor A = as_operand(A_), ends = ends_.contiguous();
-  const Experts ex(B, is8(B.scalar_type()), swapped);
-  const Tensor D = fresh(A, {T, ex.N}, out);
-  const Tensor ws = products_workspace(at, A);
-  auto stride = [](const Tensor& t, int d) { return t.defined() && t.size(d) > 1 ? t.stride(d) : 0; };
-  check_status(dg_layer_grouped_matmul(
-      A.data_ptr(), A.stride(0), type_of(A.scalar_type()), ex.B.data_ptr(), ex.ld, ex.ld_e, type_of(B.scalar_type()),
-      ex.n_major, static_cast<const int32_t*>(ends.data_ptr()), (int)E, static_cast<const float*>(ptr(sa)), stride(sa, 0),
-      static_cast<const float*>(ptr(sb)), stride(sb, 0), stride(sb, 1), D.data_ptr(), type_of(out), T, ex.N, ex.K,
-      ws.data_ptr(), status_word(at, A), at.handle()));
-  return D;
-}
-
-// A fp32 scale or None.
-Tensor scale_of(PyObject* o, const char* what) {
-  if (o == Py_None) return Tensor();
-  TORCH_CHECK_TYPE(THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kFloat, what,
-                   " must be a float32 tensor");
-  return tensor(o, what);
-}
-// The same seen as `shape` (stride 0 where it is shared).
-Tensor scale_as(Tensor t, at::IntArrayRef shape, const char* what) {
-  if (!t.defined() || t.sizes() == shape) return t;
-  if (shape.size() == 2 && t.dim() == 1) t = t.unsqueeze(1);  // one for each expert
-  bool fits = t.dim() <= (int64_t)shape.size();
-  for (int64_t d = 1; fits && d <= t.dim(); ++d) fits = t.size(-d) == 1 || t.size(-d) == shape[shape.size() - d];
-  TORCH_CHECK_VALUE(fits, what, " of shape ", t.sizes(), " does not broadcast to ", shape);
-  return t.expand(shape);
-}
-
-PyObject* grouped_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    want_args(n, 6);
-    const Tensor &A = tensor(a[0], "A"), &B = tensor(a[1], "B"), &ends = tensor(a[2], "group_ends");
-    const Tensor scale_a = scale_of(a[3], "scale_a"), scale_b = scale_of(a[4], "scale_b");
-    const at::ScalarType out = dtype(a[5]), ta = A.scalar_type(), tb = B.scalar_type();
-    check_grouped(A, B, ends);
-    TORCH_CHECK_TYPE((ta == at::kBFloat16 && tb == at::kBFloat16) || (is8(ta) && is8(tb)),
-                     "A and B must be both bfloat16 or both float8, got ", ta, " and ", tb);
-    TORCH_CHECK_VALUE(bf16_or_f32(out), "out_dtype must be bfloat16 or float32, got ", out);
-    const Tensor sa = scale_as(scale_a, {A.size(0)}, "scale_a"), sb = scale_as(scale_b, {B.size(0), B.size(2)}, "scale_b");
-    same_device(A, {&sa, &sb});
-    const Site at(A);
-    return wrap(grouped(A, B, false, ends, sa, sb, out, at));
-  });
-}
-
-// (experts, rows' columns, feats' columns): the sum over each group of
-// rows[t, :, None] * feats[t, None, :]; `swapped`: seen as its transpose.
-Tensor weight_grad(const Tensor& rows_, const Tensor& feats_, bool swapped, const Tensor& ends_, const Site& at) {
-  const Tensor rows = as_operand(rows_), feats = as_operand(feats_), ends = ends_.contiguous();
-  const int64_t T = rows.size(0), N = rows.size(1), K = feats.size(1), E = ends.size(0);
-  const Tensor out = swapped ? at::detail::empty_strided_cuda({E, K, N}, {N * K, 1, K}, rows.scalar_type(), rows.device())
-                             : at::detail::empty_cuda({E, N, K}, rows.scalar_type(), rows.device(), std::nullopt);
-  const Tensor ws = fresh(rows, {(int64_t)dg_layer_grouped_grad_workspace((int)E, N, K)}, at::kByte);
-  check_status(dg_layer_grouped_weight_grad(rows.data_ptr(), rows.stride(0), feats.data_ptr(), feats.stride(0),
-                                            static_cast<const int32_t*>(ends.data_ptr()), (int)E, out.data_ptr(),
-                                            DG_TYPE_BF16, T, N, K, ws.data_ptr(), products_workspace(at, rows).data_ptr(),
-                                            status_word(at, rows), at.handle()));
-  return out;
-}
-
-PyObject* grouped_matmul_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    want_args(n, 6);
-    const Tensor &dD = tensor(a[0], "dD"), &A = tensor(a[1], "A"), &B = tensor(a[2], "B"), &ends = tensor(a[3], "group_ends");
-    check_grouped(A, B, ends);
-    TORCH_CHECK_VALUE(dD.dim() == 2 && dD.size(0) == A.size(0) && dD.size(1) == B.size(2), "dD must be (", A.size(0), ", ",
-                      B.size(2), "), got ", dD.sizes());
-    TORCH_CHECK_TYPE(dD.scalar_type() == at::kBFloat16 && A.scalar_type() == at::kBFloat16 &&
-                         B.scalar_type() == at::kBFloat16,
-                     "dD, A and B must be bfloat16");
-    same_device(A, {&dD});
-    const Site at(A);
-    Tensor dA, dB;
-    if (a[4] == Py_True) dA = grouped(dD, B, true, ends, Tensor(), Tensor(), at::kBFloat16, at);
-    if (a[5] == Py_True)
-      dB = B.stride(2) == 1 && B.stride(1) != 1 ? weight_grad(A, dD, false, ends, at)  // contiguous along N
-                                                : weight_grad(dD, A, true, ends, at);
-    return Py_BuildValue("(NN)", wrap(dA), wrap(dB));
-  });
-}
-
-// ------------------------------------------------------- microscaled 4 bits
-
-PyObject* quantize_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    want_args(n, 1);
-    const Tensor& x = tensor(a[0], "x");
-    TORCH_CHECK_TYPE(bf16_or_f32(x.scalar_type()), "x must be bfloat16 or float32, got ", x.scalar_type());
-    TORCH_CHECK_VALUE(x.dim() >= 1, "x must have a last dimension");
-    const int64_t cols = x.size(-1);
-    same_device(x, {});
-    TORCH_CHECK_VALUE(cols % 32 == 0, "the last dimension (", cols, ") must be a multiple of 32");
-    const Site at(x);
-    Tensor x2 = as_rows(x, cols);
-    if (!aligned(x2, x2.stride(0))) x2 = fresh(x2, x2.sizes(), x2.scalar_type()).copy_(x2);
-    const int64_t rows = x2.size(0);
-    const Tensor codes = fresh(x, {rows, cols / 2}, at::kByte);
-    const Tensor scales = fresh(x, {(rows + 127) / 128, (cols + 255) / 256 * 2, 512}, at::kByte);
-    check_status(dg_layer_mx4_quantize(x2.data_ptr(), x2.stride(0), type_of(x2.scalar_type()), codes.data_ptr(),
-                                       scales.data_ptr(), rows, cols, at.handle()));
-    return Py_BuildValue("(NNLL)", wrap(codes), wrap(scales), (long long)rows, (long long)cols);
-  });
-}
-
-// A (codes, scales, rows, cols) tuple.
-struct Mx4 {
-  Tensor codes, scales;
-  int64_t rows, cols;
-  Mx4(PyObject* o, const char* what) {
-    TORCH_CHECK_TYPE(PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 4, what, " must be an MX4Tensor");
-    codes = tensor(PyTuple_GET_ITEM(o, 0), "codes");
-    scales = tensor(PyTuple_GET_ITEM(o, 1), "scales");
-    rows = PyLong_AsLongLong(PyTuple_GET_ITEM(o, 2));
-    cols = PyLong_AsLongLong(PyTuple_GET_ITEM(o, 3));
-    TORCH_CHECK_TYPE(!PyErr_Occurred(), what, ".rows and .cols must be whole numbers");
-    TORCH_CHECK_VALUE(rows >= 0 && cols >= 0 && cols % 32 == 0, what, ".cols must be a multiple of 32");
-    TORCH_CHECK_VALUE(codes.scalar_type() == at::kByte && codes.is_contiguous() && codes.dim() == 2 &&
-                          codes.size(0) == rows && codes.size(1) == cols / 2,
-                      what, ".codes must be contiguous uint8 of shape (", rows, ", ", cols / 2, ")");
-    const int64_t rt = (rows + 127) / 128, ct = (cols + 255) / 256 * 2;
-    TORCH_CHECK_VALUE(scales.scalar_type() == at::kByte && scales.is_contiguous() && scales.dim() == 3 &&
-                          scales.size(0) == rt && scales.size(1) == ct && scales.size(2) == 512,
-                      what, ".scales must be contiguous uint8 of shape (", rt, ", ", ct, ", 512)");
-    same_device(codes, {&scales});
-  }
-};
-
-PyObject* dequantize_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    want_args(n, 2);
-    const Mx4 q(a[0], "q");
-    const at::ScalarType out = dtype(a[1]);
-    TORCH_CHECK_VALUE(bf16_or_f32(out), "out_dtype must be bfloat16 or float32, got ", out);
-    const Site at(q.codes);
-    const Tensor y = fresh(q.codes, {q.rows, q.cols}, out);
-    check_status(dg_layer_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), y.data_ptr(), type_of(out), q.rows,
-                                         q.cols, at.handle()));
-    return wrap(y);
-  });
-}
-
-PyObject* mx4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded([&]() -> PyObject* {
-    want_args(n, 3);
-    const Mx4 p(a[0], "a"), q(a[1], "b");
-    const at::ScalarType out = dtype(a[2]);
-    TORCH_CHECK_VALUE(p.cols == q.cols, "a has ", p.cols, " columns, b ", q.cols);
-    TORCH_CHECK_VALUE(bf16_or_f32(out), "out_dtype must be bfloat16 or float32, got ", out);
-    same_device(p.codes, {&q.codes});
-    const Site at(p.codes);
-    const Tensor D = fresh(p.codes, {p.rows, q.rows}, out);
-    const Tensor ws = products_workspace(at, p.codes);
-    check_status(dg_layer_mx4_matmul(p.codes.data_ptr(), p.scales.data_ptr(), q.codes.data_ptr(), q.scales.data_ptr(),
-                                     D.data_ptr(), type_of(out), p.rows, q.rows, p.cols, ws.data_ptr(),
-                                     status_word(at, p.codes), at.handle()));
-    return wrap(D);
-  });
-}
-
 // ------------------------------------------------------ 8-bit blocks of 128
 
 int64_t whole(PyObject* o, const char* what) {
@@ -609,6 +412,357 @@ PyObject* block8_matmul(PyObject*, PyObject* const* args, Py_ssize_t n) {
   });
 }
 
+// ----------------------------------------------------------------- products
+
+void check_ends(const Tensor& B, const Tensor& ends) {
+  TORCH_CHECK_VALUE(ends.scalar_type() == at::kInt && ends.dim() == 1 && ends.size(0) == B.size(0),
+                    "group_ends must be an int32 vector with one ascending end for each expert");
+}
+void check_grouped(const Tensor& A, const Tensor& B, const Tensor& ends) {
+  TORCH_CHECK_VALUE(A.dim() == 2 && B.dim() == 3 && B.size(1) == A.size(1), "A must be (T, K) and B (experts, K, N), got ",
+                    A.sizes(), " and ", B.sizes());
+  check_ends(B, ends);
+  same_device(A, {&B, &ends});
+}
+
+// How a (experts, K, N) B (`swapped`: its transpose) is read: in place when its K
+// rows (or, in bf16, its N rows) are contiguous, aligned and apart from each
+// other, else from a copy with K rows.
+struct Experts {
+  Tensor B;
+  int64_t K, N, ld, ld_e;
+  int n_major;
+  Experts(const Tensor& b, bool f8, bool swapped) : B(b) {
+    const int dk = swapped ? 2 : 1, dn = swapped ? 1 : 2;
+    const int64_t E = b.size(0), sk = b.stride(dk), sn = b.stride(dn);
+    K = b.size(dk), N = b.size(dn), ld_e = b.stride(0);
+    const bool apart = E == 1 || (ld_e > 0 && ld_e * b.element_size() % 16 == 0);
+    if (apart && sk == 1 && sn >= K && aligned(b, sn)) {
+      ld = sn, n_major = 0;
+    } else if (apart && !f8 && sn == 1 && sk >= N && aligned(b, sk)) {
+      ld = sk, n_major = 1;
+    } else {
+      B = fresh(b, {E, N, K}, b.scalar_type()).copy_(swapped ? b : b.transpose(1, 2));
+      ld = K, ld_e = N * K, n_major = 0;
+    }
+  }
+};
+
+Tensor grouped(const Tensor& A_, const Tensor& B, bool swapped, const Tensor& ends_, const Tensor& sa, const Tensor& sb,
+               at::ScalarType out, const Site& at) {
+  const int64_t T = A_.size(0), E = B.size(0);
+  const Tensor A = as_operand(A_), ends = ends_.contiguous();
+  const Experts ex(B, is8(B.scalar_type()), swapped);
+  const Tensor D = fresh(A, {T, ex.N}, out);
+  const Tensor ws = products_workspace(at, A);
+  auto stride = [](const Tensor& t, int d) { return t.defined() && t.size(d) > 1 ? t.stride(d) : 0; };
+  check_status(dg_layer_grouped_matmul(
+      A.data_ptr(), A.stride(0), type_of(A.scalar_type()), ex.B.data_ptr(), ex.ld, ex.ld_e, type_of(B.scalar_type()),
+      ex.n_major, static_cast<const int32_t*>(ends.data_ptr()), (int)E, static_cast<const float*>(ptr(sa)), stride(sa, 0),
+      static_cast<const float*>(ptr(sb)), stride(sb, 0), stride(sb, 1), D.data_ptr(), type_of(out), T, ex.N, ex.K,
+      ws.data_ptr(), status_word(at, A), at.handle()));
+  return D;
+}
+
+// A fp32 scale or None.
+Tensor scale_of(PyObject* o, const char* what) {
+  if (o == Py_None) return Tensor();
+  TORCH_CHECK_TYPE(THPVariable_Check(o) && THPVariable_Unpack(o).scalar_type() == at::kFloat, what,
+                   " must be a float32 tensor");
+  return tensor(o, what);
+}
+// The same seen as `shape` (stride 0 where it is shared).
+Tensor scale_as(Tensor t, at::IntArrayRef shape, const char* what) {
+  if (!t.defined() || t.sizes() == shape) return t;
+  if (shape.size() == 2 && t.dim() == 1) t = t.unsqueeze(1);  // one for each expert
+  bool fits = t.dim() <= (int64_t)shape.size();
+  for (int64_t d = 1; fits && d <= t.dim(); ++d) fits = t.size(-d) == 1 || t.size(-d) == shape[shape.size() - d];
+  TORCH_CHECK_VALUE(fits, what, " of shape ", t.sizes(), " does not broadcast to ", shape);
+  return t.expand(shape);
+}
+
+PyObject* grouped_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 6);
+    const Tensor &A = tensor(a[0], "A"), &B = tensor(a[1], "B"), &ends = tensor(a[2], "group_ends");
+    const Tensor scale_a = scale_of(a[3], "scale_a"), scale_b = scale_of(a[4], "scale_b");
+    const at::ScalarType out = dtype(a[5]), ta = A.scalar_type(), tb = B.scalar_type();
+    check_grouped(A, B, ends);
+    TORCH_CHECK_TYPE((ta == at::kBFloat16 && tb == at::kBFloat16) || (is8(ta) && is8(tb)),
+                     "A and B must be both bfloat16 or both float8, got ", ta, " and ", tb);
+    TORCH_CHECK_VALUE(bf16_or_f32(out), "out_dtype must be bfloat16 or float32, got ", out);
+    const Tensor sa = scale_as(scale_a, {A.size(0)}, "scale_a"), sb = scale_as(scale_b, {B.size(0), B.size(2)}, "scale_b");
+    same_device(A, {&sa, &sb});
+    const Site at(A);
+    return wrap(grouped(A, B, false, ends, sa, sb, out, at));
+  });
+}
+
+Tensor new_weight_grad(const Tensor& like, int64_t E, int64_t N, int64_t K, bool swapped) {
+  return swapped ? at::detail::empty_strided_cuda({E, K, N}, {N * K, 1, K}, at::kBFloat16, like.device())
+                 : at::detail::empty_cuda({E, N, K}, at::kBFloat16, like.device(), std::nullopt);
+}
+
+// (experts, rows' columns, feats' columns): the sum over each group of
+// rows[t, :, None] * feats[t, None, :]; `swapped`: seen as its transpose.
+Tensor weight_grad(const Tensor& rows_, const Tensor& feats_, bool swapped, const Tensor& ends_, const Site& at) {
+  const Tensor rows = as_operand(rows_), feats = as_operand(feats_), ends = ends_.contiguous();
+  const int64_t T = rows.size(0), N = rows.size(1), K = feats.size(1), E = ends.size(0);
+  const Tensor out = new_weight_grad(rows, E, N, K, swapped);
+  const Tensor ws = fresh(rows, {(int64_t)dg_layer_grouped_grad_workspace((int)E, N, K)}, at::kByte);
+  check_status(dg_layer_grouped_weight_grad(rows.data_ptr(), rows.stride(0), feats.data_ptr(), feats.stride(0),
+                                            static_cast<const int32_t*>(ends.data_ptr()), (int)E, out.data_ptr(),
+                                            DG_TYPE_BF16, T, N, K, ws.data_ptr(), products_workspace(at, rows).data_ptr(),
+                                            status_word(at, rows), at.handle()));
+  return out;
+}
+
+// (experts, K, N) gradient from A's rows in 8-bit blocks; n_major: contiguous along N.
+Tensor weight_grad8(const Tensor& rows_, const Block8& feats, bool n_major, const Tensor& ends_, const Site& at) {
+  const Tensor rows = as_operand(rows_), ends = ends_.contiguous();
+  const int64_t T = rows.size(0), N = rows.size(1), K = feats.cols, E = ends.size(0);
+  const Tensor out = n_major ? new_weight_grad(rows, E, K, N, false) : new_weight_grad(rows, E, N, K, true);
+  const Tensor ws = fresh(rows, {(int64_t)dg_layer_grouped_grad8_workspace(T, (int)E, N, K)}, at::kByte);
+  check_status(dg_layer_grouped_weight_grad8(
+      rows.data_ptr(), rows.stride(0), feats.values.data_ptr(), type_of(feats.values.scalar_type()), feats.scale_ptr(),
+      feats.scales.stride(0), feats.scales.stride(1), static_cast<const int32_t*>(ends.data_ptr()), (int)E, out.data_ptr(),
+      n_major, DG_TYPE_BF16, T, N, K, ws.data_ptr(), products_workspace(at, rows).data_ptr(), status_word(at, rows), at.handle()));
+  return out;
+}
+
+PyObject* grouped_matmul_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 6);
+    const bool need_a = a[4] == Py_True, need_b = a[5] == Py_True, kept = PyTuple_Check(a[1]);
+    const Tensor &dD = tensor(a[0], "dD"), &B = tensor(a[2], "B"), &ends = tensor(a[3], "group_ends");
+    Tensor A = kept ? Tensor() : maybe(a[1], "A");
+    TORCH_CHECK_TYPE(kept || A.defined() || !need_b, "B's gradient needs A");
+    TORCH_CHECK_VALUE(dD.dim() == 2 && B.dim() == 3 && dD.size(1) == B.size(2), "dD must be (T, N) and B (experts, K, N), got ",
+                      dD.sizes(), " and ", B.sizes());
+    if (A.defined()) {
+      check_grouped(A, B, ends);
+      TORCH_CHECK_VALUE(dD.size(0) == A.size(0), "dD must be (", A.size(0), ", ", B.size(2), "), got ", dD.sizes());
+      TORCH_CHECK_TYPE(A.scalar_type() == at::kBFloat16, "dD, A and B must be bfloat16");
+    } else {
+      check_ends(B, ends);
+      same_device(dD, {&B, &ends});
+    }
+    TORCH_CHECK_TYPE(dD.scalar_type() == at::kBFloat16 && B.scalar_type() == at::kBFloat16, "dD, A and B must be bfloat16");
+    same_device(B, {&dD});
+    Tensor dA, dB;
+    if (kept) {
+      Block8 q(a[1], "A");
+      TORCH_CHECK_VALUE(q.block_rows == 1 && q.rows == dD.size(0) && q.cols == B.size(1), "an 8-bit A must be (", dD.size(0), ", ",
+                        B.size(1), ") in blocks of 1 x 128, got ", q.values.sizes(), " in blocks of ", q.block_rows, " rows");
+      same_device(dD, {&q.values, &q.scales});
+      const Site at(dD);
+      if (need_a) dA = grouped(dD, B, true, ends, Tensor(), Tensor(), at::kBFloat16, at);
+      if (need_b) {
+        q.align();
+        dB = weight_grad8(dD, q, B.stride(2) == 1 && B.stride(1) != 1, ends, at);
+      }
+      return Py_BuildValue("(NN)", wrap(dA), wrap(dB));
+    }
+    const Site at(dD);
+    if (need_a) dA = grouped(dD, B, true, ends, Tensor(), Tensor(), at::kBFloat16, at);
+    if (need_b)
+      dB = B.stride(2) == 1 && B.stride(1) != 1 ? weight_grad(A, dD, false, ends, at)  // contiguous along N
+                                                : weight_grad(dD, A, true, ends, at);
+    return Py_BuildValue("(NN)", wrap(dA), wrap(dB));
+  });
+}
+
+// ------------------------------------------------------- microscaled 4 bits
+
+PyObject* quantize_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 1);
+    const Tensor& x = tensor(a[0], "x");
+    TORCH_CHECK_TYPE(bf16_or_f32(x.scalar_type()), "x must be bfloat16 or float32, got ", x.scalar_type());
+    TORCH_CHECK_VALUE(x.dim() >= 1, "x must have a last dimension");
+    const int64_t cols = x.size(-1);
+    same_device(x, {});
+    TORCH_CHECK_VALUE(cols % 32 == 0, "the last dimension (", cols, ") must be a multiple of 32");
+    const Site at(x);
+    Tensor x2 = as_rows(x, cols);
+    if (!aligned(x2, x2.stride(0))) x2 = fresh(x2, x2.sizes(), x2.scalar_type()).copy_(x2);
+    const int64_t rows = x2.size(0);
+    const Tensor codes = fresh(x, {rows, cols / 2}, at::kByte);
+    const Tensor scales = fresh(x, {(rows + 127) / 128, (cols + 255) / 256 * 2, 512}, at::kByte);
+    check_status(dg_layer_mx4_quantize(x2.data_ptr(), x2.stride(0), type_of(x2.scalar_type()), codes.data_ptr(),
+                                       scales.data_ptr(), rows, cols, at.handle()));
+    return Py_BuildValue("(NNLL)", wrap(codes), wrap(scales), (long long)rows, (long long)cols);
+  });
+}
+
+// A (codes, scales, rows, cols) tuple.
+struct Mx4 {
+  Tensor codes, scales;
+  int64_t rows, cols;
+  Mx4(PyObject* o, const char* what) {
+    TORCH_CHECK_TYPE(PyTuple_Check(o) && PyTuple_GET_SIZE(o) == 4, what, " must be an MX4Tensor");
+    codes = tensor(PyTuple_GET_ITEM(o, 0), "codes");
+    scales = tensor(PyTuple_GET_ITEM(o, 1), "scales");
+    rows = PyLong_AsLongLong(PyTuple_GET_ITEM(o, 2));
+    cols = PyLong_AsLongLong(PyTuple_GET_ITEM(o, 3));
+    TORCH_CHECK_TYPE(!PyErr_Occurred(), what, ".rows and .cols must be whole numbers");
+    TORCH_CHECK_VALUE(rows >= 0 && cols >= 0 && cols % 32 == 0, what, ".cols must be a multiple of 32");
+    TORCH_CHECK_VALUE(codes.scalar_type() == at::kByte && codes.is_contiguous() && codes.dim() == 2 &&
+                          codes.size(0) == rows && codes.size(1) == cols / 2,
+                      what, ".codes must be contiguous uint8 of shape (", rows, ", ", cols / 2, ")");
+    const int64_t rt = (rows + 127) / 128, ct = (cols + 255) / 256 * 2;
+    TORCH_CHECK_VALUE(scales.scalar_type() == at::kByte && scales.is_contiguous() && scales.dim() == 3 &&
+                          scales.size(0) == rt && scales.size(1) == ct && scales.size(2) == 512,
+                      what, ".scales must be contiguous uint8 of shape (", rt, ", ", ct, ", 512)");
+    same_device(codes, {&scales});
+  }
+};
+
+PyObject* dequantize_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 2);
+    const Mx4 q(a[0], "q");
+    const at::ScalarType out = dtype(a[1]);
+    TORCH_CHECK_VALUE(bf16_or_f32(out), "out_dtype must be bfloat16 or float32, got ", out);
+    const Site at(q.codes);
+    const Tensor y = fresh(q.codes, {q.rows, q.cols}, out);
+    check_status(dg_layer_mx4_dequantize(q.codes.data_ptr(), q.scales.data_ptr(), y.data_ptr(), type_of(out), q.rows,
+                                         q.cols, at.handle()));
+    return wrap(y);
+  });
+}
+
+PyObject* mx4_matmul(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 3);
+    const Mx4 p(a[0], "a"), q(a[1], "b");
+    const at::ScalarType out = dtype(a[2]);
+    TORCH_CHECK_VALUE(p.cols == q.cols, "a has ", p.cols, " columns, b ", q.cols);
+    TORCH_CHECK_VALUE(bf16_or_f32(out), "out_dtype must be bfloat16 or float32, got ", out);
+    same_device(p.codes, {&q.codes});
+    const Site at(p.codes);
+    const Tensor D = fresh(p.codes, {p.rows, q.rows}, out);
+    const Tensor ws = products_workspace(at, p.codes);
+    check_status(dg_layer_mx4_matmul(p.codes.data_ptr(), p.scales.data_ptr(), q.codes.data_ptr(), q.scales.data_ptr(),
+                                     D.data_ptr(), type_of(out), p.rows, q.rows, p.cols, ws.data_ptr(),
+                                     status_word(at, p.codes), at.handle()));
+    return wrap(D);
+  });
+}
+
+// --------------------------------------------------------------- layer norm
+
+// A weight or bias of a norm: a contiguous vector, or None.
+Tensor affine_of(PyObject* o, const char* what, int64_t hidden) {
+  const Tensor t = maybe(o, what);
+  if (!t.defined()) return t;
+  TORCH_CHECK_VALUE(t.dim() == 1 && t.size(0) == hidden && t.is_contiguous(), what, " must be a contiguous vector of ", hidden, " values");
+  TORCH_CHECK_TYPE(bf16_or_f32(t.scalar_type()), what, " must be bfloat16 or float32");
+  return t;
+}
+int affine_type(const Tensor& t) { return t.defined() ? type_of(t.scalar_type()) : DG_TYPE_BF16; }
+Tensor aligned_copy(const Tensor& t) {
+  return !t.defined() || reinterpret_cast<uintptr_t>(t.data_ptr()) % 16 == 0 ? t : fresh(t, t.sizes(), t.scalar_type()).copy_(t);
+}
+
+PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 8);
+    const Tensor& x = tensor(a[0], "x");
+    const Tensor residual = maybe(a[3], "residual");
+    const double eps = PyFloat_AsDouble(a[4]);
+    if (eps == -1.0 && PyErr_Occurred()) return nullptr;
+    const at::ScalarType out = dtype(a[5]);
+    const bool keep_stats = a[6] == Py_True, keep = a[7] != Py_None, out8 = is8(out);
+    const at::ScalarType kept_type = keep ? dtype(a[7]) : at::kFloat8_e4m3fn;
+    TORCH_CHECK_TYPE(x.dim() >= 1 && bf16_or_f32(x.scalar_type()),
+                     "x must be a bfloat16 or float32 tensor with a last dimension to normalise");
+    const int64_t hidden = x.size(-1);
+    Tensor weight = affine_of(a[1], "weight", hidden), bias = affine_of(a[2], "bias", hidden);
+    if (residual.defined()) {
+      TORCH_CHECK_VALUE(residual.sizes() == x.sizes(), "residual must have x's shape");
+      TORCH_CHECK_TYPE(bf16_or_f32(residual.scalar_type()), "residual must be bfloat16 or float32");
+    }
+    TORCH_CHECK_VALUE(out == at::kBFloat16 || out8, "out_dtype must be bfloat16 or a float8 type, got ", out);
+    TORCH_CHECK_VALUE(is8(kept_type), "keep_dtype must be a float8 type, got ", kept_type);
+    TORCH_CHECK_VALUE(!(out8 || keep) || hidden % 16 == 0, "8-bit blocks need a last dimension that is a multiple of 16, got ", hidden);
+    same_device(x, {&weight, &bias, &residual});
+    const Site at(x);
+    Tensor x2 = as_rows(x, hidden), r2 = residual.defined() ? as_rows(residual, hidden) : residual;
+    if (out8 || keep) {  // (their kernels take whole vectors)
+      x2 = as_operand(x2);
+      if (r2.defined()) r2 = as_operand(r2);
+      weight = aligned_copy(weight), bias = aligned_copy(bias);
+    }
+    const int64_t rows = x2.size(0);
+    const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
+    Tensor y = out8 ? fresh(x, {rows, hidden}, out) : fresh(x, x.sizes(), out), ys, kept, ks, mean, rstd, h;
+    if (out8) ys = fresh_scales(x, rows, hidden);
+    if (keep) kept = fresh(x, {rows, hidden}, kept_type), ks = fresh_scales(x, rows, hidden);
+    if (keep_stats) mean = fresh(x, lead, at::kFloat), rstd = fresh(x, lead, at::kFloat);
+    if (residual.defined()) h = fresh(x, x.sizes(), residual.scalar_type());
+    auto stride = [](const Tensor& t, int d) { return t.defined() ? t.stride(d) : 0; };
+    check_status(dg_layer_layer_norm(
+        x2.data_ptr(), x2.stride(0), type_of(x2.scalar_type()), ptr(r2), stride(r2, 0),
+        r2.defined() ? type_of(r2.scalar_type()) : DG_TYPE_BF16, ptr(weight), affine_type(weight), ptr(bias), affine_type(bias),
+        y.data_ptr(), type_of(out), static_cast<float*>(ptr(ys)), stride(ys, 0), stride(ys, 1), ptr(h), hidden, ptr(kept),
+        type_of(kept_type), static_cast<float*>(ptr(ks)), stride(ks, 0), stride(ks, 1), static_cast<float*>(ptr(mean)),
+        static_cast<float*>(ptr(rstd)), rows, hidden, (float)eps, at.handle()));
+    return Py_BuildValue("(NNNNNNN)", wrap(y), wrap(ys), wrap(h.defined() ? h : x), wrap(mean), wrap(rstd), wrap(kept), wrap(ks));
+  });
+}
+
+PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    want_args(n, 7);
+    const Tensor &dy = tensor(a[0], "dy"), mean = tensor(a[3], "mean").contiguous(), rstd = tensor(a[4], "rstd").contiguous();
+    const Tensor dh = maybe(a[5], "d_residual");
+    TORCH_CHECK_VALUE(dy.dim() >= 1, "dy must have a last dimension");
+    TORCH_CHECK_TYPE(dy.scalar_type() == at::kBFloat16 && mean.scalar_type() == at::kFloat && rstd.scalar_type() == at::kFloat,
+                     "dy must be bfloat16, mean and rstd float32");
+    const int64_t hidden = dy.size(-1);
+    const Tensor weight = affine_of(a[2], "weight", hidden);
+    const bool want_bias = weight.defined() || a[6] != Py_None;
+    const at::ScalarType bias_type = a[6] != Py_None ? dtype(a[6]) : weight.defined() ? weight.scalar_type() : at::kBFloat16;
+    TORCH_CHECK_VALUE(bf16_or_f32(bias_type), "bias_dtype must be bfloat16 or float32, got ", bias_type);
+    int64_t rows = 1;
+    for (int64_t d = 0; d + 1 < dy.dim(); ++d) rows *= dy.size(d);
+    Tensor h, scales;
+    at::ScalarType type = at::kBFloat16;
+    if (PyTuple_Check(a[1])) {
+      Block8 q(a[1], "h");
+      TORCH_CHECK_VALUE(q.block_rows == 1 && q.rows == rows && q.cols == hidden, "an 8-bit h must be dy's rows in blocks of 1 x 128");
+      q.align();
+      h = q.values, scales = q.scales;
+    } else {
+      h = tensor(a[1], "h");
+      TORCH_CHECK_VALUE(h.sizes() == dy.sizes(), "h must have dy's shape");
+      TORCH_CHECK_TYPE(bf16_or_f32(h.scalar_type()), "h must be bfloat16, float32 or a Block8Tensor");
+      type = h.scalar_type();
+    }
+    const at::IntArrayRef lead = dy.sizes().slice(0, dy.dim() - 1);
+    TORCH_CHECK_VALUE(mean.sizes() == lead && rstd.sizes() == lead, "mean and rstd must have the shape of dy's rows");
+    TORCH_CHECK_VALUE(!dh.defined() || (dh.sizes() == dy.sizes() && dh.scalar_type() == type), "d_residual must have dy's shape and dx's type (",
+                      type, ")");
+    same_device(dy, {&h, &scales, &weight, &mean, &rstd, &dh});
+    const Site at(dy);
+    const Tensor dy2 = as_rows(dy, hidden), h2 = scales.defined() ? h : as_rows(h, hidden), d2 = dh.defined() ? as_rows(dh, hidden) : dh;
+    const Tensor dx = fresh(dy, dy.sizes(), type);
+    Tensor dw, db, ws;
+    if (weight.defined()) dw = fresh(dy, weight.sizes(), weight.scalar_type());
+    if (want_bias) {
+      db = fresh(dy, {hidden}, bias_type);
+      ws = fresh(dy, {(int64_t)dg_layer_layer_norm_backward_workspace(rows, hidden)}, at::kByte);
+    }
+    check_status(dg_layer_layer_norm_backward(
+        dy2.data_ptr(), dy2.stride(0), h2.data_ptr(), h2.stride(0), type_of(h2.scalar_type()), static_cast<const float*>(ptr(scales)),
+        scales.defined() ? scales.stride(0) : 0, scales.defined() ? scales.stride(1) : 0, ptr(weight), affine_type(weight),
+        static_cast<const float*>(mean.data_ptr()), static_cast<const float*>(rstd.data_ptr()), ptr(d2), d2.defined() ? d2.stride(0) : 0,
+        dx.data_ptr(), ptr(dw), ptr(db), type_of(bias_type), ptr(ws), rows, hidden, at.handle()));
+    return Py_BuildValue("(NNN)", wrap(dx), wrap(dw), wrap(db));
+  });
+}
+
 // ------------------------------------------------------------------- module
 
 PyObject* check(PyObject*, PyObject* const* a, Py_ssize_t n) {
@@ -662,6 +816,8 @@ PyMethodDef g_methods[] = {DGL_METHOD(add_rms_norm),
                            DGL_METHOD(quantize_block8),
                            DGL_METHOD(dequantize_block8),
                            DGL_METHOD(block8_matmul),
+                           DGL_METHOD(layer_norm),
+                           DGL_METHOD(layer_norm_backward),
                            DGL_METHOD(check),
                            DGL_METHOD(clear_workspaces),
                            DGL_METHOD(set_error),

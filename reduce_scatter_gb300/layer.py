@@ -1,6 +1,7 @@
 """Operators around the tensor-parallel GEMM, over the C ABI in
-``include/dg_layer.h``: residual add with RMS norm (16- or 8-bit output),
-products grouped by expert, microscaled 4-bit tensors and their product.
+``include/dg_layer.h``: residual add with RMS norm or layer norm (16- or 8-bit
+output), products grouped by expert, microscaled 4-bit tensors and 8-bit tensors
+with a scale for each block of 128, and their products.
 
 :mod:`reduce_scatter_gb300.ops` exports the public names.  Arguments are checked
 and marshalled, and outputs allocated with torch, by the extension
@@ -8,9 +9,9 @@ and marshalled, and outputs allocated with torch, by the extension
 ``libdg.so`` on the current stream of the inputs' device.  There is no fallback:
 without the built libraries the first call raises ``RuntimeError``.  No call
 synchronizes; each may be captured into a CUDA graph after one call outside
-capture.  ``add_rms_norm`` (bf16 output) and ``grouped_matmul`` (bf16) take part
-in autograd; their gradients can also be called directly.  No call carries on
-forward-mode tangents (``ValueError``).
+capture.  ``add_rms_norm`` and ``layer_norm`` (bf16 output), ``grouped_matmul``
+(bf16) and ``block8_linear`` take part in autograd; their gradients can also be
+called directly.  No call carries on forward-mode tangents (``ValueError``).
 
 Errors: ``ValueError`` / ``TypeError`` for arguments that the front end refuses,
 ``dg.DGError`` for what the C ABI refuses.
@@ -34,9 +35,10 @@ EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "dg_
 # Every symbol include/dg_layer.h declares.
 EXPORTS = ("dg_layer_add_rms_norm", "dg_layer_add_rms_norm_backward", "dg_layer_add_rms_norm_backward_workspace",
            "dg_layer_products_workspace", "dg_layer_grouped_matmul", "dg_layer_grouped_grad_workspace",
-           "dg_layer_grouped_weight_grad", "dg_layer_mx4_scale_bytes", "dg_layer_mx4_quantize",
+           "dg_layer_grouped_weight_grad", "dg_layer_grouped_grad8_workspace", "dg_layer_grouped_weight_grad8", "dg_layer_mx4_scale_bytes", "dg_layer_mx4_quantize",
            "dg_layer_mx4_dequantize", "dg_layer_mx4_matmul", "dg_layer_block8_quantize", "dg_layer_block8_dequantize",
-           "dg_layer_block8_matmul", "dg_layer_check", "dg_layer_last_error")
+           "dg_layer_block8_matmul", "dg_layer_layer_norm", "dg_layer_layer_norm_backward",
+           "dg_layer_layer_norm_backward_workspace", "dg_layer_check", "dg_layer_last_error")
 
 _LIB = None
 _EXT = None
@@ -58,6 +60,8 @@ def lib():
                                      i64, i64, i64, vp, vp, vp]),
             "grouped_grad_workspace": (sz, [i32, i64, i64]),
             "grouped_weight_grad": (i32, [vp, i64, vp, i64, vp, i32, vp, i32, i64, i64, i64, vp, vp, vp, vp]),
+            "grouped_grad8_workspace": (sz, [i64, i32, i64, i64]),
+            "grouped_weight_grad8": (i32, [vp, i64, vp, i32, vp, i64, i64, vp, i32, vp, i32, i32, i64, i64, i64, vp, vp, vp, vp]),
             "mx4_scale_bytes": (sz, [i64, i64]),
             "mx4_quantize": (i32, [vp, i64, i32, vp, vp, i64, i64, vp]),
             "mx4_dequantize": (i32, [vp, vp, vp, i32, i64, i64, vp]),
@@ -66,6 +70,11 @@ def lib():
             "block8_dequantize": (i32, [vp, i32, vp, i64, i64, i32, vp, i32, i64, i64, vp]),
             "block8_matmul": (i32, [vp, i32, vp, i64, i64, i32, i32, vp, i32, vp, i64, i64, i32, i32, vp, i32, i64, i64,
                                     i64, vp, vp, vp]),
+            "layer_norm": (i32, [vp, i64, i32, vp, i64, i32, vp, i32, vp, i32, vp, i32, vp, i64, i64, vp, i64, vp, i32, vp,
+                                 i64, i64, vp, vp, i64, i64, f32, vp]),
+            "layer_norm_backward_workspace": (sz, [i64, i64]),
+            "layer_norm_backward": (i32, [vp, i64, vp, i64, i32, vp, i64, i64, vp, i32, vp, vp, vp, i64, vp, vp, vp, i32, vp,
+                                          i64, i64, vp]),
             "check": (i32, [vp, vp]),
             "last_error": (ctypes.c_char_p, []),
         }
@@ -183,20 +192,26 @@ def add_rms_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tenso
 
 class _GroupedMatmul(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, A, B, ends, out_dtype):
-        ctx.save_for_backward(A, B, ends)
+    def forward(ctx, A, B, ends, out_dtype, keep_dtype):
+        kept = scales = None
+        if keep_dtype is not None and ctx.needs_input_grad[1]:
+            kept, scales, _ = (_EXT or _load()).quantize_block8(A, 1, keep_dtype, True)
+        # (A's own values are for B's gradient alone)
+        ctx.save_for_backward(A if kept is None and ctx.needs_input_grad[1] else None, kept, scales, B, ends)
         return (_EXT or _load()).grouped_matmul(A, B, ends, None, None, out_dtype)
 
     @staticmethod
     @once_differentiable
     def backward(ctx, dD):
-        A, B, ends = ctx.saved_tensors
-        dA, dB = grouped_matmul_backward(dD.to(torch.bfloat16), A, B, ends, need=ctx.needs_input_grad[:2])
-        return dA, dB, None, None
+        A, kept, scales, B, ends = ctx.saved_tensors
+        dD = dD.to(torch.bfloat16)
+        dA, dB = grouped_matmul_backward(dD, A if kept is None else Block8Tensor(kept, scales, 1), B, ends,
+                                         need=ctx.needs_input_grad[:2])
+        return dA, dB, None, None, None
 
 
 def grouped_matmul(A: torch.Tensor, B: torch.Tensor, group_ends: torch.Tensor, *, scale_a=None, scale_b=None,
-                   out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
+                   out_dtype: torch.dtype = torch.bfloat16, keep_dtype: torch.dtype | None = None) -> torch.Tensor:
     """``D[t] = A[t] @ B[e]`` for the rows ``group_ends[e - 1] <= t < group_ends[e]``.
 
     ``A`` (T, K): the rows sorted by expert; ``B`` (experts, K, N), of A's type
@@ -209,22 +224,28 @@ def grouped_matmul(A: torch.Tensor, B: torch.Tensor, group_ends: torch.Tensor, *
     (experts,) or one element: float32 factors of D's rows and of each expert's
     columns.  ``out_dtype``: bfloat16 or float32.  K % 8 == 0 (16 for float8)
     and N % 8 == 0.  Differentiable in bfloat16 without scales (the gradients are
-    products of bfloat16 operands, accumulated in fp32).
-    """
+    products of bfloat16 operands, accumulated in fp32).  ``keep_dtype``, a float8
+    type: the graph keeps A's rows in 8 bits (blocks of 1 x 128, power-of-two
+    scales) for B's gradient, half the memory; K % 16 == 0."""
+    if keep_dtype is not None and keep_dtype not in (torch.float8_e4m3fn, torch.float8_e5m2):
+        raise ValueError(f"keep_dtype must be a float8 type, got {keep_dtype}")
     if torch.is_grad_enabled() and (A.requires_grad or B.requires_grad or
                                     (scale_a is not None and getattr(scale_a, "requires_grad", False)) or
                                     (scale_b is not None and getattr(scale_b, "requires_grad", False))):
         if scale_a is not None or scale_b is not None or A.dtype != torch.bfloat16:
             raise ValueError("float8 operands and scales have no gradient: call under torch.no_grad()")
-        return _GroupedMatmul.apply(A, B, group_ends, out_dtype)
+        return _GroupedMatmul.apply(A, B, group_ends, out_dtype, keep_dtype)
     return (_EXT or _load()).grouped_matmul(A, B, group_ends, scale_a, scale_b, out_dtype)
 
 
-def grouped_matmul_backward(dD: torch.Tensor, A: torch.Tensor, B: torch.Tensor, group_ends: torch.Tensor, *,
+def grouped_matmul_backward(dD: torch.Tensor, A: torch.Tensor | Block8Tensor | None, B: torch.Tensor, group_ends: torch.Tensor, *,
                             need=(True, True)):
     """``(dA, dB)`` of the bfloat16 :func:`grouped_matmul`: ``dA[t] = dD[t] @ B[e].T``
     (0 past the last group) and ``dB[e] = A_e.T @ dD_e`` (0 for an empty group),
-    dB in B's layout; ``need``: which of the two to compute (else None)."""
+    dB in B's layout; ``need``: which of the two to compute (else None).  ``A``
+    may be a :class:`Block8Tensor` of 1 x 128 blocks, rows that were kept in 8
+    bits: its values enter dB in bfloat16 (exact with power-of-two scales); or
+    None where dB is not computed."""
     return (_EXT or _load()).grouped_matmul_backward(dD, A, B, group_ends, bool(need[0]), bool(need[1]))
 
 
@@ -316,3 +337,133 @@ def block8_matmul(a: Block8Tensor, b: Block8Tensor, *, trans_a: bool = False, tr
     sum times its two scales (their product in fp32); N % 8 == 0; ``out_dtype``
     bfloat16 or float32."""
     return (_EXT or _load()).block8_matmul(a, b, bool(trans_a), bool(trans_b), out_dtype)
+
+
+class _Block8Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, dtype, grad_dtype):
+        ext = _EXT or _load()
+        lead, ctx.grad_dtype = x.shape[:-1], grad_dtype
+        xq, wq = ext.quantize_block8(x, 128, dtype, False), ext.quantize_block8(weight, 128, dtype, False)
+        need = ctx.needs_input_grad
+        ctx.save_for_backward(*(xq[:2] if need[1] else (None, None)), *(wq[:2] if need[0] else (None, None)))
+        return ext.block8_matmul(xq, wq, False, True, torch.bfloat16).view(*lead, weight.shape[0])
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, xs, w, ws = ctx.saved_tensors
+        ext = _EXT or _load()
+        dyq = ext.quantize_block8(dy, 128, ctx.grad_dtype, False)
+        dx = dw = None
+        if w is not None:
+            dx = ext.block8_matmul(dyq, (w, ws, 128), False, False, torch.bfloat16).view(*dy.shape[:-1], w.shape[1])
+        if x is not None:
+            dw = ext.block8_matmul(dyq, (x, xs, 128), True, False, torch.bfloat16)
+        return dx, dw, None, None
+
+
+def block8_linear(x: torch.Tensor, weight: torch.Tensor, *, dtype: torch.dtype = torch.float8_e4m3fn,
+                  grad_dtype: torch.dtype = torch.float8_e5m2) -> torch.Tensor:
+    """``x @ weight.T`` with both operands in 8-bit blocks of 128 x 128: ``x``
+    (..., K) and ``weight`` (N, K) bfloat16, the result bfloat16.
+    Differentiable: the gradient that arrives is put in ``grad_dtype`` blocks of
+    128 x 128, and both gradients (bfloat16) are products of 8-bit blocks; the
+    graph keeps x and the weight in 8 bits only.  The gradients are those of
+    the product of the 8-bit values, passed on through the roundings.
+    K % 16 == 0 and N % 16 == 0."""
+    if x.dtype != torch.bfloat16 or weight.dtype != torch.bfloat16:
+        raise TypeError(f"x and weight must be bfloat16, got {x.dtype} and {weight.dtype}")
+    if x.dim() < 1 or weight.dim() != 2 or x.shape[-1] != weight.shape[1]:
+        raise ValueError(f"x must be (..., K) and weight (N, K), got {tuple(x.shape)} and {tuple(weight.shape)}")
+    if weight.shape[0] % 16 or weight.shape[1] % 16:
+        raise ValueError(f"N % 16 and K % 16 must be 0, got {tuple(weight.shape)}")
+    for d in (dtype, grad_dtype):
+        if d not in (torch.float8_e4m3fn, torch.float8_e5m2):
+            raise ValueError(f"dtype and grad_dtype must be float8 types, got {d}")
+    return _Block8Linear.apply(x, weight, dtype, grad_dtype)
+
+
+# ------------------------------------------------------------------ layer norm
+
+
+class LayerNormResult(NamedTuple):
+    """``y``: the normed rows, or their :class:`Block8Tensor` (rows of 1 x 128
+    blocks, leading dimensions flattened); ``residual``: the new residual stream
+    (``x`` itself without a residual); ``mean``, ``rstd``: the rows' means and
+    reciprocal deviations (with ``keep_stats``, else None); ``kept``: the
+    residual stream as a :class:`Block8Tensor` (with ``keep_dtype``, else
+    None)."""
+
+    y: torch.Tensor | Block8Tensor
+    residual: torch.Tensor
+    mean: torch.Tensor | None
+    rstd: torch.Tensor | None
+    kept: Block8Tensor | None
+
+
+class _LayerNorm(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, eps, keep_dtype):
+        y, _, h, mean, rstd, kept, scales = (_EXT or _load()).layer_norm(x, weight, bias, residual, eps, torch.bfloat16, True,
+                                                                         keep_dtype)
+        ctx.save_for_backward(h if kept is None else kept, scales, weight, mean, rstd)
+        ctx.x_dtype, ctx.r_dtype = x.dtype, None if residual is None else residual.dtype
+        ctx.bias_dtype = None if bias is None else bias.dtype
+        extra = (mean, rstd) + (() if kept is None else (kept, scales))
+        ctx.mark_non_differentiable(*extra)
+        ctx.set_materialize_grads(False)
+        return (y, *extra) if residual is None else (y, *extra, h)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, *rest):
+        h, scales, weight, mean, rstd = ctx.saved_tensors
+        dh = rest[-1] if ctx.r_dtype is not None else None
+        if dy is None:  # (only the sum was used)
+            return (None if dh is None else dh.to(ctx.x_dtype)), None, None, dh, None, None
+        if scales is not None:
+            h, dh = Block8Tensor(h, scales, 1), None if dh is None else dh.to(torch.bfloat16)
+        dx, dw, db = layer_norm_backward(dy, h, weight, mean, rstd, d_residual=dh, bias_dtype=ctx.bias_dtype)
+        return (dx.to(ctx.x_dtype), dw, db if ctx.bias_dtype is not None else None,
+                None if ctx.r_dtype is None else dx.to(ctx.r_dtype), None, None)
+
+
+def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.Tensor | None = None, *,
+               residual: torch.Tensor | None = None, eps: float = 1e-5, out_dtype: torch.dtype = torch.bfloat16,
+               keep_stats: bool = False, keep_dtype: torch.dtype | None = None) -> LayerNormResult:
+    """``h = x + residual`` (rounded to the residual's type; ``x`` without one) and
+    ``y = (h - mean) * rsqrt(variance + eps) * weight + bias`` over the last
+    dimension, the variance that of the whole row (divided by its length).
+
+    ``x`` (..., H), ``residual`` of x's shape, ``weight`` and ``bias`` (H,):
+    bfloat16 or float32 each.  ``out_dtype``: bfloat16, or a float8 type: then
+    ``y`` is a :class:`Block8Tensor` of 1 x 128 blocks, made from the unrounded
+    rows, as :func:`block8_matmul` takes it (H % 16 == 0).  ``keep_dtype``, a
+    float8 type: ``h`` is also given in 8-bit blocks with power-of-two scales
+    (``kept``), for :func:`layer_norm_backward` (H % 16 == 0).  Differentiable
+    with a bfloat16 output; with ``keep_dtype`` the graph then saves the 8-bit
+    rows in place of ``h``, and the gradients are those of the formula with the
+    values that they stand for (mean and deviation are the exact rows')."""
+    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias, residual)):
+        if out_dtype != torch.bfloat16:
+            raise ValueError("an 8-bit output has no gradient: call under torch.no_grad()")
+        out = _LayerNorm.apply(x, weight, bias, residual, eps, keep_dtype)
+        return LayerNormResult(out[0], x if residual is None else out[-1], out[1] if keep_stats else None,
+                               out[2] if keep_stats else None, None if keep_dtype is None else Block8Tensor(out[3], out[4], 1))
+    y, ys, h, mean, rstd, kept, scales = (_EXT or _load()).layer_norm(x, weight, bias, residual, eps, out_dtype, bool(keep_stats),
+                                                                      keep_dtype)
+    return LayerNormResult(y if ys is None else Block8Tensor(y, ys, 1), h, mean, rstd,
+                           None if kept is None else Block8Tensor(kept, scales, 1))
+
+
+def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor | Block8Tensor, weight: torch.Tensor | None, mean: torch.Tensor,
+                        rstd: torch.Tensor, *, d_residual: torch.Tensor | None = None, bias_dtype: torch.dtype | None = None):
+    """``(dx, dweight, dbias)`` of :func:`layer_norm` with a bfloat16 output: ``h``,
+    ``mean`` and ``rstd`` are the forward's ``residual`` (or ``kept``), ``mean`` and
+    ``rstd``; ``d_residual`` the gradient that reaches ``h`` on its other way, in
+    dx's type.  ``dx``, in h's type (bfloat16 for an 8-bit ``h``), is the gradient
+    of both ``x`` and ``residual``; ``dbias`` is in ``bias_dtype`` (default: the
+    weight's).  Without a weight dweight is None, and dbias too unless
+    ``bias_dtype`` is given."""
+    return (_EXT or _load()).layer_norm_backward(dy, h, weight, mean, rstd, d_residual, bias_dtype)

@@ -35,9 +35,10 @@ keep their rows of A and the B shards rotate instead).
 
 The operators around these products (:mod:`reduce_scatter_gb300.layer`) are
 exported here too: ``add_rms_norm`` and ``add_rms_norm_backward``,
+``layer_norm`` and ``layer_norm_backward``,
 ``grouped_matmul`` and ``grouped_matmul_backward``, ``quantize_mx4``,
 ``dequantize_mx4``, ``mx4_matmul``, ``quantize_block8``,
-``dequantize_block8``, ``block8_matmul``, ``check_products``.
+``dequantize_block8``, ``block8_matmul``, ``block8_linear``, ``check_products``.
 """
 
 from __future__ import annotations
@@ -47,8 +48,9 @@ import threading
 import torch
 
 from . import dg, layer
-from .layer import (Block8Tensor, MX4Tensor, NormResult, add_rms_norm, add_rms_norm_backward, block8_matmul,  # noqa: F401
-                    check_products, dequantize_block8, dequantize_mx4, grouped_matmul, grouped_matmul_backward,
+from .layer import (Block8Tensor, LayerNormResult, MX4Tensor, NormResult, add_rms_norm,  # noqa: F401
+                    add_rms_norm_backward, block8_linear, block8_matmul, check_products, dequantize_block8,
+                    dequantize_mx4, grouped_matmul, grouped_matmul_backward, layer_norm, layer_norm_backward,
                     mx4_matmul, quantize_block8, quantize_mx4)
 
 _lock = threading.Lock()

@@ -110,3 +110,97 @@ def test_derivatives_are_refused(L):
         s = torch.ones(4, 1)
         with pytest.raises(ValueError, match="forward-mode"):
             ops.block8_matmul(_q()._replace(scales=forward_ad.make_dual(s, s)), _q())
+
+
+# ---------------------------------------------------- layer norm, kept rows
+
+
+def _norm(L, x=16, ld=64, xt=dg.TYPE_BF16, r=None, rt=0, w=16, wt=0, b=16, bt=0, y=16, yt=dg.TYPE_BF16, ys=None, s=None, kept=None,
+          kt=dg.TYPE_E4M3, ks=None, rows=2, hidden=64, eps=1e-5):
+    return L.dg_layer_layer_norm(x, ld, xt, r, ld, rt, w, wt, b, bt, y, yt, ys, 1, 2, s, ld, kept, kt, ks, 1, 2, None, None, rows, hidden,
+                                 eps, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), dg.ERR_ARG), (dict(hidden=-1), dg.ERR_ARG), (dict(rows=2**31), dg.ERR_ARG), (dict(hidden=2**31 - 8), dg.ERR_ARG),
+    (dict(xt=dg.TYPE_E4M3), dg.ERR_ARG), (dict(r=16, s=16, rt=dg.TYPE_E4M3), dg.ERR_ARG), (dict(wt=dg.TYPE_E4M3), dg.ERR_ARG),
+    (dict(bt=dg.TYPE_E5M2), dg.ERR_ARG), (dict(yt=dg.TYPE_F32), dg.ERR_ARG), (dict(kept=16, kt=dg.TYPE_BF16, ks=16), dg.ERR_ARG),
+    (dict(eps=-1.0), dg.ERR_ARG), (dict(eps=float("nan")), dg.ERR_ARG), (dict(x=None), dg.ERR_ARG), (dict(y=None), dg.ERR_ARG),
+    (dict(r=16), dg.ERR_ARG), (dict(s=16), dg.ERR_ARG), (dict(yt=dg.TYPE_E4M3), dg.ERR_ARG), (dict(kept=16), dg.ERR_ARG),
+    (dict(yt=dg.TYPE_E4M3, ys=16, hidden=72), dg.ERR_SHAPE), (dict(kept=16, ks=16, hidden=40), dg.ERR_SHAPE),
+])
+def test_layer_norm_refuses(L, kw, code):
+    assert _norm(L, **kw) == code and L.dg_layer_last_error()
+
+
+def _norm_grad(L, dy=16, h=16, ht=dg.TYPE_BF16, hs=None, w=16, wt=0, mean=16, rstd=16, dh=None, dx=16, dw=16, db=16, bt=0, ws=256, rows=2,
+               hidden=64):
+    return L.dg_layer_layer_norm_backward(dy, 64, h, 64, ht, hs, 1, 2, w, wt, mean, rstd, dh, 64, dx, dw, db, bt, ws, rows, hidden, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(rows=-1), dg.ERR_ARG), (dict(hidden=2**31), dg.ERR_ARG), (dict(ht=99), dg.ERR_ARG), (dict(wt=dg.TYPE_E4M3), dg.ERR_ARG),
+    (dict(bt=dg.TYPE_E4M3), dg.ERR_ARG), (dict(ht=dg.TYPE_E4M3, hs=16, hidden=72), dg.ERR_SHAPE), (dict(ht=dg.TYPE_E4M3), dg.ERR_ARG),
+    (dict(dy=None), dg.ERR_ARG), (dict(mean=None), dg.ERR_ARG), (dict(dx=None), dg.ERR_ARG), (dict(ws=None), dg.ERR_ARG),
+    (dict(ws=8), dg.ERR_ARG), (dict(w=None, wt=dg.TYPE_E4M3), dg.ERR_ARG),
+])
+def test_layer_norm_gradient_refuses(L, kw, code):
+    assert _norm_grad(L, **kw) == code and L.dg_layer_last_error()
+
+
+def test_layer_norm_of_nothing(L):
+    assert _norm(L, rows=0, x=None, y=None) == dg.OK and _norm(L, hidden=0, x=None, y=None) == dg.OK
+    assert _norm_grad(L, hidden=0, dy=None) == dg.OK
+    assert L.dg_layer_layer_norm_backward_workspace(0, 8) == 0
+    assert L.dg_layer_layer_norm_backward_workspace(3, 8) == 2 * 3 * 8 * 4
+
+
+def test_layer_norm_front_end_refuses(L):
+    x, w = torch.ones(4, 64, dtype=BF16), torch.ones(64, dtype=BF16)
+    rows = torch.ones(4)
+    for call, error in [
+            (lambda: ops.layer_norm(x.half()), TypeError), (lambda: ops.layer_norm(torch.tensor(1.0)), TypeError),
+            (lambda: ops.layer_norm(x, w[:32]), ValueError), (lambda: ops.layer_norm(x, w.half()), TypeError),
+            (lambda: ops.layer_norm(x, w, w.view(1, 64)), ValueError), (lambda: ops.layer_norm(x, residual=x[:2]), ValueError),
+            (lambda: ops.layer_norm(x, residual=x.half()), TypeError), (lambda: ops.layer_norm(x, out_dtype=torch.float32), ValueError),
+            (lambda: ops.layer_norm(x, keep_dtype=BF16), ValueError), (lambda: ops.layer_norm(x[:, :40], out_dtype=E4M3), ValueError),
+            (lambda: ops.layer_norm(x, w, w), ValueError),  # not CUDA
+            (lambda: ops.layer_norm(x.clone().requires_grad_(), out_dtype=E4M3), ValueError),
+            (lambda: ops.layer_norm_backward(x.float(), x, w, rows, rows), TypeError),
+            (lambda: ops.layer_norm_backward(x, x[:2], w, rows, rows), ValueError),
+            (lambda: ops.layer_norm_backward(x, x, w, rows[:2], rows), ValueError),
+            (lambda: ops.layer_norm_backward(x, x, w, rows, rows.half()), TypeError),
+            (lambda: ops.layer_norm_backward(x, x, w, rows, rows, d_residual=x.float()), ValueError),
+            (lambda: ops.layer_norm_backward(x, _q(br=128), w, rows, rows), ValueError),
+            (lambda: ops.layer_norm_backward(x, _q(rows=3), w, rows, rows), ValueError),
+            (lambda: ops.layer_norm_backward(x, x, w, rows, rows, bias_dtype=E4M3), ValueError),
+            (lambda: ops.layer_norm_backward(x, x, w, rows, rows), ValueError)]:
+        with pytest.raises(error):
+            call()
+
+
+def _kept_grad(L, d=16, ld=64, v=16, vt=dg.TYPE_E4M3, s=16, ends=16, e=2, out=16, dt=dg.TYPE_BF16, t=4, n=64, k=64, ws=256, pws=256,
+               st=16):
+    return L.dg_layer_grouped_weight_grad8(d, ld, v, vt, s, 1, 4, ends, e, out, 0, dt, t, n, k, ws, pws, st, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(t=-1), dg.ERR_ARG), (dict(e=0), dg.ERR_ARG), (dict(e=1025), dg.ERR_ARG), (dict(vt=dg.TYPE_BF16), dg.ERR_ARG),
+    (dict(k=72), dg.ERR_SHAPE), (dict(n=60), dg.ERR_SHAPE), (dict(dt=dg.TYPE_E4M3), dg.ERR_ARG), (dict(v=None), dg.ERR_ARG),
+    (dict(s=None), dg.ERR_ARG), (dict(v=8), dg.ERR_ARG), (dict(ws=8), dg.ERR_ARG), (dict(ws=None), dg.ERR_ARG),
+    (dict(d=None), dg.ERR_ARG), (dict(ends=None), dg.ERR_ARG), (dict(out=None), dg.ERR_ARG), (dict(st=None), dg.ERR_ARG),
+    (dict(pws=None), dg.ERR_ARG), (dict(ld=60), dg.ERR_ARG),
+])
+def test_kept_gradient_refuses(L, kw, code):
+    assert _kept_grad(L, **kw) == code and L.dg_layer_last_error()
+
+
+def test_linear_refuses(L):
+    x, w = torch.ones(4, 64, dtype=BF16), torch.ones(32, 64, dtype=BF16)
+    for call, error in [(lambda: ops.block8_linear(x.float(), w), TypeError), (lambda: ops.block8_linear(x, w.float()), TypeError),
+                        (lambda: ops.block8_linear(x, w[:, :32]), ValueError), (lambda: ops.block8_linear(x, w[:24]), ValueError),
+                        (lambda: ops.block8_linear(x[:, :24], w[:, :24]), ValueError), (lambda: ops.block8_linear(x, w, dtype=BF16), ValueError),
+                        (lambda: ops.block8_linear(x, w, grad_dtype=BF16), ValueError), (lambda: ops.block8_linear(x, w), ValueError),
+                        (lambda: ops.grouped_matmul(x, w.view(2, 64, 16), torch.zeros(2, dtype=torch.int32), keep_dtype=BF16), ValueError)]:
+        with pytest.raises(error):
+            call()

@@ -21,6 +21,7 @@
 #include <cuda_bf16.h>
 
 #include "launch.cuh"
+#include "pairs.cuh"
 #include "ptx.cuh"
 
 namespace {
@@ -69,24 +70,6 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
                  "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15])
                :
                : "memory");
-}
-
-// Two fp32 values in one register pair: half the instructions.
-__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpair(uint64_t p, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(p));
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-__device__ __forceinline__ void fma2(uint64_t& d, uint64_t a, uint64_t b) {
-  asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(d) : "l"(a), "l"(b));
 }
 
 __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, int32_t x, int32_t y) {
@@ -261,7 +244,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
                 asm volatile("ld.shared.b64 %0, [%1];" : "=l"(cs) : "r"(table + (j * 8 + i) * 8));
                 f = mul2(f, cs);
               }
-              fma2(acc[j * 8 + i], f, s2);
+              acc[j * 8 + i] = fma2(f, s2, acc[j * 8 + i]);
             }
           }
         }
@@ -312,10 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
         float* to = slot(unit);
 #pragma unroll
         for (int i = 0; i < 64; ++i) {
-          float lo, hi;
-          unpair(acc[i], lo, hi);
-          __stcg(to + (int64_t)(side * 128 + 2 * i) * kLanes + q * 32 + lane, lo);
-          __stcg(to + (int64_t)(side * 128 + 2 * i + 1) * kLanes + q * 32 + lane, hi);
+          const float2 f = unpair(acc[i]);
+          __stcg(to + (int64_t)(side * 128 + 2 * i) * kLanes + q * 32 + lane, f.x);
+          __stcg(to + (int64_t)(side * 128 + 2 * i + 1) * kLanes + q * 32 + lane, f.y);
         }
         if (!warp_last(p.counters + 4 * w.tile + 2 * half + side, q, ways, lane)) continue;
 #pragma unroll 1
@@ -329,7 +311,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
         for (int c32 = 0; c32 < 4; ++c32) {
           float v[32];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) unpair(acc[c32 * 16 + i], v[2 * i], v[2 * i + 1]);
+          for (int i = 0; i < 16; ++i) {
+            const float2 f = unpair(acc[c32 * 16 + i]);
+            v[2 * i] = f.x, v[2 * i + 1] = f.y;
+          }
           emit(c32, v);
         }
       }

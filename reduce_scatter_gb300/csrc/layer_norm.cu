@@ -26,14 +26,6 @@ struct Affine {
   int w_f32, b_f32;
 };
 
-// A matrix in 8-bit blocks of 1 x 128 as it is written.
-struct Blocks {
-  uint8_t* values;
-  float* scales;
-  int64_t s_row, s_block;
-  int e5m2;
-};
-
 struct Args {
   const void *x, *residual;
   void *sum, *y;
@@ -45,41 +37,53 @@ struct Args {
   float eps;
 };
 
-// Eight values of w (or 1) and b (or 0).
-__device__ __forceinline__ void affine8(const Affine& a, int i, float (&w)[8], float (&b)[8]) {
+// Vector i of w (or 1) and b (or 0).
+__device__ __forceinline__ void affine8(const Affine& a, int i, Eight& w, Eight& b) {
 #pragma unroll
-  for (int j = 0; j < 8; ++j) w[j] = 1.f, b[j] = 0.f;
-  if (a.w) load_any<8>(a.w_f32 != 0, a.w, i, w);
-  if (a.b) load_any<8>(a.b_f32 != 0, a.b, i, b);
+  for (int j = 0; j < 4; ++j) w.p[j] = pair_of(1.f, 1.f), b.p[j] = 0;
+  if (a.w) load8(a.w_f32 != 0, a.w, i, w);
+  if (a.b) load8(a.b_f32 != 0, a.b, i, b);
 }
 
-// Eight values of each thread (`in`: they are in the row) as 8-bit blocks.
-__device__ __forceinline__ void store_blocks(const Blocks& o, bool pow2, int64_t row, int hidden, int i, bool in, float (&v)[8]) {
-  float m = 0.f;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    v[j] = block_value(v[j]);
-    m = fmaxf(m, in ? fabsf(v[j]) : 0.f);
-  }
-  const Quantizer q(block_max16(m), o.e5m2 != 0, pow2);
-  if (!in) return;
-#pragma unroll
-  for (int j = 0; j < 8; ++j) v[j] = q(v[j]);
-  *reinterpret_cast<uint2*>(o.values + row * hidden + i) = pack_fp8(v, o.e5m2 ? __NV_E5M2 : __NV_E4M3);
-  if ((threadIdx.x & 15) == 0) o.scales[row * o.s_row + (int64_t)(i >> 7) * o.s_block] = q.c;
-}
+// ------------------------------------------------------------- the moments
+//
+// Each warp finds the mean of its own values and the sum of the squared
+// differences from it; the warps' are then put together around the first one's
+// mean (a sum of squares grows by n (its mean - the row's)^2).  One barrier, and
+// no difference of large numbers.
 
-// The mean and the reciprocal deviation from the sum, and the sums of the
-// differences from its mean and of their squares.
 struct Moments {
   float mean, rstd;
 };
-__device__ __forceinline__ Moments moments(float mean, float2 d, int hidden, float eps) {
-  const float n = (float)hidden, off = d.x / n, v = d.y / n;
-  // (below 2^-21 of the deviation the differences' own rounding is what their sum shows)
-  const bool far = off * off > 0x1p-42f * v;
-  const float var = v - off * off;
-  return Moments{far ? mean + off : mean, rsqrtf((var < 0.f ? 0.f : var) + eps)};  // (a NaN stays)
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+// How many values each warp holds, and their reciprocals.  (Products with these in
+// place of divisions: what they leave in a mean the differences show.)
+struct Share {
+  float n, inv;
+  __device__ __forceinline__ Share(int count) : n((float)count), inv(count > 0 ? 1.f / (float)count : 0.f) {}
+};
+// The second step of a warp's: from its mean as rounded, the sums of the
+// differences from it and of their squares.  The first corrects the mean (below 2^-21 of
+// the deviation the differences' own rounding is what their sum shows).
+__device__ __forceinline__ float2 warp_moments(float mean, float d1, float d2, const Share& own) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) d1 += __shfl_xor_sync(0xffffffffu, d1, o), d2 += __shfl_xor_sync(0xffffffffu, d2, o);
+  const float off = d1 * own.inv, gone = off * d1;
+  const bool far = gone > 0x1p-42f * d2;
+  const float s = d2 - gone;
+  return make_float2(far ? mean + off : mean, !far ? d2 : s < 0.f ? 0.f : s);
+}
+// The row's from lane l's warp l (none: a share of 0) of `hidden` values.
+__device__ __forceinline__ Moments join_moments(float2 m, const Share& of, float inv_hidden, float eps) {
+  const float first = __shfl_sync(0xffffffffu, m.x, 0);
+  const float d = of.n == 0.f ? 0.f : m.x - first;
+  const float off = warp_sum(of.n * d) * inv_hidden;
+  const float s = warp_sum(of.n == 0.f ? 0.f : fmaf(of.n * (d - off), d - off, m.y));
+  return Moments{first + off, rsqrtf(fmaf(s, inv_hidden, eps))};
 }
 __device__ __forceinline__ void keep_moments(const Args& p, int64_t row, const Moments& m) {
   if (threadIdx.x == 0) {
@@ -87,37 +91,49 @@ __device__ __forceinline__ void keep_moments(const Args& p, int64_t row, const M
     if (p.rstd) p.rstd[row] = m.rstd;
   }
 }
-
-// x + r, in the type that it is stored in.
-__device__ __forceinline__ void round_sum(bool r_f32, float (&h)[8]) {
-  if (!r_f32)
+// Values of warp w whose threads hold NV vectors of 8, blockDim.x threads apart.
+template <int NV>
+__device__ __forceinline__ int warp_count(int w, int hidden) {
+  int n = 0;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) h[j] = __bfloat162float(__float2bfloat16_rn(h[j]));
+  for (int k = 0; k < NV; ++k) n += min(max(hidden - (w * 256 + k * (int)blockDim.x * 8), 0), 256);
+  return n;
 }
-__device__ __forceinline__ void store_any(bool f32, void* base, int64_t i, const float (&v)[8]) {
-  if (f32)
-    store_f32<8>(base, i, v);
-  else
-    store_bf16<8>(base, i, v);
+// A warp's moments from its vectors (those past the row: zeros, unless all are FULL).
+template <int NV, bool FULL = false>
+__device__ __forceinline__ float2 moments_of(const Eight (&h)[NV], int hidden, int i0, int step, const Share& own) {
+  uint64_t sum = add2(h[0].p[0], h[0].p[1]);
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int j = k == 0 ? 2 : 0; j < 4; ++j) sum = add2(sum, h[k].p[j]);
+  const float mean = warp_sum(sum_of(sum)) * own.inv;
+  const uint64_t minus = pair_of(-mean, -mean);
+  uint64_t d1 = 0, d2 = 0;
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+    if (FULL || i0 + k * step < hidden)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint64_t d = add2(h[k].p[j], minus);
+        d1 = add2(d1, d), d2 = fma2(d, d, d2);
+      }
+  return warp_moments(mean, sum_of(d1), sum_of(d2), own);
 }
 
 // Vector i of a row's output, from h.
 template <bool OUT8>
-__device__ __forceinline__ void finish(const Args& p, int64_t row, int i, bool in, const Moments& m, const float (&h)[8],
-                                       const float (&w)[8], const float (&b)[8]) {
-  if (p.kept.values) {
-    float v[8];
+__device__ __forceinline__ void finish(const Args& p, int64_t row, int i, bool in, const Moments& m, const Eight& h, const Eight& w,
+                                       const Eight& b) {
+  if (p.kept.values) store_blocks(p.kept, true, row, p.hidden, i, in, h);
+  const uint64_t minus = pair_of(-m.mean, -m.mean), rstd = pair_of(m.rstd, m.rstd);
+  Eight y;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = h[j];
-    store_blocks(p.kept, true, row, p.hidden, i, in, v);
-  }
-  float y[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = fmaf((h[j] - m.mean) * m.rstd, w[j], b[j]);
+  for (int j = 0; j < 4; ++j) y.p[j] = fma2(mul2(add2(h.p[j], minus), rstd), w.p[j], b.p[j]);
   if constexpr (OUT8)
     store_blocks(p.y8, false, row, p.hidden, i, in, y);
   else if (in)
-    store_bf16<8>(p.y, row * p.hidden + i, y);
+    store8(false, p.y, row * p.hidden + i, y);
 }
 
 // ------------------------------------------------------ a row in registers
@@ -125,49 +141,42 @@ __device__ __forceinline__ void finish(const Args& p, int64_t row, int i, bool i
 // NV vectors of 8 values per thread.
 template <int NV, bool OUT8>
 __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) layer_norm_kernel(const __grid_constant__ Args p) {
-  __shared__ float part[100];
+  __shared__ float2 part[32];
   begin_kernel();
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= p.rows) return;  // several rows per block only with one warp each: no barrier below
-  const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
-  float h[NV][8], sum = 0.f;
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8, warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  Eight h[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = i0 + k * step;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
+    h[k].zero();
     if (i < p.hidden) {
-      load_any<8>(p.x_f32 != 0, p.x, row * p.ld_x + i, h[k]);
+      load8(p.x_f32 != 0, p.x, row * p.ld_x + i, h[k]);
       if (p.residual) {
-        float r[8];
-        load_any<8>(p.r_f32 != 0, p.residual, row * p.ld_residual + i, r);
+        Eight r;
+        load8(p.r_f32 != 0, p.residual, row * p.ld_residual + i, r);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) h[k][j] += r[j];
+        for (int j = 0; j < 4; ++j) h[k].p[j] = add2(h[k].p[j], r.p[j]);
+        store8(p.r_f32 != 0, p.sum, row * p.ld_sum + i, h[k]);
         // the norm is of the sum as it is stored, so that the gradient sees the same values
-        round_sum(p.r_f32 != 0, h[k]);
-        store_any(p.r_f32 != 0, p.sum, row * p.ld_sum + i, h[k]);
+        if (!p.r_f32) h[k].from_bf16(h[k].to_bf16());
       }
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) sum += h[k][j];
   }
-  const float mean = row_reduce<Add>(sum, part) / (float)p.hidden;
-  float d1 = 0.f, d2 = 0.f;
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-    if (i0 + k * step < p.hidden)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float d = h[k][j] - mean;
-        d1 += d, d2 = fmaf(d, d, d2);
-      }
-  const Moments m = moments(mean, row_sum2(d1, d2, part + 34), p.hidden, p.eps);
+  float2 mine = moments_of(h, p.hidden, i0, step, Share(warp_count<NV>(threadIdx.x >> 5, p.hidden)));
+  if (warps > 1) {
+    if (lane == 0) part[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    mine = part[lane < warps ? lane : 0];
+  }
+  const Moments m = join_moments(mine, Share(lane < warps ? warp_count<NV>(lane, p.hidden) : 0), 1.f / (float)p.hidden, p.eps);
   keep_moments(p, row, m);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = i0 + k * step;
     const bool in = i < p.hidden;
-    float w[8], b[8];
+    Eight w, b;
     affine8(p.affine, in ? i : 0, w, b);
     finish<OUT8>(p, row, i, in, m, h[k], w, b);
   }
@@ -180,33 +189,51 @@ constexpr int kStreamThreads = 1024;  // per SM (64 registers each)
 constexpr int kStreamBytes = 220000;  // dynamic shared memory that the streamed kernels may take, whatever the call needs
 
 // XP, RP: 16-byte slots of eight values of x (1 bf16, 2 fp32) and of the
-// residual (0 none).
-template <int XP, int RP, bool OUT8, int STAGES>
+// residual (0 none).  A row goes through two steps, with a barrier in between: its
+// warps' moments, and the output, for which h is read from the slots again
+// (nothing is held in registers over the barrier).  With three stages the second
+// step of a row comes after the first one of the next, so that no warp waits
+// at the barrier for the slowest one's sums.
+// FULL: every thread has its NV vectors.
+template <int XP, int RP, bool OUT8, bool FULL, int STAGES>
 __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const __grid_constant__ Args p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float part[2][100];
+  __shared__ float2 part[2][32];
   constexpr int NV = kStreamVecs, PER = XP + RP;
+  constexpr bool PIPE = STAGES > 2, H32 = RP == 2 || (RP == 0 && XP == 2);
+  constexpr int HS = RP == 2 ? XP : 0;  // h's slot of a vector's
   const Slots<NV * PER> slots{smem};
   begin_kernel();
-  const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
-  auto fetch = [&](int64_t row, int stage) {
-    if (row < p.rows) {
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8, warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto in = [&](int k) { return FULL || i0 + k * step < p.hidden; };
+  // this thread's place in the next row to fetch
+  int64_t next = blockIdx.x;
+  const uint8_t* x_next = static_cast<const uint8_t*>(p.x) + (next * p.ld_x + i0) * (2 * XP);
+  const uint8_t* r_next = RP ? static_cast<const uint8_t*>(p.residual) + (next * p.ld_residual + i0) * (2 * RP) : nullptr;
+  const int64_t x_rows = gridDim.x * p.ld_x * (2 * XP), r_rows = gridDim.x * p.ld_residual * (2 * RP);
+  auto fetch = [&](int stage) {
+    if (next < p.rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int i = i0 + k * step;
-        if (i < p.hidden) {
-          const uint8_t* x = static_cast<const uint8_t*>(p.x) + (row * p.ld_x + i) * (2 * XP);
+        if (in(k)) {
 #pragma unroll
-          for (int q = 0; q < XP; ++q) slots.fetch(stage, k * PER + q, x + 16 * q);
-          if constexpr (RP != 0) {
-            const uint8_t* r = static_cast<const uint8_t*>(p.residual) + (row * p.ld_residual + i) * (2 * RP);
+          for (int q = 0; q < XP; ++q) slots.fetch(stage, k * PER + q, x_next + k * step * (2 * XP) + 16 * q);
+          if constexpr (RP != 0)
 #pragma unroll
-            for (int q = 0; q < RP; ++q) slots.fetch(stage, k * PER + XP + q, r + 16 * q);
-          }
+            for (int q = 0; q < RP; ++q) slots.fetch(stage, k * PER + XP + q, r_next + k * step * (2 * RP) + 16 * q);
         }
       }
     }
+    next += gridDim.x;
+    x_next += x_rows;
+    if (RP) r_next += r_rows;
     copies_commit();
+  };
+  auto read = [&](bool f32, int stage, int slot, Eight& v) {
+    if (f32)
+      v.from_f32(*slots.at(stage, slot), *slots.at(stage, slot + 1));
+    else
+      v.from_bf16(*slots.at(stage, slot));
   };
   // w and b in 16 bits stay in registers
   uint4 w16[NV], b16[NV];
@@ -215,69 +242,85 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
     const int i = i0 + k * step;
     w16[k] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     b16[k] = make_uint4(0, 0, 0, 0);
-    if (i < p.hidden) {
+    if (in(k)) {
       if (p.affine.w && !p.affine.w_f32) w16[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.affine.w) + i));
       if (p.affine.b && !p.affine.b_f32) b16[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.affine.b) + i));
     }
   }
-#pragma unroll
-  for (int s = 0; s < STAGES; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-  int stage = 0, flip = 0;
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
-    copies_wait<STAGES - 1>();
-    float h[NV][8], sum = 0.f;
+  const Share own(FULL ? NV * 256 : warp_count<NV>(warp, p.hidden));
+  const Share of(lane >= warps ? 0 : FULL ? NV * 256 : warp_count<NV>(lane, p.hidden));
+  const float inv_hidden = 1.f / (float)p.hidden;
+  auto sums = [&](int64_t row, int stage, int flip) {
+    Eight h[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = i0 + k * step;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[k][j] = 0.f;
-      if (i < p.hidden) {
-        slots.template read<XP == 2>(stage, k * PER, h[k]);
+      if (!FULL) h[k].zero();
+      if (in(k)) {
+        read(XP == 2, stage, k * PER, h[k]);
         if constexpr (RP != 0) {
-          float r[8];
-          slots.template read<RP == 2>(stage, k * PER + XP, r);
+          Eight r;
+          read(RP == 2, stage, k * PER + XP, r);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) h[k][j] += r[j];
+          for (int j = 0; j < 4; ++j) h[k].p[j] = add2(h[k].p[j], r.p[j]);
           if constexpr (RP == 2) {
-            store_f32<8>(p.sum, row * p.ld_sum + i, h[k]);
+            const uint4 a = h[k].to_f32(0), b = h[k].to_f32(1);
+            uint4* to = reinterpret_cast<uint4*>(static_cast<float*>(p.sum) + row * p.ld_sum + i);
+            to[0] = *slots.at(stage, k * PER + HS) = a;
+            to[1] = *slots.at(stage, k * PER + HS + 1) = b;
           } else {
             // the norm is of the sum as it is stored, so that the gradient sees the same values
-            const uint4 u = make_uint4(pack2(h[k][0], h[k][1]), pack2(h[k][2], h[k][3]), pack2(h[k][4], h[k][5]),
-                                       pack2(h[k][6], h[k][7]));
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + row * p.ld_sum + i) = u;
-            unpack8(u, h[k]);
+            const uint4 u = h[k].to_bf16();
+            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + row * p.ld_sum + i) = *slots.at(stage, k * PER) = u;
+            h[k].from_bf16(u);
           }
         }
       }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) sum += h[k][j];
     }
-    // this stage's values are in registers
-    fetch(row + (int64_t)STAGES * gridDim.x, stage);
-    stage = stage + 1 == STAGES ? 0 : stage + 1;
-    const float mean = row_reduce<Add>(sum, part[flip]) / (float)p.hidden;
-    float d1 = 0.f, d2 = 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (i0 + k * step < p.hidden)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float d = h[k][j] - mean;
-          d1 += d, d2 = fmaf(d, d, d2);
-        }
-    const Moments m = moments(mean, row_sum2(d1, d2, part[flip] + 34), p.hidden, p.eps);
+    const float2 m = moments_of<NV, FULL>(h, p.hidden, i0, step, own);
+    if (lane == 0) part[flip][warp] = m;
+  };
+  auto output = [&](int64_t row, int stage, int flip) {
+    const Moments m = join_moments(part[flip][lane < warps ? lane : 0], of, inv_hidden, p.eps);
     keep_moments(p, row, m);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = i0 + k * step;
-      const bool in = i < p.hidden;
-      float w[8], b[8];
-      unpack8(w16[k], w);
-      unpack8(b16[k], b);
-      if (in && p.affine.w_f32) load_f32<8>(p.affine.w, i, w);
-      if (in && p.affine.b_f32) load_f32<8>(p.affine.b, i, b);
-      finish<OUT8>(p, row, i, in, m, h[k], w, b);
+      Eight h, w, b;
+      w.from_bf16(w16[k]), b.from_bf16(b16[k]);
+      if (!FULL) h.zero();
+      if (in(k)) {
+        read(H32, stage, k * PER + HS, h);
+        if (p.affine.w_f32) load8(true, p.affine.w, i, w);
+        if (p.affine.b_f32) load8(true, p.affine.b, i, b);
+      }
+      finish<OUT8>(p, row, i, in(k), m, h, w, b);
     }
+  };
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) fetch(s);
+  int stage = 0, flip = 0;
+  auto after = [](int s) { return s + 1 == STAGES ? 0 : s + 1; };
+  if (PIPE) {
+    copies_wait<STAGES - 1>();
+    if (blockIdx.x < p.rows) sums(blockIdx.x, 0, 0);
+    __syncthreads();
+  }
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    if constexpr (PIPE) {
+      copies_wait<STAGES - 2>();
+      if (row + gridDim.x < p.rows) sums(row + gridDim.x, after(stage), flip ^ 1);
+      output(row, stage, flip);
+      fetch(stage);
+      __syncthreads();
+    } else {
+      copies_wait<STAGES - 1>();
+      sums(row, stage, flip);
+      __syncthreads();
+      output(row, stage, flip);
+      fetch(stage);
+    }
+    stage = after(stage);
   }
   copies_wait<0>();
 }
@@ -287,10 +330,16 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
 // (16-bit output: rows of 8-bit blocks are multiples of 16 values, and come aligned)
 template <bool X32, int RT, int N>
 __global__ void __launch_bounds__(1024) layer_norm_spread_kernel(const __grid_constant__ Args p) {
-  __shared__ float part[100];
+  __shared__ float2 part[32];
   begin_kernel();
   const int64_t row = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
   if (row >= p.rows) return;
+  const int warps = blockDim.x >> 5, lane = threadIdx.x & 31;
+  auto count = [&](int w) {
+    int n = 0;
+    for (int k = 0; k < N; ++k) n += min(max(p.hidden - (w * 32 + k * (int)blockDim.x), 0), 32);
+    return n;
+  };
   Spread<X32, N> x;
   Spread<RT == 2, N> r;
   x.load(p.x, row * p.ld_x, p.hidden);
@@ -311,7 +360,8 @@ __global__ void __launch_bounds__(1024) layer_norm_spread_kernel(const __grid_co
     }
     sum += h[k];
   }
-  const float mean = row_reduce<Add>(sum, part) / (float)p.hidden;
+  const Share own(count(threadIdx.x >> 5));
+  const float mean = warp_sum(sum) * own.inv;
   float d1 = 0.f, d2 = 0.f;
 #pragma unroll
   for (int k = 0; k < N; ++k)
@@ -319,7 +369,13 @@ __global__ void __launch_bounds__(1024) layer_norm_spread_kernel(const __grid_co
       const float d = h[k] - mean;
       d1 += d, d2 = fmaf(d, d, d2);
     }
-  const Moments m = moments(mean, row_sum2(d1, d2, part + 34), p.hidden, p.eps);
+  float2 mine = warp_moments(mean, d1, d2, own);
+  if (warps > 1) {
+    if (lane == 0) part[threadIdx.x >> 5] = mine;
+    __syncthreads();
+    mine = part[lane < warps ? lane : 0];
+  }
+  const Moments m = join_moments(mine, Share(lane < warps ? count(lane) : 0), 1.f / (float)p.hidden, p.eps);
   keep_moments(p, row, m);
 #pragma unroll
   for (int k = 0; k < N; ++k) {
@@ -369,7 +425,9 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(const __grid_cons
       load(p.r_f32 != 0, p.residual, row * p.ld_residual, from, r);
 #pragma unroll
       for (int j = 0; j < 8; ++j) h[j] += r[j];
-      round_sum(p.r_f32 != 0, h);
+      if (!p.r_f32)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[j] = __bfloat162float(__float2bfloat16_rn(h[j]));
       if (!VEC || in_row(from, 0)) {
         if (p.r_f32)
           store_chunk<VEC>(from, hidden, h, [&](int64_t i, const float(&v)[1]) { store_f32<1>(p.sum, h0 + i, v); },
@@ -393,7 +451,10 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(const __grid_cons
       d1 += d, d2 = fmaf(d, d, d2);
     }
   }
-  const Moments m = moments(mean, row_sum2(d1, d2, part + 34), p.hidden, p.eps);
+  // (the whole row as one warp's: lane 0 holds it)
+  const float2 all = row_sum2(d1, d2, part + 34);
+  const float2 one = warp_moments(mean, (threadIdx.x & 31) == 0 ? all.x : 0.f, (threadIdx.x & 31) == 0 ? all.y : 0.f, Share((int)hidden));
+  const Moments m{one.x, rsqrtf(one.y / (float)hidden + p.eps)};
   keep_moments(p, row, m);
   for (int64_t from = 0; from < hidden; from += step) {
     float h[8], w[8], b[8];
@@ -401,8 +462,10 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(const __grid_cons
     if constexpr (VEC) {
       const int i = (int)from + threadIdx.x * 8;  // (beyond the row by less than a step)
       const bool in = in_row(from, 0);
-      affine8(p.affine, in ? i : 0, w, b);
-      finish<OUT8>(p, row, i, in, m, h, w, b);
+      Eight h8, w8, b8;
+      h8.from_floats(h);
+      affine8(p.affine, in ? i : 0, w8, b8);
+      finish<OUT8>(p, row, i, in, m, h8, w8, b8);
     } else {
 #pragma unroll
       for (int j = 0; j < 8; ++j) w[j] = 1.f, b[j] = 0.f;
@@ -432,7 +495,9 @@ template <int XP, int RP, bool OUT8>
 int stream_norm(const Args& p, int sms, cudaStream_t s) {
   constexpr int stages = XP + RP > 2 ? 2 : 3;  // (192 KB for 16384 values; two fp32 operands only fit to 13744)
   int threads, blocks, bytes;
-  auto* kernel = layer_norm_stream_kernel<XP, RP, OUT8, stages>;
+  auto* kernel = layer_norm_stream_kernel<XP, RP, OUT8, false, stages>;
+  if constexpr (XP == 1 && RP < 2)
+    if (p.hidden % (32 * 8 * kStreamVecs) == 0) kernel = layer_norm_stream_kernel<XP, RP, OUT8, true, stages>;
   if (int rc = stream_shape(kernel, p.hidden, kStreamVecs * (XP + RP), stages, sms, p.rows, &threads, &blocks, &bytes)) return rc;
   return dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);
 }
@@ -490,149 +555,197 @@ struct GradArgs {
 // The type of h: bf16, fp32, or 8-bit blocks of 1 x 128.
 enum { kH16 = 0, kH32 = 1, kH8 = 2 };
 
-constexpr int kGradStages = 2;
+// 16-byte slots of a vector: dy, h, and the gradient that reaches h on its other way.
 template <int HT, bool HAS_DH>
 __host__ __device__ constexpr int grad_parts() {
   return kStreamVecs * (1 + (HT == kH32 ? 2 : 1) * (HAS_DH ? 2 : 1));
+}
+template <int HT, bool HAS_DH>
+__host__ __device__ constexpr int grad_stages() {
+  return grad_parts<HT, HAS_DH>() > 2 * kStreamVecs ? 2 : 3;
 }
 
 __device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
 }
 
-// Rows streamed like the forward's: dy, h and dh of the next row are in flight
-// while this one is reduced and written.  A row is read from its slots twice (for
-// the sums, and again for dx), which leaves registers to the weight and the two
-// gradients that are summed over the block's rows.
-template <int HT, bool HAS_DH>
-__global__ void __launch_bounds__(kStreamThreads) layer_norm_grad_stream_kernel(const __grid_constant__ GradArgs p) {
+// Rows streamed like the forward's, in the same two steps: the sums, and dx, for
+// which the row is read from its slots again, which leaves registers to the weight
+// and the two gradients that are summed over the block's rows.  With
+// e = h - mean: mean(g xh) = rstd mean(g e), dx = rstd (dy w - mean(g) - e (rstd mean(g xh))).
+template <int HT, bool HAS_DH, bool FULL>
+__global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kernel(const __grid_constant__ GradArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float part[2][66];
+  __shared__ float2 part[2][32];
   constexpr int NV = kStreamVecs, HP = HT == kH32 ? 2 : 1, PER = 1 + HP * (HAS_DH ? 2 : 1), hsz = HT == kH32 ? 4 : 2;
+  constexpr int STAGES = grad_stages<HT, HAS_DH>();
+  constexpr bool PIPE = STAGES > 2;
   const Slots<grad_parts<HT, HAS_DH>()> slots{smem};
   begin_kernel();
-  const int step = blockDim.x * 8, i0 = threadIdx.x * 8;
-  auto fetch = [&](int64_t row, int stage) {
-    if (row < p.rows) {
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8, warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto in = [&](int k) { return FULL || i0 + k * step < p.hidden; };
+  // this thread's place in the next row to fetch
+  constexpr int HB = HT == kH8 ? 1 : hsz;  // bytes of a value of h
+  int64_t next = blockIdx.x;
+  const uint8_t* dy_next = static_cast<const uint8_t*>(p.dy) + (next * p.ld_dy + i0) * 2;
+  const uint8_t* h_next = static_cast<const uint8_t*>(p.h) + (next * p.ld_h + i0) * HB;
+  const uint8_t* dh_next = HAS_DH ? static_cast<const uint8_t*>(p.dh) + (next * p.ld_dh + i0) * hsz : nullptr;
+  const int64_t dy_rows = gridDim.x * p.ld_dy * 2, h_rows = gridDim.x * p.ld_h * HB, dh_rows = gridDim.x * p.ld_dh * hsz;
+  auto fetch = [&](int stage) {
+    if (next < p.rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        const int i = i0 + k * step;
-        if (i < p.hidden) {
-          slots.fetch(stage, k * PER, static_cast<const __nv_bfloat16*>(p.dy) + row * p.ld_dy + i);
+        if (in(k)) {
+          slots.fetch(stage, k * PER, dy_next + k * step * 2);
           if constexpr (HT == kH8) {
-            copy8((uint32_t)__cvta_generic_to_shared(slots.at(stage, k * PER + 1)), static_cast<const uint8_t*>(p.h) + row * p.ld_h + i);
+            copy8((uint32_t)__cvta_generic_to_shared(slots.at(stage, k * PER + 1)), h_next + k * step);
           } else {
-            const uint8_t* h = static_cast<const uint8_t*>(p.h) + (row * p.ld_h + i) * hsz;
 #pragma unroll
-            for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + q, h + 16 * q);
+            for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + q, h_next + k * step * HB + 16 * q);
           }
-          if constexpr (HAS_DH) {
-            const uint8_t* d = static_cast<const uint8_t*>(p.dh) + (row * p.ld_dh + i) * hsz;
+          if constexpr (HAS_DH)
 #pragma unroll
-            for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + HP + q, d + 16 * q);
-          }
+            for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + HP + q, dh_next + k * step * hsz + 16 * q);
         }
       }
     }
+    next += gridDim.x;
+    dy_next += dy_rows, h_next += h_rows;
+    if (HAS_DH) dh_next += dh_rows;
     copies_commit();
   };
-  float scale_next[HT == kH8 ? NV : 1];
-  auto fetch_scale = [&](int64_t row) {
+  // a row's mean (negated) and deviation, and the scales of an 8-bit h's vectors, fetched ahead of their use
+  struct Known {
+    float m, r, s[HT == kH8 ? NV : 1];
+  };
+  auto known = [&](int64_t row, Known& n) {
+    if (row >= p.rows) return;
+    n.m = -__ldg(p.mean + row), n.r = __ldg(p.rstd + row);
     if constexpr (HT == kH8)
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        if (row < p.rows && i0 + k * step < p.hidden)
-          scale_next[k] = __ldg(p.scales + row * p.s_row + (int64_t)((i0 + k * step) >> 7) * p.s_block);
+        if (in(k)) n.s[k] = __ldg(p.scales + row * p.s_row + (int64_t)((i0 + k * step) >> 7) * p.s_block);
   };
   uint4 w16[NV];
-  float dw[NV][8], db[NV][8];
+  Eight dw[NV], db[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = i0 + k * step;
     w16[k] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    if (i < p.hidden && p.affine.w && !p.affine.w_f32)
+    if (in(k) && p.affine.w && !p.affine.w_f32)
       w16[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.affine.w) + i));
-#pragma unroll
-    for (int j = 0; j < 8; ++j) dw[k][j] = db[k][j] = 0.f;
+    dw[k].zero(), db[k].zero();
   }
+  auto wide = [&](bool f32, int stage, int slot, Eight& v) {
+    if (f32)
+      v.from_f32(*slots.at(stage, slot), *slots.at(stage, slot + 1));
+    else
+      v.from_bf16(*slots.at(stage, slot));
+  };
+  // dy, h - mean and the weight of vector k
+  auto read = [&](const Known& n, int stage, int k, uint64_t minus, Eight& dy, Eight& e, Eight& w) {
+    wide(false, stage, k * PER, dy);
+    if constexpr (HT == kH8) {
+      const uint64_t scale = pair_of(n.s[k], n.s[k]);
+      unpack_fp8(*reinterpret_cast<const uint2*>(slots.at(stage, k * PER + 1)), p.e5m2 != 0, e);
 #pragma unroll
-  for (int s = 0; s < kGradStages; ++s) fetch(blockIdx.x + (int64_t)s * gridDim.x, s);
-  fetch_scale(blockIdx.x);
-  int stage = 0, flip = 0;
-  float mean_next = 0.f, rstd_next = 0.f;
-  if (blockIdx.x < p.rows) mean_next = __ldg(p.mean + blockIdx.x), rstd_next = __ldg(p.rstd + blockIdx.x);
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
-    const float mean = mean_next, rstd = rstd_next;
-    float scale[HT == kH8 ? NV : 1];
-    if constexpr (HT == kH8)
+      for (int j = 0; j < 4; ++j) e.p[j] = add2(mul2(e.p[j], scale), minus);  // (an exact product for power-of-two scales)
+    } else {
+      wide(HT == kH32, stage, k * PER + 1, e);
 #pragma unroll
-      for (int k = 0; k < NV; ++k) scale[k] = scale_next[k];
-    if (row + gridDim.x < p.rows) mean_next = __ldg(p.mean + row + gridDim.x), rstd_next = __ldg(p.rstd + row + gridDim.x);
-    fetch_scale(row + gridDim.x);
-    copies_wait<kGradStages - 1>();
-    // dy, the normed values and the weight of vector k
-    auto read = [&](int k, float(&dy)[8], float(&xh)[8], float(&w)[8]) {
-      slots.template read<false>(stage, k * PER, dy);
-      if constexpr (HT == kH8) {
-        unpack_fp8(*reinterpret_cast<const uint2*>(slots.at(stage, k * PER + 1)), p.e5m2 ? __NV_E5M2 : __NV_E4M3, xh);
+      for (int j = 0; j < 4; ++j) e.p[j] = add2(e.p[j], minus);
+    }
+    w.from_bf16(w16[k]);
+    if (p.affine.w_f32) load8(true, p.affine.w, i0 + k * step, w);
+  };
+  const float inv_hidden = 1.f / (float)p.hidden;
+  auto sums = [&](const Known& n, int stage, int flip) {
+    const uint64_t minus = pair_of(n.m, n.m), rstd = pair_of(n.r, n.r);
+    uint64_t s1 = 0, s2 = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) xh[j] *= scale[k];
-      } else {
-        slots.template read<HT == kH32>(stage, k * PER + 1, xh);
-      }
+    for (int k = 0; k < NV; ++k)
+      if (in(k)) {
+        Eight dy, e, w;
+        read(n, stage, k, minus, dy, e, w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) xh[j] = (xh[j] - mean) * rstd;
-      unpack8(w16[k], w);
-      if (p.affine.w_f32) load_f32<8>(p.affine.w, i0 + k * step, w);
-    };
-    float s1 = 0.f, s2 = 0.f;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (i0 + k * step < p.hidden) {
-        float dy[8], xh[8], w[8];
-        read(k, dy, xh, w);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          db[k][j] += dy[j];
-          dw[k][j] = fmaf(dy[j], xh[j], dw[k][j]);
-          const float g = dy[j] * w[j];
-          s1 += g;
-          s2 = fmaf(g, xh[j], s2);
+        for (int j = 0; j < 4; ++j) {
+          db[k].p[j] = add2(db[k].p[j], dy.p[j]);
+          dw[k].p[j] = fma2(mul2(dy.p[j], rstd), e.p[j], dw[k].p[j]);
+          const uint64_t g = mul2(dy.p[j], w.p[j]);
+          s1 = add2(s1, g);
+          s2 = fma2(g, e.p[j], s2);
         }
       }
-    }
-    // two sets of partials: a block's next row may start while a slow warp reads these
-    const float2 s = row_sum2(s1, s2, part[flip]);
-    const float m1 = s.x / (float)p.hidden, m2 = s.y / (float)p.hidden;
+    float a = sum_of(s1), b = sum_of(s2);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o), b += __shfl_xor_sync(0xffffffffu, b, o);
+    if (lane == 0) part[flip][warp] = make_float2(a, b * n.r);
+  };
+  auto output = [&](const Known& n, int64_t row, int stage, int flip) {
+    const uint64_t minus = pair_of(n.m, n.m), rstd = pair_of(n.r, n.r);
+    float2 s = part[flip][lane < warps ? lane : 0];
+    if (lane >= warps) s = make_float2(0.f, 0.f);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s.x += __shfl_xor_sync(0xffffffffu, s.x, o), s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
+    const float c1 = -s.x * inv_hidden, c2 = -n.r * (s.y * inv_hidden);
+    const uint64_t m1 = pair_of(c1, c1), m2 = pair_of(c2, c2);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      const int i = i0 + k * step;
-      if (i < p.hidden) {
-        float dy[8], xh[8], w[8], d[8];
-        read(k, dy, xh, w);
-        if constexpr (HAS_DH)
-          slots.template read<HT == kH32>(stage, k * PER + 1 + HP, d);
-        else
+      if (in(k)) {
+        Eight dy, e, w, d;
+        read(n, stage, k, minus, dy, e, w);
+        if constexpr (HAS_DH) wide(HT == kH32, stage, k * PER + 1 + HP, d);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) d[j] = 0.f;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) d[j] = fmaf(rstd, fmaf(dy[j], w[j], -m1) - xh[j] * m2, d[j]);
-        if constexpr (HT == kH32)
-          store_f32<8>(p.dx, row * p.hidden + i, d);
-        else
-          store_bf16<8>(p.dx, row * p.hidden + i, d);
+        for (int j = 0; j < 4; ++j) {
+          const uint64_t t = fma2(e.p[j], m2, fma2(dy.p[j], w.p[j], m1));
+          if constexpr (HAS_DH)
+            d.p[j] = fma2(t, rstd, d.p[j]);
+          else
+            d.p[j] = mul2(t, rstd);
+        }
+        store8(HT == kH32, p.dx, row * p.hidden + i0 + k * step, d);
       }
     }
-    fetch(row + (int64_t)kGradStages * gridDim.x, stage);
-    stage ^= 1;
+  };
+  Known now, then;
+  known(blockIdx.x, now);
+#pragma unroll
+  for (int s = 0; s < STAGES; ++s) fetch(s);
+  int stage = 0, flip = 0;
+  auto after = [](int s) { return s + 1 == STAGES ? 0 : s + 1; };
+  if (PIPE) {
+    known((int64_t)blockIdx.x + gridDim.x, then);
+    copies_wait<STAGES - 1>();
+    if (blockIdx.x < p.rows) sums(now, 0, 0);
+    __syncthreads();
+  }
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+    if constexpr (PIPE) {
+      copies_wait<STAGES - 2>();
+      if (row + gridDim.x < p.rows) sums(then, after(stage), flip ^ 1);
+      output(now, row, stage, flip);
+      now = then;
+      known(row + 2 * (int64_t)gridDim.x, then);
+      fetch(stage);
+      __syncthreads();
+    } else {
+      known(row + gridDim.x, then);
+      copies_wait<STAGES - 1>();
+      sums(now, stage, flip);
+      __syncthreads();
+      output(now, row, stage, flip);
+      now = then;
+      fetch(stage);
+    }
+    stage = after(stage);
   }
   copies_wait<0>();
   if (p.partial) {
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (i0 + k * step < p.hidden) {
-        store_f32<8>(p.partial, (int64_t)blockIdx.x * p.hidden + i0 + k * step, dw[k]);
-        store_f32<8>(p.partial, (int64_t)(gridDim.x + blockIdx.x) * p.hidden + i0 + k * step, db[k]);
+      if (in(k)) {
+        store8(true, p.partial, (int64_t)blockIdx.x * p.hidden + i0 + k * step, dw[k]);
+        store8(true, p.partial, (int64_t)(gridDim.x + blockIdx.x) * p.hidden + i0 + k * step, db[k]);
       }
   }
 }
@@ -788,10 +901,12 @@ template <int HT, bool HAS_DH>
 int run_grad(const GradArgs& p, bool vec, int sms, cudaStream_t s) {
   const int n = p.hidden / 8;
   int blocks, rc;
-  if (vec && n <= 2048 && grad_parts<HT, HAS_DH>() * 16 * kGradStages * round32((n + 1) / 2) <= kStreamBytes) {
+  if (vec && n <= 2048 && grad_parts<HT, HAS_DH>() * 16 * grad_stages<HT, HAS_DH>() * round32((n + 1) / 2) <= kStreamBytes) {
     int threads, bytes;
-    auto* kernel = layer_norm_grad_stream_kernel<HT, HAS_DH>;
-    rc = stream_shape(kernel, p.hidden, grad_parts<HT, HAS_DH>(), kGradStages, sms, p.rows, &threads, &blocks, &bytes);
+    auto* kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, false>;
+    if constexpr (HT != kH32)
+      if (p.hidden % (32 * 8 * kStreamVecs) == 0) kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, true>;
+    rc = stream_shape(kernel, p.hidden, grad_parts<HT, HAS_DH>(), grad_stages<HT, HAS_DH>(), sms, p.rows, &threads, &blocks, &bytes);
     if (rc != DG_OK) return rc;
     blocks = grad_blocks(p.rows, sms, (int64_t)sms * (kStreamThreads / threads));
     rc = dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);

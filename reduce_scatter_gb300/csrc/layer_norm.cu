@@ -184,8 +184,8 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) layer_norm_kernel(const _
 
 // ------------------------------------------------------------ streamed rows
 
-constexpr int kStreamVecs = 2;        // vectors of 8 values per thread
-constexpr int kStreamThreads = 1024;  // per SM (64 registers each)
+constexpr int kStreamVecs = 4;       // vectors of 8 values per thread
+constexpr int kStreamThreads = 512;  // per SM (128 registers each)
 constexpr int kStreamBytes = 220000;  // dynamic shared memory that the streamed kernels may take, whatever the call needs
 
 // XP, RP: 16-byte slots of eight values of x (1 bf16, 2 fp32) and of the
@@ -481,9 +481,12 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(const __grid_cons
 
 // ------------------------------------------------------------ forward launch
 
+// Threads of a streamed row of n vectors.
+constexpr int stream_threads(int n) { return ((n + kStreamVecs - 1) / kStreamVecs + 31) / 32 * 32; }
+
 template <class Kernel>
 int stream_shape(Kernel kernel, int hidden, int parts, int stages, int sms, int64_t rows, int* threads, int* blocks, int* bytes) {
-  *threads = round32((hidden / 8 + kStreamVecs - 1) / kStreamVecs);
+  *threads = stream_threads(hidden / 8);
   *bytes = stages * parts * 16 * *threads;
   const int64_t most = (int64_t)sms * (kStreamThreads / *threads);
   *blocks = (int)(rows < most ? rows : most);
@@ -491,9 +494,12 @@ int stream_shape(Kernel kernel, int hidden, int parts, int stages, int sms, int6
   return DG_OK;
 }
 
+// Stages of rows of `slots` 16-byte slots a vector (192 KB for 16384 values; two fp32 operands fit to 13 744).
+constexpr int stream_stages(int slots) { return slots > 2 ? 2 : 3; }
+
 template <int XP, int RP, bool OUT8>
 int stream_norm(const Args& p, int sms, cudaStream_t s) {
-  constexpr int stages = XP + RP > 2 ? 2 : 3;  // (192 KB for 16384 values; two fp32 operands only fit to 13744)
+  constexpr int stages = stream_stages(XP + RP);
   int threads, blocks, bytes;
   auto* kernel = layer_norm_stream_kernel<XP, RP, OUT8, false, stages>;
   if constexpr (XP == 1 && RP < 2)
@@ -521,7 +527,7 @@ int run_norm(const Args& p, bool vec, int sms, cudaStream_t s) {
   const int n = p.hidden / 8;
   // Many long rows are streamed; few rows take as many threads as they have vectors,
   // for the shortest chain of loads.
-  if (p.rows > 2 * sms && n >= 256 && n <= 2048 && (XP + RP) * 2 * 16 * 2 * round32((n + 1) / 2) <= kStreamBytes)
+  if (p.rows > 2 * sms && n >= 256 && n <= 2048 && stream_stages(XP + RP) * kStreamVecs * (XP + RP) * 16 * stream_threads(n) <= kStreamBytes)
     return stream_norm<XP, RP, OUT8>(p, sms, s);
   auto launch_rows = [&](auto* kernel, int threads) {
     const int per = threads == 32 ? 4 : 1;  // one warp per row: four rows to a block
@@ -901,7 +907,7 @@ template <int HT, bool HAS_DH>
 int run_grad(const GradArgs& p, bool vec, int sms, cudaStream_t s) {
   const int n = p.hidden / 8;
   int blocks, rc;
-  if (vec && n <= 2048 && grad_parts<HT, HAS_DH>() * 16 * grad_stages<HT, HAS_DH>() * round32((n + 1) / 2) <= kStreamBytes) {
+  if (vec && n <= 2048 && grad_parts<HT, HAS_DH>() * 16 * grad_stages<HT, HAS_DH>() * stream_threads(n) <= kStreamBytes) {
     int threads, bytes;
     auto* kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, false>;
     if constexpr (HT != kH32)

@@ -119,12 +119,12 @@ __device__ __forceinline__ void unpack_fp8(uint2 u, __nv_fp8_interpretation_t fm
 }
 
 __device__ __forceinline__ void unpack_fp8(uint2 u, bool e5m2, Eight& v) {
-  const uint32_t w[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
-    const float2 f = unpack_fp8x2(w[k], e5m2 ? __NV_E5M2 : __NV_E4M3);
-    v.p[k] = pair_of(f.x, f.y);
-  }
+  float f[8];
+  if (e5m2)
+    unpack_fp8(u, __NV_E5M2, f);
+  else
+    unpack_fp8(u, __NV_E4M3, f);
+  v.from_floats(f);
 }
 
 // 8-bit blocks of 1 x 128 as they are written.

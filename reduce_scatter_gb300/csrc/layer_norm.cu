@@ -91,16 +91,35 @@ __device__ __forceinline__ void keep_moments(const Args& p, int64_t row, const M
     if (p.rstd) p.rstd[row] = m.rstd;
   }
 }
-// Values of warp w whose threads hold NV vectors of 8, blockDim.x threads apart.
+// Values of warp w whose threads hold NV vectors of 8, blockDim.x threads apart;
+// the row starts `shift` values into the first vector.
 template <int NV>
-__device__ __forceinline__ int warp_count(int w, int hidden) {
+__device__ __forceinline__ int warp_count(int w, int hidden, int shift = 0) {
   int n = 0;
 #pragma unroll
-  for (int k = 0; k < NV; ++k) n += min(max(hidden - (w * 256 + k * (int)blockDim.x * 8), 0), 256);
+  for (int k = 0; k < NV; ++k) {
+    const int from = w * 256 + k * (int)blockDim.x * 8 - shift;
+    n += max(min(from + 256, hidden) - max(from, 0), 0);
+  }
   return n;
 }
-// A warp's moments from its vectors (those past the row: zeros, unless all are FULL).
-template <int NV, bool FULL = false>
+// Values of vector i that are not in the row become 0.
+__device__ __forceinline__ void clip(Eight& v, int i, int hidden) {
+  float f[8];
+  v.to_floats(f);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) f[j] = i + j < 0 || i + j >= hidden ? 0.f : f[j];
+  v.from_floats(f);
+}
+
+// How the vectors of a row lie: every thread has its NV (kFull); whole vectors,
+// not in every thread (kVectors); or the row starts and ends inside vectors
+// (kEdges: rows without 16-byte alignment, of which each block takes those that
+// start at the same place in a vector).
+enum { kFull = 0, kVectors = 1, kEdges = 2 };
+
+// A warp's moments from its vectors (those past the row: zeros).
+template <int NV, int MODE = kVectors>
 __device__ __forceinline__ float2 moments_of(const Eight (&h)[NV], int hidden, int i0, int step, const Share& own) {
   uint64_t sum = add2(h[0].p[0], h[0].p[1]);
 #pragma unroll
@@ -111,21 +130,60 @@ __device__ __forceinline__ float2 moments_of(const Eight (&h)[NV], int hidden, i
   const uint64_t minus = pair_of(-mean, -mean);
   uint64_t d1 = 0, d2 = 0;
 #pragma unroll
-  for (int k = 0; k < NV; ++k)
-    if (FULL || i0 + k * step < hidden)
+  for (int k = 0; k < NV; ++k) {
+    const int i = i0 + k * step;
+    if (MODE == kFull || i < hidden) {
+      Eight d;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint64_t d = add2(h[k].p[j], minus);
-        d1 = add2(d1, d), d2 = fma2(d, d, d2);
-      }
+      for (int j = 0; j < 4; ++j) d.p[j] = add2(h[k].p[j], minus);
+      if (MODE == kEdges && (i < 0 || i + 8 > hidden)) clip(d, i, hidden);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d1 = add2(d1, d.p[j]), d2 = fma2(d.p[j], d.p[j], d2);
+    }
+  }
   return warp_moments(mean, sum_of(d1), sum_of(d2), own);
+}
+// Vector i into a row at `at`; of one that is not whole, what is in the row.
+template <int MODE>
+__device__ __forceinline__ void store_row8(bool f32, void* base, int64_t at, int i, int hidden, const Eight& v) {
+  if (MODE == kEdges && (i < 0 || i + 8 > hidden)) {
+    float f[8];
+    v.to_floats(f);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float one[1] = {f[j]};
+      if (i + j < 0 || i + j >= hidden) continue;
+      if (f32)
+        store_f32<1>(base, at + i + j, one);
+      else
+        store_bf16<1>(base, at + i + j, one);
+    }
+  } else {
+    store8(f32, base, at + i, v);
+  }
+}
+// Vector i of a vector of `hidden` values (its nearest ones, where it is not whole).
+template <int MODE>
+__device__ __forceinline__ void load_row8(bool f32, const void* base, int i, int hidden, Eight& v) {
+  if (MODE == kEdges) {  // (no alignment)
+    float f[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float one[1];
+      load_any<1>(f32, base, min(max(i + j, 0), hidden - 1), one);
+      f[j] = one[0];
+    }
+    v.from_floats(f);
+  } else {
+    load8(f32, base, i, v);
+  }
 }
 
 // Vector i of a row's output, from h.
-template <bool OUT8>
+template <bool OUT8, int MODE = kVectors>
 __device__ __forceinline__ void finish(const Args& p, int64_t row, int i, bool in, const Moments& m, const Eight& h, const Eight& w,
                                        const Eight& b) {
-  if (p.kept.values) store_blocks(p.kept, true, row, p.hidden, i, in, h);
+  if (MODE != kEdges && p.kept.values) store_blocks(p.kept, true, row, p.hidden, i, in, h);
   const uint64_t minus = pair_of(-m.mean, -m.mean), rstd = pair_of(m.rstd, m.rstd);
   Eight y;
 #pragma unroll
@@ -133,7 +191,7 @@ __device__ __forceinline__ void finish(const Args& p, int64_t row, int i, bool i
   if constexpr (OUT8)
     store_blocks(p.y8, false, row, p.hidden, i, in, y);
   else if (in)
-    store8(false, p.y, row * p.hidden + i, y);
+    store_row8<MODE>(false, p.y, row * p.hidden, i, p.hidden, y);
 }
 
 // ------------------------------------------------------ a row in registers
@@ -186,7 +244,7 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) layer_norm_kernel(const _
 
 constexpr int kStreamVecs = 4;       // vectors of 8 values per thread
 constexpr int kStreamThreads = 512;  // per SM (128 registers each)
-constexpr int kStreamBytes = 220000;  // dynamic shared memory that the streamed kernels may take, whatever the call needs
+constexpr int kStreamBytes = 231000;  // dynamic shared memory that the streamed kernels may take, whatever the call needs
 
 // XP, RP: 16-byte slots of eight values of x (1 bf16, 2 fp32) and of the
 // residual (0 none).  A row goes through two steps, with a barrier in between: its
@@ -194,8 +252,7 @@ constexpr int kStreamBytes = 220000;  // dynamic shared memory that the streamed
 // (nothing is held in registers over the barrier).  With three stages the second
 // step of a row comes after the first one of the next, so that no warp waits
 // at the barrier for the slowest one's sums.
-// FULL: every thread has its NV vectors.
-template <int XP, int RP, bool OUT8, bool FULL, int STAGES>
+template <int XP, int RP, bool OUT8, int MODE, int STAGES>
 __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const __grid_constant__ Args p) {
   extern __shared__ __align__(16) uint8_t smem[];
   __shared__ float2 part[2][32];
@@ -204,8 +261,16 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
   constexpr int HS = RP == 2 ? XP : 0;  // h's slot of a vector's
   const Slots<NV * PER> slots{smem};
   begin_kernel();
-  const int step = blockDim.x * 8, i0 = threadIdx.x * 8, warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto in = [&](int k) { return FULL || i0 + k * step < p.hidden; };
+  const int shift = MODE == kEdges ? (int)((blockIdx.x & 7u) * (p.hidden & 7u) & 7u) : 0;
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8 - shift, warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto in = [&](int k) { return MODE == kFull || i0 + k * step < p.hidden; };
+  // a slot of up to 16 bytes of values from i on (the start of a row that begins inside it holds the end of the row before)
+  auto copy = [&](int stage, int part, const uint8_t* src, int i, int size) {
+    if constexpr (MODE == kEdges)
+      slots.fetch(stage, part, src, min(max((p.hidden - i) * size, 0), 16));
+    else
+      slots.fetch(stage, part, src);
+  };
   // this thread's place in the next row to fetch
   int64_t next = blockIdx.x;
   const uint8_t* x_next = static_cast<const uint8_t*>(p.x) + (next * p.ld_x + i0) * (2 * XP);
@@ -217,10 +282,11 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
       for (int k = 0; k < NV; ++k) {
         if (in(k)) {
 #pragma unroll
-          for (int q = 0; q < XP; ++q) slots.fetch(stage, k * PER + q, x_next + k * step * (2 * XP) + 16 * q);
+          for (int q = 0; q < XP; ++q) copy(stage, k * PER + q, x_next + k * step * (2 * XP) + 16 * q, i0 + k * step + 4 * q, 2 * XP);
           if constexpr (RP != 0)
 #pragma unroll
-            for (int q = 0; q < RP; ++q) slots.fetch(stage, k * PER + XP + q, r_next + k * step * (2 * RP) + 16 * q);
+            for (int q = 0; q < RP; ++q)
+              copy(stage, k * PER + XP + q, r_next + k * step * (2 * RP) + 16 * q, i0 + k * step + 4 * q, 2 * RP);
         }
       }
     }
@@ -243,19 +309,20 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
     w16[k] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
     b16[k] = make_uint4(0, 0, 0, 0);
     if (in(k)) {
-      if (p.affine.w && !p.affine.w_f32) w16[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.affine.w) + i));
-      if (p.affine.b && !p.affine.b_f32) b16[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.affine.b) + i));
+      Eight v;
+      if (p.affine.w && !p.affine.w_f32) load_row8<MODE>(false, p.affine.w, i, p.hidden, v), w16[k] = v.to_bf16();
+      if (p.affine.b && !p.affine.b_f32) load_row8<MODE>(false, p.affine.b, i, p.hidden, v), b16[k] = v.to_bf16();
     }
   }
-  const Share own(FULL ? NV * 256 : warp_count<NV>(warp, p.hidden));
-  const Share of(lane >= warps ? 0 : FULL ? NV * 256 : warp_count<NV>(lane, p.hidden));
+  const Share own(MODE == kFull ? NV * 256 : warp_count<NV>(warp, p.hidden, shift));
+  const Share of(lane >= warps ? 0 : MODE == kFull ? NV * 256 : warp_count<NV>(lane, p.hidden, shift));
   const float inv_hidden = 1.f / (float)p.hidden;
   auto sums = [&](int64_t row, int stage, int flip) {
     Eight h[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = i0 + k * step;
-      if (!FULL) h[k].zero();
+      if (MODE != kFull) h[k].zero();
       if (in(k)) {
         read(XP == 2, stage, k * PER, h[k]);
         if constexpr (RP != 0) {
@@ -264,20 +331,20 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
 #pragma unroll
           for (int j = 0; j < 4; ++j) h[k].p[j] = add2(h[k].p[j], r.p[j]);
           if constexpr (RP == 2) {
-            const uint4 a = h[k].to_f32(0), b = h[k].to_f32(1);
-            uint4* to = reinterpret_cast<uint4*>(static_cast<float*>(p.sum) + row * p.ld_sum + i);
-            to[0] = *slots.at(stage, k * PER + HS) = a;
-            to[1] = *slots.at(stage, k * PER + HS + 1) = b;
+            *slots.at(stage, k * PER + HS) = h[k].to_f32(0);
+            *slots.at(stage, k * PER + HS + 1) = h[k].to_f32(1);
           } else {
             // the norm is of the sum as it is stored, so that the gradient sees the same values
             const uint4 u = h[k].to_bf16();
-            *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.sum) + row * p.ld_sum + i) = *slots.at(stage, k * PER) = u;
+            *slots.at(stage, k * PER) = u;
             h[k].from_bf16(u);
           }
+          store_row8<MODE>(RP == 2, p.sum, row * p.ld_sum, i, p.hidden, h[k]);
         }
+        if (MODE == kEdges && (i < 0 || i + 8 > p.hidden)) clip(h[k], i, p.hidden);
       }
     }
-    const float2 m = moments_of<NV, FULL>(h, p.hidden, i0, step, own);
+    const float2 m = moments_of<NV, MODE>(h, p.hidden, i0, step, own);
     if (lane == 0) part[flip][warp] = m;
   };
   auto output = [&](int64_t row, int stage, int flip) {
@@ -288,13 +355,13 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
       const int i = i0 + k * step;
       Eight h, w, b;
       w.from_bf16(w16[k]), b.from_bf16(b16[k]);
-      if (!FULL) h.zero();
+      if (MODE != kFull) h.zero();
       if (in(k)) {
         read(H32, stage, k * PER + HS, h);
-        if (p.affine.w_f32) load8(true, p.affine.w, i, w);
-        if (p.affine.b_f32) load8(true, p.affine.b, i, b);
+        if (p.affine.w_f32) load_row8<MODE>(true, p.affine.w, i, p.hidden, w);
+        if (p.affine.b_f32) load_row8<MODE>(true, p.affine.b, i, p.hidden, b);
       }
-      finish<OUT8>(p, row, i, in(k), m, h, w, b);
+      finish<OUT8, MODE>(p, row, i, in(k), m, h, w, b);
     }
   };
 #pragma unroll
@@ -484,9 +551,12 @@ __global__ void __launch_bounds__(1024) layer_norm_long_kernel(const __grid_cons
 // Threads of a streamed row of n vectors.
 constexpr int stream_threads(int n) { return ((n + kStreamVecs - 1) / kStreamVecs + 31) / 32 * 32; }
 
+// Vectors of a row; one that starts inside a vector takes another.
+constexpr int row_vectors(int hidden, bool vec) { return vec ? hidden / 8 : (hidden + 14) / 8; }
+
 template <class Kernel>
-int stream_shape(Kernel kernel, int hidden, int parts, int stages, int sms, int64_t rows, int* threads, int* blocks, int* bytes) {
-  *threads = stream_threads(hidden / 8);
+int stream_shape(Kernel kernel, int vectors, int parts, int stages, int sms, int64_t rows, int* threads, int* blocks, int* bytes) {
+  *threads = stream_threads(vectors);
   *bytes = stages * parts * 16 * *threads;
   const int64_t most = (int64_t)sms * (kStreamThreads / *threads);
   *blocks = (int)(rows < most ? rows : most);
@@ -498,13 +568,17 @@ int stream_shape(Kernel kernel, int hidden, int parts, int stages, int sms, int6
 constexpr int stream_stages(int slots) { return slots > 2 ? 2 : 3; }
 
 template <int XP, int RP, bool OUT8>
-int stream_norm(const Args& p, int sms, cudaStream_t s) {
+int stream_norm(const Args& p, bool vec, int sms, cudaStream_t s) {
   constexpr int stages = stream_stages(XP + RP);
   int threads, blocks, bytes;
-  auto* kernel = layer_norm_stream_kernel<XP, RP, OUT8, false, stages>;
+  auto* kernel = layer_norm_stream_kernel<XP, RP, OUT8, kVectors, stages>;
   if constexpr (XP == 1 && RP < 2)
-    if (p.hidden % (32 * 8 * kStreamVecs) == 0) kernel = layer_norm_stream_kernel<XP, RP, OUT8, true, stages>;
-  if (int rc = stream_shape(kernel, p.hidden, kStreamVecs * (XP + RP), stages, sms, p.rows, &threads, &blocks, &bytes)) return rc;
+    if (p.hidden % (32 * 8 * kStreamVecs) == 0) kernel = layer_norm_stream_kernel<XP, RP, OUT8, kFull, stages>;
+  if constexpr (!OUT8)
+    if (!vec) kernel = layer_norm_stream_kernel<XP, RP, false, kEdges, stages>;
+  if (int rc = stream_shape(kernel, row_vectors(p.hidden, vec), kStreamVecs * (XP + RP), stages, sms, p.rows, &threads, &blocks, &bytes))
+    return rc;
+  if (!vec) blocks = blocks / 8 * 8;  // (each block's rows start at the same place in a vector)
   return dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);
 }
 
@@ -515,20 +589,24 @@ int run_spread(const Args& p, cudaStream_t s) {
                      dim3((unsigned)((p.rows + per - 1) / per)), dim3(threads, per), 0, s, p);
 }
 
+// vec: whole vectors; dense: else, rows that follow one another by their length from aligned bases.
 template <int XP, int RP, bool OUT8>
-int run_norm(const Args& p, bool vec, int sms, cudaStream_t s) {
+int run_norm(const Args& p, bool vec, bool dense, int sms, cudaStream_t s) {
+  // Many long rows are streamed; few rows take as many threads as they have vectors,
+  // for the shortest chain of loads.
+  const int vectors = row_vectors(p.hidden, vec);
+  const bool fits = vectors <= 2048 && stream_stages(XP + RP) * kStreamVecs * (XP + RP) * 16 * stream_threads(vectors) <= kStreamBytes;
   if (!vec) {
     if constexpr (!OUT8) {
+      // 2047 x 5003: 20.8 us element by element
+      if (dense && fits && p.rows > 2 * sms && vectors >= 64) return stream_norm<XP, RP, false>(p, false, sms, s);
       if (p.hidden <= 16384) return run_spread<XP, RP>(p, s);
       return dgl::launch(layer_norm_long_kernel<false, false>, dim3((unsigned)p.rows), dim3(1024), 0, s, p);
     }
     return fail(DG_ERR_ARG, "8-bit blocks need rows of whole 16-byte vectors");
   }
-  const int n = p.hidden / 8;
-  // Many long rows are streamed; few rows take as many threads as they have vectors,
-  // for the shortest chain of loads.
-  if (p.rows > 2 * sms && n >= 256 && n <= 2048 && stream_stages(XP + RP) * kStreamVecs * (XP + RP) * 16 * stream_threads(n) <= kStreamBytes)
-    return stream_norm<XP, RP, OUT8>(p, sms, s);
+  const int n = vectors;
+  if (fits && p.rows > 2 * sms && n >= 256) return stream_norm<XP, RP, OUT8>(p, true, sms, s);
   auto launch_rows = [&](auto* kernel, int threads) {
     const int per = threads == 32 ? 4 : 1;  // one warp per row: four rows to a block
     return dgl::launch(kernel, dim3((unsigned)((p.rows + per - 1) / per)), dim3(threads, per), 0, s, p);
@@ -540,9 +618,12 @@ int run_norm(const Args& p, bool vec, int sms, cudaStream_t s) {
 }
 
 template <int XP, int RP>
-int run_out(const Args& p, bool vec, int sms, cudaStream_t s) {
-  return p.y ? run_norm<XP, RP, false>(p, vec, sms, s) : run_norm<XP, RP, true>(p, vec, sms, s);
+int run_out(const Args& p, bool vec, bool dense, int sms, cudaStream_t s) {
+  return p.y ? run_norm<XP, RP, false>(p, vec, dense, sms, s) : run_norm<XP, RP, true>(p, vec, dense, sms, s);
 }
+
+// A matrix whose rows start at the same place in a vector as those of a densely packed one (or none).
+bool like_dense(const void* p, int64_t ld, int64_t hidden) { return !p || (aligned16(p) && (ld - hidden) % 8 == 0); }
 
 // ----------------------------------------------------------------- gradient
 
@@ -571,75 +652,94 @@ __host__ __device__ constexpr int grad_stages() {
   return grad_parts<HT, HAS_DH>() > 2 * kStreamVecs ? 2 : 3;
 }
 
-__device__ __forceinline__ void copy8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+// Shared memory of a thread: its stages, and its weights.
+template <int HT, bool HAS_DH>
+__host__ __device__ constexpr int grad_bytes() {
+  return (grad_stages<HT, HAS_DH>() * grad_parts<HT, HAS_DH>() + kStreamVecs) * 16;
+}
+
+template <int BYTES>
+__device__ __forceinline__ void copy_small(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(BYTES) : "memory");
 }
 
 // Rows streamed like the forward's, in the same two steps: the sums, and dx, for
 // which the row is read from its slots again, which leaves registers to the weight
 // and the two gradients that are summed over the block's rows.  With
 // e = h - mean: mean(g xh) = rstd mean(g e), dx = rstd (dy w - mean(g) - e (rstd mean(g xh))).
-template <int HT, bool HAS_DH, bool FULL>
+template <int HT, bool HAS_DH, int MODE>
 __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kernel(const __grid_constant__ GradArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 part[2][32];
+  __shared__ float2 parts[2][16];  // (a group's warps)
   constexpr int NV = kStreamVecs, HP = HT == kH32 ? 2 : 1, PER = 1 + HP * (HAS_DH ? 2 : 1), hsz = HT == kH32 ? 4 : 2;
   constexpr int STAGES = grad_stages<HT, HAS_DH>();
   constexpr bool PIPE = STAGES > 2;
-  const Slots<grad_parts<HT, HAS_DH>()> slots{smem};
+  constexpr int PARTS = grad_parts<HT, HAS_DH>();
+  const Slots<PARTS> slots{smem + threadIdx.y * (STAGES * PARTS + NV) * 16 * blockDim.x};
+  // behind the stages: the weight's vectors of this thread, in bf16 (in registers they crowded out the row's)
+  auto weight_slot = [&](int k) { return slots.at(0, STAGES * PARTS + k); };
   begin_kernel();
-  const int step = blockDim.x * 8, i0 = threadIdx.x * 8, warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  auto in = [&](int k) { return FULL || i0 + k * step < p.hidden; };
+  // this group of threads takes the rows unit, unit + units, ...
+  const uint32_t unit = blockIdx.x * blockDim.y + threadIdx.y, units = gridDim.x * blockDim.y, rows = (uint32_t)p.rows;
+  const int shift = MODE == kEdges ? (int)((unit & 7u) * (p.hidden & 7u) & 7u) : 0;
+  const int step = blockDim.x * 8, i0 = threadIdx.x * 8 - shift, warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  auto in = [&](int k) { return MODE == kFull || i0 + k * step < p.hidden; };
+  auto copy = [&](int stage, int part, const uint8_t* src, int i, int size) {  // (as in the forward)
+    if constexpr (MODE == kEdges)
+      slots.fetch(stage, part, src, min(max((p.hidden - i) * size, 0), 16));
+    else
+      slots.fetch(stage, part, src);
+  };
   // this thread's place in the next row to fetch
   constexpr int HB = HT == kH8 ? 1 : hsz;  // bytes of a value of h
-  int64_t next = blockIdx.x;
-  const uint8_t* dy_next = static_cast<const uint8_t*>(p.dy) + (next * p.ld_dy + i0) * 2;
-  const uint8_t* h_next = static_cast<const uint8_t*>(p.h) + (next * p.ld_h + i0) * HB;
-  const uint8_t* dh_next = HAS_DH ? static_cast<const uint8_t*>(p.dh) + (next * p.ld_dh + i0) * hsz : nullptr;
-  const int64_t dy_rows = gridDim.x * p.ld_dy * 2, h_rows = gridDim.x * p.ld_h * HB, dh_rows = gridDim.x * p.ld_dh * hsz;
+  uint32_t next = unit;
+  const uint8_t* dy_next = static_cast<const uint8_t*>(p.dy) + ((int64_t)next * p.ld_dy + i0) * 2;
+  const uint8_t* h_next = static_cast<const uint8_t*>(p.h) + ((int64_t)next * p.ld_h + i0) * HB;
+  const uint8_t* dh_next = HAS_DH ? static_cast<const uint8_t*>(p.dh) + ((int64_t)next * p.ld_dh + i0) * hsz : nullptr;
   auto fetch = [&](int stage) {
-    if (next < p.rows) {
+    if (next < rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         if (in(k)) {
-          slots.fetch(stage, k * PER, dy_next + k * step * 2);
-          if constexpr (HT == kH8) {
-            copy8((uint32_t)__cvta_generic_to_shared(slots.at(stage, k * PER + 1)), h_next + k * step);
+          const int i = i0 + k * step;
+          copy(stage, k * PER, dy_next + k * step * 2, i, 2);
+          if constexpr (HT == kH8) {  // eight values and their scale in one slot
+            const uint32_t slot = (uint32_t)__cvta_generic_to_shared(slots.at(stage, k * PER + 1));
+            copy_small<8>(slot, h_next + k * step);
+            copy_small<4>(slot + 8, p.scales + (int64_t)next * p.s_row + (int64_t)(i >> 7) * p.s_block);
           } else {
 #pragma unroll
-            for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + q, h_next + k * step * HB + 16 * q);
+            for (int q = 0; q < HP; ++q) copy(stage, k * PER + 1 + q, h_next + k * step * HB + 16 * q, i + 4 * q, hsz);
           }
           if constexpr (HAS_DH)
 #pragma unroll
-            for (int q = 0; q < HP; ++q) slots.fetch(stage, k * PER + 1 + HP + q, dh_next + k * step * hsz + 16 * q);
+            for (int q = 0; q < HP; ++q) copy(stage, k * PER + 1 + HP + q, dh_next + k * step * hsz + 16 * q, i + 4 * q, hsz);
         }
       }
     }
-    next += gridDim.x;
-    dy_next += dy_rows, h_next += h_rows;
-    if (HAS_DH) dh_next += dh_rows;
+    next += units;
+    dy_next += units * p.ld_dy * 2, h_next += units * p.ld_h * HB;
+    if (HAS_DH) dh_next += units * p.ld_dh * hsz;
     copies_commit();
   };
-  // a row's mean (negated) and deviation, and the scales of an 8-bit h's vectors, fetched ahead of their use
+  // a row's mean (negated) and deviation, fetched ahead of their use
   struct Known {
-    float m, r, s[HT == kH8 ? NV : 1];
+    float m, r;
   };
-  auto known = [&](int64_t row, Known& n) {
-    if (row >= p.rows) return;
-    n.m = -__ldg(p.mean + row), n.r = __ldg(p.rstd + row);
-    if constexpr (HT == kH8)
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (in(k)) n.s[k] = __ldg(p.scales + row * p.s_row + (int64_t)((i0 + k * step) >> 7) * p.s_block);
+  auto known = [&](uint32_t row, Known& n) {
+    if (row < rows) n.m = -__ldg(p.mean + row), n.r = __ldg(p.rstd + row);
   };
-  uint4 w16[NV];
   Eight dw[NV], db[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = i0 + k * step;
-    w16[k] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    if (in(k) && p.affine.w && !p.affine.w_f32)
-      w16[k] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.affine.w) + i));
+    uint4 w16 = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
+    if (in(k) && p.affine.w && !p.affine.w_f32) {
+      Eight v;
+      load_row8<MODE>(false, p.affine.w, i, p.hidden, v);
+      w16 = v.to_bf16();
+    }
+    *weight_slot(k) = w16;
     dw[k].zero(), db[k].zero();
   }
   auto wide = [&](bool f32, int stage, int slot, Eight& v) {
@@ -649,22 +749,34 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
       v.from_bf16(*slots.at(stage, slot));
   };
   // dy, h - mean and the weight of vector k
-  auto read = [&](const Known& n, int stage, int k, uint64_t minus, Eight& dy, Eight& e, Eight& w) {
+  auto read = [&](int stage, int k, uint64_t minus, Eight& dy, Eight& e, Eight& w) {
     wide(false, stage, k * PER, dy);
     if constexpr (HT == kH8) {
-      const uint64_t scale = pair_of(n.s[k], n.s[k]);
-      unpack_fp8(*reinterpret_cast<const uint2*>(slots.at(stage, k * PER + 1)), p.e5m2 != 0, e);
+      const uint4 u = *slots.at(stage, k * PER + 1);
+      const uint64_t scale = pair_of(__uint_as_float(u.z), __uint_as_float(u.z));
+      unpack_fp8(make_uint2(u.x, u.y), p.e5m2 != 0, e);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) e.p[j] = add2(mul2(e.p[j], scale), minus);  // (an exact product for power-of-two scales)
+      for (int j = 0; j < 4; ++j) e.p[j] = fma2(e.p[j], scale, minus);
     } else {
       wide(HT == kH32, stage, k * PER + 1, e);
 #pragma unroll
       for (int j = 0; j < 4; ++j) e.p[j] = add2(e.p[j], minus);
     }
-    w.from_bf16(w16[k]);
-    if (p.affine.w_f32) load8(true, p.affine.w, i0 + k * step, w);
+    const int i = i0 + k * step;
+    if (MODE == kEdges && (i < 0 || i + 8 > p.hidden)) clip(dy, i, p.hidden), clip(e, i, p.hidden);
+    w.from_bf16(*weight_slot(k));
+    if (p.affine.w_f32) load_row8<MODE>(true, p.affine.w, i, p.hidden, w);
   };
   const float inv_hidden = 1.f / (float)p.hidden;
+  const int first_warp = threadIdx.y * warps;
+  auto group_sync = [&]() {
+    if (blockDim.y == 1)
+      __syncthreads();
+    else if (warps == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + (int)threadIdx.y), "r"((int)blockDim.x) : "memory");
+  };
   auto sums = [&](const Known& n, int stage, int flip) {
     const uint64_t minus = pair_of(n.m, n.m), rstd = pair_of(n.r, n.r);
     uint64_t s1 = 0, s2 = 0;
@@ -672,7 +784,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     for (int k = 0; k < NV; ++k)
       if (in(k)) {
         Eight dy, e, w;
-        read(n, stage, k, minus, dy, e, w);
+        read(stage, k, minus, dy, e, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           db[k].p[j] = add2(db[k].p[j], dy.p[j]);
@@ -685,11 +797,11 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     float a = sum_of(s1), b = sum_of(s2);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) a += __shfl_xor_sync(0xffffffffu, a, o), b += __shfl_xor_sync(0xffffffffu, b, o);
-    if (lane == 0) part[flip][warp] = make_float2(a, b * n.r);
+    if (lane == 0) parts[flip][first_warp + warp] = make_float2(a, b * n.r);
   };
-  auto output = [&](const Known& n, int64_t row, int stage, int flip) {
+  auto output = [&](const Known& n, uint32_t row, int stage, int flip) {
     const uint64_t minus = pair_of(n.m, n.m), rstd = pair_of(n.r, n.r);
-    float2 s = part[flip][lane < warps ? lane : 0];
+    float2 s = parts[flip][first_warp + (lane < warps ? lane : 0)];
     if (lane >= warps) s = make_float2(0.f, 0.f);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) s.x += __shfl_xor_sync(0xffffffffu, s.x, o), s.y += __shfl_xor_sync(0xffffffffu, s.y, o);
@@ -699,7 +811,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     for (int k = 0; k < NV; ++k) {
       if (in(k)) {
         Eight dy, e, w, d;
-        read(n, stage, k, minus, dy, e, w);
+        read(stage, k, minus, dy, e, w);
         if constexpr (HAS_DH) wide(HT == kH32, stage, k * PER + 1 + HP, d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -709,36 +821,36 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
           else
             d.p[j] = mul2(t, rstd);
         }
-        store8(HT == kH32, p.dx, row * p.hidden + i0 + k * step, d);
+        store_row8<MODE>(HT == kH32, p.dx, (int64_t)row * p.hidden, i0 + k * step, p.hidden, d);
       }
     }
   };
   Known now, then;
-  known(blockIdx.x, now);
+  known(unit, now);
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) fetch(s);
   int stage = 0, flip = 0;
   auto after = [](int s) { return s + 1 == STAGES ? 0 : s + 1; };
   if (PIPE) {
-    known((int64_t)blockIdx.x + gridDim.x, then);
+    known(unit + units, then);
     copies_wait<STAGES - 1>();
-    if (blockIdx.x < p.rows) sums(now, 0, 0);
-    __syncthreads();
+    if (unit < rows) sums(now, 0, 0);
+    group_sync();
   }
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
+  for (uint32_t row = unit; row < rows; row += units, flip ^= 1) {
     if constexpr (PIPE) {
       copies_wait<STAGES - 2>();
-      if (row + gridDim.x < p.rows) sums(then, after(stage), flip ^ 1);
+      if (row + units < rows) sums(then, after(stage), flip ^ 1);
       output(now, row, stage, flip);
       now = then;
-      known(row + 2 * (int64_t)gridDim.x, then);
+      known(row + 2 * units, then);
       fetch(stage);
-      __syncthreads();
+      group_sync();
     } else {
-      known(row + gridDim.x, then);
+      known(row + units, then);
       copies_wait<STAGES - 1>();
       sums(now, stage, flip);
-      __syncthreads();
+      group_sync();
       output(now, row, stage, flip);
       now = then;
       fetch(stage);
@@ -746,13 +858,28 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     stage = after(stage);
   }
   copies_wait<0>();
-  if (p.partial) {
+  if (!p.partial) return;
+  // the groups' gradients side by side in shared memory, added up in their order to one row of `partial` for the block
+  __syncthreads();
+  float* const hand = reinterpret_cast<float*>(smem);
+  const int both = 2 * p.hidden;
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (in(k)) {
-        store8(true, p.partial, (int64_t)blockIdx.x * p.hidden + i0 + k * step, dw[k]);
-        store8(true, p.partial, (int64_t)(gridDim.x + blockIdx.x) * p.hidden + i0 + k * step, db[k]);
-      }
+  for (int k = 0; k < NV; ++k)
+    if (in(k)) {
+      float* to = hand + threadIdx.y * both + i0 + k * step;
+      float a[8], b[8];
+      dw[k].to_floats(a), db[k].to_floats(b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (MODE != kEdges || (i0 + k * step + j >= 0 && i0 + k * step + j < p.hidden)) to[j] = a[j], to[p.hidden + j] = b[j];
+    }
+  __syncthreads();
+  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < both; c += blockDim.x * blockDim.y) {
+    float v = hand[c];
+    for (int g = 1; g < blockDim.y; ++g) v += hand[g * both + c];
+    // (weight rows first, then the bias's)
+    const int64_t at = c < p.hidden ? blockIdx.x : gridDim.x + blockIdx.x;
+    p.partial[at * p.hidden + (c < p.hidden ? c : c - p.hidden)] = v;
   }
 }
 
@@ -903,19 +1030,31 @@ int grad_blocks(int64_t rows, int sms, int64_t most) {
   return (int)(rows < n ? rows : n);
 }
 
+// vec, dense: as in the forward.
 template <int HT, bool HAS_DH>
-int run_grad(const GradArgs& p, bool vec, int sms, cudaStream_t s) {
-  const int n = p.hidden / 8;
+int run_grad(const GradArgs& p, bool vec, bool dense, int sms, cudaStream_t s) {
+  const int n = row_vectors(p.hidden, vec);
   int blocks, rc;
-  if (vec && n <= 2048 && grad_parts<HT, HAS_DH>() * 16 * grad_stages<HT, HAS_DH>() * stream_threads(n) <= kStreamBytes) {
-    int threads, bytes;
-    auto* kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, false>;
+  // (2047 x 5003 element by element: 45 us)
+  const bool edges = HT != kH8 && !vec && dense && p.rows >= 8 && n >= 64;
+  if ((vec || edges) && n <= 2048 && grad_bytes<HT, HAS_DH>() * stream_threads(n) <= kStreamBytes) {
+    auto* kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, kVectors>;
     if constexpr (HT != kH32)
-      if (p.hidden % (32 * 8 * kStreamVecs) == 0) kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, true>;
-    rc = stream_shape(kernel, p.hidden, grad_parts<HT, HAS_DH>(), grad_stages<HT, HAS_DH>(), sms, p.rows, &threads, &blocks, &bytes);
-    if (rc != DG_OK) return rc;
-    blocks = grad_blocks(p.rows, sms, (int64_t)sms * (kStreamThreads / threads));
-    rc = dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);
+      if (p.hidden % (32 * 8 * kStreamVecs) == 0) kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, kFull>;
+    if constexpr (HT != kH8)
+      if (!vec) kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, kEdges>;
+    DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes));
+    const int threads = stream_threads(n), bytes = grad_bytes<HT, HAS_DH>() * threads;
+    // groups of threads, each with rows of its own, that fill an SM, and one block to an SM: its groups add their
+    // weight gradients up, so that fewer partial rows go through memory (4096 x 1024: 1024 blocks of one warp
+    // took 17.6 us, most of it there)
+    const int most = kStreamThreads / threads < kStreamBytes / bytes ? kStreamThreads / threads : kStreamBytes / bytes;
+    const int64_t want = (p.rows + sms - 1) / sms;
+    const int groups = (int)(want < most ? want : most);
+    const int64_t n_blocks = (p.rows + groups - 1) / groups;
+    blocks = (int)(n_blocks < sms ? n_blocks : sms);
+    if (!vec) blocks = blocks / 8 * 8;  // (eight rows at least: a group's rows start at the same place in a vector)
+    rc = dgl::launch(kernel, dim3(blocks), dim3(threads, groups), bytes * groups, s, p);
   } else {
     const bool small = HT != kH8 && p.hidden <= 1024, regs = HT != kH8 && p.hidden <= 8192;
     const int threads = small ? round32((p.hidden + 3) / 4) : regs ? round32((p.hidden + 15) / 16) : 1024;
@@ -988,10 +1127,12 @@ extern "C" int dg_layer_layer_norm(const void* x, int64_t ld_x, int x_type, cons
   p.affine = Affine{weight, bias, weight && weight_type == DG_TYPE_F32, bias && bias_type == DG_TYPE_F32};
   p.ld_x = ld_x, p.ld_residual = ld_residual, p.ld_sum = ld_sum, p.rows = rows;
   p.hidden = (int)hidden, p.x_f32 = x_type == DG_TYPE_F32, p.r_f32 = residual_type == DG_TYPE_F32, p.eps = eps;
+  const bool dense = like_dense(x, ld_x, hidden) && like_dense(residual, ld_residual, hidden) && like_dense(sum_out, ld_sum, hidden) &&
+                     aligned16(y);
   const int rp = !residual ? 0 : residual_type == DG_TYPE_F32 ? 2 : 1;
   if (x_type == DG_TYPE_F32)
-    return rp == 0 ? run_out<2, 0>(p, vec, sms, s) : rp == 1 ? run_out<2, 1>(p, vec, sms, s) : run_out<2, 2>(p, vec, sms, s);
-  return rp == 0 ? run_out<1, 0>(p, vec, sms, s) : rp == 1 ? run_out<1, 1>(p, vec, sms, s) : run_out<1, 2>(p, vec, sms, s);
+    return rp == 0 ? run_out<2, 0>(p, vec, dense, sms, s) : rp == 1 ? run_out<2, 1>(p, vec, dense, sms, s) : run_out<2, 2>(p, vec, dense, sms, s);
+  return rp == 0 ? run_out<1, 0>(p, vec, dense, sms, s) : rp == 1 ? run_out<1, 1>(p, vec, dense, sms, s) : run_out<1, 2>(p, vec, dense, sms, s);
 }
 
 extern "C" size_t dg_layer_layer_norm_backward_workspace(int64_t rows, int64_t hidden) {
@@ -1033,7 +1174,8 @@ extern "C" int dg_layer_layer_norm_backward(const void* dy, int64_t ld_dy, const
   p.partial = sums ? static_cast<float*>(workspace) : nullptr;
   p.ld_dy = ld_dy, p.ld_h = ld_h, p.ld_dh = ld_dh, p.rows = rows, p.hidden = (int)hidden;
   p.e5m2 = h_type == DG_TYPE_E5M2, p.w_f32 = weight_type == DG_TYPE_F32, p.b_f32 = dbias_type == DG_TYPE_F32;
-  if (h8) return dh ? run_grad<kH8, true>(p, vec, sms, s) : run_grad<kH8, false>(p, vec, sms, s);
-  if (h_type == DG_TYPE_F32) return dh ? run_grad<kH32, true>(p, vec, sms, s) : run_grad<kH32, false>(p, vec, sms, s);
-  return dh ? run_grad<kH16, true>(p, vec, sms, s) : run_grad<kH16, false>(p, vec, sms, s);
+  const bool dense = like_dense(dy, ld_dy, hidden) && like_dense(h, ld_h, hidden) && like_dense(dh, ld_dh, hidden) && aligned16(dx);
+  if (h8) return dh ? run_grad<kH8, true>(p, vec, false, sms, s) : run_grad<kH8, false>(p, vec, false, sms, s);
+  if (h_type == DG_TYPE_F32) return dh ? run_grad<kH32, true>(p, vec, dense, sms, s) : run_grad<kH32, false>(p, vec, dense, sms, s);
+  return dh ? run_grad<kH16, true>(p, vec, dense, sms, s) : run_grad<kH16, false>(p, vec, dense, sms, s);
 }

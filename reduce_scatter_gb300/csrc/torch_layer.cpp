@@ -312,11 +312,8 @@ int64_t whole(PyObject* o, const char* what) {
   return v;
 }
 
-// Scales of a rows x cols matrix: those of neighbouring rows lie next to each other.
-Tensor fresh_scales(const Tensor& like, int64_t rows, int64_t cols) {
-  const int64_t blocks = (cols + 127) / 128;
-  return at::detail::empty_strided_cuda({rows, blocks}, {1, rows > 0 ? rows : 1}, at::kFloat, like.device());
-}
+// Scales of a matrix: those of a row of blocks lie next to each other, as a row's are written and read.
+Tensor fresh_scales(const Tensor& like, int64_t rows, int64_t cols) { return fresh(like, {rows, (cols + 127) / 128}, at::kFloat); }
 
 PyObject* quantize_block8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {

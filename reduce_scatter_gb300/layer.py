@@ -296,9 +296,7 @@ def mx4_matmul(a: MX4Tensor, b: MX4Tensor, *, out_dtype: torch.dtype = torch.bfl
 class Block8Tensor(NamedTuple):
     """A matrix in 8 bits with a scale for each block of 128: ``values`` (rows,
     cols), contiguous, float8_e4m3fn or float8_e5m2; ``scales`` float32
-    (ceil(rows / block_rows), ceil(cols / 128)), of any strides (those that
-    :func:`quantize_block8` makes have neighbouring rows next to each other);
-    ``block_rows``: 1 or 128, the rows that share a scale.  Stands for
+    (ceil(rows / block_rows), ceil(cols / 128)), of any strides; ``block_rows``: 1 or 128, the rows that share a scale.  Stands for
     ``values * scales``, each scale over its block."""
 
     values: torch.Tensor

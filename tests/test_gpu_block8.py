@@ -176,7 +176,7 @@ def test_product_of_special_values():
 def test_scales_of_any_strides_and_views():
     a, b = ops.quantize_block8(rand((70, 400), 16)), ops.quantize_block8(rand((136, 400), 17), block_rows=128)
     want = ops.block8_matmul(a, b)
-    rows = ops.Block8Tensor(a.values, a.scales.contiguous(), 1)
+    rows = ops.Block8Tensor(a.values, a.scales.t().contiguous().t(), 1)
     wide = torch.full((4, 9), float("nan"), device="cuda")
     wide[::2, 1::2] = b.scales
     assert torch.equal(ops.block8_matmul(rows, ops.Block8Tensor(b.values, wide[::2, 1::2], 128)), want)

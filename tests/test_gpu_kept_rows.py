@@ -75,7 +75,7 @@ def test_strides_and_both_gradients():
     plain = ops.dequantize_block8(kept)
     wA, wB = ops.grouped_matmul_backward(dd, plain, W.transpose(1, 2), cuda_ends(ends))
     assert torch.equal(dA, wA) and torch.equal(dB, wB)
-    rows = ops.Block8Tensor(kept.values, kept.scales.contiguous(), 1)
+    rows = ops.Block8Tensor(kept.values, kept.scales.t().contiguous().t(), 1)
     assert torch.equal(ops.grouped_matmul_backward(dd, rows, W.transpose(1, 2), cuda_ends(ends), need=(False, True))[1], wB)
     only, none = ops.grouped_matmul_backward(dd, None, W.transpose(1, 2), cuda_ends(ends), need=(True, False))
     assert torch.equal(only, wA) and none is None

@@ -22,6 +22,8 @@ EPS = 1e-5
 # one warp per row; register kernels of 1, 2 and 8 vectors; streamed rows; the looping kernel; odd sizes element-wise
 SIZES = [(1, 8), (5, 128), (1, 1), (3, 33), (7, 1000), (2, 1001), (700, 2048), (3, 4099), (2, 8192), (700, 8208), (1, 16384),
          (400, 16384), (2, 24576), (1, 32784), (1, 16387), (1, 40001), (330, 2064)]
+# many rows that start and end inside vectors: streamed
+ODD = [(700, 1001), (331, 4099), (500, 777), (310, 16369), (320, 8190), (400, 502)]
 
 
 def inputs(rows, hidden, seed, xt=BF16, rt=None, wt=BF16):
@@ -69,7 +71,7 @@ def check_blocks(q, y, e_y, dtype):
     assert_within(q.values.float(), v, step / 2 * (1 + 4 * U32) + slack * 1.25, "values")  # (a step may grow within the slack)
 
 
-@pytest.mark.parametrize("rows,hidden", SIZES)
+@pytest.mark.parametrize("rows,hidden", SIZES + ODD)
 @pytest.mark.parametrize("xt,rt", [(BF16, None), (BF16, BF16), (BF16, F32), (F32, None), (F32, F32), (F32, BF16)])
 def test_16_bit_output(rows, hidden, xt, rt):
     x, r, w, b = inputs(rows, hidden, 1, xt, rt, F32 if rows == 7 or hidden == 8208 else BF16)
@@ -169,6 +171,25 @@ def test_strides_shapes_and_streams():
     assert none.y.shape == (2, 6, 0) and torch.isnan(none.rstd).all()
 
 
+def test_odd_rows_in_wider_ones():
+    # rows that start where densely packed ones would, in a wider matrix; neighbours that are not finite stay out
+    wide = torch.full((400, 1009), float("nan"), device="cuda", dtype=BF16)
+    x = wide[:, :1001]
+    x.copy_(rand((400, 1001), 48))
+    w, b, r = rand((1001,), 49), rand((1001,), 50), rand((400, 1001), 51)
+    got, want = ops.layer_norm(x, w, b, residual=r, keep_stats=True), ops.layer_norm(x.contiguous(), w, b, residual=r, keep_stats=True)
+    assert torch.equal(got.y, want.y) and torch.equal(got.residual, want.residual) and torch.equal(got.mean, want.mean)
+    f = ops.layer_norm(x, w, b, keep_stats=True)
+    dwide = torch.full((400, 1009), float("inf"), device="cuda", dtype=BF16)
+    dy = dwide[:, :1001]
+    dy.copy_(rand((400, 1001), 52))
+    for one, two in zip(ops.layer_norm_backward(dy, x, w, f.mean, f.rstd), ops.layer_norm_backward(dy.contiguous(), x.contiguous(), w, f.mean, f.rstd)):
+        assert torch.equal(one, two) and torch.isfinite(one).all()
+    off = rand((400 * 1001 + 1,), 53)[1:].view(400, 1001)  # (a start off 16 bytes)
+    _, _, _, y, _, _, e_y = norm64(off, None, w, b)
+    assert_within(ops.layer_norm(off, w, b).y, y, e_y + U16 * (y.abs() + e_y), "y")
+
+
 # ----------------------------------------------------------------- gradient
 
 
@@ -202,7 +223,7 @@ def check_grad(got, want, w16, b16):
         assert_within(got[2], db, e_db + (U16 * (db.abs() + e_db) if b16 else U32 * db.abs()), "db")
 
 
-@pytest.mark.parametrize("rows,hidden", SIZES + [(1300, 512), (20, 8195), (9, 16390)])
+@pytest.mark.parametrize("rows,hidden", SIZES + ODD + [(1300, 512), (20, 8195), (9, 16390), (8, 510), (1500, 1023)])
 @pytest.mark.parametrize("ht", [BF16, F32])
 @pytest.mark.parametrize("has_dh", [False, True])
 def test_gradient(rows, hidden, ht, has_dh):
@@ -227,7 +248,7 @@ def test_gradient_from_kept_rows(rows, hidden, dtype, has_dh):
     values = ops.dequantize_block8(f.kept, out_dtype=F32)
     check_grad(got, grad64(dy, values.double(), f.mean, f.rstd, w, dh, True), True, True)
     scaled = ops.quantize_block8(x, dtype=dtype)            # scales that are no powers of two, rows next to each other or not
-    for scales in (scaled.scales, scaled.scales.contiguous()):
+    for scales in (scaled.scales, scaled.scales.t().contiguous().t()):
         q = ops.Block8Tensor(scaled.values, scales, 1)
         got = ops.layer_norm_backward(dy, q, w, f.mean, f.rstd, d_residual=dh)
         want = grad64(dy, q.values.float().double() * spread(scales.double(), 1, rows, hidden), f.mean, f.rstd, w, dh, True)

@@ -20,6 +20,7 @@
 
 #include <cuda_bf16.h>
 
+#include "block8_few.h"
 #include "launch.cuh"
 #include "pairs.cuh"
 #include "ptx.cuh"
@@ -82,22 +83,6 @@ __device__ __forceinline__ void store_box(const CUtensorMap* map, uint32_t src, 
 template <int N>
 __device__ __forceinline__ void stores_read() {
   asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
-}
-
-// Whether this warp is the last of the `ways` whose partial sums make up its box
-// of a cut tile.  Four warps share a word, 8 bits each, which the last one
-// takes back to 0.
-__device__ __forceinline__ bool warp_last(uint32_t* word, int field, int ways, int lane) {
-  __threadfence();
-  __syncwarp();
-  int last = 0;
-  if (lane == 0) {
-    last = ((atomicAdd(word, 1u << (8 * field)) >> (8 * field)) & 255u) == (uint32_t)ways - 1;
-    if (last) atomicSub(word, (uint32_t)ways << (8 * field));
-  }
-  last = __shfl_sync(0xffffffffu, last, 0);
-  if (last) __threadfence();
-  return last != 0;
 }
 
 // COLS: b has a scale for each row (1 x 128).
@@ -386,9 +371,14 @@ extern "C" int dg_layer_block8_matmul(const void* a, int a_type, const float* a_
   const int64_t tiles = ((M + kTile - 1) / kTile) * ((N + kTile - 1) / kTile);
   if (tiles > INT32_MAX) return fail(DG_ERR_ARG, "M x N is too large (%lld tiles)", (long long)tiles);
   Args p{};
+  const bool f32 = d_type == DG_TYPE_F32;
+  if (M <= kFewRows && !trans_a) {  // (8 rows of 8192 x 28672: 62 us here)
+    const FewRows f{a, b, a_type, b_type, !trans_b, a_scales, b_scales, sa_row, sa_block, trans_b ? sb_row : sb_block,
+                    trans_b ? sb_block : sb_row, a_block_rows == 128 ? 7 : 0, b_block_rows == 128 ? 7 : 0, D, f32, M, N, K, workspace, status};
+    return block8_few(f, stream);
+  }
   if (int rc = operand(&p.a, a, trans_a, M, K, sa_row, sa_block, a_block_rows, &p.sa_m, &p.sa_k, &p.a_shift)) return rc;
   if (int rc = operand(&p.b, b, !trans_b, N, K, sb_row, sb_block, b_block_rows, &p.sb_n, &p.sb_k, &p.b_shift)) return rc;
-  const bool f32 = d_type == DG_TYPE_F32;
   const int64_t dd[2] = {N, M}, dp[1] = {N};
   if (int rc = encode_map(&p.d, D, f32 ? 4 : 2, 2, dd, dp, 32)) return rc;
   p.rows = (int)M, p.cols = (int)N, p.kblocks = (int)((K + kBlockK - 1) / kBlockK), p.row_tiles = (int)((M + kTile - 1) / kTile);

@@ -467,6 +467,22 @@ __device__ __forceinline__ bool cut_last(uint32_t* counter, int ways, volatile u
   return last;
 }
 
+// Whether this warp is the last of the `ways` whose partial sums make up its box
+// of a cut tile.  Four warps share a word, 8 bits each, which the last one
+// takes back to 0.
+__device__ __forceinline__ bool warp_last(uint32_t* word, int field, int ways, int lane) {
+  __threadfence();
+  __syncwarp();
+  int last = 0;
+  if (lane == 0) {
+    last = ((atomicAdd(word, 1u << (8 * field)) >> (8 * field)) & 255u) == (uint32_t)ways - 1;
+    if (last) atomicSub(word, (uint32_t)ways << (8 * field));
+  }
+  last = __shfl_sync(0xffffffffu, last, 0);
+  if (last) __threadfence();
+  return last != 0;
+}
+
 // ------------------------------------------------------------ epilogue stores
 
 // A warp's box of 32 features x 32 rows from registers (v[i]: row i, this

@@ -312,8 +312,13 @@ int64_t whole(PyObject* o, const char* what) {
   return v;
 }
 
-// Scales of a matrix: those of a row of blocks lie next to each other, as a row's are written and read.
-Tensor fresh_scales(const Tensor& like, int64_t rows, int64_t cols) { return fresh(like, {rows, (cols + 127) / 128}, at::kFloat); }
+// Scales of a matrix for a product: those of neighbouring rows lie next to each
+// other, as its threads, a row each, read them (by_row: those of a row, as a norm's do).
+Tensor fresh_scales(const Tensor& like, int64_t rows, int64_t cols, bool by_row = false) {
+  const int64_t blocks = (cols + 127) / 128;
+  if (by_row) return fresh(like, {rows, blocks}, at::kFloat);
+  return at::detail::empty_strided_cuda({rows, blocks}, {1, rows > 0 ? rows : 1}, at::kFloat, like.device());
+}
 
 PyObject* quantize_block8(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded([&]() -> PyObject* {
@@ -695,7 +700,7 @@ PyObject* layer_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::IntArrayRef lead = x.sizes().slice(0, x.dim() - 1);
     Tensor y = out8 ? fresh(x, {rows, hidden}, out) : fresh(x, x.sizes(), out), ys, kept, ks, mean, rstd, h;
     if (out8) ys = fresh_scales(x, rows, hidden);
-    if (keep) kept = fresh(x, {rows, hidden}, kept_type), ks = fresh_scales(x, rows, hidden);
+    if (keep) kept = fresh(x, {rows, hidden}, kept_type), ks = fresh_scales(x, rows, hidden, true);
     if (keep_stats) mean = fresh(x, lead, at::kFloat), rstd = fresh(x, lead, at::kFloat);
     if (residual.defined()) h = fresh(x, x.sizes(), residual.scalar_type());
     auto stride = [](const Tensor& t, int d) { return t.defined() ? t.stride(d) : 0; };

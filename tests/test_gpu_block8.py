@@ -146,6 +146,20 @@ def test_product(m, n, k, abr, bbr):
     ops.check_products()
 
 
+@pytest.mark.parametrize("m,n,k", [(1, 256, 4096), (16, 8, 128), (17, 264, 272), (33, 520, 8192), (48, 2048, 1040), (65, 13312, 2064),
+                                   (96, 128, 28672), (127, 3328, 4112), (128, 1032, 128), (128, 20000, 512)])
+@pytest.mark.parametrize("abr,bbr,tb", [(1, 128, True), (1, 1, True), (128, 128, False), (128, 1, True), (1, 128, False)])
+def test_product_of_few_rows(m, n, k, abr, bbr, tb):
+    if not tb:
+        n = (n + 15) // 16 * 16
+    a = ops.quantize_block8(rand((m, k), 30) * torch.exp(rand((m, 1), 31)), block_rows=abr, dtype=E5M2 if m == 33 else E4M3)
+    b = ops.quantize_block8(rand((n, k) if tb else (k, n), 32) * torch.exp(rand((n if tb else k, 1), 33)), block_rows=bbr)
+    first = check_product(a, b, False, tb, BF16)
+    check_product(a, b, False, tb, F32)
+    assert torch.equal(first, ops.block8_matmul(a, b, trans_b=tb))
+    ops.check_products()
+
+
 @pytest.mark.parametrize("m,n,k", [(16, 16, 16), (128, 256, 128), (272, 528, 1000), (1024, 304, 130), (400, 2048, 8192), (2064, 784, 528)])
 @pytest.mark.parametrize("ta,tb", [(True, True), (False, False), (True, False)])
 def test_product_of_transposes(m, n, k, ta, tb):

@@ -92,7 +92,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
   fence_after();
   const uint32_t tmem = *s_tmem, base = smem_u32(smem);
   const int total = (p.feats + kPairFeats - 1) / kPairFeats;
-  const Cut cut = cut_of(total, units, p.per_unit, p.kblocks, (float)p.rows * (float)total);
+  // (leaving and joining sums costs about 20 K blocks, as for a step of rows elsewhere: 96x2048x8192 31.6 us uncut)
+  const Cut cut = cut_of(total, units, p.per_unit, p.kblocks, (float)kChunk * (float)total);
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0;

@@ -113,7 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
   fence_after();
   const uint32_t tmem = *s_tmem, base = smem_u32(smem);
   const int total = p.row_tiles * p.raster.nf;
-  const Cut cut = cut_of(total, units, p.per_unit, p.kblocks, (float)p.rows * (float)p.raster.nf);
+  // (leaving and joining a tile's sums costs about 20 of its K blocks, which are slow ones)
+  const Cut cut = cut_of(total, units, p.per_unit, p.kblocks, (float)kChunk * (float)total);
 
   if (warp == 0) {
     uint32_t stage = 0, phase = 0;

@@ -15,7 +15,7 @@ struct QuantArgs {
   uint8_t* values;
   float* scales;
   int64_t ld_x, rows, cols, s_row, s_block;  // scales' strides: from row (or row block) to row, from column block to column block
-  int e5m2, pow2;
+  int e5m2;
 };
 
 // 16 values of a thread.
@@ -31,40 +31,58 @@ struct Raw16 {
 #pragma unroll
     for (int k = 0; k < (F32 ? 4 : 2); ++k) u[k] = make_uint4(0, 0, 0, 0);
   }
-  __device__ __forceinline__ void get(int half, float (&v)[8]) const {
-    if constexpr (F32) {
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        const uint4 a = u[2 * half + k];
-        v[4 * k] = __uint_as_float(a.x), v[4 * k + 1] = __uint_as_float(a.y);
-        v[4 * k + 2] = __uint_as_float(a.z), v[4 * k + 3] = __uint_as_float(a.w);
-      }
-    } else {
-      unpack8(u[half], v);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) v[k] = block_value(v[k]);
+  __device__ __forceinline__ void get(int half, Eight& v) const {
+    if constexpr (F32)
+      v.from_f32(u[2 * half], u[2 * half + 1]);
+    else
+      v.from_bf16(u[half]);
   }
+  // The largest magnitude, past NaN (an infinity is seen).
   __device__ __forceinline__ float top() const {
-    float m = 0.f;
+    if constexpr (F32) {
+      float m = 0.f;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float v[8];
-      get(h, v);
+      for (int h = 0; h < 2; ++h) {
+        Eight e;
+        float v[8];
+        get(h, e);
+        e.to_floats(v);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
+        for (int k = 0; k < 8; ++k) m = fmaxf(m, fabsf(v[k]));
+      }
+      return m;
+    } else {  // (two values at a time)
+      const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+      uint32_t m = 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) asm("max.bf16x2 %0, %0, %1;" : "+r"(m) : "r"(w[k] & 0x7fff7fffu));
+      return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
     }
-    return m;
   }
-  __device__ __forceinline__ uint4 quantize(const Quantizer& q, __nv_fp8_interpretation_t fmt) const {
+  // Infinities as NaN, so that they do not enter the block's scale.
+  __device__ __forceinline__ void drop_infinities() {
+    auto word = [](uint32_t& w) {
+      if constexpr (F32) {
+        if ((w & 0x7fffffffu) == 0x7f800000u) w |= 0x400000u;
+      } else {
+        if ((w & 0x7fffu) == 0x7f80u) w |= 0x40u;
+        if ((w & 0x7fff0000u) == 0x7f800000u) w |= 0x400000u;
+      }
+    };
+#pragma unroll
+    for (int k = 0; k < (F32 ? 4 : 2); ++k) word(u[k].x), word(u[k].y), word(u[k].z), word(u[k].w);
+  }
+  template <bool POW2>
+  __device__ __forceinline__ uint4 quantize(const Quantizer& q, bool e5m2) const {
     uint2 w[2];
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
+      Eight e;
       float v[8];
-      get(h, v);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[k] = q(v[k]);
-      w[h] = pack_fp8(v, fmt);
+      get(h, e);
+      q.template all<POW2>(e);
+      e.to_floats(v);
+      w[h] = e5m2 ? pack_fp8(v, __NV_E5M2) : pack_fp8(v, __NV_E4M3);
     }
     return make_uint4(w[0].x, w[0].y, w[1].x, w[1].y);
   }
@@ -73,12 +91,11 @@ struct Raw16 {
 // Blocks of 1 x 128: eight threads to a block, a warp to 512 columns of a row;
 // each warp takes kRowsEach rows, whose loads are in flight together.
 constexpr int kQuantWarps = 8, kRowsEach = 4;
-template <bool F32>
+template <bool F32, bool POW2>
 __global__ void __launch_bounds__(32 * kQuantWarps) block8_rows_kernel(const __grid_constant__ QuantArgs p) {
   begin_kernel();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int64_t row0 = (int64_t)blockIdx.x * (kQuantWarps * kRowsEach) + warp;
-  const __nv_fp8_interpretation_t fmt = p.e5m2 ? __NV_E5M2 : __NV_E4M3;
   for (int64_t seg = blockIdx.y; seg * 512 < p.cols; seg += gridDim.y) {
     const int64_t col = seg * 512 + lane * 16;
     Raw16<F32> x[kRowsEach];
@@ -93,12 +110,20 @@ __global__ void __launch_bounds__(32 * kQuantWarps) block8_rows_kernel(const __g
 #pragma unroll
     for (int k = 0; k < kRowsEach; ++k) {
       const int64_t row = row0 + k * kQuantWarps;
-      float m = x[k].top();
+      auto block_top = [&]() {
+        float m = x[k].top();
 #pragma unroll
-      for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-      const Quantizer q(m, p.e5m2 != 0, p.pow2 != 0);
+        for (int o = 4; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        return m;
+      };
+      float m = block_top();
+      if (__any_sync(0xffffffffu, isinf(m))) {
+        x[k].drop_infinities();
+        m = block_top();
+      }
+      const Quantizer q(m, p.e5m2 != 0, POW2);
       if (row < p.rows && col < p.cols) {
-        *reinterpret_cast<uint4*>(p.values + row * p.cols + col) = x[k].quantize(q, fmt);
+        *reinterpret_cast<uint4*>(p.values + row * p.cols + col) = x[k].template quantize<POW2>(q, p.e5m2 != 0);
         if ((lane & 7) == 0) p.scales[row * p.s_row + (col / 128) * p.s_block] = q.c;
       }
     }
@@ -106,11 +131,10 @@ __global__ void __launch_bounds__(32 * kQuantWarps) block8_rows_kernel(const __g
 }
 
 // Blocks of 128 x 128: a thread block each.
-template <bool F32>
+template <bool F32, bool POW2>
 __global__ void __launch_bounds__(256) block8_tiles_kernel(const __grid_constant__ QuantArgs p) {
   __shared__ float part[8];
   begin_kernel();
-  const __nv_fp8_interpretation_t fmt = p.e5m2 ? __NV_E5M2 : __NV_E4M3;
   const int64_t row0 = (int64_t)blockIdx.x * 128 + (threadIdx.x >> 3);
   for (int64_t blk = blockIdx.y; blk * 128 < p.cols; blk += gridDim.y) {
     const int64_t col = blk * 128 + (threadIdx.x & 7) * 16;
@@ -123,21 +147,30 @@ __global__ void __launch_bounds__(256) block8_tiles_kernel(const __grid_constant
       else
         x[k].zero();
     }
+    auto block_top = [&]() {  // (the barrier before it: the last one's partials have been read)
+      m = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) m = fmaxf(m, x[k].top());
+      for (int k = 0; k < 4; ++k) m = fmaxf(m, x[k].top());
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
-    __syncthreads();
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      __syncthreads();
+      if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = m;
+      __syncthreads();
 #pragma unroll
-    for (int k = 0; k < 8; ++k) m = fmaxf(m, part[k]);
-    __syncthreads();  // (the next block's partials)
-    const Quantizer q(m, p.e5m2 != 0, p.pow2 != 0);
+      for (int k = 0; k < 8; ++k) m = fmaxf(m, part[k]);
+    };
+    block_top();
+    if (isinf(m)) {  // (all threads have the same)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k].drop_infinities();
+      block_top();
+    }
+    const Quantizer q(m, p.e5m2 != 0, POW2);
     if (threadIdx.x == 0) p.scales[blockIdx.x * p.s_row + blk * p.s_block] = q.c;
 #pragma unroll
     for (int k = 0; k < 4; ++k)
       if (row0 + 32 * k < p.rows && col < p.cols)
-        *reinterpret_cast<uint4*>(p.values + (row0 + 32 * k) * p.cols + col) = x[k].quantize(q, fmt);
+        *reinterpret_cast<uint4*>(p.values + (row0 + 32 * k) * p.cols + col) = x[k].template quantize<POW2>(q, p.e5m2 != 0);
   }
 }
 
@@ -211,12 +244,14 @@ extern "C" int dg_layer_block8_quantize(const void* x, int64_t ld_x, int x_type,
   if (!x || !values || !scales) return fail(DG_ERR_ARG, "x, values and scales must not be null");
   const bool f32 = x_type == DG_TYPE_F32;
   if (!aligned16(values) || !rows16(x, ld_x, f32 ? 4 : 2)) return fail(DG_ERR_ARG, "x, its pitch and values must be multiples of 16 bytes");
-  const QuantArgs p{x, static_cast<uint8_t*>(values), scales, ld_x, rows, cols, s_row, s_block, type == DG_TYPE_E5M2, pow2 != 0};
+  const QuantArgs p{x, static_cast<uint8_t*>(values), scales, ld_x, rows, cols, s_row, s_block, type == DG_TYPE_E5M2};
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (block_rows == 1)
-    return dgl::launch(f32 ? block8_rows_kernel<true> : block8_rows_kernel<false>, grid_of(rows, kQuantWarps * kRowsEach, cols, 512),
+    return dgl::launch(f32 ? (pow2 ? block8_rows_kernel<true, true> : block8_rows_kernel<true, false>)
+                           : (pow2 ? block8_rows_kernel<false, true> : block8_rows_kernel<false, false>), grid_of(rows, kQuantWarps * kRowsEach, cols, 512),
                        dim3(32 * kQuantWarps), 0, s, p);
-  return dgl::launch(f32 ? block8_tiles_kernel<true> : block8_tiles_kernel<false>, grid_of(rows, 128, cols, 128), dim3(256), 0, s, p);
+  return dgl::launch(f32 ? (pow2 ? block8_tiles_kernel<true, true> : block8_tiles_kernel<true, false>)
+                         : (pow2 ? block8_tiles_kernel<false, true> : block8_tiles_kernel<false, false>), grid_of(rows, 128, cols, 128), dim3(256), 0, s, p);
 }
 
 extern "C" int dg_layer_block8_dequantize(const void* values, int type, const float* scales, int64_t s_row, int64_t s_block,

@@ -54,6 +54,21 @@ struct Quantizer {
     const float t = x * num, q = t * rcp;
     return fmaf(fmaf(-den, q, t), rcp, q);
   }
+  // The same of eight values (POW2: den is 1).
+  template <bool POW2>
+  __device__ __forceinline__ void all(Eight& v) const {
+    const uint64_t n = pair_of(num, num), r = pair_of(rcp, rcp), d = pair_of(-den, -den);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t t = mul2(v.p[k], n);
+      if constexpr (POW2) {
+        v.p[k] = t;
+      } else {
+        const uint64_t q = mul2(t, r);
+        v.p[k] = fma2(fma2(d, q, t), r, q);
+      }
+    }
+  }
 };
 
 // x as it enters a block: an infinity as NaN.
@@ -67,9 +82,8 @@ __device__ __forceinline__ float block_max16(float m) {
 }
 
 // The same scale and one multiplier, for values that are themselves the result of
-// fp32 arithmetic, where nothing lies exactly halfway (or for powers of two,
-// where the product is exact): four roundings from x to the 8 bits' own, and a
-// handful of instructions a block instead of two divisions.
+// fp32 arithmetic, where nothing lies exactly halfway (or for powers of two, where
+// the product is exact): two roundings from x to the 8 bits' own.
 struct Multiplier {
   float c, mul;
   __device__ __forceinline__ Multiplier(float amax, bool e5m2, bool pow2) {
@@ -83,11 +97,16 @@ struct Multiplier {
       c = __uint_as_float((uint32_t)f << 23);
       mul = __uint_as_float((uint32_t)(254 - f) << 23);
     } else {
-      c = amax * (e5m2 ? 1.f / kE5M2Max : 1.f / kE4M3Max);
+      // quotients from reciprocals and their residuals (of a power of two less where a reciprocal would be subnormal)
+      const float top = e5m2 ? kE5M2Max : kE4M3Max, inv = e5m2 ? 1.f / kE5M2Max : 1.f / kE4M3Max, c0 = amax * inv;
+      c = fmaf(fmaf(-top, c0, amax), inv, c0);
       least = !(c > kMinScale);
-      float r;  // of amax without its exponent, so that neither it nor its reciprocal is subnormal
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(__uint_as_float((b & 0x7fffffu) | 0x3f800000u)));
-      mul = __uint_as_float((uint32_t)(254 + top_exp - e) << 23 | 0x600000u) * r;
+      const float a = __uint_as_float((b & 0x7fffffu) | 0x3f800000u), n = __uint_as_float((uint32_t)(254 + top_exp - e) << 23 | 0x600000u);
+      float r;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(a));
+      r = fmaf(fmaf(-a, r, 1.f), r, r);
+      const float q = n * r;
+      mul = fmaf(fmaf(-a, q, n), r, q);
     }
     if (least) c = kMinScale, mul = 0x1p126f;
     if (amax == 0.f) c = mul = 1.f;
@@ -163,6 +182,60 @@ __device__ __forceinline__ void store_blocks(const Blocks& o, bool pow2, int64_t
   v.to_floats(f);
   *reinterpret_cast<uint2*>(o.values + row * hidden + i) = o.e5m2 ? pack_fp8(f, __NV_E5M2) : pack_fp8(f, __NV_E4M3);
   if ((threadIdx.x & 15) == 0) o.scales[row * o.s_row + (int64_t)(i >> 7) * o.s_block] = by.c;
+}
+
+// The same of four vectors of each thread, `step` values apart.  The sixteen threads
+// of a half warp hold four blocks: they share out the largest magnitudes as they
+// reduce them (5 exchanges instead of 16), so that each finds one block's scale
+// and passes its multiplier on.
+__device__ __forceinline__ void store_blocks4(const Blocks& o, bool pow2, int64_t row, int hidden, int i0, int step, Eight (&v)[4]) {
+  const int lane = threadIdx.x & 31;
+  const bool odd = lane & 1, second = lane & 2;
+  const int block = (odd ? 2 : 0) + (second ? 1 : 0);  // this lane's
+  auto top = [&]() {
+    float m[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[8];
+      v[k].to_floats(f);
+      m[k] = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) m[k] = fmaxf(m[k], fabsf(f[j]));  // (passes over NaN)
+      if (i0 + k * step >= hidden) m[k] = 0.f;
+    }
+    const float a = fmaxf(odd ? m[2] : m[0], __shfl_xor_sync(0xffffffffu, odd ? m[0] : m[2], 1));
+    const float b = fmaxf(odd ? m[3] : m[1], __shfl_xor_sync(0xffffffffu, odd ? m[1] : m[3], 1));
+    float c = fmaxf(second ? b : a, __shfl_xor_sync(0xffffffffu, second ? a : b, 2));
+    c = fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 4));
+    return fmaxf(c, __shfl_xor_sync(0xffffffffu, c, 8));
+  };
+  float m = top();
+  if (__any_sync(0xffffffffu, isinf(m))) {  // an infinity does not enter the scale
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      float f[8];
+      v[k].to_floats(f);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) f[j] = block_value(f[j]);
+      v[k].from_floats(f);
+    }
+    m = top();
+  }
+  const Multiplier by(m, o.e5m2 != 0, pow2);
+  const int first = i0 - (lane & 15) * 8;  // of this half warp's first block
+  if ((lane & 15) < 4 && first + block * step < hidden)
+    o.scales[row * o.s_row + (int64_t)((first + block * step) >> 7) * o.s_block] = by.c;
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const float f = __shfl_sync(0xffffffffu, by.mul, (lane & 16) + ((k >> 1) | (k & 1) << 1));
+    const uint64_t mul = pair_of(f, f);
+    if (i0 + k * step >= hidden) continue;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[k].p[j] = mul2(v[k].p[j], mul);
+    float g[8];
+    v[k].to_floats(g);
+    *reinterpret_cast<uint2*>(o.values + row * hidden + i0 + k * step) = o.e5m2 ? pack_fp8(g, __NV_E5M2) : pack_fp8(g, __NV_E4M3);
+  }
 }
 
 inline bool is_fp8(int t) { return t == DG_TYPE_E4M3 || t == DG_TYPE_E5M2; }

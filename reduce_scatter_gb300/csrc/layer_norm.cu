@@ -180,10 +180,10 @@ __device__ __forceinline__ void load_row8(bool f32, const void* base, int i, int
 }
 
 // Vector i of a row's output, from h.
-template <bool OUT8, int MODE = kVectors>
+template <bool OUT8>
 __device__ __forceinline__ void finish(const Args& p, int64_t row, int i, bool in, const Moments& m, const Eight& h, const Eight& w,
                                        const Eight& b) {
-  if (MODE != kEdges && p.kept.values) store_blocks(p.kept, true, row, p.hidden, i, in, h);
+  if (p.kept.values) store_blocks(p.kept, true, row, p.hidden, i, in, h);
   const uint64_t minus = pair_of(-m.mean, -m.mean), rstd = pair_of(m.rstd, m.rstd);
   Eight y;
 #pragma unroll
@@ -191,7 +191,7 @@ __device__ __forceinline__ void finish(const Args& p, int64_t row, int i, bool i
   if constexpr (OUT8)
     store_blocks(p.y8, false, row, p.hidden, i, in, y);
   else if (in)
-    store_row8<MODE>(false, p.y, row * p.hidden, i, p.hidden, y);
+    store8(false, p.y, row * p.hidden + i, y);
 }
 
 // ------------------------------------------------------ a row in registers
@@ -244,6 +244,7 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) layer_norm_kernel(const _
 
 constexpr int kStreamVecs = 4;       // vectors of 8 values per thread
 constexpr int kStreamThreads = 512;  // per SM (128 registers each)
+constexpr int kSmBytes = 233472, kBlockBytes = 1024 + 1024;  // shared memory of an SM, and what a block takes besides
 constexpr int kStreamBytes = 231000;  // dynamic shared memory that the streamed kernels may take, whatever the call needs
 
 // XP, RP: 16-byte slots of eight values of x (1 bf16, 2 fp32) and of the
@@ -301,18 +302,20 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
     else
       v.from_bf16(*slots.at(stage, slot));
   };
-  // w and b in 16 bits stay in registers
-  uint4 w16[NV], b16[NV];
+  // w in 16 bits stays in registers, b behind the stages (both in registers left too few for a row's output)
+  auto bias_slot = [&](int k) { return slots.at(0, STAGES * NV * PER + k); };
+  uint4 w16[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = i0 + k * step;
     w16[k] = make_uint4(0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u);
-    b16[k] = make_uint4(0, 0, 0, 0);
+    uint4 b16 = make_uint4(0, 0, 0, 0);
     if (in(k)) {
       Eight v;
       if (p.affine.w && !p.affine.w_f32) load_row8<MODE>(false, p.affine.w, i, p.hidden, v), w16[k] = v.to_bf16();
-      if (p.affine.b && !p.affine.b_f32) load_row8<MODE>(false, p.affine.b, i, p.hidden, v), b16[k] = v.to_bf16();
+      if (p.affine.b && !p.affine.b_f32) load_row8<MODE>(false, p.affine.b, i, p.hidden, v), b16 = v.to_bf16();
     }
+    *bias_slot(k) = b16;
   }
   const Share own(MODE == kFull ? NV * 256 : warp_count<NV>(warp, p.hidden, shift));
   const Share of(lane >= warps ? 0 : MODE == kFull ? NV * 256 : warp_count<NV>(lane, p.hidden, shift));
@@ -350,19 +353,36 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
   auto output = [&](int64_t row, int stage, int flip) {
     const Moments m = join_moments(part[flip][lane < warps ? lane : 0], of, inv_hidden, p.eps);
     keep_moments(p, row, m);
+    const uint64_t minus = pair_of(-m.mean, -m.mean), rstd = pair_of(m.rstd, m.rstd);
+    auto stored = [&](int k) {
+      Eight h;
+      if (MODE != kFull) h.zero();
+      if (in(k)) read(H32, stage, k * PER + HS, h);
+      return h;
+    };
+    if (MODE != kEdges && p.kept.values) {
+      static_assert(NV == 4, "store_blocks4 takes four vectors");
+      Eight h[NV];
+#pragma unroll
+      for (int k = 0; k < NV; ++k) h[k] = stored(k);
+      store_blocks4(p.kept, true, row, p.hidden, i0, step, h);
+    }
+    Eight y[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = i0 + k * step;
-      Eight h, w, b;
-      w.from_bf16(w16[k]), b.from_bf16(b16[k]);
-      if (MODE != kFull) h.zero();
+      const Eight h = stored(k);
+      Eight w, b;
+      w.from_bf16(w16[k]), b.from_bf16(*bias_slot(k));
       if (in(k)) {
-        read(H32, stage, k * PER + HS, h);
         if (p.affine.w_f32) load_row8<MODE>(true, p.affine.w, i, p.hidden, w);
         if (p.affine.b_f32) load_row8<MODE>(true, p.affine.b, i, p.hidden, b);
       }
-      finish<OUT8, MODE>(p, row, i, in(k), m, h, w, b);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) y[k].p[j] = fma2(mul2(add2(h.p[j], minus), rstd), w.p[j], b.p[j]);
+      if (!OUT8 && in(k)) store_row8<MODE>(false, p.y, row * p.hidden, i, p.hidden, y[k]);
     }
+    if constexpr (OUT8) store_blocks4(p.y8, false, row, p.hidden, i0, step, y);
   };
 #pragma unroll
   for (int s = 0; s < STAGES; ++s) fetch(s);
@@ -557,8 +577,9 @@ constexpr int row_vectors(int hidden, bool vec) { return vec ? hidden / 8 : (hid
 template <class Kernel>
 int stream_shape(Kernel kernel, int vectors, int parts, int stages, int sms, int64_t rows, int* threads, int* blocks, int* bytes) {
   *threads = stream_threads(vectors);
-  *bytes = stages * parts * 16 * *threads;
-  const int64_t most = (int64_t)sms * (kStreamThreads / *threads);
+  *bytes = (stages * parts + kStreamVecs) * 16 * *threads;
+  const int by_threads = kStreamThreads / *threads, by_bytes = kSmBytes / (*bytes + kBlockBytes);
+  const int64_t most = (int64_t)sms * (by_threads < by_bytes ? by_threads : by_bytes);
   *blocks = (int)(rows < most ? rows : most);
   DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes));
   return DG_OK;
@@ -595,7 +616,7 @@ int run_norm(const Args& p, bool vec, bool dense, int sms, cudaStream_t s) {
   // Many long rows are streamed; few rows take as many threads as they have vectors,
   // for the shortest chain of loads.
   const int vectors = row_vectors(p.hidden, vec);
-  const bool fits = vectors <= 2048 && stream_stages(XP + RP) * kStreamVecs * (XP + RP) * 16 * stream_threads(vectors) <= kStreamBytes;
+  const bool fits = vectors <= 2048 && (stream_stages(XP + RP) * (XP + RP) + 1) * kStreamVecs * 16 * stream_threads(vectors) <= kStreamBytes;
   if (!vec) {
     if constexpr (!OUT8) {
       // 2047 x 5003: 20.8 us element by element

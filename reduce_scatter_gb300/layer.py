@@ -443,7 +443,9 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     with a bfloat16 output; with ``keep_dtype`` the graph then saves the 8-bit
     rows in place of ``h``, and the gradients are those of the formula with the
     values that they stand for (mean and deviation are the exact rows')."""
-    if torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in (x, weight, bias, residual)):
+    if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad) or
+                                    (bias is not None and bias.requires_grad) or
+                                    (residual is not None and residual.requires_grad)):
         if out_dtype != torch.bfloat16:
             raise ValueError("an 8-bit output has no gradient: call under torch.no_grad()")
         out = _LayerNorm.apply(x, weight, bias, residual, eps, keep_dtype)

@@ -137,15 +137,6 @@ __device__ __forceinline__ void unpack_fp8(uint2 u, __nv_fp8_interpretation_t fm
   }
 }
 
-__device__ __forceinline__ void unpack_fp8(uint2 u, bool e5m2, Eight& v) {
-  float f[8];
-  if (e5m2)
-    unpack_fp8(u, __NV_E5M2, f);
-  else
-    unpack_fp8(u, __NV_E4M3, f);
-  v.from_floats(f);
-}
-
 // 8-bit blocks of 1 x 128 as they are written.
 struct Blocks {
   uint8_t* values;

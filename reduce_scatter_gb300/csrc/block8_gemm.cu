@@ -148,8 +148,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
       for (Walk walk(cut, unit, units, total); ok && walk.get(w);) {
         for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
           const uint32_t buf = it & 1;
-          if (!(ok = mbar_wait_warp(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
           if (!(ok = mbar_wait_warp(p.watch, full + 8 * stage, phase, 0x300u | stage))) break;
+          if (!(ok = mbar_wait_warp(p.watch, tempty + 8 * buf, ((it >> 1) & 1) ^ 1, 0x200u | buf))) break;
           fence_after();
           const uint32_t sp = base + stage * kStage;
           const uint64_t ad = desc_k_major(sp), bd = desc_k_major(sp + kStageP);  // (MN-major: one swizzle span wide, the same fields)
@@ -157,8 +157,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
           if (elect_one()) {
 #pragma unroll
             for (uint32_t s = 0; s < 4; ++s) mma_pair<true>(d, ad + s * a_step, bd + s * b_step, p.idesc, s != 0);
-            commit_pair(empty + 8 * stage);
             commit_pair(tfull + 8 * buf);
+            commit_pair(empty + 8 * stage);
           }
           __syncwarp();
           if (++stage == kStages) stage = 0, phase ^= 1;

@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) layer_norm_kernel(const _
 constexpr int kStreamVecs = 4;       // vectors of 8 values per thread
 constexpr int kStreamThreads = 512;  // per SM (128 registers each)
 constexpr int kSmBytes = 233472, kBlockBytes = 1024 + 1024;  // shared memory of an SM, and what a block takes besides
-constexpr int kStreamBytes = 231000;  // dynamic shared memory that the streamed kernels may take, whatever the call needs
+constexpr int kStreamBytes = 231936;  // dynamic shared memory that the streamed kernels may take, whatever the call needs
 
 // XP, RP: 16-byte slots of eight values of x (1 bf16, 2 fp32) and of the
 // residual (0 none).  A row goes through two steps, with a barrier in between: its
@@ -657,11 +657,12 @@ struct GradArgs {
   void *dx, *dweight, *dbias;
   float* partial;  // weight, then bias: blocks x hidden each; null without them
   int64_t ld_dy, ld_h, ld_dh, rows;
-  int hidden, e5m2, w_f32, b_f32;
+  int hidden, w_f32, b_f32;
 };
 
-// The type of h: bf16, fp32, or 8-bit blocks of 1 x 128.
-enum { kH16 = 0, kH32 = 1, kH8 = 2 };
+// The type of h: bf16, fp32, or 8-bit blocks of 1 x 128 (of e4m3 and of e5m2 values).
+enum { kH16 = 0, kH32 = 1, kH8 = 2, kH8wide = 3 };
+__host__ __device__ constexpr bool in_blocks(int ht) { return ht >= kH8; }
 
 // 16-byte slots of a vector: dy, h, and the gradient that reaches h on its other way.
 template <int HT, bool HAS_DH>
@@ -673,10 +674,11 @@ __host__ __device__ constexpr int grad_stages() {
   return grad_parts<HT, HAS_DH>() > 2 * kStreamVecs ? 2 : 3;
 }
 
-// Shared memory of a thread: its stages, and its weights.
+// Shared memory of a group of threads: their stages and their weights, and the scales of an 8-bit h's rows.
 template <int HT, bool HAS_DH>
-__host__ __device__ constexpr int grad_bytes() {
-  return (grad_stages<HT, HAS_DH>() * grad_parts<HT, HAS_DH>() + kStreamVecs) * 16;
+__host__ __device__ constexpr int grad_bytes(int threads) {
+  return (grad_stages<HT, HAS_DH>() * grad_parts<HT, HAS_DH>() + kStreamVecs) * 16 * threads +
+         (in_blocks(HT) ? (grad_stages<HT, HAS_DH>() + 1) * threads : 0);  // (a float for 128 values, of which a thread has 32)
 }
 
 template <int BYTES>
@@ -696,7 +698,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
   constexpr int STAGES = grad_stages<HT, HAS_DH>();
   constexpr bool PIPE = STAGES > 2;
   constexpr int PARTS = grad_parts<HT, HAS_DH>();
-  const Slots<PARTS> slots{smem + threadIdx.y * (STAGES * PARTS + NV) * 16 * blockDim.x};
+  const Slots<PARTS> slots{smem + threadIdx.y * grad_bytes<HT, HAS_DH>(blockDim.x)};
+  float* const row_scales = reinterpret_cast<float*>(slots.base + (STAGES * PARTS + NV) * 16 * blockDim.x);
   // behind the stages: the weight's vectors of this thread, in bf16 (in registers they crowded out the row's)
   auto weight_slot = [&](int k) { return slots.at(0, STAGES * PARTS + k); };
   begin_kernel();
@@ -712,8 +715,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
       slots.fetch(stage, part, src);
   };
   // this thread's place in the next row to fetch
-  constexpr int HB = HT == kH8 ? 1 : hsz;  // bytes of a value of h
+  constexpr int HB = in_blocks(HT) ? 1 : hsz;  // bytes of a value of h
   uint32_t next = unit;
+  int scale_next = 0;
   const uint8_t* dy_next = static_cast<const uint8_t*>(p.dy) + ((int64_t)next * p.ld_dy + i0) * 2;
   const uint8_t* h_next = static_cast<const uint8_t*>(p.h) + ((int64_t)next * p.ld_h + i0) * HB;
   const uint8_t* dh_next = HAS_DH ? static_cast<const uint8_t*>(p.dh) + ((int64_t)next * p.ld_dh + i0) * hsz : nullptr;
@@ -724,10 +728,8 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
         if (in(k)) {
           const int i = i0 + k * step;
           copy(stage, k * PER, dy_next + k * step * 2, i, 2);
-          if constexpr (HT == kH8) {  // eight values and their scale in one slot
-            const uint32_t slot = (uint32_t)__cvta_generic_to_shared(slots.at(stage, k * PER + 1));
-            copy_small<8>(slot, h_next + k * step);
-            copy_small<4>(slot + 8, p.scales + (int64_t)next * p.s_row + (int64_t)(i >> 7) * p.s_block);
+          if constexpr (in_blocks(HT)) {
+            copy_small<8>((uint32_t)__cvta_generic_to_shared(slots.at(stage, k * PER + 1)), h_next + k * step);
           } else {
 #pragma unroll
             for (int q = 0; q < HP; ++q) copy(stage, k * PER + 1 + q, h_next + k * step * HB + 16 * q, i + 4 * q, hsz);
@@ -738,17 +740,31 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
         }
       }
     }
+    // a row's scales: one each for its first threads, which all read (so there is a place more than there are stages: the
+    // one written here was last read before a barrier)
+    if (in_blocks(HT)) {
+      if (next < rows && (int)threadIdx.x * 128 < p.hidden)
+        copy_small<4>((uint32_t)__cvta_generic_to_shared(row_scales + scale_next * (blockDim.x / 4) + threadIdx.x),
+                      p.scales + (int64_t)next * p.s_row + threadIdx.x * p.s_block);
+      scale_next = scale_next == STAGES ? 0 : scale_next + 1;
+    }
     next += units;
     dy_next += units * p.ld_dy * 2, h_next += units * p.ld_h * HB;
     if (HAS_DH) dh_next += units * p.ld_dh * hsz;
     copies_commit();
   };
-  // a row's mean (negated) and deviation, fetched ahead of their use
+  // a row's mean (negated) and deviation, fetched ahead of their use, and the place of its scales
   struct Known {
     float m, r;
+    int at;
   };
+  int scale_known = 0;
   auto known = [&](uint32_t row, Known& n) {
     if (row < rows) n.m = -__ldg(p.mean + row), n.r = __ldg(p.rstd + row);
+    if (in_blocks(HT)) {
+      n.at = scale_known * (blockDim.x / 4);
+      scale_known = scale_known == STAGES ? 0 : scale_known + 1;
+    }
   };
   Eight dw[NV], db[NV];
 #pragma unroll
@@ -770,12 +786,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
       v.from_bf16(*slots.at(stage, slot));
   };
   // dy, h - mean and the weight of vector k
-  auto read = [&](int stage, int k, uint64_t minus, Eight& dy, Eight& e, Eight& w) {
+  auto read = [&](const Known& n, int stage, int k, uint64_t minus, Eight& dy, Eight& e, Eight& w) {
     wide(false, stage, k * PER, dy);
-    if constexpr (HT == kH8) {
-      const uint4 u = *slots.at(stage, k * PER + 1);
-      const uint64_t scale = pair_of(__uint_as_float(u.z), __uint_as_float(u.z));
-      unpack_fp8(make_uint2(u.x, u.y), p.e5m2 != 0, e);
+    if constexpr (in_blocks(HT)) {
+      const float s = row_scales[n.at + ((i0 + k * step) >> 7)];
+      const uint64_t scale = pair_of(s, s);
+      float f[8];
+      unpack_fp8(*reinterpret_cast<const uint2*>(slots.at(stage, k * PER + 1)), HT == kH8 ? __NV_E4M3 : __NV_E5M2, f);
+      e.from_floats(f);
 #pragma unroll
       for (int j = 0; j < 4; ++j) e.p[j] = fma2(e.p[j], scale, minus);
     } else {
@@ -805,7 +823,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     for (int k = 0; k < NV; ++k)
       if (in(k)) {
         Eight dy, e, w;
-        read(stage, k, minus, dy, e, w);
+        read(n, stage, k, minus, dy, e, w);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           db[k].p[j] = add2(db[k].p[j], dy.p[j]);
@@ -832,7 +850,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     for (int k = 0; k < NV; ++k) {
       if (in(k)) {
         Eight dy, e, w, d;
-        read(stage, k, minus, dy, e, w);
+        read(n, stage, k, minus, dy, e, w);
         if constexpr (HAS_DH) wide(HT == kH32, stage, k * PER + 1 + HP, d);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -852,24 +870,27 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
   for (int s = 0; s < STAGES; ++s) fetch(s);
   int stage = 0, flip = 0;
   auto after = [](int s) { return s + 1 == STAGES ? 0 : s + 1; };
+  // (an 8-bit h's scales come through other threads' copies: a barrier after every wait)
   if (PIPE) {
     known(unit + units, then);
-    copies_wait<STAGES - 1>();
+    copies_wait<STAGES - 2>();
+    if (in_blocks(HT)) group_sync();
     if (unit < rows) sums(now, 0, 0);
     group_sync();
   }
   for (uint32_t row = unit; row < rows; row += units, flip ^= 1) {
     if constexpr (PIPE) {
-      copies_wait<STAGES - 2>();
       if (row + units < rows) sums(then, after(stage), flip ^ 1);
       output(now, row, stage, flip);
       now = then;
       known(row + 2 * units, then);
       fetch(stage);
+      copies_wait<STAGES - 2>();
       group_sync();
     } else {
       known(row + units, then);
       copies_wait<STAGES - 1>();
+      if (in_blocks(HT)) group_sync();
       sums(now, stage, flip);
       group_sync();
       output(now, row, stage, flip);
@@ -980,8 +1001,8 @@ __global__ void __launch_bounds__(1024) layer_norm_grad_long_kernel(const __grid
     auto value = [&](int64_t i, float& dy, float& xh, float& w) {
       float d[1], h[1], v[1] = {1.f};
       load_bf16<1>(p.dy, row * p.ld_dy + i, d);
-      if constexpr (HT == kH8)
-        h[0] = unpack_fp8x2(static_cast<const uint8_t*>(p.h)[row * p.ld_h + i], p.e5m2 ? __NV_E5M2 : __NV_E4M3).x *
+      if constexpr (in_blocks(HT))
+        h[0] = unpack_fp8x2(static_cast<const uint8_t*>(p.h)[row * p.ld_h + i], HT == kH8 ? __NV_E4M3 : __NV_E5M2).x *
                __ldg(p.scales + row * p.s_row + (i >> 7) * p.s_block);
       else
         load_any<1>(HT == kH32, p.h, row * p.ld_h + i, h);
@@ -1057,15 +1078,15 @@ int run_grad(const GradArgs& p, bool vec, bool dense, int sms, cudaStream_t s) {
   const int n = row_vectors(p.hidden, vec);
   int blocks, rc;
   // (2047 x 5003 element by element: 45 us)
-  const bool edges = HT != kH8 && !vec && dense && p.rows >= 8 && n >= 64;
-  if ((vec || edges) && n <= 2048 && grad_bytes<HT, HAS_DH>() * stream_threads(n) <= kStreamBytes) {
+  const bool edges = !in_blocks(HT) && !vec && dense && p.rows >= 8 && n >= 64;
+  if ((vec || edges) && n <= 2048 && grad_bytes<HT, HAS_DH>(stream_threads(n)) <= kStreamBytes) {
     auto* kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, kVectors>;
     if constexpr (HT != kH32)
       if (p.hidden % (32 * 8 * kStreamVecs) == 0) kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, kFull>;
-    if constexpr (HT != kH8)
+    if constexpr (!in_blocks(HT))
       if (!vec) kernel = layer_norm_grad_stream_kernel<HT, HAS_DH, kEdges>;
     DGL_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStreamBytes));
-    const int threads = stream_threads(n), bytes = grad_bytes<HT, HAS_DH>() * threads;
+    const int threads = stream_threads(n), bytes = grad_bytes<HT, HAS_DH>(threads);
     // groups of threads, each with rows of its own, that fill an SM, and one block to an SM: its groups add their
     // weight gradients up, so that fewer partial rows go through memory (4096 x 1024: 1024 blocks of one warp
     // took 17.6 us, most of it there)
@@ -1077,11 +1098,11 @@ int run_grad(const GradArgs& p, bool vec, bool dense, int sms, cudaStream_t s) {
     if (!vec) blocks = blocks / 8 * 8;  // (eight rows at least: a group's rows start at the same place in a vector)
     rc = dgl::launch(kernel, dim3(blocks), dim3(threads, groups), bytes * groups, s, p);
   } else {
-    const bool small = HT != kH8 && p.hidden <= 1024, regs = HT != kH8 && p.hidden <= 8192;
+    const bool small = !in_blocks(HT) && p.hidden <= 1024, regs = !in_blocks(HT) && p.hidden <= 8192;
     const int threads = small ? round32((p.hidden + 3) / 4) : regs ? round32((p.hidden + 15) / 16) : 1024;
     blocks = grad_blocks(p.rows, sms, (int64_t)sms * (threads < 512 ? 512 / threads : 1));
     auto* kernel = layer_norm_grad_long_kernel<HT, HAS_DH>;
-    if constexpr (HT != kH8) {
+    if constexpr (!in_blocks(HT)) {
       if (small)
         kernel = layer_norm_grad_kernel<HT == kH32, 4, HAS_DH>;
       else if (regs)
@@ -1194,9 +1215,10 @@ extern "C" int dg_layer_layer_norm_backward(const void* dy, int64_t ld_dy, const
   p.mean = mean, p.rstd = rstd, p.dx = dx, p.dweight = dweight, p.dbias = dbias;
   p.partial = sums ? static_cast<float*>(workspace) : nullptr;
   p.ld_dy = ld_dy, p.ld_h = ld_h, p.ld_dh = ld_dh, p.rows = rows, p.hidden = (int)hidden;
-  p.e5m2 = h_type == DG_TYPE_E5M2, p.w_f32 = weight_type == DG_TYPE_F32, p.b_f32 = dbias_type == DG_TYPE_F32;
+  p.w_f32 = weight_type == DG_TYPE_F32, p.b_f32 = dbias_type == DG_TYPE_F32;
   const bool dense = like_dense(dy, ld_dy, hidden) && like_dense(h, ld_h, hidden) && like_dense(dh, ld_dh, hidden) && aligned16(dx);
-  if (h8) return dh ? run_grad<kH8, true>(p, vec, false, sms, s) : run_grad<kH8, false>(p, vec, false, sms, s);
+  if (h_type == DG_TYPE_E4M3) return dh ? run_grad<kH8, true>(p, vec, false, sms, s) : run_grad<kH8, false>(p, vec, false, sms, s);
+  if (h8) return dh ? run_grad<kH8wide, true>(p, vec, false, sms, s) : run_grad<kH8wide, false>(p, vec, false, sms, s);
   if (h_type == DG_TYPE_F32) return dh ? run_grad<kH32, true>(p, vec, dense, sms, s) : run_grad<kH32, false>(p, vec, dense, sms, s);
   return dh ? run_grad<kH16, true>(p, vec, dense, sms, s) : run_grad<kH16, false>(p, vec, dense, sms, s);
 }

@@ -242,6 +242,7 @@ __global__ void __launch_bounds__(NV > 2 ? 512 : 1024) layer_norm_kernel(const _
 
 // ------------------------------------------------------------ streamed rows
 
+constexpr int kStages = 2;           // (three, or the next row's sums ahead of this one's output: 178 us instead of 167 for 8192 x 16384 to e4m3)
 constexpr int kStreamVecs = 4;       // vectors of 8 values per thread
 constexpr int kStreamThreads = 512;  // per SM (128 registers each)
 constexpr int kSmBytes = 233472, kBlockBytes = 1024 + 1024;  // shared memory of an SM, and what a block takes besides
@@ -250,15 +251,13 @@ constexpr int kStreamBytes = 231936;  // dynamic shared memory that the streamed
 // XP, RP: 16-byte slots of eight values of x (1 bf16, 2 fp32) and of the
 // residual (0 none).  A row goes through two steps, with a barrier in between: its
 // warps' moments, and the output, for which h is read from the slots again
-// (nothing is held in registers over the barrier).  With three stages the second
-// step of a row comes after the first one of the next, so that no warp waits
-// at the barrier for the slowest one's sums.
-template <int XP, int RP, bool OUT8, int MODE, int STAGES>
+// (nothing is held in registers over the barrier).
+template <int XP, int RP, bool OUT8, int MODE>
 __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const __grid_constant__ Args p) {
   extern __shared__ __align__(16) uint8_t smem[];
-  __shared__ float2 part[2][32];
+  __shared__ float2 part[2][32];  // (of two rows by turns: a warp's next sums may come before a slow one has read these)
   constexpr int NV = kStreamVecs, PER = XP + RP;
-  constexpr bool PIPE = STAGES > 2, H32 = RP == 2 || (RP == 0 && XP == 2);
+  constexpr bool H32 = RP == 2 || (RP == 0 && XP == 2);
   constexpr int HS = RP == 2 ? XP : 0;  // h's slot of a vector's
   const Slots<NV * PER> slots{smem};
   begin_kernel();
@@ -303,7 +302,7 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
       v.from_bf16(*slots.at(stage, slot));
   };
   // w in 16 bits stays in registers, b behind the stages (both in registers left too few for a row's output)
-  auto bias_slot = [&](int k) { return slots.at(0, STAGES * NV * PER + k); };
+  auto bias_slot = [&](int k) { return slots.at(0, kStages * NV * PER + k); };
   uint4 w16[NV];
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -320,7 +319,7 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
   const Share own(MODE == kFull ? NV * 256 : warp_count<NV>(warp, p.hidden, shift));
   const Share of(lane >= warps ? 0 : MODE == kFull ? NV * 256 : warp_count<NV>(lane, p.hidden, shift));
   const float inv_hidden = 1.f / (float)p.hidden;
-  auto sums = [&](int64_t row, int stage, int flip) {
+  auto sums = [&](int64_t row, int stage) {
     Eight h[NV];
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -348,10 +347,10 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
       }
     }
     const float2 m = moments_of<NV, MODE>(h, p.hidden, i0, step, own);
-    if (lane == 0) part[flip][warp] = m;
+    if (lane == 0) part[stage][warp] = m;
   };
-  auto output = [&](int64_t row, int stage, int flip) {
-    const Moments m = join_moments(part[flip][lane < warps ? lane : 0], of, inv_hidden, p.eps);
+  auto output = [&](int64_t row, int stage) {
+    const Moments m = join_moments(part[stage][lane < warps ? lane : 0], of, inv_hidden, p.eps);
     keep_moments(p, row, m);
     const uint64_t minus = pair_of(-m.mean, -m.mean), rstd = pair_of(m.rstd, m.rstd);
     auto stored = [&](int k) {
@@ -385,29 +384,14 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
     if constexpr (OUT8) store_blocks4(p.y8, false, row, p.hidden, i0, step, y);
   };
 #pragma unroll
-  for (int s = 0; s < STAGES; ++s) fetch(s);
-  int stage = 0, flip = 0;
-  auto after = [](int s) { return s + 1 == STAGES ? 0 : s + 1; };
-  if (PIPE) {
-    copies_wait<STAGES - 1>();
-    if (blockIdx.x < p.rows) sums(blockIdx.x, 0, 0);
+  for (int s = 0; s < kStages; ++s) fetch(s);
+  int stage = 0;
+  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, stage ^= 1) {
+    copies_wait<kStages - 1>();
+    sums(row, stage);
     __syncthreads();
-  }
-  for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, flip ^= 1) {
-    if constexpr (PIPE) {
-      copies_wait<STAGES - 2>();
-      if (row + gridDim.x < p.rows) sums(row + gridDim.x, after(stage), flip ^ 1);
-      output(row, stage, flip);
-      fetch(stage);
-      __syncthreads();
-    } else {
-      copies_wait<STAGES - 1>();
-      sums(row, stage, flip);
-      __syncthreads();
-      output(row, stage, flip);
-      fetch(stage);
-    }
-    stage = after(stage);
+    output(row, stage);
+    fetch(stage);
   }
   copies_wait<0>();
 }
@@ -574,10 +558,13 @@ constexpr int stream_threads(int n) { return ((n + kStreamVecs - 1) / kStreamVec
 // Vectors of a row; one that starts inside a vector takes another.
 constexpr int row_vectors(int hidden, bool vec) { return vec ? hidden / 8 : (hidden + 14) / 8; }
 
+// Shared memory of a block: its stages of `slots` 16-byte slots a vector, and the bias.
+constexpr int stream_bytes(int slots, int threads) { return (kStages * slots + 1) * kStreamVecs * 16 * threads; }
+
 template <class Kernel>
-int stream_shape(Kernel kernel, int vectors, int parts, int stages, int sms, int64_t rows, int* threads, int* blocks, int* bytes) {
+int stream_shape(Kernel kernel, int vectors, int slots, int sms, int64_t rows, int* threads, int* blocks, int* bytes) {
   *threads = stream_threads(vectors);
-  *bytes = (stages * parts + kStreamVecs) * 16 * *threads;
+  *bytes = stream_bytes(slots, *threads);
   const int by_threads = kStreamThreads / *threads, by_bytes = kSmBytes / (*bytes + kBlockBytes);
   const int64_t most = (int64_t)sms * (by_threads < by_bytes ? by_threads : by_bytes);
   *blocks = (int)(rows < most ? rows : most);
@@ -585,19 +572,15 @@ int stream_shape(Kernel kernel, int vectors, int parts, int stages, int sms, int
   return DG_OK;
 }
 
-// Stages of rows of `slots` 16-byte slots a vector (192 KB for 16384 values; two fp32 operands fit to 13 744).
-constexpr int stream_stages(int slots) { return slots > 2 ? 2 : 3; }
-
 template <int XP, int RP, bool OUT8>
 int stream_norm(const Args& p, bool vec, int sms, cudaStream_t s) {
-  constexpr int stages = stream_stages(XP + RP);
   int threads, blocks, bytes;
-  auto* kernel = layer_norm_stream_kernel<XP, RP, OUT8, kVectors, stages>;
+  auto* kernel = layer_norm_stream_kernel<XP, RP, OUT8, kVectors>;
   if constexpr (XP == 1 && RP < 2)
-    if (p.hidden % (32 * 8 * kStreamVecs) == 0) kernel = layer_norm_stream_kernel<XP, RP, OUT8, kFull, stages>;
+    if (p.hidden % (32 * 8 * kStreamVecs) == 0) kernel = layer_norm_stream_kernel<XP, RP, OUT8, kFull>;
   if constexpr (!OUT8)
-    if (!vec) kernel = layer_norm_stream_kernel<XP, RP, false, kEdges, stages>;
-  if (int rc = stream_shape(kernel, row_vectors(p.hidden, vec), kStreamVecs * (XP + RP), stages, sms, p.rows, &threads, &blocks, &bytes))
+    if (!vec) kernel = layer_norm_stream_kernel<XP, RP, false, kEdges>;
+  if (int rc = stream_shape(kernel, row_vectors(p.hidden, vec), XP + RP, sms, p.rows, &threads, &blocks, &bytes))
     return rc;
   if (!vec) blocks = blocks / 8 * 8;  // (each block's rows start at the same place in a vector)
   return dgl::launch(kernel, dim3(blocks), dim3(threads), bytes, s, p);
@@ -616,7 +599,7 @@ int run_norm(const Args& p, bool vec, bool dense, int sms, cudaStream_t s) {
   // Many long rows are streamed; few rows take as many threads as they have vectors,
   // for the shortest chain of loads.
   const int vectors = row_vectors(p.hidden, vec);
-  const bool fits = vectors <= 2048 && (stream_stages(XP + RP) * (XP + RP) + 1) * kStreamVecs * 16 * stream_threads(vectors) <= kStreamBytes;
+  const bool fits = vectors <= 2048 && stream_bytes(XP + RP, stream_threads(vectors)) <= kStreamBytes;
   if (!vec) {
     if constexpr (!OUT8) {
       // 2047 x 5003: 20.8 us element by element
@@ -669,11 +652,12 @@ template <int HT, bool HAS_DH>
 __host__ __device__ constexpr int grad_parts() {
   return kStreamVecs * (1 + (HT == kH32 ? 2 : 1) * (HAS_DH ? 2 : 1));
 }
+// Two stages; three, with the next row's sums ahead of this one's output, for rows in
+// blocks (8192 x 16384 159 us instead of 185; of 16 bits 164 instead of 146).
 template <int HT, bool HAS_DH>
 __host__ __device__ constexpr int grad_stages() {
-  return grad_parts<HT, HAS_DH>() > 2 * kStreamVecs ? 2 : 3;
+  return in_blocks(HT) && !HAS_DH ? 3 : 2;
 }
-
 // Shared memory of a group of threads: their stages and their weights, and the scales of an 8-bit h's rows.
 template <int HT, bool HAS_DH>
 __host__ __device__ constexpr int grad_bytes(int threads) {

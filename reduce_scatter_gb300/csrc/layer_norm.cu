@@ -886,26 +886,36 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
   copies_wait<0>();
   if (!p.partial) return;
   // the groups' gradients side by side in shared memory, added up in their order to one row of `partial` for the block
+  // (weight rows first, then the bias's).  A place is left out after every eight values: threads that are eight apart
+  // write to different banks (without: 3 to 6 us a call).
+  auto place = [](int c) { return c + (c >> 3); };
   __syncthreads();
+  static_assert(grad_bytes<HT, HAS_DH>(32) >= 2 * 4 * (32 * NV * 8 * 9 / 8), "a group's gradients fit into its stages");
   float* const hand = reinterpret_cast<float*>(smem);
-  const int both = 2 * p.hidden;
+  const int each = place(p.hidden), all = blockDim.x * blockDim.y;
 #pragma unroll
   for (int k = 0; k < NV; ++k)
     if (in(k)) {
-      float* to = hand + threadIdx.y * both + i0 + k * step;
+      const int i = i0 + k * step;
+      float* to = hand + threadIdx.y * 2 * each;
       float a[8], b[8];
       dw[k].to_floats(a), db[k].to_floats(b);
 #pragma unroll
       for (int j = 0; j < 8; ++j)
-        if (MODE != kEdges || (i0 + k * step + j >= 0 && i0 + k * step + j < p.hidden)) to[j] = a[j], to[p.hidden + j] = b[j];
+        if (MODE != kEdges || (i + j >= 0 && i + j < p.hidden)) to[place(i + j)] = a[j], to[each + place(i + j)] = b[j];
     }
   __syncthreads();
-  for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < both; c += blockDim.x * blockDim.y) {
-    float v = hand[c];
-    for (int g = 1; g < blockDim.y; ++g) v += hand[g * both + c];
-    // (weight rows first, then the bias's)
-    const int64_t at = c < p.hidden ? blockIdx.x : gridDim.x + blockIdx.x;
-    p.partial[at * p.hidden + (c < p.hidden ? c : c - p.hidden)] = v;
+#pragma unroll 1
+  for (int bias = 0; bias < 2; ++bias) {
+    float* to = p.partial + (int64_t)(bias * gridDim.x + blockIdx.x) * p.hidden;
+    const float* from = hand + bias * each;
+#pragma unroll 4
+    for (int c = threadIdx.y * blockDim.x + threadIdx.x; c < p.hidden; c += all) {
+      float v = from[place(c)];
+#pragma unroll 4
+      for (int g = 1; g < blockDim.y; ++g) v += from[g * 2 * each + place(c)];
+      to[c] = v;
+    }
   }
 }
 
@@ -1017,43 +1027,44 @@ __global__ void __launch_bounds__(1024) layer_norm_grad_long_kernel(const __grid
 }
 
 // The weight's and the bias's gradient (blockIdx.y): sums over the blocks' partial
-// rows, in a fixed order: 32 columns x 32 threads, each thread a strided share of
-// the rows, then a tree.
-__global__ void __launch_bounds__(1024) layer_norm_weight_grad_kernel(const __grid_constant__ GradArgs p, int blocks) {
-  __shared__ float s[32][33];
+// rows, in a fixed order: 32 columns x kSumRows threads, each thread a strided share of
+// the rows, then one after the other.  (32 threads a column: two rounds of blocks
+// for rows of 5003 values.)
+constexpr int kSumRows = 16;
+__global__ void __launch_bounds__(32 * kSumRows) layer_norm_weight_grad_kernel(const __grid_constant__ GradArgs p, int blocks) {
+  __shared__ float s[kSumRows][32];
   begin_kernel();
   const float* partial = p.partial + (blockIdx.y ? (int64_t)blocks * p.hidden : 0);
   const int64_t col = (int64_t)blockIdx.x * 32 + threadIdx.x;
   float v = 0.f;
   if (col < p.hidden)
 #pragma unroll 8
-    for (int b = threadIdx.y; b < blocks; b += 32) v += partial[(int64_t)b * p.hidden + col];
+    for (int b = threadIdx.y; b < blocks; b += kSumRows) v += __ldcg(partial + (int64_t)b * p.hidden + col);
   s[threadIdx.y][threadIdx.x] = v;
   __syncthreads();
-  v = s[threadIdx.x][threadIdx.y];
+  void* to = blockIdx.y ? p.dbias : p.dweight;
+  if (threadIdx.y != 0 || col >= p.hidden || !to) return;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  const int64_t out = (int64_t)blockIdx.x * 32 + threadIdx.y;
-  if (threadIdx.x == 0 && out < p.hidden) {
-    void* to = blockIdx.y ? p.dbias : p.dweight;
-    if (!to) return;
-    if (blockIdx.y ? p.b_f32 : p.w_f32)
-      static_cast<float*>(to)[out] = v;
-    else
-      static_cast<__nv_bfloat16*>(to)[out] = __float2bfloat16_rn(v);
-  }
+  for (int k = 1; k < kSumRows; ++k) v += s[k][threadIdx.x];
+  if (blockIdx.y ? p.b_f32 : p.w_f32)
+    static_cast<float*>(to)[col] = v;
+  else
+    static_cast<__nv_bfloat16*>(to)[col] = __float2bfloat16_rn(v);
 }
 
 // Blocks of the gradient kernels: a fixed bound that the workspace is sized by.
-constexpr int kGradBlocks = 1216;
+// (Rows of more than 4096 values take the threads of a whole SM, or of half of one.)
+int64_t most_blocks(int64_t rows, int64_t hidden) {
+  const int64_t most = hidden <= 4096 ? 1216 : 304;
+  return rows < most ? rows : most;
+}
 
-// `most` blocks fill the SMs; a block takes four rows at least where there are
+// `fill` blocks fill the SMs; a block takes four rows at least where there are
 // enough of them, so that the partial sums stay small beside the rows.
-int grad_blocks(int64_t rows, int sms, int64_t most) {
-  if (most > kGradBlocks) most = kGradBlocks;
-  const int64_t want = rows / 4 > sms ? rows / 4 : sms;
-  const int64_t n = want < most ? want : most;
-  return (int)(rows < n ? rows : n);
+int grad_blocks(int64_t rows, int64_t hidden, int sms, int64_t fill) {
+  const int64_t want = rows / 4 > sms ? rows / 4 : sms, most = most_blocks(rows, hidden);
+  const int64_t n = want < fill ? want : fill;
+  return (int)(n < most ? n : most);
 }
 
 // vec, dense: as in the forward.
@@ -1078,13 +1089,14 @@ int run_grad(const GradArgs& p, bool vec, bool dense, int sms, cudaStream_t s) {
     const int64_t want = (p.rows + sms - 1) / sms;
     const int groups = (int)(want < most ? want : most);
     const int64_t n_blocks = (p.rows + groups - 1) / groups;
-    blocks = (int)(n_blocks < sms ? n_blocks : sms);
+    const int64_t fill = sms < most_blocks(p.rows, p.hidden) ? sms : most_blocks(p.rows, p.hidden);
+    blocks = (int)(n_blocks < fill ? n_blocks : fill);
     if (!vec) blocks = blocks / 8 * 8;  // (eight rows at least: a group's rows start at the same place in a vector)
     rc = dgl::launch(kernel, dim3(blocks), dim3(threads, groups), bytes * groups, s, p);
   } else {
     const bool small = !in_blocks(HT) && p.hidden <= 1024, regs = !in_blocks(HT) && p.hidden <= 8192;
     const int threads = small ? round32((p.hidden + 3) / 4) : regs ? round32((p.hidden + 15) / 16) : 1024;
-    blocks = grad_blocks(p.rows, sms, (int64_t)sms * (threads < 512 ? 512 / threads : 1));
+    blocks = grad_blocks(p.rows, p.hidden, sms, (int64_t)sms * (threads < 512 ? 512 / threads : 1));
     auto* kernel = layer_norm_grad_long_kernel<HT, HAS_DH>;
     if constexpr (!in_blocks(HT)) {
       if (small)
@@ -1095,7 +1107,7 @@ int run_grad(const GradArgs& p, bool vec, bool dense, int sms, cudaStream_t s) {
     rc = dgl::launch(kernel, dim3(blocks), dim3(threads), 0, s, p);
   }
   if (rc != DG_OK || !p.partial) return rc;
-  return dgl::launch(layer_norm_weight_grad_kernel, dim3((unsigned)((p.hidden + 31) / 32), 2), dim3(32, 32), 0, s, p, blocks);
+  return dgl::launch(layer_norm_weight_grad_kernel, dim3((unsigned)((p.hidden + 31) / 32), 2), dim3(32, kSumRows), 0, s, p, blocks);
 }
 
 // Rows of no values: the deviation's reciprocal and the mean of nothing, a NaN.
@@ -1163,7 +1175,7 @@ extern "C" int dg_layer_layer_norm(const void* x, int64_t ld_x, int x_type, cons
 
 extern "C" size_t dg_layer_layer_norm_backward_workspace(int64_t rows, int64_t hidden) {
   if (rows <= 0 || hidden <= 0) return 0;
-  return 2 * (size_t)(rows < kGradBlocks ? rows : kGradBlocks) * (size_t)hidden * sizeof(float);
+  return 2 * (size_t)most_blocks(rows, hidden) * (size_t)hidden * sizeof(float);
 }
 
 extern "C" int dg_layer_layer_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, int h_type,

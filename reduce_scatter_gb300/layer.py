@@ -296,8 +296,9 @@ def mx4_matmul(a: MX4Tensor, b: MX4Tensor, *, out_dtype: torch.dtype = torch.bfl
 class Block8Tensor(NamedTuple):
     """A matrix in 8 bits with a scale for each block of 128: ``values`` (rows,
     cols), contiguous, float8_e4m3fn or float8_e5m2; ``scales`` float32
-    (ceil(rows / block_rows), ceil(cols / 128)), of any strides; ``block_rows``: 1 or 128, the rows that share a scale.  Stands for
-    ``values * scales``, each scale over its block."""
+    (ceil(rows / block_rows), ceil(cols / 128)), of any strides; ``block_rows``:
+    1 or 128, the rows that share a scale.  Stands for ``values * scales``, each
+    scale over its block."""
 
     values: torch.Tensor
     scales: torch.Tensor
@@ -337,15 +338,20 @@ def block8_matmul(a: Block8Tensor, b: Block8Tensor, *, trans_a: bool = False, tr
     return (_EXT or _load()).block8_matmul(a, b, bool(trans_a), bool(trans_b), out_dtype)
 
 
+def _linear8(x, weight, dtype):
+    """(the product, x and the weight in 8-bit blocks)"""
+    ext = _EXT or _load()
+    xq, wq = ext.quantize_block8(x, 128, dtype, False), ext.quantize_block8(weight, 128, dtype, False)
+    return ext.block8_matmul(xq, wq, False, True, torch.bfloat16).view(*x.shape[:-1], weight.shape[0]), xq, wq
+
+
 class _Block8Linear(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, dtype, grad_dtype):
-        ext = _EXT or _load()
-        lead, ctx.grad_dtype = x.shape[:-1], grad_dtype
-        xq, wq = ext.quantize_block8(x, 128, dtype, False), ext.quantize_block8(weight, 128, dtype, False)
-        need = ctx.needs_input_grad
+        y, xq, wq = _linear8(x, weight, dtype)
+        need, ctx.grad_dtype = ctx.needs_input_grad, grad_dtype
         ctx.save_for_backward(*(xq[:2] if need[1] else (None, None)), *(wq[:2] if need[0] else (None, None)))
-        return ext.block8_matmul(xq, wq, False, True, torch.bfloat16).view(*lead, weight.shape[0])
+        return y
 
     @staticmethod
     @once_differentiable
@@ -379,7 +385,9 @@ def block8_linear(x: torch.Tensor, weight: torch.Tensor, *, dtype: torch.dtype =
     for d in (dtype, grad_dtype):
         if d not in (torch.float8_e4m3fn, torch.float8_e5m2):
             raise ValueError(f"dtype and grad_dtype must be float8 types, got {d}")
-    return _Block8Linear.apply(x, weight, dtype, grad_dtype)
+    if torch.is_grad_enabled() and (x.requires_grad or weight.requires_grad):
+        return _Block8Linear.apply(x, weight, dtype, grad_dtype)
+    return _linear8(x, weight, dtype)[0]
 
 
 # ------------------------------------------------------------------ layer norm
@@ -442,7 +450,8 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     (``kept``), for :func:`layer_norm_backward` (H % 16 == 0).  Differentiable
     with a bfloat16 output; with ``keep_dtype`` the graph then saves the 8-bit
     rows in place of ``h``, and the gradients are those of the formula with the
-    values that they stand for (mean and deviation are the exact rows')."""
+    values that they stand for (mean and deviation are the exact rows'), those of
+    ``x`` and ``residual`` rounded to bfloat16 whatever their types."""
     if torch.is_grad_enabled() and (x.requires_grad or (weight is not None and weight.requires_grad) or
                                     (bias is not None and bias.requires_grad) or
                                     (residual is not None and residual.requires_grad)):

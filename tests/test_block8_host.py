@@ -204,3 +204,20 @@ def test_linear_refuses(L):
                         (lambda: ops.grouped_matmul(x, w.view(2, 64, 16), torch.zeros(2, dtype=torch.int32), keep_dtype=BF16), ValueError)]:
         with pytest.raises(error):
             call()
+
+
+def test_forward_mode_is_refused(L):
+    x, w = torch.ones(4, 64, dtype=BF16), torch.ones(32, 64, dtype=BF16)
+    rows = torch.ones(4)
+    with forward_ad.dual_level():
+        def dual(t):
+            return forward_ad.make_dual(t, torch.ones_like(t))
+
+        for call in (lambda: ops.block8_linear(dual(x), w), lambda: ops.layer_norm(dual(x)),
+                     lambda: ops.layer_norm(x, dual(w[0])), lambda: ops.layer_norm(x, w[0], dual(w[0])),
+                     lambda: ops.layer_norm(x, residual=dual(x)), lambda: ops.layer_norm_backward(dual(x), x, None, rows, rows),
+                     lambda: ops.layer_norm_backward(x, dual(x), None, rows, rows),
+                     lambda: ops.layer_norm_backward(x, x, None, dual(rows), rows),
+                     lambda: ops.layer_norm_backward(x, x, None, rows, rows, d_residual=dual(x))):
+            with pytest.raises(ValueError, match="forward-mode"):
+                call()

@@ -210,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                   const float t = __uint_as_float(u[i + k]);
-                  acc[c][i + k] = fmaf(COLS ? t * b : t, f[k], acc[c][i + k]);
+                  acc[c][i + k] = fmaf(t, COLS ? f[k] * b : f[k], acc[c][i + k]);
                 }
               }
             }

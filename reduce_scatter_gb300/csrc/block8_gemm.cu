@@ -10,8 +10,18 @@
 // thread), while the tensor cores fill the other one.  Rows lie on the
 // accumulator's lanes here, so that a thread's sums share their row's scale, and
 // a warp's 128 columns the scale of b's 128 x 128 block: one factor per thread
-// and K block, and no operand but the accumulator itself.  (b with a scale for
-// each row of 1 x 128 costs a product more per sum, and its scales' reads.)
+// and K block, and no operand but the accumulator itself.
+//
+// b with a scale for each row (1 x 128) costs a product more per sum, and the scales'
+// way into the registers: loads from shared memory and from tensor memory share the
+// way back, and a row a thread would read 128 column scales a K block (8192^3: 1021
+// us).  There tensor memory is read so that a thread has four rows of 32 columns (16
+// lanes at a time): a quarter of the scales, which asynchronous copies bring into a
+// ring of four K blocks in shared memory (743 us).
+//
+// Bound by the tensor cores' and the summing warps' share of tensor and shared
+// memory: 8192^3 427 us (2.6 PFLOP/s); the products alone 303, without the sums'
+// arithmetic 303, with half of it 390.
 //
 // Warp 0 loads (TMA, 128-byte swizzle), warp 1 issues the MMAs (even CTA of the
 // pair), warps 2-9 add up and store.  Either operand may lie with its other
@@ -38,6 +48,7 @@ constexpr uint32_t kSmem = kStages * kStage + kEpiWarps * 2 * kBox + 256 + 1024;
 constexpr uint32_t kTmemCols = 2 * kTile;
 constexpr int64_t kSlot = (int64_t)cut_slot_floats(kTile);
 constexpr int kBand = 8;
+constexpr int kAhead = 3;     // K blocks by which the column scales are ahead (a power of two less one)
 
 struct Args {
   CUtensorMap a, b, d;     // boxes of 128 bytes x 128 rows; of 128 bytes x 32 rows
@@ -47,6 +58,7 @@ struct Args {
   const float *sa, *sb;
   int64_t sa_m, sa_k, sb_n, sb_k;
   int a_shift, b_shift;
+  int cols_next;           // b's scales of neighbouring columns lie next to each other, in whole vectors of 16 bytes
   uint32_t idesc;
   Raster raster;
   Divider per_unit;
@@ -151,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
     const int q = warp & 3;            // the lanes that this warp may read
     const int side = (warp - 2) >> 2;  // its half of the columns
     const uint32_t box = smem_u32(boxes) + (uint32_t)(warp - 2) * 2 * kBox;
-    const uint32_t col_table = box + kBox;  // COLS: two tables of 128 column scales in the second box
+    const uint32_t col_table = box + kBox;  // COLS: the 128 column scales of kAhead + 1 K blocks by turns, in the second box
     uint32_t it = 0;
     bool ok = true;
     Item w;
@@ -165,54 +177,87 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
       uint64_t acc[64];
 #pragma unroll
       for (int i = 0; i < 64; ++i) acc[i] = 0;
-      float a_next = __ldg(sa + w.kb0 * p.sa_k), b_next[COLS ? 4 : 1];
+      float a_next = __ldg(sa + w.kb0 * p.sa_k), b_next = COLS ? 0.f : __ldg(sb + w.kb0 * p.sb_k);
+      // (copied past the registers, which the sums fill)
       auto fetch_cols = [&](int kb) {
-        if constexpr (COLS) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            b_next[i] = __ldg(p.sb + (int64_t)min(n0 + lane * 4 + i, p.cols - 1) * p.sb_n + kb * p.sb_k);
-        } else {
-          b_next[0] = __ldg(sb + kb * p.sb_k);
+        if (kb < w.kb1) {
+          const uint32_t to = col_table + (uint32_t)(kb & kAhead) * 512;
+          if (p.cols_next) {
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + lane * 16),
+                         "l"(p.sb + min(n0 + 4 * lane, p.cols - 4) + kb * p.sb_k)
+                         : "memory");
+          } else {
+#pragma unroll 1
+            for (int i = lane; i < 128; i += 32)
+              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to + i * 4),
+                           "l"(p.sb + min(n0 + i, p.cols - 1) * p.sb_n + kb * p.sb_k)
+                           : "memory");
+          }
         }
+        asm volatile("cp.async.commit_group;" ::: "memory");
       };
-      fetch_cols(w.kb0);
       if constexpr (COLS) {
         if (lane == 0) stores_read<0>();  // the last tile's stores have left the box
         __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kAhead; ++i) fetch_cols(w.kb0 + i);
       }
       for (int kb = w.kb0; kb < w.kb1; ++kb, ++it) {
         const uint32_t buf = it & 1;
-        const float s = COLS ? a_next : a_next * b_next[0];
+        const float s = COLS ? a_next : a_next * b_next;
         const uint64_t s2 = pair_of(s, s);
-        const uint32_t table = col_table + (uint32_t)(kb & 1) * 512;
-        if constexpr (COLS) {
-          asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(table + lane * 16), "f"(b_next[0]), "f"(b_next[1]),
-                       "f"(b_next[2]), "f"(b_next[3])
-                       : "memory");
-          __syncwarp();
-        }
+        const uint32_t table = col_table + (uint32_t)(kb & kAhead) * 512 + (lane & 3) * 8;  // (this thread's first columns)
+        uint64_t rows[2][2];  // COLS: the scales of the four rows that a thread reads
         const int kn = min(kb + 1, w.kb1 - 1);
         a_next = __ldg(sa + kn * p.sa_k);
-        fetch_cols(kn);
+        if constexpr (COLS) {
+          asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+          __syncwarp();  // every lane's part is there, and the table that is written next has been read
+          fetch_cols(kb + kAhead);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float r = __shfl_sync(0xffffffffu, s, 8 * i + (lane >> 2));
+            rows[i >> 1][i & 1] = pair_of(r, r);
+          }
+        } else {
+          b_next = __ldg(sb + kn * p.sb_k);
+        }
         if (!(ok = mbar_wait_warp(p.watch, tfull + 8 * buf, (it >> 1) & 1, 0x400u | buf))) break;
         fence_after();
         if (mine) {
           const uint32_t at = tmem + ((uint32_t)(q * 32) << 16) + buf * kTile + side * 128;
-          uint32_t u[2][16];
-          tmem_ld16(at, u[0]);
+          if constexpr (COLS) {
+            // steps of 16 columns, their lower and upper 16 rows
+            uint64_t cs[2];
+            uint32_t u[2][8];
+            tmem_ld_rows16(at, u[0]);
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            tmem_ld_wait(u[j & 1]);
-            if (j < 7) tmem_ld16(at + (j + 1) * 16, u[(j + 1) & 1]);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              uint64_t f = pair_of(__uint_as_float(u[j & 1][2 * i]), __uint_as_float(u[j & 1][2 * i + 1]));
-              if constexpr (COLS) {
-                uint64_t cs;
-                asm volatile("ld.shared.b64 %0, [%1];" : "=l"(cs) : "r"(table + (j * 8 + i) * 8));
-                f = mul2(f, cs);
+            for (int j = 0; j < 16; ++j) {
+              if ((j & 1) == 0) {
+                asm volatile("ld.shared.b64 %0, [%1];" : "=l"(cs[0]) : "r"(table + j * 32));
+                asm volatile("ld.shared.b64 %0, [%1];" : "=l"(cs[1]) : "r"(table + j * 32 + 32));
               }
-              acc[j * 8 + i] = fma2(f, s2, acc[j * 8 + i]);
+              uint64_t both[4];  // the products of the scales
+#pragma unroll
+              for (int i = 0; i < 4; ++i) both[i] = mul2(cs[i >> 1], rows[j & 1][i & 1]);
+              tmem_ld_wait(u[j & 1]);
+              if (j < 15) tmem_ld_rows16(at + (j + 1) / 2 * 16 + ((uint32_t)((j + 1) & 1) << 20), u[(j + 1) & 1]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                acc[j * 4 + i] = fma2(pair_of(__uint_as_float(u[j & 1][2 * i]), __uint_as_float(u[j & 1][2 * i + 1])), both[i], acc[j * 4 + i]);
+            }
+          } else {
+            uint32_t u[2][16];
+            tmem_ld16(at, u[0]);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              tmem_ld_wait(u[j & 1]);
+              if (j < 7) tmem_ld16(at + (j + 1) * 16, u[(j + 1) & 1]);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const uint64_t f = pair_of(__uint_as_float(u[j & 1][2 * i]), __uint_as_float(u[j & 1][2 * i + 1]));
+                acc[j * 8 + i] = fma2(f, s2, acc[j * 8 + i]);
+              }
             }
           }
         }
@@ -222,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
       }
       if (!ok) break;
       if (!mine) continue;
-      // 32 columns of this warp's box, from v (this lane's row)
+      // 32 columns of this warp's box, from v (this lane's row; COLS: four rows and eight columns of it, as they were read)
       auto emit = [&](int c32, const float(&v)[32]) {
         constexpr int per_box = OUT32 ? 1 : 2;  // such steps in 128 bytes
         const int b = c32 / per_box, part = c32 % per_box;
@@ -232,23 +277,37 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
           if (lane == 0) stores_read<1>();  // the store before the last one has left its box
           __syncwarp();
         }
-        const uint32_t row = to + lane * 128;
+        if constexpr (COLS) {
 #pragma unroll
-        for (int i = 0; i < (OUT32 ? 8 : 4); ++i) {
-          uint32_t x[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int i = 0; i < 16; ++i) {
+            const int row = (i & 4) * 4 + (i & 1) * 8 + (lane >> 2), col = part * 32 + (i >> 3) * 16 + (i & 2) * 4 + (lane & 3) * 2;
+            const uint32_t bytes = (uint32_t)col * (OUT32 ? 4 : 2), at = to + row * 128 + (((bytes >> 4) ^ (row & 7)) << 4) + (bytes & 15);
             if constexpr (OUT32) {
-              x[k] = __float_as_uint(v[4 * i + k]);
+              asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v[2 * i]), "f"(v[2 * i + 1]) : "memory");
             } else {
-              const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
-              x[k] = *reinterpret_cast<const uint32_t*>(&h);
+              const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+              asm volatile("st.shared.b32 [%0], %1;" ::"r"(at), "r"(*reinterpret_cast<const uint32_t*>(&h)) : "memory");
             }
           }
-          const uint32_t chunk = (uint32_t)(part * 4 + i) ^ (lane & 7);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + chunk * 16), "r"(x[0]), "r"(x[1]), "r"(x[2]),
-                       "r"(x[3])
-                       : "memory");
+        } else {
+          const uint32_t row = to + lane * 128;
+#pragma unroll
+          for (int i = 0; i < (OUT32 ? 8 : 4); ++i) {
+            uint32_t x[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              if constexpr (OUT32) {
+                x[k] = __float_as_uint(v[4 * i + k]);
+              } else {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(v[8 * i + 2 * k], v[8 * i + 2 * k + 1]);
+                x[k] = *reinterpret_cast<const uint32_t*>(&h);
+              }
+            }
+            const uint32_t chunk = (uint32_t)(part * 4 + i) ^ (lane & 7);
+            asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(row + chunk * 16), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                         "r"(x[3])
+                         : "memory");
+          }
         }
         if (part == per_box - 1) {
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -288,6 +347,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
       }
     }
     if (!ok) settle();
+    if (COLS) asm volatile("cp.async.wait_group 0;" ::: "memory");
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
   }
   fence_before();
@@ -373,6 +433,7 @@ extern "C" int dg_layer_block8_matmul(const void* a, int a_type, const float* a_
   p.partial = reinterpret_cast<float*>(p.counters + kCutCounters);
   p.watch = Watch{static_cast<unsigned long long*>(status), next_tag(), 4000000000ull};
   const bool cols = p.b_shift == 0;
+  p.cols_next = cols && p.sb_n == 1 && p.sb_k % 4 == 0 && aligned16(b_scales);
   if (cols) return f32 ? run<true, true>(p, s) : run<true, false>(p, s);
   return f32 ? run<false, true>(p, s) : run<false, false>(p, s);
 }

@@ -227,6 +227,21 @@ __device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[16]) {
                : "memory");
 }
 
+// 16 lanes x 16 columns: thread i gets columns 2 (i % 4) and the next one of lane i / 4, then of lane i / 4 + 8, and the
+// same eight columns on; and the wait for them.
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t taddr, uint32_t (&v)[8]) {
+  asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+               : "r"(taddr)
+               : "memory");
+}
+__device__ __forceinline__ void tmem_ld_wait(uint32_t (&v)[8]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7])
+               :
+               : "memory");
+}
+
 // Shared-memory descriptors of operand tiles that TMA wrote with the 128-byte
 // swizzle: version 1 (bit 46), swizzle code 2 (bits 61-63), offsets in 16-byte
 // units.  K-major: rows of 128 bytes along K, groups of 8 rows 1024 bytes apart

@@ -237,3 +237,27 @@ def test_streams_graphs_and_repetition():
         also = ops.block8_matmul(ops.quantize_block8(x), b)
         assert torch.equal(got, also)
     ops.check_products()
+
+
+@pytest.mark.parametrize("m", [5, 128, 300])
+def test_scales_whose_product_alone_is_in_range(m):
+    # 2^120 and 2^-120: the scales are multiplied with each other first, whichever blocks they belong to
+    for a_rows, b_rows in ((1, 1), (128, 1), (1, 128), (128, 128)):
+        a = ops.quantize_block8(rand((m, 512), 60), block_rows=a_rows, pow2=True)
+        b = ops.quantize_block8(rand((272, 512), 61), block_rows=b_rows, pow2=True)
+        want = check_product(a, b, False, True, F32)
+        for e in (120, -120):
+            far = ops.Block8Tensor(a.values, a.scales * 2.0 ** e, a_rows)
+            assert torch.equal(ops.block8_matmul(far, ops.Block8Tensor(b.values, b.scales * 2.0 ** -e, b_rows), out_dtype=F32), want)
+    ops.check_products()
+
+
+@pytest.mark.parametrize("m,n,k", [(129, 128, 512), (600, 1000, 1040), (2048, 8, 4096)])
+def test_column_scales_of_any_strides(m, n, k):
+    a, b = ops.quantize_block8(rand((m, k), 62)), ops.quantize_block8(rand((n, k), 63) * torch.exp(rand((n, 1), 64)))
+    want = check_product(a, b, False, True, BF16)
+    blocks = b.scales.shape[1]
+    for scales in (b.scales.contiguous(), torch.full((n, 2 * blocks + 1), float("nan"), device="cuda")[:, 1::2].copy_(b.scales),
+                   torch.empty(blocks * (n + 1) + 1, device="cuda")[1:].view(blocks, n + 1)[:, :n].t().copy_(b.scales)):
+        assert torch.equal(ops.block8_matmul(a, ops.Block8Tensor(b.values, scales, 1)), want)
+    ops.check_products()

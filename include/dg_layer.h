@@ -69,9 +69,10 @@ int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h,
  *     y = (h - mean(h)) * rsqrt(mean((h - mean(h))^2) + eps) * weight + bias
  * written as bf16 (y_type DG_TYPE_BF16), or as 8-bit blocks of 1 x 128
  * (DG_TYPE_E4M3 / E5M2; scales of block (i, j) at y_scales[i * ys_row + j *
- * ys_block]) as dg_layer_block8_quantize makes them of y in fp32.  kept: NULL,
- * or h in 8-bit blocks of 1 x 128 with power-of-two scales (kept_type), for the
- * gradient.  x, residual, weight, bias: bf16 or fp32 each; residual, weight and
+ * ys_block]) of the unrounded y: the scales of dg_layer_block8_quantize, the
+ * values by one multiplier for a block (two fp32 roundings before the last one).
+ * kept: NULL, or h in 8-bit blocks of 1 x 128 with power-of-two scales
+ * (kept_type), for the gradient: bit for bit dg_layer_block8_quantize's.  x, residual, weight, bias: bf16 or fp32 each; residual, weight and
  * bias may be NULL (then 0, 1 and 0); sum_out: h in the residual's type,
  * required with a residual.  mean_out, rstd_out: NULL, or fp32 per row.  ld_*:
  * elements from row to row; y and kept are densely packed.  Any hidden (rows of

@@ -48,13 +48,8 @@ struct Quantizer {
     if (least) c = kMinScale, num = 0x1p126f;
     if (amax == 0.f) c = num = 1.f;
   }
-  // The correctly rounded quotient from the correctly rounded reciprocal: one
-  // product and one residual (Markstein's theorem).
-  __device__ __forceinline__ float operator()(float x) const {
-    const float t = x * num, q = t * rcp;
-    return fmaf(fmaf(-den, q, t), rcp, q);
-  }
-  // The same of eight values (POW2: den is 1).
+  // The correctly rounded quotients from the correctly rounded reciprocal: one
+  // product and one residual (Markstein's theorem).  (POW2: den is 1.)
   template <bool POW2>
   __device__ __forceinline__ void all(Eight& v) const {
     const uint64_t n = pair_of(num, num), r = pair_of(rcp, rcp), d = pair_of(-den, -den);
@@ -97,7 +92,8 @@ struct Multiplier {
       c = __uint_as_float((uint32_t)f << 23);
       mul = __uint_as_float((uint32_t)(254 - f) << 23);
     } else {
-      // quotients from reciprocals and their residuals (of a power of two less where a reciprocal would be subnormal)
+      // quotients from reciprocals and their residuals, Newton's step and Markstein's (of a power of two less where a
+      // reciprocal would be subnormal)
       const float top = e5m2 ? kE5M2Max : kE4M3Max, inv = e5m2 ? 1.f / kE5M2Max : 1.f / kE4M3Max, c0 = amax * inv;
       c = fmaf(fmaf(-top, c0, amax), inv, c0);
       least = !(c > kMinScale);

@@ -205,6 +205,10 @@ __device__ __forceinline__ void store_chunk(int64_t from, int64_t hidden, const 
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
+// By way of L1, for the halves of 32 bytes that two copies share: past it each would fetch the whole from L2.
+__device__ __forceinline__ void copy_half(uint32_t dst, const void* src, int bytes = 16) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
 // The first `bytes` of 16 (zeros for the rest).
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src, int bytes) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
@@ -236,6 +240,9 @@ struct Slots {
   }
   __device__ __forceinline__ void fetch(int stage, int part, const void* src, int bytes) const {
     copy16((uint32_t)__cvta_generic_to_shared(at(stage, part)), src, bytes);
+  }
+  __device__ __forceinline__ void fetch_half(int stage, int part, const void* src, int bytes = 16) const {
+    copy_half((uint32_t)__cvta_generic_to_shared(at(stage, part)), src, bytes);
   }
   // eight values: one slot of bf16 or two of fp32
   template <bool F32>

@@ -10,6 +10,8 @@
 // last pair adds the others' up in the order of K, and the accumulators in
 // between go on filling while a pair leaves its own.  The loads of four K blocks go out
 // together, rows before K blocks, so that neighbouring addresses follow each other.
+// 8 x 8192 x 28672: 47 us (5.0 TB/s; as whole tiles of 256 rows 62), 64 x 8192 x
+// 8192 24 (31), 128 rows 30.
 
 #include "block8_few.h"
 

@@ -14,6 +14,11 @@
 // a warp, so that its largest magnitude is four shuffles away.  Many rows are
 // streamed as in norm.cu: a block walks rows, each thread with its vectors of the
 // next rows in flight into its own slots of shared memory.
+//
+// 8192 x 16384 in 16 bits: 101 us (5.3 TB/s), with a residual 185 (5.8), with a
+// residual to e4m3 166 (5.7), kept too 133; its gradient 138 (5.8), from kept rows 158.
+// What is left of the way to a copy's rate is instructions: two steps of 512 threads
+// over a row, with a barrier in between.
 
 #include "block8.cuh"
 

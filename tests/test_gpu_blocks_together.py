@@ -145,3 +145,42 @@ def test_a_weight_with_a_tangent_is_refused():
         dual = torch.autograd.forward_ad.make_dual(w, torch.ones_like(w))
         with pytest.raises(ValueError, match="forward-mode"):
             ops.block8_linear(x, dual)
+
+
+def test_a_captured_step_with_autograd():
+    # forward and backward of norm, 8-bit linear and experts with kept rows in one graph, as torch's own recipe captures them
+    x, r, g, b = rand((200, 512), 50), rand((200, 512), 51), rand((512,), 52, 0.2) + 1, rand((512,), 53, 0.1)
+    w, W = rand((256, 512), 54, 0.1), rand((3, 64, 256), 55, 0.1)
+    ends = torch.tensor([50, 50, 199], dtype=torch.int32, device="cuda")
+    leaves = [t.requires_grad_() for t in (g, b, w, W)]
+
+    def step():
+        n = ops.layer_norm(x, g, b, residual=r, keep_dtype=E4M3)
+        y = ops.grouped_matmul(ops.block8_linear(n.y, w), W.transpose(1, 2), ends, keep_dtype=E5M2)
+        (y.float().pow(2).sum() + n.residual.float().sum()).backward()
+
+    def clear():
+        for t in leaves:
+            t.grad = None
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            step()
+            clear()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    captured = [t.grad for t in leaves]
+    for seed in (56, 57):
+        x.copy_(rand(x.shape, seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in captured]
+        clear()
+        step()
+        assert all(torch.equal(a, t.grad) for a, t in zip(got, leaves))
+        clear()
+    ops.check_products()

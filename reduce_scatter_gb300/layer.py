@@ -12,6 +12,8 @@ synchronizes; each may be captured into a CUDA graph after one call outside
 capture.  ``add_rms_norm`` and ``layer_norm`` (bf16 output), ``grouped_matmul``
 (bf16) and ``block8_linear`` take part in autograd; their gradients can also be
 called directly.  No call carries on forward-mode tangents (``ValueError``).
+Where a backward pass is captured, no autograd graph of the same leaves from
+outside the capture may be alive: torch would join the streams of both.
 
 Errors: ``ValueError`` / ``TypeError`` for arguments that the front end refuses,
 ``dg.DGError`` for what the C ABI refuses.
@@ -35,8 +37,8 @@ EXT_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_lib", "dg_
 # Every symbol include/dg_layer.h declares.
 EXPORTS = ("dg_layer_add_rms_norm", "dg_layer_add_rms_norm_backward", "dg_layer_add_rms_norm_backward_workspace",
            "dg_layer_products_workspace", "dg_layer_grouped_matmul", "dg_layer_grouped_grad_workspace",
-           "dg_layer_grouped_weight_grad", "dg_layer_grouped_grad8_workspace", "dg_layer_grouped_weight_grad8", "dg_layer_mx4_scale_bytes", "dg_layer_mx4_quantize",
-           "dg_layer_mx4_dequantize", "dg_layer_mx4_matmul", "dg_layer_block8_quantize", "dg_layer_block8_dequantize",
+           "dg_layer_grouped_weight_grad", "dg_layer_grouped_grad8_workspace", "dg_layer_grouped_weight_grad8",
+           "dg_layer_mx4_scale_bytes", "dg_layer_mx4_quantize", "dg_layer_mx4_dequantize", "dg_layer_mx4_matmul", "dg_layer_block8_quantize", "dg_layer_block8_dequantize",
            "dg_layer_block8_matmul", "dg_layer_layer_norm", "dg_layer_layer_norm_backward",
            "dg_layer_layer_norm_backward_workspace", "dg_layer_check", "dg_layer_last_error")
 

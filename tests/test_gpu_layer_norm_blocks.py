@@ -341,3 +341,32 @@ def test_gradient_shapes_and_graph():
     g2 = ops.layer_norm(x, w, b, keep_stats=True, keep_dtype=E4M3)
     for one, two in zip(out, ops.layer_norm_backward(flat[0], g2.kept, w, g2.mean, g2.rstd)):
         assert torch.equal(one, two)
+
+
+# ----------------------------- rows that leave an SM one at a time, with few threads
+
+WIDE = [(310, 8200), (320, 9216), (330, 10256), (310, 12288), (400, 12280), (1000, 8208)]
+
+
+@pytest.mark.parametrize("rows,hidden", WIDE)
+@pytest.mark.parametrize("xt,rt,wt", [(BF16, None, BF16), (BF16, BF16, F32), (BF16, F32, BF16)])
+def test_wide_rows(rows, hidden, xt, rt, wt):
+    x, r, w, b = inputs(rows, hidden, 101, xt, rt, wt)
+    got = ops.layer_norm(x, w, b, residual=r, keep_stats=True)
+    h, mu, rstd, y, e_mu, e_rstd, e_y = norm64(x, r, w, b)
+    assert torch.equal(got.residual, h)
+    check_stats(got, mu, rstd, e_mu, e_rstd)
+    assert_within(got.y, y, e_y + U16 * (y.abs() + e_y), "y")
+    if hidden % 16:
+        return
+    got = ops.layer_norm(x, w, b, residual=r, out_dtype=E4M3, keep_dtype=E5M2, keep_stats=True)
+    check_blocks(got.y, y, e_y, E4M3)
+    check_stats(got, mu, rstd, e_mu, e_rstd)
+    v, c = quantized(h, 1, E5M2, True)
+    assert torch.equal(got.residual, h) and torch.equal(got.kept.scales.double(), c) and torch.equal(got.kept.values.float().double(), v)
+    x[3, hidden - 1], x[4, 0] = float("inf"), float("nan")
+    bad = ops.layer_norm(x, w, b, residual=r, out_dtype=E4M3, keep_dtype=E5M2)
+    others = torch.arange(rows, device="cuda") // 2 != 1
+    others[4] = False
+    assert torch.equal(bad.y.values.view(torch.uint8)[others], got.y.values.view(torch.uint8)[others])
+    assert torch.isnan(bad.y.values[3:5].float()).all() and not torch.isnan(bad.kept.values[3, :-1].float()).any()

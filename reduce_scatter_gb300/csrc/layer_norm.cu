@@ -137,14 +137,13 @@ __device__ __forceinline__ float2 moments_of(const Eight (&h)[NV], int hidden, i
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     const int i = i0 + k * step;
-    if (MODE == kFull || i < hidden) {
-      Eight d;
+    const uint64_t from = MODE == kFull || i < hidden ? minus : 0;  // (zeros stay zeros, without a branch)
+    Eight d;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d.p[j] = add2(h[k].p[j], minus);
-      if (MODE == kEdges && (i < 0 || i + 8 > hidden)) clip(d, i, hidden);
+    for (int j = 0; j < 4; ++j) d.p[j] = add2(h[k].p[j], from);
+    if (MODE == kEdges && (i < 0 || i + 8 > hidden)) clip(d, i, hidden);
 #pragma unroll
-      for (int j = 0; j < 4; ++j) d1 = add2(d1, d.p[j]), d2 = fma2(d.p[j], d.p[j], d2);
-    }
+    for (int j = 0; j < 4; ++j) d1 = add2(d1, d.p[j]), d2 = fma2(d.p[j], d.p[j], d2);
   }
   return warp_moments(mean, sum_of(d1), sum_of(d2), own);
 }
@@ -271,13 +270,15 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
   auto in = [&](int k) { return MODE == kFull || i0 + k * step < p.hidden; };
   // a slot of up to 16 bytes of values from i on (the start of a row that begins inside it holds the end of the row before)
   auto copy = [&](int stage, int part, const uint8_t* src, int i, int size) {  // (8192 x 8192 in fp32 past L1: 102 us, now 72)
-    const int bytes = MODE == kEdges ? min(max((p.hidden - i) * size, 0), 16) : 16;
+    // (zeros past the row, so that only stores ask where it ends: with a branch for each vector 4099 x 8208 52 us, now 47)
+    const int bytes = MODE == kFull ? 16 : MODE == kEdges ? min(max((p.hidden - i) * size, 0), 16) : i < p.hidden ? 16 : 0;
+    if (MODE != kFull && bytes == 0) src = static_cast<const uint8_t*>(p.x);
     if (size == 4)
       slots.fetch_half(stage, part, src, bytes);
-    else if (MODE == kEdges)
-      slots.fetch(stage, part, src, bytes);
-    else
+    else if (MODE == kFull)
       slots.fetch(stage, part, src);
+    else
+      slots.fetch(stage, part, src, bytes);
   };
   // this thread's place in the next row to fetch
   int64_t next = blockIdx.x;
@@ -288,14 +289,12 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
     if (next < p.rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (in(k)) {
 #pragma unroll
-          for (int q = 0; q < XP; ++q) copy(stage, k * PER + q, x_next + k * step * (2 * XP) + 16 * q, i0 + k * step + 4 * q, 2 * XP);
-          if constexpr (RP != 0)
+        for (int q = 0; q < XP; ++q) copy(stage, k * PER + q, x_next + k * step * (2 * XP) + 16 * q, i0 + k * step + 4 * q, 2 * XP);
+        if constexpr (RP != 0)
 #pragma unroll
-            for (int q = 0; q < RP; ++q)
-              copy(stage, k * PER + XP + q, r_next + k * step * (2 * RP) + 16 * q, i0 + k * step + 4 * q, 2 * RP);
-        }
+          for (int q = 0; q < RP; ++q)
+            copy(stage, k * PER + XP + q, r_next + k * step * (2 * RP) + 16 * q, i0 + k * step + 4 * q, 2 * RP);
       }
     }
     next += gridDim.x;
@@ -332,27 +331,24 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       const int i = i0 + k * step;
-      if (MODE != kFull) h[k].zero();
-      if (in(k)) {
-        read(XP == 2, stage, k * PER, h[k]);
-        if constexpr (RP != 0) {
-          Eight r;
-          read(RP == 2, stage, k * PER + XP, r);
+      read(XP == 2, stage, k * PER, h[k]);
+      if constexpr (RP != 0) {
+        Eight r;
+        read(RP == 2, stage, k * PER + XP, r);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) h[k].p[j] = add2(h[k].p[j], r.p[j]);
-          if constexpr (RP == 2) {
-            *slots.at(stage, k * PER + HS) = h[k].to_f32(0);
-            *slots.at(stage, k * PER + HS + 1) = h[k].to_f32(1);
-          } else {
-            // the norm is of the sum as it is stored, so that the gradient sees the same values
-            const uint4 u = h[k].to_bf16();
-            *slots.at(stage, k * PER) = u;
-            h[k].from_bf16(u);
-          }
-          store_row8<MODE>(RP == 2, p.sum, row * p.ld_sum, i, p.hidden, h[k]);
+        for (int j = 0; j < 4; ++j) h[k].p[j] = add2(h[k].p[j], r.p[j]);
+        if constexpr (RP == 2) {
+          *slots.at(stage, k * PER + HS) = h[k].to_f32(0);
+          *slots.at(stage, k * PER + HS + 1) = h[k].to_f32(1);
+        } else {
+          // the norm is of the sum as it is stored, so that the gradient sees the same values
+          const uint4 u = h[k].to_bf16();
+          *slots.at(stage, k * PER) = u;
+          h[k].from_bf16(u);
         }
-        if (MODE == kEdges && (i < 0 || i + 8 > p.hidden)) clip(h[k], i, p.hidden);
+        if (in(k)) store_row8<MODE>(RP == 2, p.sum, row * p.ld_sum, i, p.hidden, h[k]);
       }
+      if (MODE == kEdges && (i < 0 || i + 8 > p.hidden)) clip(h[k], i, p.hidden);
     }
     const float2 m = moments_of<NV, MODE>(h, p.hidden, i0, step, own);
     if (lane == 0) part[stage][warp] = m;
@@ -363,8 +359,7 @@ __global__ void __launch_bounds__(kStreamThreads) layer_norm_stream_kernel(const
     const uint64_t minus = pair_of(-m.mean, -m.mean), rstd = pair_of(m.rstd, m.rstd);
     auto stored = [&](int k) {
       Eight h;
-      if (MODE != kFull) h.zero();
-      if (in(k)) read(H32, stage, k * PER + HS, h);
+      read(H32, stage, k * PER + HS, h);
       return h;
     };
     if (MODE != kEdges && p.kept.values) {
@@ -690,6 +685,9 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
   constexpr int STAGES = grad_stages<HT, HAS_DH>();
   constexpr bool PIPE = STAGES > 2;
   constexpr int PARTS = grad_parts<HT, HAS_DH>();
+  // every thread takes all of its vectors, zeros past the row, and only stores ask (4099 x 8208 71 us, now 55); not where a
+  // row's scales end with it, nor where the vectors at its ends are clipped (2047 x 5003 with d_residual 34 us, 31 as it is)
+  constexpr bool ALL = MODE == kVectors && !in_blocks(HT);
   const Slots<PARTS> slots{smem + threadIdx.y * grad_bytes<HT, HAS_DH>(blockDim.x)};
   float* const row_scales = reinterpret_cast<float*>(slots.base + (STAGES * PARTS + NV) * 16 * blockDim.x);
   // behind the stages: the weight's vectors of this thread, in bf16 (in registers they crowded out the row's)
@@ -701,13 +699,14 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
   const int step = blockDim.x * 8, i0 = threadIdx.x * 8 - shift, warps = blockDim.x >> 5, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto in = [&](int k) { return MODE == kFull || i0 + k * step < p.hidden; };
   auto copy = [&](int stage, int part, const uint8_t* src, int i, int size) {  // (as in the forward)
-    const int bytes = MODE == kEdges ? min(max((p.hidden - i) * size, 0), 16) : 16;
+    const int bytes = MODE == kFull ? 16 : MODE == kEdges ? min(max((p.hidden - i) * size, 0), 16) : i < p.hidden ? 16 : 0;
+    if (MODE != kFull && bytes == 0) src = static_cast<const uint8_t*>(p.dy);
     if (size == 4)
       slots.fetch_half(stage, part, src, bytes);
-    else if (MODE == kEdges)
-      slots.fetch(stage, part, src, bytes);
-    else
+    else if (MODE == kFull)
       slots.fetch(stage, part, src);
+    else
+      slots.fetch(stage, part, src, bytes);
   };
   // this thread's place in the next row to fetch
   constexpr int HB = in_blocks(HT) ? 1 : hsz;  // bytes of a value of h
@@ -720,7 +719,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     if (next < rows) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        if (in(k)) {
+        if (ALL || in(k)) {
           const int i = i0 + k * step;
           copy(stage, k * PER, dy_next + k * step * 2, i, 2);
           if constexpr (in_blocks(HT)) {
@@ -799,7 +798,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     const int i = i0 + k * step;
     if (MODE == kEdges && (i < 0 || i + 8 > p.hidden)) clip(dy, i, p.hidden), clip(e, i, p.hidden);
     w.from_bf16(*weight_slot(k));
-    if (p.affine.w_f32) load_row8<MODE>(true, p.affine.w, i, p.hidden, w);
+    if (p.affine.w_f32 && in(k)) load_row8<MODE>(true, p.affine.w, i, p.hidden, w);
   };
   const float inv_hidden = 1.f / (float)p.hidden;
   const int first_warp = threadIdx.y * warps;
@@ -816,7 +815,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     uint64_t s1 = 0, s2 = 0;
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (in(k)) {
+      if (ALL || in(k)) {
         Eight dy, e, w;
         read(n, stage, k, minus, dy, e, w);
 #pragma unroll
@@ -843,7 +842,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
     const uint64_t m1 = pair_of(c1, c1), m2 = pair_of(c2, c2);
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
-      if (in(k)) {
+      if (ALL || in(k)) {
         Eight dy, e, w, d;
         read(n, stage, k, minus, dy, e, w);
         if constexpr (HAS_DH) wide(HT == kH32, stage, k * PER + 1 + HP, d);
@@ -855,7 +854,7 @@ __global__ void __launch_bounds__(kStreamThreads, 1) layer_norm_grad_stream_kern
           else
             d.p[j] = mul2(t, rstd);
         }
-        store_row8<MODE>(HT == kH32, p.dx, (int64_t)row * p.hidden, i0 + k * step, p.hidden, d);
+        if (in(k)) store_row8<MODE>(HT == kH32, p.dx, (int64_t)row * p.hidden, i0 + k * step, p.hidden, d);
       }
     }
   };

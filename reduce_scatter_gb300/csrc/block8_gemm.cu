@@ -267,6 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1) block8_
       }
       if (!ok) break;
       if (!mine) continue;
+      if constexpr (!COLS) {  // the last tile's stores have left the boxes, which at an edge are an odd number (a count that
+                              // goes on over the tiles, in place of the wait: other registers, 8192^3 427 -> 543 us)
+        if (lane == 0) stores_read<0>();
+        __syncwarp();
+      }
       // 32 columns of this warp's box, from v (this lane's row; COLS: four rows and eight columns of it, as they were read)
       auto emit = [&](int c32, const float(&v)[32]) {
         constexpr int per_box = OUT32 ? 1 : 2;  // such steps in 128 bytes

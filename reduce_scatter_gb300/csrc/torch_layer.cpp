@@ -734,6 +734,7 @@ PyObject* layer_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (PyTuple_Check(a[1])) {
       Block8 q(a[1], "h");
       TORCH_CHECK_VALUE(q.block_rows == 1 && q.rows == rows && q.cols == hidden, "an 8-bit h must be dy's rows in blocks of 1 x 128");
+      same_device(dy, {&q.values, &q.scales});
       q.align();
       h = q.values, scales = q.scales;
     } else {

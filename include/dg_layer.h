@@ -72,12 +72,14 @@ int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h,
  * ys_block]) of the unrounded y: the scales of dg_layer_block8_quantize, the
  * values by one multiplier for a block (two fp32 roundings before the last one).
  * kept: NULL, or h in 8-bit blocks of 1 x 128 with power-of-two scales
- * (kept_type), for the gradient: bit for bit dg_layer_block8_quantize's.  x, residual, weight, bias: bf16 or fp32 each; residual, weight and
- * bias may be NULL (then 0, 1 and 0); sum_out: h in the residual's type,
- * required with a residual.  mean_out, rstd_out: NULL, or fp32 per row.  ld_*:
- * elements from row to row; y and kept are densely packed.  Any hidden (rows of
- * no values have NaN as their mean and deviation); 8-bit blocks need hidden %
- * 16 == 0 and pointers and pitches of 16 bytes.  Statistics are computed in fp32. */
+ * (kept_type), for the gradient: bit for bit dg_layer_block8_quantize's.
+ * x, residual, weight, bias: bf16 or fp32 each; residual, weight and bias may
+ * be NULL (then 0, 1 and 0); sum_out: h in the residual's type, required with
+ * a residual.  mean_out, rstd_out: NULL, or fp32 per row.  ld_*: elements from
+ * row to row; y and kept are densely packed.  Any hidden up to 2^31 - 8193
+ * (rows of no values have NaN as their mean and deviation); 8-bit blocks need
+ * hidden % 16 == 0 and pointers and pitches of 16 bytes.  Statistics are
+ * computed in fp32. */
 int dg_layer_layer_norm(const void* x, int64_t ld_x, int x_type, const void* residual, int64_t ld_residual,
                         int residual_type, const void* weight, int weight_type, const void* bias, int bias_type,
                         void* y, int y_type, float* y_scales, int64_t ys_row, int64_t ys_block, void* sum_out,
@@ -95,7 +97,7 @@ int dg_layer_layer_norm(const void* x, int64_t ld_x, int x_type, const void* res
  * weight: NULL for 1; dweight (in weight_type), dbias (in dbias_type): NULL if not wanted.
  * workspace: dg_layer_layer_norm_backward_workspace() bytes, 16-byte aligned
  * (not needed without dweight and dbias).  The row sums are added in a fixed
- * order (the same bits every time). */
+ * order (the same bits every time).  hidden up to 2^31 - 8193. */
 size_t dg_layer_layer_norm_backward_workspace(int64_t rows, int64_t hidden);
 int dg_layer_layer_norm_backward(const void* dy, int64_t ld_dy, const void* h, int64_t ld_h, int h_type,
                                  const float* h_scales, int64_t hs_row, int64_t hs_block, const void* weight,

@@ -1193,7 +1193,7 @@ extern "C" int dg_layer_layer_norm_backward(const void* dy, int64_t ld_dy, const
                                             int weight_type, const float* mean, const float* rstd, const void* dh, int64_t ld_dh,
                                             void* dx, void* dweight, void* dbias, int dbias_type, void* workspace, int64_t rows,
                                             int64_t hidden, void* stream) {
-  if (rows < 0 || hidden < 0 || rows > INT32_MAX || hidden > INT32_MAX)
+  if (rows < 0 || hidden < 0 || rows > INT32_MAX || hidden > INT32_MAX - 8192)
     return fail(DG_ERR_ARG, "rows %lld, hidden %lld out of range", (long long)rows, (long long)hidden);
   const bool h8 = is_fp8(h_type);
   if (!h8 && !bf16_or_f32(h_type)) return fail(DG_ERR_ARG, "h is bf16, fp32, e4m3 or e5m2 (got type %d)", h_type);

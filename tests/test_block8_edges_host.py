@@ -31,3 +31,13 @@ def test_a_host_tensor_is_refused_wherever_it_starts(start):
                  lambda: ops.grouped_matmul_backward(x[:, :8], kept, B, ends)):
         with pytest.raises(ValueError, match="CUDA"):
             call()
+
+
+@pytest.mark.parametrize("hidden", [2**31 - 8191, 2**31 - 31, 2**31 - 8, 2**31 - 1])
+def test_rows_longer_than_the_norm_takes(L, hidden):
+    # (the last ones' columns, rounded up to whole blocks of threads, are beyond 32 bits)
+    grad = L.dg_layer_layer_norm_backward(16, hidden, 16, hidden, dg.TYPE_BF16, None, 1, 1, None, 0, 16, 16, None, hidden, 16, 16, 16,
+                                          dg.TYPE_BF16, 256, 1, hidden, None)
+    norm = L.dg_layer_layer_norm(16, hidden, dg.TYPE_BF16, None, 0, 0, None, 0, None, 0, 16, dg.TYPE_BF16, None, 1, 1, None, 0, None,
+                                 dg.TYPE_E4M3, None, 1, 1, None, None, 1, hidden, 1e-5, None)
+    assert grad == norm == dg.ERR_ARG and b"out of range" in L.dg_layer_last_error()

@@ -70,7 +70,8 @@ int dg_layer_add_rms_norm_backward(const void* dy, int64_t ld_dy, const void* h,
  * written as bf16 (y_type DG_TYPE_BF16), or as 8-bit blocks of 1 x 128
  * (DG_TYPE_E4M3 / E5M2; scales of block (i, j) at y_scales[i * ys_row + j *
  * ys_block]) of the unrounded y: the scales of dg_layer_block8_quantize, the
- * values by one multiplier for a block (two fp32 roundings before the last one).
+ * values by one multiplier for a block (two fp32 roundings before the last one:
+ * what lies halfway between two 8-bit values may go to either).
  * kept: NULL, or h in 8-bit blocks of 1 x 128 with power-of-two scales
  * (kept_type), for the gradient: bit for bit dg_layer_block8_quantize's.
  * x, residual, weight, bias: bf16 or fp32 each; residual, weight and bias may

@@ -77,8 +77,11 @@ __device__ __forceinline__ float block_max16(float m) {
 }
 
 // The same scale and one multiplier, for values that are themselves the result of
-// fp32 arithmetic, where nothing lies exactly halfway (or for powers of two, where
-// the product is exact): two roundings from x to the 8 bits' own.
+// fp32 arithmetic (or for powers of two, where the product is exact): two
+// roundings from x to the 8 bits' own, so what lies within 3 2^-24 of itself from
+// halfway between two 8-bit values may go to either.  Values of few bits do lie
+// there (the norm of rows of one value, or with weights of zero, is the bias): the
+// Quantizer takes the even neighbour of those, this one of the two.
 struct Multiplier {
   float c, mul;
   __device__ __forceinline__ Multiplier(float amax, bool e5m2, bool pow2) {

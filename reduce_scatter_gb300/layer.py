@@ -447,7 +447,9 @@ def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None, bias: torch.
     ``x`` (..., H), ``residual`` of x's shape, ``weight`` and ``bias`` (H,):
     bfloat16 or float32 each.  ``out_dtype``: bfloat16, or a float8 type: then
     ``y`` is a :class:`Block8Tensor` of 1 x 128 blocks, made from the unrounded
-    rows, as :func:`block8_matmul` takes it (H % 16 == 0).  ``keep_dtype``, a
+    rows, as :func:`block8_matmul` takes it (H % 16 == 0), with the scales of
+    :func:`quantize_block8` and the nearest values (either one of those halfway
+    between two).  ``keep_dtype``, a
     float8 type: ``h`` is also given in 8-bit blocks with power-of-two scales
     (``kept``), for :func:`layer_norm_backward` (H % 16 == 0).  Differentiable
     with a bfloat16 output; with ``keep_dtype`` the graph then saves the 8-bit

@@ -144,8 +144,8 @@ int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const void* A, in
 
 /* The same from rows that were kept in 8 bits: A = values (e4m3 / e5m2, T x K,
  * densely packed, 16-byte aligned) times a scale for each block of 1 x 128
- * columns, of block (i, j) at scales[i * s_row + j * s_block], rounded to bf16
- * (exact for power-of-two scales).  K % 16 == 0.  n_major: dB is experts x K x
+ * columns, of block (i, j) at scales[i * s_row + j * s_block]: the fp32 products
+ * rounded to bf16, as dg_layer_block8_dequantize gives them.  K % 16 == 0.  n_major: dB is experts x K x
  * N (dB[e, k, n]) instead.  workspace:
  * dg_layer_grouped_grad8_workspace() bytes, 16-byte aligned. */
 size_t dg_layer_grouped_grad8_workspace(int64_t T, int experts, int64_t N, int64_t K);
@@ -193,16 +193,17 @@ int dg_layer_mx4_matmul(const void* a_codes, const void* a_scales, const void* b
 int dg_layer_block8_quantize(const void* x, int64_t ld_x, int x_type, void* values, int type, float* scales,
                              int64_t s_row, int64_t s_block, int block_rows, int pow2, int64_t rows, int64_t cols,
                              void* stream);
-/* The values times their scales, as bf16 (one rounding) or fp32, densely packed, 16-byte aligned. */
+/* The values times their scales: the fp32 products, or these rounded to bf16 (exact
+ * for power-of-two scales from 2^-117 on); densely packed, 16-byte aligned. */
 int dg_layer_block8_dequantize(const void* values, int type, const float* scales, int64_t s_row, int64_t s_block,
                                int block_rows, void* y, int y_type, int64_t rows, int64_t cols, void* stream);
 /* Product of two such tensors,
  *     D[m, n] = sum over blocks j of 128 k of sa[m, j] sb[n, j] sum_{k in j} A[m, k] B[n, k]
  * (fp32 sums; a block's two scales are multiplied first, in fp32).  a holds A
  * (M x K) or, with trans_a, its transpose (K x M); b holds the transpose (N x K)
- * of the product's second matrix with trans_b, or that matrix (K x N) without.  An operand whose rows
- * are K's has blocks of 128 rows.  D: bf16 or fp32 (d_type), M x N densely
- * packed.  N % 8 == 0, the columns of a and of b % 16 == 0; M, N, K <= 2^31 - 256.
+ * of the product's second matrix with trans_b, or that matrix (K x N) without.
+ * An operand whose rows are K's has blocks of 128 rows.  D: bf16 or fp32
+ * (d_type), M x N densely packed.  N % 8 == 0, the columns of a and of b % 16 == 0; M, N, K <= 2^31 - 256.
  * workspace as for dg_layer_grouped_matmul. */
 int dg_layer_block8_matmul(const void* a, int a_type, const float* a_scales, int64_t sa_row, int64_t sa_block,
                            int a_block_rows, int trans_a, const void* b, int b_type, const float* b_scales,

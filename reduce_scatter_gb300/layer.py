@@ -246,8 +246,8 @@ def grouped_matmul_backward(dD: torch.Tensor, A: torch.Tensor | Block8Tensor | N
     (0 past the last group) and ``dB[e] = A_e.T @ dD_e`` (0 for an empty group),
     dB in B's layout; ``need``: which of the two to compute (else None).  ``A``
     may be a :class:`Block8Tensor` of 1 x 128 blocks, rows that were kept in 8
-    bits: its values enter dB in bfloat16 (exact with power-of-two scales); or
-    None where dB is not computed."""
+    bits: its values enter dB as :func:`dequantize_block8` gives them in bfloat16
+    (exact with power-of-two scales); or None where dB is not computed."""
     return (_EXT or _load()).grouped_matmul_backward(dD, A, B, group_ends, bool(need[0]), bool(need[1]))
 
 
@@ -314,7 +314,7 @@ def quantize_block8(x: torch.Tensor, *, block_rows: int = 1, dtype: torch.dtype 
     ``max|x| / top`` (``top``: the type's largest finite value; 1 for a block of
     zeros, at least 2^-126), the values nearest to ``x * top / max|x|``, ties to
     even.  ``pow2`` rounds the scale up to a power of two, so that the values
-    are exact in bfloat16.  A NaN or an infinity becomes NaN, alone, and does
+    are exact in bfloat16 (scales from 2^-117 on).  A NaN or an infinity becomes NaN, alone, and does
     not enter the scale.  cols % 16 == 0.  Not differentiable: an ``x`` that
     requires a gradient is refused outside ``torch.no_grad()``."""
     if x.requires_grad and torch.is_grad_enabled():
@@ -323,8 +323,8 @@ def quantize_block8(x: torch.Tensor, *, block_rows: int = 1, dtype: torch.dtype 
 
 
 def dequantize_block8(q: Block8Tensor, *, out_dtype: torch.dtype = torch.bfloat16) -> torch.Tensor:
-    """The (rows, cols) values of ``q`` in bfloat16 (one rounding; none for
-    power-of-two scales) or float32."""
+    """The (rows, cols) values of ``q`` in float32 (the products of value and scale),
+    or these rounded to bfloat16 (exact for power-of-two scales from 2^-117 on)."""
     return (_EXT or _load()).dequantize_block8(q, out_dtype)
 
 

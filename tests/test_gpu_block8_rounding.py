@@ -1,15 +1,15 @@
 """Where the roundings of 8-bit blocks fall: the norm's blocks of values that lie
-halfway between two 8-bit ones."""
+halfway between two 8-bit ones, values brought back with any scale."""
 
 import pytest
 import torch
 
 from reduce_scatter_gb300 import ops
 from tests.layer_common import U32, assert_within, rand
-from tests.test_gpu_block8 import FP8, pow2, quantized
+from tests.test_gpu_block8 import FP8, pow2, quantized, spread
 
 pytestmark = pytest.mark.gpu
-BF16 = torch.bfloat16
+BF16, F32 = torch.bfloat16, torch.float32
 E4M3, E5M2 = torch.float8_e4m3fn, torch.float8_e5m2
 
 
@@ -50,3 +50,18 @@ def test_norm_blocks_of_values_halfway(rows, hidden, dtype, ties):
     far = ((v.abs() / step % 1) - 0.5).abs() * step > off
     assert torch.equal(q[far], want[far])
     assert not ties or (~far).double().mean() > 0.9
+
+
+@pytest.mark.parametrize("rows,cols,block_rows", [(3, 128, 1), (200, 272, 128), (257, 1040, 1), (1000, 4112, 128)])
+@pytest.mark.parametrize("dtype", [E4M3, E5M2])
+def test_values_are_the_rounded_products(rows, cols, block_rows, dtype):
+    # value times scale in fp32, then bf16; exact for powers of two from 2^-117 on
+    q = ops.quantize_block8(rand((rows, cols), 4) * torch.exp(rand((rows, 1), 5)), block_rows=block_rows, dtype=dtype)
+    for s in (1.0, 2.0 ** -100, 2.0 ** -126 / float(q.scales.min())):
+        p = ops.Block8Tensor(q.values, q.scales * s, block_rows)
+        product = q.values.float() * spread(p.scales, block_rows, rows, cols)
+        assert torch.equal(ops.dequantize_block8(p), product.to(BF16)) and torch.equal(ops.dequantize_block8(p, out_dtype=F32), product)
+    g = torch.Generator(device="cuda").manual_seed(6)
+    powers = pow2(torch.randint(-117, 100, q.scales.shape, device="cuda", generator=g))
+    p = ops.Block8Tensor(q.values, powers.float(), block_rows)
+    assert torch.equal(ops.dequantize_block8(p).double(), q.values.float().double() * spread(powers, block_rows, rows, cols))

@@ -147,7 +147,8 @@ int dg_layer_grouped_weight_grad(const void* dD, int64_t ld_d, const void* A, in
  * columns, of block (i, j) at scales[i * s_row + j * s_block]: the fp32 products
  * rounded to bf16, as dg_layer_block8_dequantize gives them.  K % 16 == 0.  n_major: dB is experts x K x
  * N (dB[e, k, n]) instead.  workspace:
- * dg_layer_grouped_grad8_workspace() bytes, 16-byte aligned. */
+ * dg_layer_grouped_grad8_workspace() bytes, 16-byte aligned; the T x K bf16
+ * values are in it. */
 size_t dg_layer_grouped_grad8_workspace(int64_t T, int experts, int64_t N, int64_t K);
 int dg_layer_grouped_weight_grad8(const void* dD, int64_t ld_d, const void* values, int type, const float* scales,
                                   int64_t s_row, int64_t s_block, const int32_t* ends, int experts, void* dB,

@@ -228,7 +228,8 @@ def grouped_matmul(A: torch.Tensor, B: torch.Tensor, group_ends: torch.Tensor, *
     and N % 8 == 0.  Differentiable in bfloat16 without scales (the gradients are
     products of bfloat16 operands, accumulated in fp32).  ``keep_dtype``, a float8
     type: the graph keeps A's rows in 8 bits (blocks of 1 x 128, power-of-two
-    scales) for B's gradient, half the memory; K % 16 == 0."""
+    scales) for B's gradient, half the memory between the passes; while the
+    gradient is computed, a bfloat16 copy of all rows is there too.  K % 16 == 0."""
     if keep_dtype is not None and keep_dtype not in (torch.float8_e4m3fn, torch.float8_e5m2):
         raise ValueError(f"keep_dtype must be a float8 type, got {keep_dtype}")
     if torch.is_grad_enabled() and (A.requires_grad or B.requires_grad or
@@ -247,7 +248,8 @@ def grouped_matmul_backward(dD: torch.Tensor, A: torch.Tensor | Block8Tensor | N
     dB in B's layout; ``need``: which of the two to compute (else None).  ``A``
     may be a :class:`Block8Tensor` of 1 x 128 blocks, rows that were kept in 8
     bits: its values enter dB as :func:`dequantize_block8` gives them in bfloat16
-    (exact with power-of-two scales); or None where dB is not computed."""
+    (exact with power-of-two scales), through a workspace of T x K of them; or
+    None where dB is not computed."""
     return (_EXT or _load()).grouped_matmul_backward(dD, A, B, group_ends, bool(need[0]), bool(need[1]))
 
 

@@ -228,6 +228,4 @@ __device__ __forceinline__ void store_blocks4(const Blocks& o, bool pow2, int64_
   }
 }
 
-inline bool is_fp8(int t) { return t == DG_TYPE_E4M3 || t == DG_TYPE_E5M2; }
-
 }  // namespace dgl

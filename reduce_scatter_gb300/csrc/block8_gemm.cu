@@ -374,8 +374,6 @@ int run(Args& p, cudaStream_t s) {
   return dgl::launch(block8_kernel<COLS, OUT32>, dim3((unsigned)(sms / 2 * 2)), dim3(kThreads), kSmem, s, p);
 }
 
-bool is8(int type) { return type == DG_TYPE_E4M3 || type == DG_TYPE_E5M2; }
-
 constexpr int64_t kMaxSize = INT32_MAX - 255;
 
 // One operand: its map, and the strides of its scales.
@@ -397,7 +395,7 @@ extern "C" int dg_layer_block8_matmul(const void* a, int a_type, const float* a_
                                       int64_t M, int64_t N, int64_t K, void* workspace, void* status, void* stream) {
   if (M < 0 || N < 0 || K < 0 || M > kMaxSize || N > kMaxSize || K > kMaxSize)
     return fail(DG_ERR_ARG, "M %lld, N %lld, K %lld out of range", (long long)M, (long long)N, (long long)K);
-  if (!is8(a_type) || !is8(b_type)) return fail(DG_ERR_ARG, "a and b hold e4m3 or e5m2 (types %d, %d)", a_type, b_type);
+  if (!is_fp8(a_type) || !is_fp8(b_type)) return fail(DG_ERR_ARG, "a and b hold e4m3 or e5m2 (types %d, %d)", a_type, b_type);
   if (d_type != DG_TYPE_BF16 && d_type != DG_TYPE_F32) return fail(DG_ERR_ARG, "D is bf16 or fp32 (got type %d)", d_type);
   if ((a_block_rows != 1 && a_block_rows != 128) || (b_block_rows != 1 && b_block_rows != 128))
     return fail(DG_ERR_ARG, "a block has 1 or 128 rows (got %d, %d)", a_block_rows, b_block_rows);

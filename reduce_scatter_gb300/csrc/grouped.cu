@@ -548,7 +548,6 @@ int run(Args& p, int64_t most_tiles, cudaStream_t s) {
 }
 
 uint32_t format_of(int type) { return type == DG_TYPE_BF16 ? 1u : type == DG_TYPE_E5M2 ? 1u : 0u; }
-bool is8(int type) { return type == DG_TYPE_E4M3 || type == DG_TYPE_E5M2; }
 
 // A size rounded up to whole tiles or K blocks, and their first coordinates, fit 32 bits.
 constexpr int64_t kMaxSize = INT32_MAX - 255;
@@ -578,7 +577,7 @@ extern "C" int dg_layer_grouped_matmul(const void* A, int64_t ld_a, int a_type, 
                                        int64_t sb_n, void* D, int d_type, int64_t T, int64_t N, int64_t K,
                                        void* workspace, void* status, void* stream) {
   if (int rc = check_sizes(T, N, K, experts)) return rc;
-  const bool f8 = is8(a_type) && is8(b_type);
+  const bool f8 = is_fp8(a_type) && is_fp8(b_type);
   if (!f8 && (a_type != DG_TYPE_BF16 || b_type != DG_TYPE_BF16))
     return fail(DG_ERR_ARG, "A and B are both bf16 or both 8-bit (types %d, %d)", a_type, b_type);
   if (f8 && b_n_major) return fail(DG_ERR_ARG, "an 8-bit B must be contiguous along K");
@@ -683,7 +682,7 @@ extern "C" int dg_layer_grouped_weight_grad8(const void* dD, int64_t ld_d, const
                                              int d_type, int64_t T, int64_t N, int64_t K, void* workspace,
                                              void* products_workspace, void* status, void* stream) {
   if (int rc = check_sizes(T, N, K, experts)) return rc;
-  if (!is8(type)) return fail(DG_ERR_ARG, "8-bit blocks hold e4m3 or e5m2 (got type %d)", type);
+  if (!is_fp8(type)) return fail(DG_ERR_ARG, "8-bit blocks hold e4m3 or e5m2 (got type %d)", type);
   if (K % 16) return fail(DG_ERR_SHAPE, "K %% 16 must be 0 (got %lld)", (long long)K);
   if (d_type != DG_TYPE_BF16 && d_type != DG_TYPE_F32) return fail(DG_ERR_ARG, "dB is bf16 or fp32 (got type %d)", d_type);
   if (N % 8) return fail(DG_ERR_SHAPE, "N %% 8 must be 0 (got %lld)", (long long)N);

@@ -45,6 +45,7 @@ int encode_map(CUtensorMap* map, const void* base, int esz, int rank, const int6
 // row tiles.
 int encode_scale_map(CUtensorMap* map, const void* base, int64_t kblocks, int64_t row_tiles, int box_tiles);
 
+inline bool is_fp8(int type) { return type == DG_TYPE_E4M3 || type == DG_TYPE_E5M2; }
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 }  // namespace dgl

@@ -14,14 +14,15 @@
 //
 // b with a scale for each row (1 x 128) costs a product more per sum, and the scales'
 // way into the registers: loads from shared memory and from tensor memory share the
-// way back, and a row a thread would read 128 column scales a K block (8192^3: 1021
+// way back, and a row a thread would read 128 column scales a K block (8192^3: 1233
 // us).  There tensor memory is read so that a thread has four rows of 32 columns (16
 // lanes at a time): a quarter of the scales, which asynchronous copies bring into a
-// ring of four K blocks in shared memory (743 us).
+// ring of four K blocks in shared memory (745 us).
 //
 // Bound by the tensor cores' and the summing warps' share of tensor and shared
 // memory: 8192^3 427 us (2.6 PFLOP/s); the products alone 303, without the sums'
-// arithmetic 303, with half of it 390.
+// arithmetic 303, with half of it 390.  To fp32 657 us with the same loop: it is
+// sensitive to where the compiler keeps the sums (see the stores' wait below).
 //
 // Warp 0 loads (TMA, 128-byte swizzle), warp 1 issues the MMAs (even CTA of the
 // pair), warps 2-9 add up and store.  Either operand may lie with its other
